@@ -255,12 +255,201 @@ fa_status fa_bias_gelu_dropout(const void *x, const void *bias, const uint32_t *
                                int64_t rows, int64_t cols, float p, fa_stream_t stream);
 
 /*
+ * fa_rope — rotary positions of queries and keys, and their gradient.
+ *
+ * The first `rot` channels of every row are taken in pairs; pair i of a row
+ * at position t is turned by the angle t * f_i and scaled:
+ *     a' = factor * (a cos(t f_i) - b sin(t f_i))
+ *     b' = factor * (b cos(t f_i) + a sin(t f_i))
+ * Channels from rot on are copied.  Angles are exact for any position: the
+ * frequencies are 64-bit fractions of a turn, and position times frequency
+ * modulo one turn is an integer product.  Results are rounded to bf16 once.
+ *
+ * Arguments
+ *   q, k       device pointers, bf16, (B, Hq, N, d) and (B, Hk, N, d); k may be
+ *              NULL (then k_out is NULL and Hk 0).
+ *   q_strides, k_strides, q_out_strides, k_out_strides
+ *              host pointers to the views' three strides in elements (batch,
+ *              head, position; channels adjoin), or NULL for contiguous.
+ *              Any non-negative strides for the inputs (0 repeats); outputs
+ *              may not repeat a place.  Rows and strides that are 16-byte
+ *              aligned run fast, others are handled a pair at a time.
+ *   q_out, k_out  the results; each may be its own input (same pointer and
+ *              strides), and may share no place with anything else.
+ *   freqs      device pointer, rot/2 uint64: f_i / (2 pi) * 2^64, rounded
+ *              (turns per position in units of 2^-64 of a turn).
+ *   rot        turned channels: even, 2 .. d.  d: a multiple of 8 from 8 to 128.
+ *   interleaved  0: pair i is channels (i, i + rot/2); 1: channels (2i, 2i + 1).
+ *   factor     finite; scales the turned channels (1, or what a long-context
+ *              scaling asks for).
+ *   inverse    1: the transposed map (angles negated, same factor), which is
+ *              the gradient: given dLoss/dq_out and dLoss/dk_out as q and k, it
+ *              gives dLoss/dq and dLoss/dk.
+ *   positions  device pointer, (B, N) integers of position_bytes (4 or 8) each,
+ *              batches position_stride elements apart (0: one row for all), or
+ *              NULL.  Negative positions turn backwards.
+ *   lens       device pointer, int32 (B), or NULL: row i stands at position
+ *              lens[b] - N + i (the newest N of a sequence).  With neither,
+ *              row i stands at position i; both is FA_ERR_INVALID_ARG.
+ *   stream     CUDA stream the one launch is enqueued on.
+ *
+ * Errors: FA_ERR_INVALID_ARG (null pointers, sizes, overlaps, strides that
+ * overlap), FA_ERR_UNSUPPORTED (d, misaligned pointers: 2 bytes for tensors, 8
+ * for freqs, their size for positions and lens).  Ownership, asynchrony and
+ * launch as for fa_fwd.
+ */
+fa_status fa_rope(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, void *q_out,
+                  const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides, int64_t B, int64_t Hq,
+                  int64_t Hk, int64_t N, int64_t d, const uint64_t *freqs, int64_t rot, int interleaved, float factor,
+                  int inverse, const void *positions, int position_bytes, int64_t position_stride,
+                  const int32_t *lens, fa_stream_t stream);
+
+/*
+ * The 4-bit cache (fa_qcache_*): keys and values of decode in pages, 9/16 byte
+ * a value.
+ *
+ * A stored value is e2m1 * e4m3 * scale: a code of sign, two exponent bits and
+ * one mantissa bit (0, .5, 1, 1.5, 2, 3, 4, 6), one e4m3 scale for 16 channels
+ * of a row, and one fp32 scale a tensor (k_scale, v_scale: the same in every
+ * call on a cache; with 1, blocks whose largest magnitude lies between 0.1 and
+ * 2688 are held at full precision).  Rounding: the block's scale is the
+ * largest magnitude / (6 * scale) to the nearest e4m3 (at most 448, 0 below
+ * 2^-10), each code the nearest to value / (e4m3 * scale), halves to even,
+ * magnitudes beyond 6 to 6.  Infinities are held as the largest value of their
+ * block, NaN as the largest positive one.
+ *
+ * Shared arguments
+ *   pool      device pointer, 16-byte aligned: num_pages * Hkv blocks of
+ *             72 * D bytes, D = 64 for d <= 64, else 128 (channels past d are
+ *             held as zeros).  Block (page, head) is block page * Hkv + head
+ *             and holds 64 keys and values of one kv head.  Its layout, with
+ *             key x = 0..63, channel c, channel block b = 0 .. D/16-1, p = D/64:
+ *               K codes   byte x*D/2 + c/2 (low nibble the even channel)
+ *               K scales  byte 32*D + ((x%8)*4 + b/p)*8*p + (x/8)*p + b%p
+ *               V codes   byte 36*D + (x/2)*D + c (low nibble the even key)
+ *               V scales  byte 68*D + (((x/2)%4)*D/16 + b)*16 + (x/8)*2 + x%2
+ *   table     device pointer, int32 (B, max_pages): key j of sequence b lies in
+ *             page table[b][j / 64], row j % 64.  Entries past a sequence's
+ *             last page are not read.
+ *   lens      device pointer, int32 (B): keys of each sequence, new ones
+ *             included; 0 is a sequence without keys (negative counts as 0).
+ *   Hkv       kv heads.  d: a multiple of 8 from 8 to 128.
+ *   B <= 65535, num_pages * Hkv and B * max_pages * 64 below 2^31.
+ * Lengths and tables are read on the device when the call runs, so a captured
+ * call follows their values at replay.  An entry outside 0 .. num_pages-1 and
+ * a length beyond max_pages * 64 are skipped (no such key is read or written)
+ * and reported by fa_check_device_status as FA_ERR_INVALID_ARG.  Ownership,
+ * asynchrony, launches and overlaps as for fa_fwd: a written tensor may
+ * overlap nothing else of the call unless said otherwise.
+ */
+
+/*
+ * fa_qcache_append — rounds the newest N keys and values of every sequence
+ * into the cache: row i of k and v becomes key lens[b] - N + i.  Rows of
+ * negative position are padding (prompts of unequal lengths aligned at their
+ * ends) and are skipped.  Nothing but the new keys' places changes.
+ *   k, v      device pointers, bf16, 16-byte aligned, (B, Hkv, N, d) with strides
+ *             in elements (batch, head, position; multiples of 8), or NULL
+ *             for contiguous.
+ *   k_scale, v_scale  finite, > 0.
+ * No two sequences of a call may append to one page.
+ */
+fa_status fa_qcache_append(const void *k, const int64_t *k_strides, const void *v, const int64_t *v_strides,
+                           int64_t B, int64_t Hkv, int64_t N, int64_t d, float k_scale, float v_scale, void *pool,
+                           int64_t num_pages, const int32_t *table, int64_t max_pages, const int32_t *lens,
+                           fa_stream_t stream);
+
+/*
+ * fa_qcache_read — the cache's keys and values as bf16 (each stored value
+ * rounded once), contiguous (B, Hkv, N, d), 16-byte aligned: keys 0 .. N-1 of
+ * every sequence, or with newest = 1 keys lens[b] - N .. lens[b] - 1.  Rows
+ * where no key is are zero.
+ */
+fa_status fa_qcache_read(const void *pool, int64_t num_pages, const int32_t *table, int64_t max_pages,
+                         const int32_t *lens, void *k, void *v, int64_t B, int64_t Hkv, int64_t N, int64_t d,
+                         int newest, float k_scale, float v_scale, fa_stream_t stream);
+
+/*
+ * fa_qcache_decode_workspace_bytes — workspace of fa_qcache_decode for these
+ * sizes on the current device.
+ */
+fa_status fa_qcache_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t d,
+                                           int64_t max_pages, size_t *bytes);
+
+/*
+ * fa_qcache_decode — attention of a few query rows against the 4-bit cache:
+ * fa_decode's operation over the stored values, with grouped heads and
+ * sequences of unequal lengths.  Query head h reads kv head h / (H / Hkv);
+ * query i of sequence b sees keys 0 .. lens[b]-1, or with causal = 1 keys
+ * 0 .. lens[b] - Nq + i.  A query that sees no key gives O = 0 and
+ * L = -infinity.
+ *   q         device pointer, bf16, contiguous (B, H, Nq, d), 16-byte aligned;
+ *             1 <= Nq <= 8, H a multiple of Hkv, B <= 2048.
+ *   o         bf16 (B, H, Nq, d), lse fp32 (B, H, Nq): fully written.
+ *   causal    0 or 1.  scale, k_scale, v_scale: finite, > 0.
+ *   workspace, workspace_bytes
+ *             device scratch, 16-byte aligned, of at least
+ *             fa_qcache_decode_workspace_bytes(...).  Nothing in it needs to
+ *             start at zero; calls that may run at the same time must not
+ *             share it.
+ * The work is divided from the lengths on the device; results do not depend
+ * on timing.
+ */
+fa_status fa_qcache_decode(const void *q, const void *pool, int64_t num_pages, const int32_t *table,
+                           int64_t max_pages, const int32_t *lens, void *o, float *lse, int64_t B, int64_t H,
+                           int64_t Hkv, int64_t Nq, int64_t d, int causal, float scale, float k_scale, float v_scale,
+                           void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_qcache_weights — adds up the attention weight each cached key receives,
+ * the measure that fa_qcache_evict goes by:
+ *     weights_out[b][h][j] = weights[b][h][j] + sum over the query rows of kv
+ *     head h that see key j of exp(scale * q . k_j - lse)
+ * for j < lens[b]; other entries are copied.
+ *   q, causal, scale, k_scale, and the cache  as for fa_qcache_decode.
+ *   lse       fp32 (B, H, Nq), as fa_qcache_decode returned it (rows of
+ *             -infinity give nothing).
+ *   weights, weights_out  fp32 (B, Hkv, W); they may be the same tensor.  Keys
+ *             from W on are not counted.
+ */
+fa_status fa_qcache_weights(const void *q, const float *lse, const void *pool, int64_t num_pages,
+                            const int32_t *table, int64_t max_pages, const int32_t *lens, const float *weights,
+                            float *weights_out, int64_t W, int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t d,
+                            int causal, float scale, float k_scale, fa_stream_t stream);
+
+/*
+ * fa_qcache_evict — cuts every sequence back to `keep` keys.  Each kv head
+ * keeps the first `sink` keys, the last `recent`, and of those between the
+ * keep - sink - recent with the largest weights (of equal weights the lowest
+ * positions; -0 equals 0; NaN counts as less than any number).  Sequences of
+ * at most `keep` keys keep them all.  Kept keys stay in order and move to
+ * places 0, 1, ... of table_out.
+ *   table_out device pointer, int32 (B, max_pages_out), with room for the kept
+ *             keys.  Per sequence its pages are either the first pages of
+ *             `table` (the cache is compacted in place) or pages that hold no
+ *             key that this call reads; two sequences share none.
+ *   weights   fp32 (B, Hkv, W); a key from W on counts as weight 0.
+ *   weights_out  fp32 (B, Hkv, W): the kept keys' weights at their new places,
+ *             0 after them.
+ *   kept      int32 (B, Hkv, keep): the former place of each kept key, rising;
+ *             -1 after the last.
+ *   lens_out  int32 (B): min(lens, keep).
+ *   keep >= 1, sink >= 0, recent >= 0, sink + recent <= keep.
+ * Places of the last destination page behind the kept keys are cleared.
+ */
+fa_status fa_qcache_evict(void *pool, int64_t num_pages, const int32_t *table, int64_t max_pages, const int32_t *lens,
+                          const int32_t *table_out, int64_t max_pages_out, const float *weights, float *weights_out,
+                          int64_t W, int32_t *kept, int32_t *lens_out, int64_t B, int64_t Hkv, int64_t d,
+                          int64_t keep, int64_t sink, int64_t recent, fa_stream_t stream);
+
+/*
  * fa_check_device_status — synchronises `stream`, reads and clears the
  * device-side status word of the current device.  Returns FA_ERR_TIMEOUT if a
  * kernel launched since the last check gave up a bounded wait (its outputs are
  * then incomplete), FA_ERR_CUDA if the copy or synchronisation failed or a
  * kernel refused to run (shared memory not 1024-byte aligned), FA_OK
- * otherwise.  `where`, if not NULL, receives the code of the first wait that
+ * otherwise; FA_ERR_INVALID_ARG if a cache call met a page or a length outside
+ * its pool or page table (and skipped it).  `where`, if not NULL, receives the code of the first wait that
  * gave up (0 if none).
  *
  * The status word is per device, not per stream: it collects the reports of
@@ -276,7 +465,8 @@ fa_status fa_check_device_status(fa_stream_t stream, uint32_t *where);
  * fa_get_device_status — fa_check_device_status without the wait code:
  * synchronises `stream`, reads and clears the device status word of the
  * current device, and returns FA_OK, FA_ERR_TIMEOUT (a kernel gave up a
- * bounded wait; its outputs are incomplete) or FA_ERR_CUDA.  The deferred
+ * bounded wait; its outputs are incomplete), FA_ERR_INVALID_ARG (a page or
+ * length out of range was skipped) or FA_ERR_CUDA.  The deferred
  * report of errors that happen inside a launch ("Writing and Benchmarking
  * Custom Kernels" §10.2.1: kernel errors surface only at a later
  * synchronisation).

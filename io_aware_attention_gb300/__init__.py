@@ -26,6 +26,22 @@ sizes).
 is the fused elementwise chain (bias add, tanh GELU, dropout with a packed
 keep mask drawn by the caller) in one HBM read and one write.
 
+    freqs, factor = io_aware_attention_gb300.rope_frequencies(d, base=10000.0)
+    q, k = io_aware_attention_gb300.rope(q, k, freqs, factor=factor)
+    dq, dk = io_aware_attention_gb300.rope_bwd(dq, dk, freqs, factor=factor)
+
+turns queries and keys by their positions (half or interleaved pairs, all or
+part of the head, any position), and gives the gradient.
+
+    pool = io_aware_attention_gb300.qcache_pool(num_pages, Hkv, d)
+    io_aware_attention_gb300.qcache_append(k, v, pool, table, lens)
+    o, lse = io_aware_attention_gb300.qcache_decode(q, pool, table, lens)
+    weights = io_aware_attention_gb300.qcache_weights(q, lse, pool, table, lens, weights)
+    kept, lens, weights = io_aware_attention_gb300.qcache_evict(pool, table, lens, weights, keep)
+
+is decode over a paged cache held in 4 bits: grouped heads, sequences of
+unequal lengths, and eviction of the keys that gathered the least attention.
+
 The ``*_into`` forms write into caller-provided tensors; their shapes, dtypes
 and devices are checked here, because the C ABI sees only pointers and sizes.
 Work is enqueued on ``stream``, by default the current stream, of the current
@@ -42,11 +58,15 @@ import os
 from . import _build
 
 __all__ = ["fwd", "fwd_into", "bwd", "bwd_into", "bwd_workspace_bytes", "bias_gelu_dropout", "decode", "decode_into", "decode_workspace_bytes", "check_device_status", "get_device_status",
+           "rope", "rope_into", "rope_bwd", "rope_frequencies", "qcache_pool", "qcache_append", "qcache_read",
+           "qcache_decode", "qcache_decode_into", "qcache_decode_workspace_bytes", "qcache_weights", "qcache_evict",
            "set_wait_limit_ns", "debug_skip_k_tile", "debug_set_schedule", "FaError", "library", "library_path", "version", "STATUS"]
 
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_CUDA",
           4: "FA_ERR_TIMEOUT", 5: "FA_ERR_TOO_LARGE"}
-EXPORTS = ["fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_bias_gelu_dropout", "fa_decode", "fa_decode_workspace_bytes", "fa_decode_static", "fa_check_device_status", "fa_get_device_status",
+EXPORTS = ["fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_bias_gelu_dropout", "fa_decode", "fa_decode_workspace_bytes", "fa_decode_static",
+           "fa_rope", "fa_qcache_append", "fa_qcache_read", "fa_qcache_decode", "fa_qcache_decode_workspace_bytes",
+           "fa_qcache_weights", "fa_qcache_evict", "fa_check_device_status", "fa_get_device_status",
            "fa_set_wait_limit_ns", "fa_debug_skip_k_tile", "fa_debug_set_schedule", "fa_debug_decode_plan", "fa_status_string",
            "fa_version"]
 
@@ -94,6 +114,21 @@ def library():
     lib.fa_decode_static.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, ctypes.c_int, ctypes.c_float,
                                      vp]
     lib.fa_decode_static.restype = ctypes.c_int
+    ci, cf, sz = ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    lib.fa_rope.argtypes = [vp] * 8 + [i64] * 5 + [vp, i64, ci, cf, ci, vp, ci, i64, vp, vp]
+    lib.fa_rope.restype = ctypes.c_int
+    lib.fa_qcache_append.argtypes = [vp] * 4 + [i64] * 4 + [cf, cf, vp, i64, vp, i64, vp, vp]
+    lib.fa_qcache_append.restype = ctypes.c_int
+    lib.fa_qcache_read.argtypes = [vp, i64, vp, i64, vp, vp, vp] + [i64] * 4 + [ci, cf, cf, vp]
+    lib.fa_qcache_read.restype = ctypes.c_int
+    lib.fa_qcache_decode.argtypes = [vp, vp, i64, vp, i64, vp, vp, vp] + [i64] * 5 + [ci, cf, cf, cf, vp, sz, vp]
+    lib.fa_qcache_decode.restype = ctypes.c_int
+    lib.fa_qcache_decode_workspace_bytes.argtypes = [i64] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.fa_qcache_decode_workspace_bytes.restype = ctypes.c_int
+    lib.fa_qcache_weights.argtypes = [vp, vp, vp, i64, vp, i64, vp, vp, vp] + [i64] * 6 + [ci, cf, cf, vp]
+    lib.fa_qcache_weights.restype = ctypes.c_int
+    lib.fa_qcache_evict.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, vp] + [i64] * 6 + [vp]
+    lib.fa_qcache_evict.restype = ctypes.c_int
     lib.fa_check_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.fa_check_device_status.restype = ctypes.c_int
     lib.fa_get_device_status.argtypes = [vp]
@@ -377,9 +412,348 @@ def decode(q, k, v, causal: bool = False, scale: float | None = None, stream=Non
         return decode_into(q, k, v, o, lse, ws, causal, scale, stream)
 
 
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: int = 0, slow: float = 1.0, fast: float = 32.0, device="cuda"):
+    """The frequencies of rotary positions over ``rot`` channels, for
+    :func:`rope`: an int64 tensor (rot/2) of turns per position in units of
+    2^-64 of a turn, and the factor that scales the turned channels.
+
+    Pair i turns base ** (-2 i / rot) radians a position.  ``scaling`` stretches
+    that to contexts ``factor`` times as long: "linear" divides every frequency
+    by it; "base" raises the base so that the slowest pair is divided by it and
+    the fastest kept; "parts" divides the pairs that make fewer than ``slow``
+    turns over ``original_length`` positions, keeps those that make more than
+    ``fast``, blends linearly between, and scales the channels by
+    0.1 ln(factor) + 1."""
+    import torch
+
+    if rot < 2 or rot % 2 or not (math.isfinite(base) and base > 1.0):
+        raise ValueError("rot must be even and at least 2, base above 1")
+    if scaling not in ("none", "linear", "base", "parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if scaling != "none" and not (math.isfinite(factor) and factor >= 1.0):
+        raise ValueError("factor must be at least 1")
+    if scaling == "parts" and not (original_length > 0 and 0 < slow < fast):
+        raise ValueError("parts needs original_length > 0 and 0 < slow < fast")
+    if scaling == "base" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "parts" else 1.0
+    words = []
+    for i in range(rot // 2):
+        f = base ** (-2.0 * i / rot) / (2.0 * math.pi)  # turns a position
+        if scaling == "linear":
+            f /= factor
+        elif scaling == "parts":
+            keep = min(1.0, max(0.0, (original_length * f - slow) / (fast - slow)))
+            f = f * keep + f / factor * (1.0 - keep)
+        u = int(round(f * 2.0 ** 64)) & (2 ** 64 - 1)
+        words.append(u - 2 ** 64 if u >= 2 ** 63 else u)
+    return torch.tensor(words, dtype=torch.int64, device=device), amplitude
+
+
+def _check_rows(name, t, dev=None):
+    """A bf16 CUDA tensor (B, H, N, d) whose channels adjoin."""
+    import torch
+
+    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4:
+        raise ValueError(f"{name} must be a CUDA bf16 (B, H, N, d) tensor")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}'s channels must adjoin (last stride 1)")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+
+
+def _strides(t):
+    """A host array of the batch, head and position strides, or None when contiguous."""
+    if t.is_contiguous():
+        return None
+    return (ctypes.c_int64 * 3)(t.stride(0), t.stride(1), t.stride(2))
+
+
+def _check_int32(name, t, shape, dev):
+    import torch
+
+    if not t.is_cuda or t.get_device() != dev or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor on cuda:{dev}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def rope_into(q, k, q_out, k_out, freqs, positions=None, lens=None, layout: str = "half", factor: float = 1.0,
+              inverse: bool = False, stream=None):
+    """:func:`rope` into caller-provided tensors of q's and k's shapes (each
+    may be its own input; strided views are fine)."""
+    import torch
+
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"unknown layout {layout!r}")
+    _check_rows("q", q)
+    dev = q.get_device()
+    _check_rows("q_out", q_out, dev)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have the shape of q")
+    B, H, N, d = q.shape
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    Hk = 0
+    if k is not None:
+        _check_rows("k", k, dev)
+        _check_rows("k_out", k_out, dev)
+        if k_out.shape != k.shape or (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
+            raise ValueError(f"k must be (B, Hk, N, d) like q, and k_out like k: {tuple(q.shape)} {tuple(k.shape)}")
+        Hk = k.shape[1]
+    if not freqs.is_cuda or freqs.get_device() != dev or freqs.dtype != torch.int64 or freqs.dim() != 1 \
+            or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous CUDA int64 vector (see rope_frequencies)")
+    pos_ptr, pos_bytes, pos_stride = 0, 0, 0
+    if positions is not None:
+        if not positions.is_cuda or positions.get_device() != dev or positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError("positions must be a CUDA int32 or int64 tensor")
+        if tuple(positions.shape) not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions must be (N,) or (B, N), the positions of a sequence adjoining")
+        pos_ptr, pos_bytes = positions.data_ptr(), positions.element_size()
+        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    if lens is not None:
+        _check_int32("lens", lens, (B,), dev)
+    _on_current_device(dev)
+    rc = library().fa_rope(q.data_ptr(), _strides(q), 0 if k is None else k.data_ptr(),
+                           None if k is None else _strides(k), q_out.data_ptr(), _strides(q_out),
+                           0 if k is None else k_out.data_ptr(), None if k is None else _strides(k_out), B, H, Hk, N,
+                           d, freqs.data_ptr(), 2 * freqs.numel(), int(layout == "interleaved"), float(factor),
+                           int(bool(inverse)), pos_ptr, pos_bytes, pos_stride,
+                           0 if lens is None else lens.data_ptr(), _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_rope")
+    return q_out, k_out
+
+
+def rope(q, k, freqs, positions=None, lens=None, layout: str = "half", factor: float = 1.0, inverse: bool = False,
+         stream=None):
+    """Turns q (B, H, N, d) and k (B, Hk, N, d; or None) by their positions and
+    returns new contiguous tensors.  freqs and factor: :func:`rope_frequencies`;
+    2 * len(freqs) channels are turned, the others copied.  positions: int32 or
+    int64 (N,) or (B, N); or lens, int32 (B,): row i stands at lens[b] - N + i;
+    or neither: row i stands at i.  Strided views (heads of a fused
+    projection) are taken as they are."""
+    import torch
+
+    _check_rows("q", q)
+    with torch.cuda.device(q.device):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        return rope_into(q, k, q_out, k_out, freqs, positions, lens, layout, factor, inverse, stream)
+
+
+def rope_bwd(dq, dk, freqs, positions=None, lens=None, layout: str = "half", factor: float = 1.0, stream=None):
+    """The gradient of :func:`rope`: dLoss/dq and dLoss/dk from the gradients of
+    its results (the transposed map; the other arguments as in the forward)."""
+    return rope(dq, dk, freqs, positions, lens, layout, factor, True, stream)
+
+
+QCACHE_PAGE = 64
+
+
+def qcache_pool(num_pages: int, Hkv: int, d: int, device="cuda"):
+    """An empty pool for a 4-bit cache: uint8 (num_pages, Hkv, 72 * D), D = 64
+    for d <= 64, else 128.  A page holds 64 keys of every kv head; its
+    contents need not start at anything."""
+    import torch
+
+    if num_pages < 1 or Hkv < 1 or d < 8 or d > 128 or d % 8:
+        raise ValueError("num_pages and Hkv must be positive, d a multiple of 8 up to 128")
+    return torch.empty((num_pages, Hkv, 72 * (64 if d <= 64 else 128)), dtype=torch.uint8, device=device)
+
+
+def _check_qcache(pool, table, lens, d):
+    """The cache's tensors; returns (device, B, num_pages, Hkv, max_pages)."""
+    import torch
+
+    if not pool.is_cuda or pool.dtype != torch.uint8 or pool.dim() != 3 or not pool.is_contiguous():
+        raise ValueError("pool must be a contiguous CUDA uint8 (pages, Hkv, bytes) tensor (see qcache_pool)")
+    if d is not None and pool.shape[2] != 72 * (64 if d <= 64 else 128):
+        raise ValueError(f"pool was made for another head size than {d}")
+    if pool.shape[2] not in (72 * 64, 72 * 128):
+        raise ValueError("pool's blocks must hold 72 * 64 or 72 * 128 bytes")
+    dev = pool.get_device()
+    if table.dim() != 2:
+        raise ValueError("table must be (B, max_pages)")
+    _check_int32("table", table, None, dev)
+    _check_int32("lens", lens, (table.shape[0],), dev)
+    return dev, table.shape[0], pool.shape[0], pool.shape[1], table.shape[1]
+
+
+def qcache_append(k, v, pool, table, lens, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """Rounds k and v (B, Hkv, N, d) into the cache as the newest N keys of each
+    sequence: row i becomes key lens[b] - N + i (rows of negative position are
+    padding).  lens counts the new keys already."""
+    _check_rows("k", k)
+    _check_rows("v", v)
+    B, Hkv, N, d = k.shape
+    dev, Bc, num_pages, Hp, max_pages = _check_qcache(pool, table, lens, d)
+    if v.shape != k.shape or Bc != B or Hp != Hkv or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"k and v must be (B, Hkv, N, d) of the cache's batch, heads and device: {tuple(k.shape)} "
+                         f"{tuple(v.shape)}")
+    _on_current_device(dev)
+    rc = library().fa_qcache_append(k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), B, Hkv, N, d,
+                                    float(k_scale), float(v_scale), pool.data_ptr(), num_pages, table.data_ptr(),
+                                    max_pages, lens.data_ptr(), _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_qcache_append")
+
+
+def qcache_read(pool, table, lens, n: int, d: int, newest: bool = False, k_scale: float = 1.0, v_scale: float = 1.0,
+                stream=None):
+    """Keys 0 .. n-1 (or the newest n) of every sequence as bf16 tensors k and v
+    (B, Hkv, n, d); rows where no key is are zero."""
+    import torch
+
+    dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, d)
+    if n < 1:
+        raise ValueError("n must be positive")
+    with torch.cuda.device(dev):
+        k = torch.empty((B, Hkv, n, d), dtype=torch.bfloat16, device=pool.device)
+        v = torch.empty_like(k)
+        rc = library().fa_qcache_read(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
+                                      k.data_ptr(), v.data_ptr(), B, Hkv, n, d, int(bool(newest)), float(k_scale),
+                                      float(v_scale), _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_qcache_read")
+    return k, v
+
+
+def _check_qcache_query(q, pool, table, lens):
+    import torch
+
+    if not q.is_cuda or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.dim() != 4:
+        raise ValueError("q must be a contiguous CUDA bf16 (B, H, Nq, d) tensor")
+    B, H, Nq, d = q.shape
+    dev, Bc, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, d)
+    if Bc != B or q.get_device() != dev:
+        raise ValueError("q and the cache must have one batch size and be on one device")
+    return dev, num_pages, Hkv, max_pages
+
+
+def qcache_decode_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, d: int, max_pages: int) -> int:
+    """Workspace bytes fa_qcache_decode needs for these sizes on the current device."""
+    out = ctypes.c_size_t(0)
+    rc = library().fa_qcache_decode_workspace_bytes(int(B), int(H), int(Hkv), int(Nq), int(d), int(max_pages),
+                                                    ctypes.byref(out))
+    if rc != 0:
+        raise FaError(rc, "fa_qcache_decode_workspace_bytes")
+    return int(out.value)
+
+
+def qcache_decode_into(q, pool, table, lens, o, lse, workspace, causal: bool = False, scale: float | None = None,
+                       k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """:func:`qcache_decode` into caller-provided o (bf16, like q), lse (fp32,
+    (B, H, Nq)) and workspace (a contiguous CUDA tensor of at least
+    qcache_decode_workspace_bytes bytes)."""
+    import torch
+
+    dev, num_pages, Hkv, max_pages = _check_qcache_query(q, pool, table, lens)
+    B, H, Nq, d = q.shape
+    _check_out("o", o, q.shape, torch.bfloat16, q.device)
+    _check_out("lse", lse, (B, H, Nq), torch.float32, q.device)
+    if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    _on_current_device(dev)
+    rc = library().fa_qcache_decode(q.data_ptr(), pool.data_ptr(), num_pages, table.data_ptr(), max_pages,
+                                    lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, d,
+                                    int(bool(causal)), float(scale), float(k_scale), float(v_scale),
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_qcache_decode")
+    return o, lse
+
+
+def qcache_decode(q, pool, table, lens, causal: bool = False, scale: float | None = None, k_scale: float = 1.0,
+                  v_scale: float = 1.0, stream=None):
+    """Attention of q (B, H, Nq, d), Nq <= 8, against the 4-bit cache: query head
+    h reads kv head h // (H // Hkv), query i sees the keys of its sequence (up
+    to key lens[b] - Nq + i when causal).  Returns ``(o (B, H, Nq, d) bf16, lse
+    (B, H, Nq) fp32)``; a query that sees no key gives 0 and -inf."""
+    import torch
+
+    dev, _, Hkv, max_pages = _check_qcache_query(q, pool, table, lens)
+    B, H, Nq, d = q.shape
+    with torch.cuda.device(dev):
+        ws = torch.empty(qcache_decode_workspace_bytes(B, H, Hkv, Nq, d, max_pages), dtype=torch.uint8, device=q.device)
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        return qcache_decode_into(q, pool, table, lens, o, lse, ws, causal, scale, k_scale, v_scale, stream)
+
+
+def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, scale: float | None = None,
+                   k_scale: float = 1.0, out=None, stream=None):
+    """weights (B, Hkv, W) fp32 plus the attention weight that q's rows give each
+    cached key: exp(scale q.k - lse) summed over the query rows of the key's kv
+    head, with q, causal and scale as in the decode call that returned lse.
+    ``out`` may be weights itself."""
+    import torch
+
+    dev, num_pages, Hkv, max_pages = _check_qcache_query(q, pool, table, lens)
+    B, H, Nq, d = q.shape
+    _check_out("lse", lse, (B, H, Nq), torch.float32, q.device)
+    if weights.dim() != 3:
+        raise ValueError("weights must be (B, Hkv, W)")
+    _check_out("weights", weights, (B, Hkv, weights.shape[2]), torch.float32, q.device)
+    if out is not None:
+        _check_out("out", out, weights.shape, torch.float32, q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty_like(weights)
+        rc = library().fa_qcache_weights(q.data_ptr(), lse.data_ptr(), pool.data_ptr(), num_pages, table.data_ptr(),
+                                         max_pages, lens.data_ptr(), weights.data_ptr(), out.data_ptr(),
+                                         weights.shape[2], B, H, Hkv, Nq, d, int(bool(causal)), float(scale),
+                                         float(k_scale), _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_qcache_weights")
+    return out
+
+
+def qcache_evict(pool, table, lens, weights, keep: int, sink: int = 0, recent: int = 0, table_out=None, stream=None):
+    """Cuts every sequence back to its ``keep`` keys: the first ``sink``, the last
+    ``recent`` and the heaviest between (a choice per kv head; of equal weights
+    the lowest positions).  The kept keys move, in order, to the pages of
+    table_out, or within the sequence's own pages when it is None.  Returns
+    ``(kept, lens, weights)``: the kept keys' former positions, int32 (B, Hkv,
+    keep), -1 after the last; the new lengths; the kept keys' weights at their
+    new places, 0 after them (like weights)."""
+    import torch
+
+    dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, None)
+    if weights.dim() != 3:
+        raise ValueError("weights must be (B, Hkv, W)")
+    _check_out("weights", weights, (B, Hkv, weights.shape[2]), torch.float32, pool.device)
+    if table_out is None:
+        table_out = table
+    elif table_out.dim() != 2 or table_out.shape[0] != B:
+        raise ValueError("table_out must be (B, max_pages_out)")
+    _check_int32("table_out", table_out, None, dev)
+    if keep < 1 or sink < 0 or recent < 0 or sink + recent > keep:
+        raise ValueError("keep must be positive, sink and recent not negative and together at most keep")
+    with torch.cuda.device(dev):
+        kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=pool.device)
+        lens_out = torch.empty_like(lens)
+        weights_out = torch.empty_like(weights)
+        rc = library().fa_qcache_evict(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
+                                       table_out.data_ptr(), table_out.shape[1], weights.data_ptr(),
+                                       weights_out.data_ptr(), weights.shape[2], kept.data_ptr(), lens_out.data_ptr(),
+                                       B, Hkv, pool.shape[2] // 72, keep, sink, recent, _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_qcache_evict")
+    return kept, lens_out, weights_out
+
+
 def check_device_status(stream=None) -> int:
     """Synchronises the stream and returns the device status (0 = ok, 4 = a wait
-    timed out); raises FaError on a CUDA error."""
+    timed out, 1 = a cache call skipped a page or length out of range); raises
+    FaError on a CUDA error."""
     where = ctypes.c_uint32(0)
     rc = library().fa_check_device_status(_stream_handle(stream), ctypes.byref(where))
     if rc == 3:
@@ -389,7 +763,8 @@ def check_device_status(stream=None) -> int:
 
 def get_device_status(stream=None) -> int:
     """fa_get_device_status: synchronises the stream and returns the device
-    status (0 = ok, 4 = a wait timed out); raises FaError on a CUDA error."""
+    status (0 = ok, 4 = a wait timed out, 1 = a cache call skipped a page or
+    length out of range); raises FaError on a CUDA error."""
     rc = library().fa_get_device_status(_stream_handle(stream))
     if rc == 3:
         raise FaError(rc, "fa_get_device_status")

@@ -15,6 +15,8 @@
 #include "fa_decode_kernel.cuh"
 #include "fa_ew_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
+#include "fa_qcache_kernel.cuh"
+#include "fa_rope_kernel.cuh"
 
 namespace {
 
@@ -515,6 +517,181 @@ void* static_scratch(int dev)
     return p;
 }
 
+// ---------------------------------------------------------- rotary positions
+
+// Extent in elements of a (B, heads, N, d) view with element strides s.
+int64_t extent(const int64_t s[3], int64_t B, int64_t H, int64_t N, int64_t d)
+{
+    return (B - 1) * s[0] + (H - 1) * s[1] + (N - 1) * s[2] + d;
+}
+
+// Strides of a view: non-negative, small enough that extents fit.
+bool strides_ok(const int64_t s[3], int64_t B, int64_t H, int64_t N)
+{
+    const int64_t LIM = (int64_t)1 << 59;
+    const int64_t n[3] = {B, H, N};
+    for (int i = 0; i < 3; ++i)
+        if (s[i] < 0 || (n[i] > 1 && s[i] > LIM / (n[i] - 1))) return false;
+    return true;
+}
+
+// No two elements of the view share a place: taken by rising stride, each
+// dimension steps over all that the ones before it span.
+bool no_overlap_within(const int64_t s[3], int64_t B, int64_t H, int64_t N, int64_t d)
+{
+    int64_t st[3] = {s[0], s[1], s[2]}, n[3] = {B, H, N};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (st[j] < st[i]) std::swap(st[i], st[j]), std::swap(n[i], n[j]);
+    int64_t span = d;
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] == 1) continue;
+        if (st[i] < span) return false;
+        span += (n[i] - 1) * st[i];
+    }
+    return true;
+}
+
+struct RopeView {
+    const void* p;
+    int64_t s[3], H;
+};
+
+// Whether two views may share a place.  Views of one buffer that interleave
+// row by row (the queries and keys of a fused projection) do not when each
+// position's heads stay within its row pitch.
+bool may_overlap(const RopeView& x, const RopeView& y, int64_t B, int64_t N, int64_t d)
+{
+    if (!overlaps(x.p, (size_t)extent(x.s, B, x.H, N, d) * 2, y.p, (size_t)extent(y.s, B, y.H, N, d) * 2)) return false;
+    const int64_t pitch = x.s[2];
+    if (pitch <= 0 || y.s[2] != pitch || x.s[0] % pitch || y.s[0] % pitch) return true;
+    const int64_t bytes = (int64_t)(reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p));
+    if (bytes % 2) return true;
+    const int64_t at = ((bytes / 2) % pitch + pitch) % pitch;
+    const int64_t nx = (x.H - 1) * x.s[1] + d, ny = (y.H - 1) * y.s[1] + d;
+    return !(nx <= at && at + ny <= pitch);
+}
+
+template <bool VEC>
+fa_status launch_rope(const fa::rope::Params& p, dim3 block, int64_t blocks, cudaStream_t st)
+{
+    return launch_pdl(fa::rope::fa_rope_kernel<VEC>, dim3((unsigned)blocks), block, 0, st, p) == cudaSuccess ? FA_OK
+                                                                                                           : FA_ERR_CUDA;
+}
+
+// --------------------------------------------------------------- 4-bit cache
+
+// The sizes of a cache, as every call on one gives them.
+fa_status qcache_check(const void* pool, int64_t num_pages, const int32_t* table, int64_t max_pages,
+                       const int32_t* lens, int64_t B, int64_t Hkv, int64_t d)
+{
+    if (!pool || !table || !lens) return FA_ERR_INVALID_ARG;
+    if (B < 1 || Hkv < 1 || d < 1 || num_pages < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
+    if (!head_size_ok(d)) return FA_ERR_UNSUPPORTED;
+    if (B > 65535 || Hkv > 65535 || num_pages > INT32_MAX / Hkv || max_pages > INT32_MAX / fa::qc::PAGE / B)
+        return FA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(pool) & 15u) != 0 ||
+        ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lens)) & 3u) != 0)
+        return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+size_t qcache_block_bytes(int64_t d) { return (size_t)(72 * padded_head_size(d)); }
+
+bool scale_ok(float s) { return std::isfinite(s) && s > 0.0f; }
+
+// A written range of `n` bytes at p may overlap none of the cache's tensors.
+bool hits_cache(const void* p, size_t n, const void* pool, int64_t num_pages, int64_t Hkv, int64_t d,
+                const int32_t* table, int64_t max_pages, const int32_t* lens, int64_t B)
+{
+    return overlaps(p, n, pool, (size_t)(num_pages * Hkv) * qcache_block_bytes(d)) ||
+           overlaps(p, n, table, (size_t)(B * max_pages) * 4) || overlaps(p, n, lens, (size_t)B * 4);
+}
+
+// Query rows of a kv head and how the kernels take them: NT column tiles of 8
+// rows at a time.
+struct QRows {
+    int64_t rows, rb;
+    int nt;
+};
+QRows qcache_rows(int64_t group, int64_t Nq)
+{
+    QRows r;
+    r.rows = group * Nq;
+    r.nt = r.rows <= 8 ? 1 : 2;
+    r.rb = (r.rows + 8 * r.nt - 1) / (8 * r.nt);
+    return r;
+}
+
+template <int D, int NT>
+size_t qcache_decode_smem(int64_t B)
+{
+    return (size_t)(2 * fa::qc::WARPS * fa::qc::Partial<D, 8 * NT>::FLOATS + B + 1) * 4;
+}
+
+size_t qcache_part_bytes(int64_t Dp, int nt) { return (size_t)(8 * nt) * (size_t)(Dp + 2) * 4; }
+
+// Blocks of the decode kernel: one an SM, no more than there can be pages.
+int64_t qcache_decode_blocks(int sms, int64_t B, int64_t Hkv, int64_t rb, int64_t max_pages)
+{
+    return std::min<int64_t>(sms, B * Hkv * rb * max_pages);
+}
+
+size_t qcache_decode_ws(int64_t blocks, int64_t Dp, int nt)
+{
+    return (size_t)blocks * (2 * qcache_part_bytes(Dp, nt) + 8);
+}
+
+template <typename K>
+fa_status allow_smem(K kernel, size_t bytes, std::atomic<int>* done, int dev)
+{
+    if (dev < 0 || dev >= MAX_DEVICES) return FA_ERR_CUDA;
+    if (done[dev].load(std::memory_order_acquire)) return FA_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+        return FA_ERR_CUDA;
+    done[dev].store(1, std::memory_order_release);
+    return FA_OK;
+}
+
+template <int D, int NT>
+fa_status launch_qcache_decode(const fa::qc::DecParams& p, int64_t blocks, int dev, cudaStream_t st)
+{
+    static std::atomic<int> done[MAX_DEVICES];
+    const fa_status as = allow_smem(fa::qc::fa_qcache_decode_kernel<D, NT>, qcache_decode_smem<D, NT>(fa::qc::MAX_B), done, dev);
+    if (as != FA_OK) return as;
+    if (launch_pdl(fa::qc::fa_qcache_decode_kernel<D, NT>, dim3((unsigned)blocks), dim3(fa::qc::THREADS),
+                   qcache_decode_smem<D, NT>(p.B), st, p) != cudaSuccess ||
+        launch_pdl(fa::qc::fa_qcache_combine_kernel<D, NT>, dim3((unsigned)blocks, 8 * NT), dim3(256), 0, st, p) !=
+            cudaSuccess)
+        return FA_ERR_CUDA;
+    return FA_OK;
+}
+
+template <int D, int NT>
+fa_status launch_qcache_weights(const fa::qc::DecParams& p, int64_t blocks, cudaStream_t st)
+{
+    return launch_pdl(fa::qc::fa_qcache_weights_kernel<D, NT>, dim3((unsigned)blocks), dim3(fa::qc::THREADS),
+                      (size_t)(p.B + 1) * 4, st, p) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
+// What decode and weights share: the query side.
+fa_status qcache_query_check(const void* q, int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t max_pages,
+                             int causal, float scale, float k_scale)
+{
+    if (!q) return FA_ERR_INVALID_ARG;
+    if (H < 1 || Nq < 1 || H % Hkv != 0 || (causal != 0 && causal != 1) || !scale_ok(scale) || !scale_ok(k_scale) ||
+        !scale_ok((float)((double)scale * 1.4426950408889634074 * (double)k_scale)))
+        return FA_ERR_INVALID_ARG;
+    if (Nq > fa::qc::MAX_NQ || B > fa::qc::MAX_B) return FA_ERR_UNSUPPORTED;
+    if (H > INT32_MAX / 8 / B) return FA_ERR_INVALID_ARG;
+    const QRows r = qcache_rows(H / Hkv, Nq);
+    if (B * Hkv * r.rb > INT32_MAX / max_pages) return FA_ERR_INVALID_ARG;  // units are counted in 32 bits
+    if ((reinterpret_cast<uintptr_t>(q) & 15u) != 0) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
 // Clears the status bits a check has read (and the wait code, if it is still
 // the one read), leaving bits that kernels on other streams set since.
 __global__ void fa_clear_status_kernel(unsigned int bits, unsigned int where)
@@ -795,6 +972,404 @@ fa_status fa_bias_gelu_dropout(const void* x, const void* bias, const uint32_t* 
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+fa_status fa_rope(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides, void* q_out,
+                  const int64_t* q_out_strides, void* k_out, const int64_t* k_out_strides, int64_t B, int64_t Hq,
+                  int64_t Hk, int64_t N, int64_t d, const uint64_t* freqs, int64_t rot, int interleaved, float factor,
+                  int inverse, const void* positions, int position_bytes, int64_t position_stride,
+                  const int32_t* lens, fa_stream_t stream)
+{
+    // ---- argument checks (no CUDA call before these pass)
+    if (!q || !q_out || !freqs || (k == nullptr) != (k_out == nullptr)) return FA_ERR_INVALID_ARG;
+    if (B < 1 || Hq < 1 || Hk < 0 || N < 1 || d < 1 || (k ? Hk < 1 : Hk != 0)) return FA_ERR_INVALID_ARG;
+    if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1) || !std::isfinite(factor))
+        return FA_ERR_INVALID_ARG;
+    if (rot < 2 || rot > d || rot % 2 != 0) return FA_ERR_INVALID_ARG;
+    if (positions && ((position_bytes != 4 && position_bytes != 8) || position_stride < 0)) return FA_ERR_INVALID_ARG;
+    if (positions && lens) return FA_ERR_INVALID_ARG;
+    if (!head_size_ok(d)) return FA_ERR_UNSUPPORTED;
+    const int64_t LIM = (int64_t)1 << 59;
+    if (Hq > INT32_MAX / 2 || Hk > INT32_MAX / 2 || B > LIM / (Hq + Hk) || B * (Hq + Hk) > LIM / N ||
+        B * (Hq + Hk) * N > LIM / d || (positions && position_stride > LIM / B))
+        return FA_ERR_INVALID_ARG;
+    RopeView v[4] = {{q, {}, Hq}, {k, {}, Hk}, {q_out, {}, Hq}, {k_out, {}, Hk}};
+    const int64_t* given[4] = {q_strides, k_strides, q_out_strides, k_out_strides};
+    const int count = k ? 2 : 1;
+    bool aligned = true;
+    for (int i = 0; i < 4; ++i) {
+        if (i % 2 >= count) continue;
+        v[i].s[0] = given[i] ? given[i][0] : v[i].H * N * d;
+        v[i].s[1] = given[i] ? given[i][1] : N * d;
+        v[i].s[2] = given[i] ? given[i][2] : d;
+        if (!strides_ok(v[i].s, B, v[i].H, N)) return FA_ERR_INVALID_ARG;
+        const int64_t n[3] = {B, v[i].H, N};
+        for (int j = 0; j < 3; ++j) aligned &= n[j] == 1 || v[i].s[j] % 8 == 0;
+        aligned &= (reinterpret_cast<uintptr_t>(v[i].p) & 15u) == 0;
+        if ((reinterpret_cast<uintptr_t>(v[i].p) & 1u) != 0) return FA_ERR_UNSUPPORTED;
+    }
+    const uintptr_t pos_mask = positions ? (uintptr_t)position_bytes - 1 : 0;
+    if ((reinterpret_cast<uintptr_t>(freqs) & 7u) != 0 || (reinterpret_cast<uintptr_t>(positions) & pos_mask) != 0 ||
+        (reinterpret_cast<uintptr_t>(lens) & 3u) != 0)
+        return FA_ERR_UNSUPPORTED;
+    for (int i = 0; i < count; ++i) {
+        const RopeView& out = v[2 + i];
+        if (!no_overlap_within(out.s, B, out.H, N, d)) return FA_ERR_INVALID_ARG;
+        const size_t nb = (size_t)extent(out.s, B, out.H, N, d) * 2;
+        if (overlaps(out.p, nb, freqs, (size_t)rot * 4) || (lens && overlaps(out.p, nb, lens, (size_t)B * 4)) ||
+            (positions &&
+             overlaps(out.p, nb, positions, (size_t)((B - 1) * position_stride + N) * (size_t)position_bytes)))
+            return FA_ERR_INVALID_ARG;
+        for (int j = 0; j < count; ++j) {
+            const RopeView& in = v[j];
+            const bool in_place = i == j && out.p == in.p && (B == 1 || out.s[0] == in.s[0]) &&
+                                  (out.H == 1 || out.s[1] == in.s[1]) && (N == 1 || out.s[2] == in.s[2]);
+            if (!in_place && may_overlap(out, in, B, N, d)) return FA_ERR_INVALID_ARG;
+        }
+    }
+    if (count == 2 && may_overlap(v[2], v[3], B, N, d)) return FA_ERR_INVALID_ARG;
+
+    // ---- device
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+
+    fa::rope::Params p = {};
+    for (int i = 0; i < 2; ++i) {
+        p.in[i] = {static_cast<__nv_bfloat16*>(const_cast<void*>(v[i].p)), v[i].s[0], v[i].s[1], v[i].s[2]};
+        p.out[i] = {static_cast<__nv_bfloat16*>(const_cast<void*>(v[2 + i].p)), v[2 + i].s[0], v[2 + i].s[1], v[2 + i].s[2]};
+    }
+    p.heads[0] = (int)Hq;
+    p.heads[1] = (int)Hk;
+    p.freqs = freqs;
+    p.positions = positions;
+    p.pos_sb = position_stride;
+    p.lens = lens;
+    p.wide = position_bytes == 8;
+    p.n = N;
+    p.d = (int)d;
+    p.rot = (int)rot;
+    p.interleaved = interleaved;
+    p.factor = factor;
+    p.sign = inverse ? -1.0f : 1.0f;
+    // Whole 16-byte vectors turn together when the halves (or the end of the
+    // turned part) fall on vector borders; else one pair at a time.
+    const bool vec = aligned && (interleaved ? rot % 8 == 0 : rot % 16 == 0);
+    const int64_t units = !vec ? d / 2 : interleaved ? (d + 15) / 16 : rot / 16 + (d - rot + 15) / 16;
+    const int64_t room = fa::rope::THREADS / units;
+    const int64_t ny = std::min<int64_t>(N, room), nz = std::max<int64_t>(1, std::min<int64_t>(room / ny, Hq + Hk));
+    // Heads a thread walks with its angles: more spread them over more
+    // heads, fewer give more threads.
+    const int64_t total = Hq + Hk, tiles = (N + ny - 1) / ny;
+    const int64_t per = std::min<int64_t>((total + nz - 1) / nz, 2 * fa::rope::U);
+    const int64_t head_tiles = (total + nz * per - 1) / (nz * per);
+    if (tiles > INT32_MAX || B * head_tiles > INT32_MAX / tiles) return FA_ERR_INVALID_ARG;
+    p.tiles = (int)tiles;
+    p.head_tiles = (int)head_tiles;
+    p.heads_per_thread = (int)per;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const dim3 block((unsigned)units, (unsigned)ny, (unsigned)nz);
+    return vec ? launch_rope<true>(p, block, B * tiles * head_tiles, st)
+               : launch_rope<false>(p, block, B * tiles * head_tiles, st);
+}
+
+fa_status fa_qcache_append(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides, int64_t B,
+                           int64_t Hkv, int64_t N, int64_t d, float k_scale, float v_scale, void* pool,
+                           int64_t num_pages, const int32_t* table, int64_t max_pages, const int32_t* lens,
+                           fa_stream_t stream)
+{
+    if (!k || !v) return FA_ERR_INVALID_ARG;
+    const fa_status cs = qcache_check(pool, num_pages, table, max_pages, lens, B, Hkv, d);
+    if (cs != FA_OK) return cs;
+    if (N < 1 || N > INT32_MAX / 2 || !scale_ok(k_scale) || !scale_ok(v_scale) || !scale_ok(6.0f * k_scale) ||
+        !scale_ok(6.0f * v_scale))
+        return FA_ERR_INVALID_ARG;
+    const int64_t LIM = (int64_t)1 << 59;
+    if (B * Hkv > LIM / N || B * Hkv * N > LIM / d) return FA_ERR_INVALID_ARG;
+    int64_t s[2][3];
+    const int64_t* given[2] = {k_strides, v_strides};
+    const void* rows[2] = {k, v};
+    for (int i = 0; i < 2; ++i) {
+        s[i][0] = given[i] ? given[i][0] : Hkv * N * d;
+        s[i][1] = given[i] ? given[i][1] : N * d;
+        s[i][2] = given[i] ? given[i][2] : d;
+        if (!strides_ok(s[i], B, Hkv, N)) return FA_ERR_INVALID_ARG;
+        const int64_t n[3] = {B, Hkv, N};
+        for (int j = 0; j < 3; ++j)
+            if (n[j] > 1 && s[i][j] % 8 != 0) return FA_ERR_UNSUPPORTED;
+        if ((reinterpret_cast<uintptr_t>(rows[i]) & 15u) != 0) return FA_ERR_UNSUPPORTED;
+        const size_t nb = (size_t)extent(s[i], B, Hkv, N, d) * 2;
+        if (overlaps(pool, (size_t)(num_pages * Hkv) * qcache_block_bytes(d), rows[i], nb)) return FA_ERR_INVALID_ARG;
+    }
+    if (overlaps(pool, (size_t)(num_pages * Hkv) * qcache_block_bytes(d), table, (size_t)(B * max_pages) * 4) ||
+        overlaps(pool, (size_t)(num_pages * Hkv) * qcache_block_bytes(d), lens, (size_t)B * 4))
+        return FA_ERR_INVALID_ARG;
+
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    fa::qc::RowParams p = {};
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.ksb = s[0][0], p.ksh = s[0][1], p.ksn = s[0][2];
+    p.vsb = s[1][0], p.vsh = s[1][1], p.vsn = s[1][2];
+    p.pool = static_cast<uint8_t*>(pool);
+    p.table = table;
+    p.lens = lens;
+    p.n = N;
+    p.hkv = (int)Hkv;
+    p.d = (int)d;
+    p.max_pages = (int)max_pages;
+    p.num_pages = (int)num_pages;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.k_six = 6.0f * k_scale;
+    p.v_six = 6.0f * v_scale;
+    // Pages that N keys can touch, wherever they begin.
+    const int64_t pages = std::min<int64_t>((N - 1 + fa::qc::PAGE - 1) / fa::qc::PAGE + 1, max_pages);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const dim3 grid((unsigned)pages, (unsigned)Hkv, (unsigned)B);
+    const cudaError_t e =
+        padded_head_size(d) == 128
+            ? launch_pdl(fa::qc::fa_qcache_append_kernel<128>, grid, dim3(fa::qc::ROW_THREADS), 0, st, p)
+            : launch_pdl(fa::qc::fa_qcache_append_kernel<64>, grid, dim3(fa::qc::ROW_THREADS), 0, st, p);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_qcache_read(const void* pool, int64_t num_pages, const int32_t* table, int64_t max_pages,
+                         const int32_t* lens, void* k, void* v, int64_t B, int64_t Hkv, int64_t N, int64_t d,
+                         int newest, float k_scale, float v_scale, fa_stream_t stream)
+{
+    if (!k || !v) return FA_ERR_INVALID_ARG;
+    const fa_status cs = qcache_check(pool, num_pages, table, max_pages, lens, B, Hkv, d);
+    if (cs != FA_OK) return cs;
+    if (N < 1 || N > INT32_MAX / 2 || (newest != 0 && newest != 1) || !scale_ok(k_scale) || !scale_ok(v_scale))
+        return FA_ERR_INVALID_ARG;
+    const int64_t LIM = (int64_t)1 << 59;
+    if (B * Hkv > LIM / N || B * Hkv * N > LIM / d) return FA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15u) != 0) return FA_ERR_UNSUPPORTED;
+    const size_t nb = (size_t)(B * Hkv * N * d) * 2;
+    if (overlaps(k, nb, v, nb) || hits_cache(k, nb, pool, num_pages, Hkv, d, table, max_pages, lens, B) ||
+        hits_cache(v, nb, pool, num_pages, Hkv, d, table, max_pages, lens, B))
+        return FA_ERR_INVALID_ARG;
+
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    fa::qc::RowParams p = {};
+    p.ko = static_cast<__nv_bfloat16*>(k);
+    p.vo = static_cast<__nv_bfloat16*>(v);
+    p.pool = static_cast<uint8_t*>(const_cast<void*>(pool));
+    p.table = table;
+    p.lens = lens;
+    p.n = N;
+    p.hkv = (int)Hkv;
+    p.d = (int)d;
+    p.max_pages = (int)max_pages;
+    p.num_pages = (int)num_pages;
+    p.newest = newest;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const dim3 grid((unsigned)((N + fa::qc::PAGE - 1) / fa::qc::PAGE), (unsigned)Hkv, (unsigned)B);
+    const cudaError_t e =
+        padded_head_size(d) == 128
+            ? launch_pdl(fa::qc::fa_qcache_read_kernel<128>, grid, dim3(fa::qc::ROW_THREADS), 0, st, p)
+            : launch_pdl(fa::qc::fa_qcache_read_kernel<64>, grid, dim3(fa::qc::ROW_THREADS), 0, st, p);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_qcache_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t d, int64_t max_pages,
+                                           size_t* bytes)
+{
+    if (!bytes || B < 1 || H < 1 || Hkv < 1 || Nq < 1 || d < 1 || max_pages < 1 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
+    if (!head_size_ok(d) || Nq > fa::qc::MAX_NQ || B > fa::qc::MAX_B) return FA_ERR_UNSUPPORTED;
+    if (H > INT32_MAX / 8 / B) return FA_ERR_INVALID_ARG;
+    const QRows r = qcache_rows(H / Hkv, Nq);
+    if (max_pages > INT32_MAX / fa::qc::PAGE / B || B * Hkv * r.rb > INT32_MAX / max_pages) return FA_ERR_INVALID_ARG;
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    *bytes = qcache_decode_ws(qcache_decode_blocks(info.sms, B, Hkv, r.rb, max_pages), padded_head_size(d), r.nt);
+    return FA_OK;
+}
+
+fa_status fa_qcache_decode(const void* q, const void* pool, int64_t num_pages, const int32_t* table, int64_t max_pages,
+                           const int32_t* lens, void* o, float* lse, int64_t B, int64_t H, int64_t Hkv, int64_t Nq,
+                           int64_t d, int causal, float scale, float k_scale, float v_scale, void* workspace,
+                           size_t workspace_bytes, fa_stream_t stream)
+{
+    if (!o || !lse || !workspace) return FA_ERR_INVALID_ARG;
+    const fa_status cs = qcache_check(pool, num_pages, table, max_pages, lens, B, Hkv, d);
+    if (cs != FA_OK) return cs;
+    const fa_status qs = qcache_query_check(q, B, H, Hkv, Nq, max_pages, causal, scale, k_scale);
+    if (qs != FA_OK) return qs;
+    if (!scale_ok(v_scale)) return FA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(workspace)) & 15u) != 0 ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+        return FA_ERR_UNSUPPORTED;
+    const size_t qb = (size_t)(B * H * Nq * d) * 2, lb = (size_t)(B * H * Nq) * 4;
+    if (overlaps(o, qb, q, qb) || overlaps(o, qb, lse, lb) || overlaps(lse, lb, q, qb) ||
+        hits_cache(o, qb, pool, num_pages, Hkv, d, table, max_pages, lens, B) ||
+        hits_cache(lse, lb, pool, num_pages, Hkv, d, table, max_pages, lens, B))
+        return FA_ERR_INVALID_ARG;
+
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    const QRows r = qcache_rows(H / Hkv, Nq);
+    const int64_t Dp = padded_head_size(d);
+    const int64_t blocks = qcache_decode_blocks(info.sms, B, Hkv, r.rb, max_pages);
+    const size_t need = qcache_decode_ws(blocks, Dp, r.nt);
+    if (workspace_bytes < need || overlaps(workspace, need, q, qb) || overlaps(workspace, need, o, qb) ||
+        overlaps(workspace, need, lse, lb) ||
+        hits_cache(workspace, need, pool, num_pages, Hkv, d, table, max_pages, lens, B))
+        return FA_ERR_INVALID_ARG;
+    fa::qc::DecParams p = {};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.pool = static_cast<const uint8_t*>(pool);
+    p.table = table;
+    p.lens = lens;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.ws = static_cast<float*>(workspace);
+    p.desc = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + (size_t)blocks * 2 * qcache_part_bytes(Dp, r.nt));
+    p.B = (int)B;
+    p.hkv = (int)Hkv;
+    p.nq = (int)Nq;
+    p.rows = (int)r.rows;
+    p.rb = (int)r.rb;
+    p.d = (int)d;
+    p.max_pages = (int)max_pages;
+    p.num_pages = (int)num_pages;
+    p.causal = causal;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634074 * (double)k_scale);
+    p.v_scale = v_scale;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (Dp == 128)
+        return r.nt == 1 ? launch_qcache_decode<128, 1>(p, blocks, dev, st) : launch_qcache_decode<128, 2>(p, blocks, dev, st);
+    return r.nt == 1 ? launch_qcache_decode<64, 1>(p, blocks, dev, st) : launch_qcache_decode<64, 2>(p, blocks, dev, st);
+}
+
+fa_status fa_qcache_weights(const void* q, const float* lse, const void* pool, int64_t num_pages, const int32_t* table,
+                            int64_t max_pages, const int32_t* lens, const float* weights, float* weights_out,
+                            int64_t W, int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t d, int causal,
+                            float scale, float k_scale, fa_stream_t stream)
+{
+    if (!lse || !weights || !weights_out) return FA_ERR_INVALID_ARG;
+    const fa_status cs = qcache_check(pool, num_pages, table, max_pages, lens, B, Hkv, d);
+    if (cs != FA_OK) return cs;
+    const fa_status qs = qcache_query_check(q, B, H, Hkv, Nq, max_pages, causal, scale, k_scale);
+    if (qs != FA_OK) return qs;
+    if (W < 1 || W > INT32_MAX) return FA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(weights) |
+          reinterpret_cast<uintptr_t>(weights_out)) & 3u) != 0)
+        return FA_ERR_UNSUPPORTED;
+    const size_t qb = (size_t)(B * H * Nq * d) * 2, lb = (size_t)(B * H * Nq) * 4, wb = (size_t)(B * Hkv * W) * 4;
+    if ((weights != weights_out && overlaps(weights_out, wb, weights, wb)) || overlaps(weights_out, wb, q, qb) ||
+        overlaps(weights_out, wb, lse, lb) ||
+        hits_cache(weights_out, wb, pool, num_pages, Hkv, d, table, max_pages, lens, B))
+        return FA_ERR_INVALID_ARG;
+
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    const QRows r = qcache_rows(H / Hkv, Nq);
+    fa::qc::DecParams p = {};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.pool = static_cast<const uint8_t*>(pool);
+    p.table = table;
+    p.lens = lens;
+    p.lse_in = lse;
+    p.w_in = weights;
+    p.w_out = weights_out;
+    p.w_len = W;
+    p.B = (int)B;
+    p.hkv = (int)Hkv;
+    p.nq = (int)Nq;
+    p.rows = (int)r.rows;
+    p.rb = (int)r.rb;
+    p.d = (int)d;
+    p.max_pages = (int)max_pages;
+    p.num_pages = (int)num_pages;
+    p.causal = causal;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634074 * (double)k_scale);
+    const int64_t blocks = std::min<int64_t>((int64_t)info.sms * 2, B * Hkv * max_pages);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (padded_head_size(d) == 128)
+        return r.nt == 1 ? launch_qcache_weights<128, 1>(p, blocks, st) : launch_qcache_weights<128, 2>(p, blocks, st);
+    return r.nt == 1 ? launch_qcache_weights<64, 1>(p, blocks, st) : launch_qcache_weights<64, 2>(p, blocks, st);
+}
+
+fa_status fa_qcache_evict(void* pool, int64_t num_pages, const int32_t* table, int64_t max_pages, const int32_t* lens,
+                          const int32_t* table_out, int64_t max_pages_out, const float* weights, float* weights_out,
+                          int64_t W, int32_t* kept, int32_t* lens_out, int64_t B, int64_t Hkv, int64_t d, int64_t keep,
+                          int64_t sink, int64_t recent, fa_stream_t stream)
+{
+    if (!table_out || !weights || !weights_out || !kept || !lens_out) return FA_ERR_INVALID_ARG;
+    const fa_status cs = qcache_check(pool, num_pages, table, max_pages, lens, B, Hkv, d);
+    if (cs != FA_OK) return cs;
+    if (W < 1 || W > INT32_MAX || keep < 1 || keep > INT32_MAX / 2 || sink < 0 || recent < 0 || sink > keep ||
+        recent > keep - sink)
+        return FA_ERR_INVALID_ARG;
+    const int64_t need = (keep + fa::qc::PAGE - 1) / fa::qc::PAGE;
+    if (max_pages_out < std::min(need, max_pages) || max_pages_out > INT32_MAX / fa::qc::PAGE / B) return FA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(table_out) | reinterpret_cast<uintptr_t>(weights) |
+          reinterpret_cast<uintptr_t>(weights_out) | reinterpret_cast<uintptr_t>(kept) |
+          reinterpret_cast<uintptr_t>(lens_out)) & 3u) != 0)
+        return FA_ERR_UNSUPPORTED;
+    const size_t wb = (size_t)(B * Hkv * W) * 4, kb = (size_t)(B * Hkv * keep) * 4, lb = (size_t)B * 4;
+    const size_t tb = (size_t)(B * max_pages_out) * 4;
+    const void* outs[3] = {weights_out, kept, lens_out};
+    const size_t out_b[3] = {wb, kb, lb};
+    for (int i = 0; i < 3; ++i) {
+        if (overlaps(outs[i], out_b[i], weights, wb) || overlaps(outs[i], out_b[i], table_out, tb) ||
+            hits_cache(outs[i], out_b[i], pool, num_pages, Hkv, d, table, max_pages, lens, B))
+            return FA_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 3; ++j)
+            if (overlaps(outs[i], out_b[i], outs[j], out_b[j])) return FA_ERR_INVALID_ARG;
+    }
+    const size_t pb = (size_t)(num_pages * Hkv) * qcache_block_bytes(d);
+    if (overlaps(pool, pb, table, (size_t)(B * max_pages) * 4) || overlaps(pool, pb, lens, lb) ||
+        overlaps(pool, pb, table_out, tb) || overlaps(pool, pb, weights, wb))
+        return FA_ERR_INVALID_ARG;
+
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    fa::qc::EvictParams p = {};
+    p.pool = static_cast<uint8_t*>(pool);
+    p.table = table;
+    p.lens = lens;
+    p.table_out = table_out;
+    p.w_in = weights;
+    p.w_out = weights_out;
+    p.kept = kept;
+    p.lens_out = lens_out;
+    p.w_len = W;
+    p.hkv = (int)Hkv;
+    p.max_pages = (int)max_pages;
+    p.max_pages_out = (int)max_pages_out;
+    p.num_pages = (int)num_pages;
+    p.keep = (int)keep;
+    p.sink = (int)sink;
+    p.recent = (int)recent;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const dim3 grid((unsigned)Hkv, (unsigned)B);
+    if (launch_pdl(fa::qc::fa_qcache_select_kernel, grid, dim3(fa::qc::SEL_THREADS), 0, st, p) != cudaSuccess)
+        return FA_ERR_CUDA;
+    const cudaError_t e =
+        padded_head_size(d) == 128
+            ? launch_pdl(fa::qc::fa_qcache_move_kernel<128>, grid, dim3(fa::qc::ROW_THREADS), 0, st, p)
+            : launch_pdl(fa::qc::fa_qcache_move_kernel<64>, grid, dim3(fa::qc::ROW_THREADS), 0, st, p);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 fa_status fa_check_device_status(fa_stream_t stream, uint32_t* where)
 {
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -807,7 +1382,9 @@ fa_status fa_check_device_status(fa_stream_t stream, uint32_t* where)
         return FA_ERR_CUDA;
     if (where) *where = h[1];
     if (h[0] != 0u) {
-        const fa_status st_code = (h[0] & fa::STATUS_TIMEOUT) ? FA_ERR_TIMEOUT : FA_ERR_CUDA;
+        const fa_status st_code = (h[0] & fa::STATUS_TIMEOUT)    ? FA_ERR_TIMEOUT
+                                  : (h[0] & fa::STATUS_BAD_SMEM) ? FA_ERR_CUDA
+                                                                 : FA_ERR_INVALID_ARG;  // STATUS_BAD_PAGE
         // Clear what was read, atomically on the device: a bit that a kernel
         // on another stream set in between stays for the next check.
         fa_clear_status_kernel<<<1, 1, 0, st>>>(h[0], h[1]);

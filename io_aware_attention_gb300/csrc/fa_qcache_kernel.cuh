@@ -1,0 +1,1244 @@
+// A paged key/value cache held in 4 bits, for decode on sm_103a: rows are
+// appended and read back, and a few query rows attend to it.
+//
+// A stored value is  e2m1 * e4m3 * scale:  a sign, two exponent bits and one
+// mantissa bit a value (0, .5, 1, 1.5, 2, 3, 4, 6), one e4m3 scale for 16
+// channels of a row and one fp32 scale a tensor.  That is 9/16 byte a value
+// against bf16's 2, and decode, bound by reading the cache, can run 3.6 times
+// as fast.  The product e2m1 * e4m3 has at most 6 significant bits and lies
+// between 2^-10 and 2688, so it is exact in fp16: the tensor cores' operands
+// are the stored values, not roundings of them.
+//
+// A page holds PAGE = 64 keys of one kv head in one block of 72 * D bytes,
+// D = 64 or 128 stored channels (smaller head sizes are padded with zeros).
+// Rows are laid out so that a lane's share of a tensor-core operand is 16
+// consecutive bytes (8 at D = 64), neighbouring lanes' shares adjoin, and one
+// cvt turns a byte into a register of the operand:
+//   K codes   at 0:     byte x*D/2 + c/2 of key x, low nibble the even channel;
+//   K scales  at 32*D:  byte ((x%8)*4 + b/p)*8*p + (x/8)*p + b%p of channel
+//                       block b, p = D/64 (a lane's 8 keys are together);
+//   V codes   at 36*D:  byte (x/2)*D + c, low nibble the even key (the
+//                       contraction over keys wants pairs of keys);
+//   V scales  at 68*D:  byte (((x/2)%4)*D/16 + b)*16 + (x/8)*2 + x%2.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "ptx.cuh"
+
+namespace fa {
+
+constexpr uint32_t STATUS_BAD_PAGE = 4u;  // a page table entry outside the pool: its keys were skipped
+
+namespace qc {
+
+constexpr int PAGE = 64;
+constexpr int MAX_B = 2048;   // sequences of a call (their page counts' prefix sums sit in shared memory)
+constexpr int MAX_NQ = 8;
+constexpr float LN2 = 0.69314718055994530942f;
+
+template <int D>
+struct Block {
+    static_assert(D == 64 || D == 128, "stored channels");
+    static constexpr int P = D / 64;             // channel blocks per lane of a key row
+    static constexpr int NB = D / 16;            // channel blocks
+    static constexpr int KS = 32 * D, VC = 36 * D, VS = 68 * D, BYTES = 72 * D;
+    __host__ __device__ static constexpr int kcode(int x) { return x * (D / 2); }
+    __host__ __device__ static constexpr int kscale(int x, int b)
+    {
+        return KS + ((x % 8) * 4 + b / P) * 8 * P + (x / 8) * P + b % P;
+    }
+    __host__ __device__ static constexpr int vcode(int x) { return VC + (x / 2) * D; }
+    __host__ __device__ static constexpr int vscale(int x, int b)
+    {
+        return VS + (((x / 2) % 4) * NB + b) * 16 + (x / 8) * 2 + x % 2;
+    }
+};
+
+// Two e2m1 values (byte `i` of w, low nibble first) as exact fp16.
+template <int I>
+__device__ __forceinline__ uint32_t e2m1x2(uint32_t w)
+{
+    uint32_t r;
+    if constexpr (I == 0)
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+    else if constexpr (I == 1)
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+    else if constexpr (I == 2)
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
+    else
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+// Two e4m3 values as exact fp16.
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t two_bytes)
+{
+    uint32_t r;
+    const uint16_t h = (uint16_t)two_bytes;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+// d += A (16 x 16, rows) * B (16 x 8, columns), fp16 operands, fp32 sums.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ----------------------------------------------------------------- rounding
+
+// A scale for 16 channels from their largest magnitude: amax / (6 scale) in
+// e4m3, to nearest (halves to even), at most 448.  Returns its byte.
+__device__ __forceinline__ uint32_t scale_byte(float amax, float six)
+{
+    const float t = fminf(__fdiv_rn(amax, six), 448.0f);
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(t));
+    return r & 0xFFu;
+}
+
+__device__ __forceinline__ float scale_value(uint32_t byte)
+{
+    const uint32_t h = e4m3x2(byte & 0xFFu);
+    return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
+}
+
+// Two quotients x / (e4m3 * scale) as e2m1, to nearest, halves to even,
+// magnitudes above 6 to 6: `lo` in the low nibble.  inv is the reciprocal in
+// fp32, which puts a quotient that is half way between two codes up to 2^-23
+// off it (bf16 inputs meet exact halves often); adding and subtracting
+// 1.5 * 2^9 rounds to a multiple of 2^-14 first, which brings those back and
+// moves no other: a quotient of an 8-bit and a 4-bit significand that is not
+// half way differs from there by 2^-10 at least.
+__device__ __forceinline__ uint32_t codes2(float lo, float hi, float inv)
+{
+    constexpr float C = 768.0f;
+    const float a = __fadd_rn(__fmaf_rn(lo, inv, C), -C), b = __fadd_rn(__fmaf_rn(hi, inv, C), -C);
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b32 %0, {t, t, t, t};\n\t}" : "=r"(r) : "f"(b), "f"(a));
+    return r & 0xFFu;
+}
+
+__device__ __forceinline__ void unpack8(const uint4 w, float* f)
+{
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(v[i] << 16);
+        f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    }
+}
+
+// ------------------------------------------------------------ append, read
+
+struct RowParams {
+    const __nv_bfloat16 *k, *v;    // append: new rows, (B, Hkv, N, d) by strides
+    __nv_bfloat16 *ko, *vo;        // read: contiguous (B, Hkv, N, d)
+    int64_t ksb, ksh, ksn, vsb, vsh, vsn;
+    uint8_t* pool;
+    const int32_t *table, *lens;
+    int64_t n;
+    int hkv, d, max_pages, num_pages, tiles;
+    int newest;                    // row i is position lens - N + i (else i)
+    float k_scale, v_scale, k_six, v_six;
+};
+
+// The 16 channels of block b of row p (d of them exist), zeros past d or when !have.
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, int b, int d, bool have, float (&f)[16])
+{
+    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+    if (have && b * 16 < d) w0 = *reinterpret_cast<const uint4*>(p + b * 16);
+    if (have && b * 16 + 8 < d) w1 = *reinterpret_cast<const uint4*>(p + b * 16 + 8);
+    unpack8(w0, f);
+    unpack8(w1, f + 8);
+}
+
+__device__ __forceinline__ float amax16(const float (&f)[16])
+{
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
+    return m;
+}
+
+// The page of position x of sequence b, or -1 (and the status bit).
+__device__ __forceinline__ int page_of(const int32_t* table, int max_pages, int num_pages, int b, int slot)
+{
+    int id = -1;
+    if (slot < max_pages) id = table[(int64_t)b * max_pages + slot];
+    return id >= 0 && id < num_pages ? id : -1;
+}
+
+constexpr int ROW_THREADS = 256;
+
+// Append: block (tile, kv head, sequence) writes one page's share of the new
+// rows.  New keys are positions lens - N .. lens - 1; rows of negative
+// position are padding and go nowhere.  A byte of V holds two keys: where
+// only one of them is new, the other nibble is kept.  One block writes all
+// of a page's new rows, so no two blocks share a byte.
+template <int D>
+__global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const RowParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    using L = Block<D>;
+    const int b = blockIdx.z, h = blockIdx.y;
+    const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.max_pages * PAGE);
+    const int64_t first = max((int64_t)p.lens[b] - p.n, (int64_t)0);  // first new position
+    const int64_t shift = p.n - p.lens[b];                           // row of position x: x + shift
+    const int64_t page0 = first / PAGE + blockIdx.x;
+    const int x0 = (int)max(first - page0 * PAGE, (int64_t)0);
+    const int x1 = (int)min(len - page0 * PAGE, (int64_t)PAGE);
+    if (p.lens[b] > len && blockIdx.x == 0 && threadIdx.x == 0)
+        atomicOr(&g_status, STATUS_BAD_PAGE);  // longer than its page table
+    if (x0 >= x1) return;
+    const int id = page_of(p.table, p.max_pages, p.num_pages, b, (int)page0);
+    if (id < 0) {
+        if (threadIdx.x == 0) atomicOr(&g_status, STATUS_BAD_PAGE);
+        return;
+    }
+    uint8_t* const blk = p.pool + ((int64_t)id * p.hkv + h) * L::BYTES;
+    const __nv_bfloat16* const kr = p.k + b * p.ksb + h * p.ksh + (page0 * PAGE + shift) * p.ksn;
+    const __nv_bfloat16* const vr = p.v + b * p.vsb + h * p.vsh + (page0 * PAGE + shift) * p.vsn;
+    for (int t = threadIdx.x; t < (x1 - x0) * L::NB; t += ROW_THREADS) {
+        const int x = x0 + t / L::NB, c = t % L::NB;
+        float f[16];
+        load16(kr + x * p.ksn, c, p.d, true, f);
+        const uint32_t sb = scale_byte(amax16(f), p.k_six);
+        const float s = scale_value(sb) * p.k_scale;
+        const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i / 4] |= codes2(f[2 * i], f[2 * i + 1], inv) << (8 * (i % 4));
+        *reinterpret_cast<uint2*>(blk + L::kcode(x) + c * 8) = make_uint2(w[0], w[1]);
+        blk[L::kscale(x, c)] = (uint8_t)sb;
+    }
+    const int j0 = x0 / 2, j1 = (x1 + 1) / 2;
+    for (int t = threadIdx.x; t < (j1 - j0) * L::NB; t += ROW_THREADS) {
+        const int j = j0 + t / L::NB, c = t % L::NB;
+        const bool even = 2 * j >= x0, odd = 2 * j + 1 < x1;
+        float f[16], g[16];
+        load16(vr + 2 * j * p.vsn, c, p.d, even, f);
+        load16(vr + (2 * j + 1) * p.vsn, c, p.d, odd, g);
+        const uint32_t sf = scale_byte(amax16(f), p.v_six), sg = scale_byte(amax16(g), p.v_six);
+        const float vf = scale_value(sf) * p.v_scale, vg = scale_value(sg) * p.v_scale;
+        const float nf = vf > 0.f ? __frcp_rn(vf) : 0.f, ng = vg > 0.f ? __frcp_rn(vg) : 0.f;
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // channels 2i, 2i + 1 of both keys
+            const uint32_t a = codes2(f[2 * i], f[2 * i + 1], nf), e = codes2(g[2 * i], g[2 * i + 1], ng);
+            const uint32_t two = (a & 15u) | ((e & 15u) << 4) | ((a >> 4) << 8) | ((e >> 4) << 12);
+            w[i / 2] |= two << (16 * (i % 2));
+        }
+        uint4* const at = reinterpret_cast<uint4*>(blk + L::vcode(2 * j) + c * 16);
+        if (!(even && odd)) {
+            const uint4 old = *at;
+            const uint32_t mine = even ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
+            w[0] = (w[0] & mine) | (old.x & ~mine);
+            w[1] = (w[1] & mine) | (old.y & ~mine);
+            w[2] = (w[2] & mine) | (old.z & ~mine);
+            w[3] = (w[3] & mine) | (old.w & ~mine);
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
+        if (even) blk[L::vscale(2 * j, c)] = (uint8_t)sf;
+        if (odd) blk[L::vscale(2 * j + 1, c)] = (uint8_t)sg;
+    }
+}
+
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float s)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    return ptx::pack_bf16x2(f.x * s, f.y * s);
+}
+
+// Read: rows first .. first + N - 1 of every sequence as bf16 (rounded once:
+// the stored value times the tensor's scale); rows where no key is are zero.
+// Block (tile of 64 rows, kv head, sequence).
+template <int D>
+__global__ void __launch_bounds__(ROW_THREADS) fa_qcache_read_kernel(const RowParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    using L = Block<D>;
+    const int b = blockIdx.z, h = blockIdx.y;
+    const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.max_pages * PAGE);
+    const int64_t shift = p.newest ? (int64_t)p.lens[b] - p.n : 0;
+    const int64_t i0 = (int64_t)blockIdx.x * PAGE;
+    const int rows = (int)min(p.n - i0, (int64_t)PAGE);
+    const int64_t out0 = (((int64_t)b * p.hkv + h) * p.n + i0) * p.d;
+    for (int t = threadIdx.x; t < rows * L::NB; t += ROW_THREADS) {
+        const int r = t / L::NB, c = t % L::NB;
+        if (c * 16 >= p.d) continue;
+        const int64_t pos = i0 + r + shift;
+        uint32_t kw[8] = {}, vw[8] = {};
+        if (pos >= 0 && pos < len) {
+            const int id = page_of(p.table, p.max_pages, p.num_pages, b, (int)(pos / PAGE));
+            if (id < 0) {
+                atomicOr(&g_status, STATUS_BAD_PAGE);
+            } else {
+                const int x = (int)(pos % PAGE);
+                const uint8_t* const blk = p.pool + ((int64_t)id * p.hkv + h) * L::BYTES;
+                const uint2 kc = *reinterpret_cast<const uint2*>(blk + L::kcode(x) + c * 8);
+                const float ks = scale_value(blk[L::kscale(x, c)]) * p.k_scale;
+                const uint4 vc = *reinterpret_cast<const uint4*>(blk + L::vcode(x) + c * 16);
+                const float vs = scale_value(blk[L::vscale(x, c)]) * p.v_scale;
+                kw[0] = scaled_bf16x2(e2m1x2<0>(kc.x), ks);
+                kw[1] = scaled_bf16x2(e2m1x2<1>(kc.x), ks);
+                kw[2] = scaled_bf16x2(e2m1x2<2>(kc.x), ks);
+                kw[3] = scaled_bf16x2(e2m1x2<3>(kc.x), ks);
+                kw[4] = scaled_bf16x2(e2m1x2<0>(kc.y), ks);
+                kw[5] = scaled_bf16x2(e2m1x2<1>(kc.y), ks);
+                kw[6] = scaled_bf16x2(e2m1x2<2>(kc.y), ks);
+                kw[7] = scaled_bf16x2(e2m1x2<3>(kc.y), ks);
+                const uint32_t v4[4] = {vc.x, vc.y, vc.z, vc.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // 4 channels' bytes: this key's nibbles, packed two to a byte
+                    const uint32_t n = (x % 2 ? v4[i] >> 4 : v4[i]) & 0x0F0F0F0Fu;
+                    const uint32_t two = n | (n >> 4);  // bytes 0 and 2 hold channels (0, 1) and (2, 3)
+                    vw[2 * i] = scaled_bf16x2(e2m1x2<0>(two), vs);
+                    vw[2 * i + 1] = scaled_bf16x2(e2m1x2<2>(two), vs);
+                }
+            }
+        }
+        __nv_bfloat16* const ko = p.ko + out0 + (int64_t)r * p.d + c * 16;
+        __nv_bfloat16* const vo = p.vo + out0 + (int64_t)r * p.d + c * 16;
+        ptx::st_global_v4(ko, kw[0], kw[1], kw[2], kw[3]);
+        ptx::st_global_v4(vo, vw[0], vw[1], vw[2], vw[3]);
+        if (c * 16 + 8 < p.d) {
+            ptx::st_global_v4(ko + 8, kw[4], kw[5], kw[6], kw[7]);
+            ptx::st_global_v4(vo + 8, vw[4], vw[5], vw[6], vw[7]);
+        }
+    }
+}
+
+// ---------------------------------------------------------- the work's division
+
+// The calls over whole caches (decode, weights) divide a list of units: all
+// pages of sequence 0's first (kv head, row block), of its second one, and so
+// on, then sequence 1's.  The list's length follows from the lengths in
+// device memory, so every block builds the page counts' prefix sums itself
+// and takes an equal run of units: unequal sequences cost no idle blocks, and
+// no plan is made on the host.
+struct Work {
+    const int* prefix;  // B + 1 sums of page counts (shared memory)
+    int B, hr;          // hr: kv heads x row blocks
+
+    struct Unit {
+        int b, hr, page, pages;
+    };
+    __device__ __forceinline__ int total() const { return prefix[B] * hr; }
+    __device__ __forceinline__ Unit at(int x) const
+    {
+        const int y = x / hr;
+        int lo = 0, hi = B;  // prefix[lo] <= y < prefix[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] <= y) lo = mid;
+            else hi = mid;
+        }
+        Unit u;
+        u.b = lo;
+        u.pages = prefix[lo + 1] - prefix[lo];
+        const int rem = x - prefix[lo] * hr;
+        u.hr = rem / u.pages;
+        u.page = rem - u.hr * u.pages;
+        return u;
+    }
+};
+
+// A sequence's length, at most what its page table holds.
+__device__ __forceinline__ int length_of(const int32_t* lens, int b, int max_pages)
+{
+    return (int)min((int64_t)max(lens[b], 0), (int64_t)max_pages * PAGE);
+}
+
+// prefix[0 .. B] by a block of NTHREADS threads (scratch: one int per warp).
+template <int NTHREADS>
+__device__ __forceinline__ void page_prefix(const int32_t* lens, int B, int max_pages, int* prefix, int* scratch)
+{
+    constexpr int W = NTHREADS / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int base = 0;
+    if (tid == 0) prefix[0] = 0;
+    for (int b0 = 0; b0 < B; b0 += NTHREADS) {
+        const int b = b0 + tid;
+        int v = b < B ? (length_of(lens, b, max_pages) + PAGE - 1) / PAGE : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += n;
+        }
+        if (lane == 31) scratch[warp] = v;
+        __syncthreads();
+        int before = base, all = base;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const int n = scratch[w];
+            if (w < warp) before += n;
+            all += n;
+        }
+        if (b < B) prefix[b + 1] = before + v;
+        base = all;
+        __syncthreads();
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------------- decode
+
+struct DecParams {
+    const __nv_bfloat16* q;       // (B, H, nq, d): the rows of a kv head's group adjoin
+    const uint8_t* pool;          // (num_pages, hkv, 72 * D)
+    const int32_t *table, *lens;  // (B, max_pages), (B)
+    __nv_bfloat16* o;             // (B, H, nq, d)
+    float* lse;                   // (B, H, nq)
+    float* ws;                    // 2 partial results a block
+    int* desc;                    // 2 ints a block: the split segment that begins there (or -1), its last block
+    int B, hkv, nq, rows, rb;     // rows: query rows of a kv head; rb: blocks of them
+    int d, max_pages, num_pages, causal;
+    float scale_log2;             // scale * log2(e) * k_scale
+    float v_scale;
+    const float* lse_in;          // weights: (B, H, nq)
+    const float* w_in;            // (B, hkv, w_len)
+    float* w_out;
+    int64_t w_len;
+};
+
+constexpr int WARPS = 8;
+constexpr int THREADS = WARPS * 32;
+
+// A probability is held as 2^(x - max + SHIFT) in fp16 (11 bits): 1 becomes
+// 2^15, within fp16's range, and weights down to 2^-29 of the largest keep
+// full precision, so that a long cache of small weights is not rounded away.
+constexpr float SHIFT = 15.0f;
+
+template <int NBYTES>
+struct Chunk {  // a lane's share of a row: 16 or 8 bytes
+    uint32_t w[NBYTES / 4];
+    __device__ __forceinline__ void load(const uint8_t* p)
+    {
+        if constexpr (NBYTES == 16) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[0] = v.x, w[1] = v.y;
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t dup_lo(uint32_t h2) { return __byte_perm(h2, h2, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t h2) { return __byte_perm(h2, h2, 0x3232); }
+
+// Query rows of one (sequence, kv head, row block), as the B operand of the
+// score product, and what a lane needs of them: lane (g, t) = (lane / 4,
+// lane % 4) holds row g's channels D/4 t .. and, of the columns 2t and
+// 2t + 1 whose scores it gets, the factor to base-2 scores and the count of
+// keys they see.  Rows are scaled by a power of two so that their largest
+// entry lies in [2^14, 2^15): bf16 entries down to 2^-31 of it are exact in
+// fp16 whatever the row's size.
+template <int D, int NT>
+struct Rows {
+    uint32_t q[NT][D / 16][2];
+    float sc[NT][2];
+    int lim[NT][2];
+    int len, min_lim;
+
+    __device__ __forceinline__ void load(const DecParams& p, int b, int hr, int len_)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int h = hr / p.rb, r0 = (hr - h * p.rb) * (8 * NT);
+        const int64_t row0 = ((int64_t)b * p.hkv + h) * p.rows;
+        len = len_;
+        min_lim = p.causal ? len - p.nq + 1 : len;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = r0 + nt * 8 + g;
+            float f[D / 4];
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+                uint4 w = make_uint4(0, 0, 0, 0);
+                const int c = D / 4 * t + 8 * e;
+                if (row < p.rows && c < p.d) w = *reinterpret_cast<const uint4*>(p.q + (row0 + row) * p.d + c);
+                unpack8(w, f + 8 * e);
+            }
+            float am = 0.f;
+#pragma unroll
+            for (int e = 0; e < D / 4; ++e) am = fmaxf(am, fabsf(f[e]));
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+            const int ex = (int)(__float_as_uint(am) >> 23) - 127;
+            const int k = am > 0.f && ex < 128 ? min(126, max(-126, 14 - ex)) : 0;
+            const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+            const float down = p.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                q[nt][c][0] = pack_h2(f[4 * c] * up, f[4 * c + 1] * up);
+                q[nt][c][1] = pack_h2(f[4 * c + 2] * up, f[4 * c + 3] * up);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                sc[nt][j] = __shfl_sync(0xffffffffu, down, (2 * t + j) * 4);
+                const int r = r0 + nt * 8 + 2 * t + j;
+                lim[nt][j] = p.causal && r < p.rows ? len - p.nq + r % p.nq + 1 : len;
+            }
+        }
+    }
+};
+
+// Scores of a page, transposed: S^T = K Q^T, 16 keys by 8 query rows a
+// product, so that few rows waste no tensor work.  Lane (g, t) of s[r][nt]
+// holds keys 16r + g (entries 0, 1) and 16r + 8 + g (2, 3) against rows 2t and
+// 2t + 1.  blk: a page's block in shared or global memory.
+template <int D, int NT>
+__device__ __forceinline__ void page_scores(const uint8_t* blk, const Rows<D, NT>& rows, float (&s)[4][NT][4])
+{
+    using L = Block<D>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    Chunk<8 * L::P> sc;
+    sc.load(blk + L::KS + lane * (8 * L::P));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        Chunk<D / 8> k0, k1;
+        k0.load(blk + L::kcode(16 * r + g) + t * (D / 8));
+        k1.load(blk + L::kcode(16 * r + 8 + g) + t * (D / 8));
+        uint32_t s0[L::P], s1[L::P];  // scales of the lane's channel blocks, rows g and g + 8
+        if constexpr (D == 128) {
+            const uint32_t a = e4m3x2(sc.w[r]), b = e4m3x2(sc.w[r] >> 16);
+            s0[0] = dup_lo(a), s0[1] = dup_hi(a);
+            s1[0] = dup_lo(b), s1[1] = dup_hi(b);
+        } else {
+            const uint32_t a = e4m3x2(sc.w[r / 2] >> (16 * (r % 2)));
+            s0[0] = dup_lo(a);
+            s1[0] = dup_hi(a);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[r][nt][e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            const uint32_t w0 = k0.w[c / 2], w1 = k1.w[c / 2];
+            const uint32_t f0 = s0[c / 4], f1 = s1[c / 4];
+            const uint32_t a0 = hmul2(c % 2 ? e2m1x2<2>(w0) : e2m1x2<0>(w0), f0);
+            const uint32_t a1 = hmul2(c % 2 ? e2m1x2<2>(w1) : e2m1x2<0>(w1), f1);
+            const uint32_t a2 = hmul2(c % 2 ? e2m1x2<3>(w0) : e2m1x2<1>(w0), f0);
+            const uint32_t a3 = hmul2(c % 2 ? e2m1x2<3>(w1) : e2m1x2<1>(w1), f1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(s[r][nt], a0, a1, a2, a3, rows.q[nt][c][0], rows.q[nt][c][1]);
+        }
+    }
+}
+
+// Running softmax of a warp over a segment's pages, O transposed: lane (g, t)
+// of o[m][nt] holds channels D/8 g + 2m (entries 0, 1) and D/8 g + 2m + 1
+// (2, 3) of rows 2t and 2t + 1.
+template <int D, int NT>
+struct State {
+    float o[D / 16][NT][4];
+    // Largest unscaled score (differences to it are scaled, so that the
+    // largest key's weight is 1 however large the scores are); this lane's
+    // share of the sum (times 2^SHIFT).
+    float m[NT][2], l[NT][2];
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) m[nt][j] = -INFINITY, l[nt][j] = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[c][nt][e] = 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void add_page(const uint8_t* blk, const Rows<D, NT>& rows, int page)
+    {
+        using L = Block<D>;
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        float s[4][NT][4];
+        page_scores<D, NT>(blk, rows, s);
+        const int key0 = page * PAGE;
+        const bool whole = key0 + PAGE <= rows.min_lim;  // every row sees every key
+        bool rises = false;
+        float mm[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (!whole) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        if (key0 + 16 * r + g >= rows.lim[nt][j]) s[r][nt][j] = -INFINITY;
+                        if (key0 + 16 * r + 8 + g >= rows.lim[nt][j]) s[r][nt][2 + j] = -INFINITY;
+                    }
+                }
+                float x = fmaxf(s[0][nt][j], s[0][nt][2 + j]);
+#pragma unroll
+                for (int r = 1; r < 4; ++r) x = fmaxf(x, fmaxf(s[r][nt][j], s[r][nt][2 + j]));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                mm[nt][j] = fmaxf(m[nt][j], x);
+                rises |= mm[nt][j] > m[nt][j];
+            }
+        if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float f[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    f[j] = m[nt][j] == -INFINITY ? 0.f : ptx::ex2((m[nt][j] - mm[nt][j]) * rows.sc[nt][j]);
+                    l[nt][j] *= f[j];
+                    m[nt][j] = mm[nt][j];
+                }
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    o[c][nt][0] *= f[0];
+                    o[c][nt][1] *= f[1];
+                    o[c][nt][2] *= f[0];
+                    o[c][nt][3] *= f[1];
+                }
+            }
+        }
+        uint32_t pb[4][NT][2];  // probabilities as the B operand: keys 2t, 2t + 1 (and + 8) of row g
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float top[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) top[j] = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = s[r][nt][e];
+                    float pr = ptx::ex2(fmaf(x - top[e & 1], rows.sc[nt][e & 1], SHIFT));
+                    if (!whole && x == -INFINITY) pr = 0.f;
+                    l[nt][e & 1] += pr;
+                    s[r][nt][e] = pr;
+                }
+                pb[r][nt][0] = transpose8x8(pack_h2(s[r][nt][0], s[r][nt][1]));
+                pb[r][nt][1] = transpose8x8(pack_h2(s[r][nt][2], s[r][nt][3]));
+            }
+        }
+        // O^T += V^T P^T: a scale belongs to a key and a block of channels,
+        // so it multiplies the operand (exactly), two keys at a time.
+        const int b = g * (D / 8) / 16;
+        Chunk<16> sc;
+        sc.load(blk + L::VS + (t * L::NB + b) * 16);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            Chunk<D / 8> v0, v1;
+            v0.load(blk + L::vcode(16 * r + 2 * t) + g * (D / 8));
+            v1.load(blk + L::vcode(16 * r + 8 + 2 * t) + g * (D / 8));
+            uint32_t w = sc.w[r];
+            if (!whole) {  // places of no key hold anything: their weight is 0, and 0 * NaN must not be formed
+                const int left = rows.len - (key0 + 16 * r + 2 * t);
+                if (left < 10) w &= left <= 0 ? 0u : left == 1 ? 0xFFu : left <= 8 ? 0xFFFFu : 0xFFFFFFu;
+            }
+            const uint32_t f0 = e4m3x2(w), f1 = e4m3x2(w >> 16);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                const uint32_t w0 = v0.w[c / 2], w1 = v1.w[c / 2];
+                const uint32_t a0 = hmul2(c % 2 ? e2m1x2<2>(w0) : e2m1x2<0>(w0), f0);
+                const uint32_t a1 = hmul2(c % 2 ? e2m1x2<3>(w0) : e2m1x2<1>(w0), f0);
+                const uint32_t a2 = hmul2(c % 2 ? e2m1x2<2>(w1) : e2m1x2<0>(w1), f1);
+                const uint32_t a3 = hmul2(c % 2 ? e2m1x2<3>(w1) : e2m1x2<1>(w1), f1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma(o[c][nt], a0, a1, a2, a3, pb[r][nt][0], pb[r][nt][1]);
+            }
+        }
+    }
+
+    // The end of a segment: base-2 maxima, and the sums over the warp's lanes
+    // that share a row.
+    __device__ __forceinline__ void close(const Rows<D, NT>& rows)
+    {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
+                l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
+                l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
+                m[nt][j] = m[nt][j] == -INFINITY ? m[nt][j] : m[nt][j] * rows.sc[nt][j];
+            }
+    }
+};
+
+// A partial result: R rows of D unnormalised outputs, then their maxima and sums.
+template <int D, int R>
+struct Partial {
+    static constexpr int FLOATS = R * (D + 2);
+    static __device__ __forceinline__ int o(int row) { return row * D; }
+    static __device__ __forceinline__ int m(int row) { return R * D + row; }
+    static __device__ __forceinline__ int l(int row) { return R * D + R + row; }
+};
+
+__device__ __forceinline__ float natural_lse(float m, float l)
+{
+    return l > 0.f || !(l == l) ? (m + ptx::lg2(l) - SHIFT) * LN2 : -INFINITY;
+}
+
+// Decode.  Block c takes units [c T / G, (c + 1) T / G) of the T pages, and its
+// warps equal runs of those.  A segment (all pages of one sequence, kv head
+// and row block) that lies within a warp's run is written out at once; the
+// pieces of others go to shared memory, where the block joins neighbouring
+// warps' pieces of a segment; pieces of segments that cross blocks go to the
+// workspace (two a block at most) for the combine kernel.
+template <int D, int NT>
+__global__ void __launch_bounds__(THREADS, 1) fa_qcache_decode_kernel(const DecParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    constexpr int R = 8 * NT;
+    using PS = Partial<D, R>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* const slots = reinterpret_cast<float*>(smem);             // 2 * WARPS partial results
+    int* const prefix = reinterpret_cast<int*>(slots + 2 * WARPS * PS::FLOATS);
+    __shared__ int scratch[WARPS];
+    __shared__ int slot_seg[2 * WARPS];   // segment of each slot, or -1
+    __shared__ int slot_ends[2 * WARPS];  // bit 0: the segment begins in it, bit 1: ends
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    if (tid < 2 * WARPS) slot_seg[tid] = -1;
+    page_prefix<THREADS>(p.lens, p.B, p.max_pages, prefix, scratch);
+    Work work{prefix, p.B, p.hkv * p.rb};
+
+    // Sequences of no key: nothing is seen.
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (lane == 0 && warp == 0 && p.lens[b] > p.max_pages * (int64_t)PAGE) atomicOr(&g_status, STATUS_BAD_PAGE);
+        if (prefix[b + 1] != prefix[b]) continue;
+        const int64_t n = (int64_t)p.hkv * p.rows, at = b * n;
+        for (int64_t e = tid; e < n * (p.d / 8); e += THREADS) ptx::st_global_v4(p.o + at * p.d + e * 8, 0, 0, 0, 0);
+        for (int64_t e = tid; e < n; e += THREADS) p.lse[at + e] = -INFINITY;
+    }
+
+    const int T = work.total();
+    const int G = min((int)gridDim.x, T);
+    const int cta = blockIdx.x;
+    if (cta >= G) {
+        if (tid == 0) p.desc[2 * cta] = -1;
+        return;
+    }
+    const int lo = (int)((int64_t)cta * T / G), hi = (int)((int64_t)(cta + 1) * T / G);
+    const int nw = min(WARPS, hi - lo);
+    int slot = 0;
+    if (warp < nw) {
+        const int x0 = lo + (int)((int64_t)(hi - lo) * warp / nw), x1 = lo + (int)((int64_t)(hi - lo) * (warp + 1) / nw);
+        Rows<D, NT> rows;
+        State<D, NT> st;
+        int seg = -1, begins = 0, last_page = 0, seg_pages = 0;
+        auto finish = [&] {
+            st.close(rows);
+            const int ends = last_page == seg_pages - 1;
+            if (begins && ends) {
+                const int b = seg / work.hr, hr = seg - b * work.hr, h = hr / p.rb;
+                const int r0 = (hr - h * p.rb) * R;
+                const int64_t row0 = ((int64_t)b * p.hkv + h) * p.rows;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int row = r0 + nt * 8 + 2 * t + j;
+                        if (row >= p.rows) continue;
+                        const float f = st.l[nt][j] == 0.f ? 0.f : p.v_scale / st.l[nt][j];
+                        uint32_t w[D / 16];
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) w[c] = ptx::pack_bf16x2(st.o[c][nt][j] * f, st.o[c][nt][2 + j] * f);
+                        __nv_bfloat16* const out = p.o + (row0 + row) * p.d + g * (D / 8);
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            if (g * (D / 8) + 8 * c < p.d) ptx::st_global_v4(out + 8 * c, w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                        if (g == 0) p.lse[row0 + row] = natural_lse(st.m[nt][j], st.l[nt][j]);
+                    }
+                return;
+            }
+            const int at = warp * 2 + slot++;
+            float* const f = slots + at * PS::FLOATS;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = nt * 8 + 2 * t + j;
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c)
+                        *reinterpret_cast<float2*>(f + PS::o(row) + g * (D / 8) + 2 * c) = make_float2(st.o[c][nt][j], st.o[c][nt][2 + j]);
+                    if (g == 0) {
+                        f[PS::m(row)] = st.m[nt][j];
+                        f[PS::l(row)] = st.l[nt][j];
+                    }
+                }
+            if (lane == 0) {
+                slot_seg[at] = seg;
+                slot_ends[at] = begins | (ends << 1);
+            }
+        };
+        for (int base = x0; base < x1; base += 32) {
+            // The next 32 units' places, one a lane.
+            int my_seg = 0, my_page = 0, my_pages = 0, my_blk = -1;
+            if (base + lane < x1) {
+                const Work::Unit u = work.at(base + lane);
+                my_seg = u.b * work.hr + u.hr;
+                my_page = u.page;
+                my_pages = u.pages;
+                const int id = page_of(p.table, p.max_pages, p.num_pages, u.b, u.page);
+                if (id < 0) atomicOr(&g_status, STATUS_BAD_PAGE);
+                else my_blk = id * p.hkv + u.hr / p.rb;
+            }
+            const int n = min(32, x1 - base);
+            for (int i = 0; i < n; ++i) {
+                const int s = __shfl_sync(0xffffffffu, my_seg, i);
+                const int page = __shfl_sync(0xffffffffu, my_page, i);
+                const int blk = __shfl_sync(0xffffffffu, my_blk, i);
+                if (s != seg) {
+                    if (seg >= 0) finish();
+                    seg = s;
+                    begins = page == 0;
+                    seg_pages = __shfl_sync(0xffffffffu, my_pages, i);
+                    const int b = s / work.hr;
+                    rows.load(p, b, s - b * work.hr, length_of(p.lens, b, p.max_pages));
+                    st.clear();
+                }
+                last_page = page;
+                if (blk >= 0) st.add_page(p.pool + (int64_t)blk * Block<D>::BYTES, rows, page);
+            }
+        }
+        finish();
+    }
+    __syncthreads();
+
+    // Join the warps' pieces.
+    if (tid == 0) p.desc[2 * cta] = -1;
+    int a = 0;
+    while (a < 2 * WARPS) {
+        const int seg = slot_seg[a];
+        if (seg < 0) {
+            ++a;
+            continue;
+        }
+        int z = a;  // last slot of the run
+        for (int e = a + 1; e < 2 * WARPS; ++e) {
+            if (slot_seg[e] < 0) continue;
+            if (slot_seg[e] != seg) break;
+            z = e;
+        }
+        const bool begins = slot_ends[a] & 1, ends = slot_ends[z] & 2;
+        const int b = seg / work.hr, hr = seg - b * work.hr, h = hr / p.rb;
+        const int r0 = (hr - h * p.rb) * R;
+        const int64_t row0 = ((int64_t)b * p.hkv + h) * p.rows;
+        float* const part = p.ws + ((int64_t)cta * 2 + (begins ? 1 : 0)) * PS::FLOATS;
+        for (int e = tid; e < R * (D / 2); e += THREADS) {
+            const int r = e / (D / 2), c = e % (D / 2) * 2;
+            float mx = -INFINITY;
+            for (int k = a; k <= z; ++k)
+                if (slot_seg[k] >= 0) mx = fmaxf(mx, slots[k * PS::FLOATS + PS::m(r)]);
+            float x = 0.f, y = 0.f, l = 0.f;
+            for (int k = a; k <= z; ++k) {
+                if (slot_seg[k] < 0) continue;
+                const float* const f = slots + k * PS::FLOATS;
+                const float mk = f[PS::m(r)];
+                const float wk = mk == -INFINITY ? 0.f : ptx::ex2(mk - mx);
+                const float2 v = *reinterpret_cast<const float2*>(f + PS::o(r) + c);
+                x = fmaf(v.x, wk, x);
+                y = fmaf(v.y, wk, y);
+                l = fmaf(f[PS::l(r)], wk, l);
+            }
+            if (begins && ends) {
+                if (r0 + r >= p.rows) continue;
+                const float f = l == 0.f ? 0.f : p.v_scale / l;
+                if (c < p.d)
+                    *reinterpret_cast<uint32_t*>(p.o + (row0 + r0 + r) * p.d + c) = ptx::pack_bf16x2(x * f, y * f);
+                if (c == 0) p.lse[row0 + r0 + r] = natural_lse(mx, l);
+            } else {
+                *reinterpret_cast<float2*>(part + PS::o(r) + c) = make_float2(x, y);
+                if (c == 0) {
+                    part[PS::m(r)] = mx;
+                    part[PS::l(r)] = l;
+                }
+            }
+        }
+        if (begins && !ends && tid == 0) {
+            // The block that holds the segment's last unit x: the c with c T / G <= x < (c + 1) T / G.
+            const int x = prefix[b] * work.hr + (hr + 1) * (prefix[b + 1] - prefix[b]) - 1;
+            p.desc[2 * cta] = seg;
+            p.desc[2 * cta + 1] = (int)(((int64_t)(x + 1) * G - 1) / T);
+        }
+        a = z + 1;
+    }
+}
+
+// Joins the pieces of the segment that begins in block blockIdx.x and ends in
+// a later one: its own second piece and the first pieces of the blocks after.
+// Every row is one block's; 8 groups of 32 threads take every eighth piece.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) fa_qcache_combine_kernel(const DecParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    constexpr int R = 8 * NT, V = D / 32;
+    using PS = Partial<D, R>;
+    const int cta = blockIdx.x, r = blockIdx.y;
+    const int seg = p.desc[2 * cta];
+    if (seg < 0) return;
+    const int parts = p.desc[2 * cta + 1] - cta + 1;
+    const int HR = p.hkv * p.rb;
+    const int b = seg / HR, hr = seg - b * HR, h = hr / p.rb;
+    const int row = (hr - h * p.rb) * R + r;
+    if (row >= p.rows) return;
+    const int grp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float mx = -INFINITY, l = 0.f, o[V] = {};
+    for (int k = grp; k < parts; k += 8) {
+        const float* const f = p.ws + ((int64_t)(cta + k) * 2 + (k == 0 ? 1 : 0)) * PS::FLOATS;
+        const float mk = f[PS::m(r)], lk = f[PS::l(r)];
+        const float mn = fmaxf(mx, mk);
+        const float wa = mx == -INFINITY ? 0.f : ptx::ex2(mx - mn), wb = mk == -INFINITY ? 0.f : ptx::ex2(mk - mn);
+        l = l * wa + lk * wb;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = o[e] * wa + f[PS::o(r) + lane * V + e] * wb;
+        mx = mn;
+    }
+    __shared__ float sm[8], sl[8], so[8][D];
+    if (lane == 0) sm[grp] = mx, sl[grp] = l;
+#pragma unroll
+    for (int e = 0; e < V; ++e) so[grp][lane * V + e] = o[e];
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c >= D) return;
+    mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, sm[k]);
+    float x = 0.f;
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float w = sm[k] == -INFINITY ? 0.f : ptx::ex2(sm[k] - mx);
+        l += sl[k] * w;
+        x += so[k][c] * w;
+    }
+    const int64_t at = ((int64_t)b * p.hkv + h) * p.rows + row;
+    if (c < p.d) p.o[at * p.d + c] = __float2bfloat16_rn(l == 0.f ? 0.f : x * (p.v_scale / l));
+    if (c == 0) p.lse[at] = natural_lse(mx, l);
+}
+
+// ------------------------------------------------------------------ weights
+
+// w_out[key] = w_in[key] + sum over the rows of the key's kv head of
+// exp(scale q.k - lse): the attention weight that the rows gave each key,
+// from the logsumexps that decode returned.  Only K is read.
+template <int D, int NT>
+__global__ void __launch_bounds__(THREADS) fa_qcache_weights_kernel(const DecParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    extern __shared__ __align__(16) uint8_t smem[];
+    int* const prefix = reinterpret_cast<int*>(smem);
+    __shared__ int scratch[WARPS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    page_prefix<THREADS>(p.lens, p.B, p.max_pages, prefix, scratch);
+    // One unit is a page of a kv head: all its row blocks, so that every key's weight is one warp's.
+    Work work{prefix, p.B, p.hkv};
+    // Places behind the sequences' ends.
+    for (int64_t bh = blockIdx.x; bh < (int64_t)p.B * p.hkv; bh += gridDim.x) {
+        const int b = (int)(bh / p.hkv);
+        if (tid == 0 && bh % p.hkv == 0 && p.lens[b] > p.max_pages * (int64_t)PAGE) atomicOr(&g_status, STATUS_BAD_PAGE);
+        if (p.w_out == p.w_in) continue;
+        for (int64_t e = length_of(p.lens, b, p.max_pages) + tid; e < p.w_len; e += THREADS)
+            p.w_out[bh * p.w_len + e] = p.w_in[bh * p.w_len + e];
+    }
+    const int T = work.total();
+    const int all = gridDim.x * WARPS, G = min(all, T), me = blockIdx.x + gridDim.x * warp;
+    if (me >= G) return;
+    const int x0 = (int)((int64_t)me * T / G), x1 = (int)((int64_t)(me + 1) * T / G);
+    Rows<D, NT> rows;
+    float off[NT][2];
+    int have = -1;  // segment (with row block) whose rows are loaded
+    for (int x = x0; x < x1; ++x) {
+        const Work::Unit u = work.at(x);
+        const int id = page_of(p.table, p.max_pages, p.num_pages, u.b, u.page);
+        const int len = length_of(p.lens, u.b, p.max_pages);
+        if (id < 0 && lane == 0) atomicOr(&g_status, STATUS_BAD_PAGE);
+        float sum[8] = {};
+        for (int rbi = 0; rbi < p.rb; ++rbi) {
+            const int seg = (u.b * p.hkv + u.hr) * p.rb + rbi;
+            if (seg != have) {
+                have = seg;
+                rows.load(p, u.b, u.hr * p.rb + rbi, len);
+                const int64_t row0 = ((int64_t)u.b * p.hkv + u.hr) * p.rows;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = rbi * 8 * NT + nt * 8 + 2 * t + j;
+                        const float e = r < p.rows ? p.lse_in[row0 + r] : -INFINITY;
+                        // A row that saw nothing (or is none) gives nothing.
+                        off[nt][j] = e == -INFINITY ? -INFINITY : -e * 1.4426950408889634f;
+                    }
+            }
+            if (id < 0) continue;
+            float s[4][NT][4];
+            page_scores<D, NT>(p.pool + ((int64_t)id * p.hkv + u.hr) * Block<D>::BYTES, rows, s);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int key = u.page * PAGE + 16 * r + 8 * half + g;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (key < rows.lim[nt][j] && off[nt][j] != -INFINITY)
+                                sum[2 * r + half] += ptx::ex2(fmaf(s[r][nt][2 * half + j], rows.sc[nt][j], off[nt][j]));
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+            sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+        }
+        const int64_t at = ((int64_t)u.b * p.hkv + u.hr) * p.w_len;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t key = (int64_t)u.page * PAGE + 8 * e + g;
+            if (e / 2 == t && key < len && key < p.w_len) p.w_out[at + key] = p.w_in[at + key] + sum[e];
+        }
+    }
+}
+
+// ----------------------------------------------------------------- eviction
+
+struct EvictParams {
+    uint8_t* pool;
+    const int32_t *table, *lens, *table_out;
+    const float* w_in;   // (B, hkv, w_len)
+    float* w_out;
+    int32_t *kept, *lens_out;
+    int64_t w_len;
+    int hkv, max_pages, max_pages_out, num_pages;
+    int keep, sink, recent;
+};
+
+// Floats in the order of their values as unsigned integers: equal values
+// (-0 and 0 among them) are equal, NaN comes last.
+__device__ __forceinline__ uint32_t order_of(float w)
+{
+    if (!(w == w)) return 0u;
+    const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+constexpr int SEL_THREADS = 1024;
+
+// Chooses the keys that stay, one block a kv head of a sequence: the first
+// `sink`, the last `recent`, and of those between the keep - sink - recent
+// with the largest weights (of equal weights the lowest places), found by
+// radix selection: four histograms of 8 bits of order_of, largest digit
+// first, give the smallest weight that stays and how many of that weight do.
+__global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const EvictParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t bh = (int64_t)b * p.hkv + h;
+    const int len = length_of(p.lens, b, p.max_pages);
+    const int count = min(len, p.keep);
+    const float* const w = p.w_in + bh * p.w_len;
+    float* const wo = p.w_out + bh * p.w_len;
+    int32_t* const kept = p.kept + bh * p.keep;
+    auto weight = [&](int x) { return x < p.w_len ? w[x] : 0.f; };
+    auto put = [&](int at, int x) {
+        kept[at] = x;
+        if (at < p.w_len) wo[at] = weight(x);
+    };
+    if (h == 0 && tid == 0) {
+        p.lens_out[b] = count;
+        if (p.lens[b] > p.max_pages * (int64_t)PAGE) atomicOr(&g_status, STATUS_BAD_PAGE);
+    }
+    for (int64_t e = count + tid; e < p.w_len; e += SEL_THREADS) wo[e] = 0.f;
+    for (int e = count + tid; e < p.keep; e += SEL_THREADS) kept[e] = -1;
+    if (len <= p.keep) {
+        for (int e = tid; e < len; e += SEL_THREADS) put(e, e);
+        return;
+    }
+    const int first = p.sink, last = len - p.recent;  // the choice lies between
+    for (int e = tid; e < p.sink; e += SEL_THREADS) put(e, e);
+    for (int e = tid; e < p.recent; e += SEL_THREADS) put(p.keep - p.recent + e, last + e);
+    int need = p.keep - p.sink - p.recent;
+    if (need == 0) return;
+
+    __shared__ int hist[256];
+    __shared__ int found[2];
+    __shared__ int sums[SEL_THREADS / 32];
+    uint32_t prefix = 0, mask = 0;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        if (tid < 256) hist[tid] = 0;
+        __syncthreads();
+        for (int e = first + tid; e < last; e += SEL_THREADS) {
+            const uint32_t u = order_of(weight(e));
+            if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // Lane l holds digits 255 - 8l down to 248 - 8l.
+            int c[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
+            int upto = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int n = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += n;
+            }
+            int above = upto - sum;
+            if (above < need && need <= upto) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (above < need && need <= above + c[i]) {
+                        found[0] = 255 - 8 * lane - i;
+                        found[1] = need - above;
+                    }
+                    above += c[i];
+                }
+            }
+        }
+        __syncthreads();
+        prefix |= (uint32_t)found[0] << shift;
+        mask |= 255u << shift;
+        need = found[1];
+        __syncthreads();
+    }
+    // Everything above `prefix` stays, and the first `need` equal to it.
+    int base = 0;  // larger ones so far (low half), equal ones (high half) in separate counts
+    int base_eq = 0;
+    for (int e0 = first; e0 < last; e0 += SEL_THREADS) {
+        const int e = e0 + tid;
+        uint32_t u = 0;
+        bool gt = false, eq = false;
+        if (e < last) {
+            u = order_of(weight(e));
+            gt = u > prefix;
+            eq = u == prefix;
+        }
+        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+        if (lane == 0) sums[warp] = __popc(mg) | (__popc(me) << 16);
+        __syncthreads();
+        int before = 0, all = 0;
+        {
+            int v = sums[lane];
+            int upto = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int n = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += n;
+            }
+            all = __shfl_sync(0xffffffffu, upto, 31);
+            before = __shfl_sync(0xffffffffu, upto - v, warp);
+        }
+        const uint32_t below = (1u << lane) - 1u;
+        const int ng = base + (before & 0xffff) + __popc(mg & below);
+        const int ne = base_eq + (before >> 16) + __popc(me & below);
+        if (gt || (eq && ne < need)) put(p.sink + ng + min(ne, need), e);
+        base += all & 0xffff;
+        base_eq += all >> 16;
+        __syncthreads();
+    }
+}
+
+// Moves the kept rows to the front, a page of the destination at a time, one
+// block a kv head of a sequence.  The destination's pages may be the
+// sequence's own: row j comes from place kept[j] >= j, so writing a page
+// overwrites no row that a later page still needs, and the page is read
+// whole into shared memory before it is written.
+template <int D>
+__global__ void __launch_bounds__(ROW_THREADS) fa_qcache_move_kernel(const EvictParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    using L = Block<D>;
+    __shared__ __align__(16) uint8_t buf[L::BYTES];
+    __shared__ int src[PAGE];
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int64_t bh = (int64_t)b * p.hkv + h;
+    const int count = min(length_of(p.lens, b, p.max_pages), p.keep);
+    auto block = [&](int id) { return p.pool + ((int64_t)id * p.hkv + h) * L::BYTES; };
+    for (int x0 = 0; x0 < count; x0 += PAGE) {
+        const int out = page_of(p.table_out, p.max_pages_out, p.num_pages, b, x0 / PAGE);
+        if (tid < PAGE) src[tid] = x0 + tid < count ? p.kept[bh * p.keep + x0 + tid] : -1;
+        __syncthreads();
+        for (int t = tid; t < PAGE * L::NB; t += ROW_THREADS) {
+            const int x = t / L::NB, c = t % L::NB;
+            uint2 code = make_uint2(0, 0);
+            uint8_t sc = 0;
+            if (src[x] >= 0) {
+                const int id = page_of(p.table, p.max_pages, p.num_pages, b, src[x] / PAGE);
+                if (id >= 0) {
+                    const uint8_t* const blk = block(id);
+                    code = *reinterpret_cast<const uint2*>(blk + L::kcode(src[x] % PAGE) + c * 8);
+                    sc = blk[L::kscale(src[x] % PAGE, c)];
+                } else {
+                    atomicOr(&g_status, STATUS_BAD_PAGE);
+                }
+            }
+            *reinterpret_cast<uint2*>(buf + L::kcode(x) + c * 8) = code;
+            buf[L::kscale(x, c)] = sc;
+        }
+        for (int t = tid; t < PAGE / 2 * L::NB; t += ROW_THREADS) {
+            const int j = t / L::NB, c = t % L::NB;
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int odd = 0; odd < 2; ++odd) {
+                const int s = src[2 * j + odd];
+                uint8_t sc = 0;
+                const int id = s >= 0 ? page_of(p.table, p.max_pages, p.num_pages, b, s / PAGE) : -1;
+                if (id >= 0) {
+                    const uint8_t* const blk = block(id);
+                    const uint4 v = *reinterpret_cast<const uint4*>(blk + L::vcode(s % PAGE) + c * 16);
+                    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] |= ((s % 2 ? a[i] >> 4 : a[i]) & 0x0F0F0F0Fu) << (4 * odd);
+                    sc = blk[L::vscale(s % PAGE, c)];
+                }
+                buf[L::vscale(2 * j + odd, c)] = sc;
+            }
+            *reinterpret_cast<uint4*>(buf + L::vcode(2 * j) + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncthreads();
+        if (out >= 0) {
+            uint4* const to = reinterpret_cast<uint4*>(block(out));
+            for (int t = tid; t < L::BYTES / 16; t += ROW_THREADS) to[t] = reinterpret_cast<const uint4*>(buf)[t];
+        } else if (tid == 0) {
+            atomicOr(&g_status, STATUS_BAD_PAGE);
+        }
+        __syncthreads();  // the page's writes before later pages' reads, and buf's reads before its next writes
+    }
+}
+
+}  // namespace qc
+}  // namespace fa

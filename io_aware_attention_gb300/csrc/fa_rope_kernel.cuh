@@ -1,0 +1,214 @@
+// Rotary positions for sm_103a: the channels of a query or key row are taken
+// in pairs (a, b), and pair i of the row at position t is turned by the angle
+// t * f_i:
+//
+//   a' = factor * (a cos - b sin),   b' = factor * (b cos + a sin)
+//
+// Pair i is channels (i, i + rot/2) in the half layout and (2i, 2i + 1) in the
+// interleaved one; channels from rot on pass through.  The map is linear, so
+// its gradient is the same map with the angle negated (the transpose).
+//
+// Angles.  f_i comes as turns per position in 64-bit fixed point (units of
+// 2^-64 of a turn), so t * f_i modulo one turn is the low 64 bits of one
+// integer product: no reduction, and no position is too far (an fp32 product
+// t * f_i is off by 0.03 rad at t = 10^6).  The top 32 bits, read as a signed
+// fraction of half a turn, go to sincospif: the angle is then within 2^-32 of
+// a turn plus the fraction's rounding to fp32 (2^-24 relative).
+//
+// The work is bound by memory: 4 bytes moved per element against 3 flops.  A
+// thread owns one unit of channels (two 16-byte vectors holding 8 whole
+// pairs) of one position, computes its 8 angles once, and walks heads with
+// them, U heads' loads in flight.  Queries and keys go in one launch.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "ptx.cuh"
+
+namespace fa {
+namespace rope {
+
+constexpr int THREADS = 256;
+constexpr int U = 4;  // heads in flight per thread
+
+struct View {
+    __nv_bfloat16* p;
+    int64_t sb, sh, sn;  // elements between batches, heads, positions
+};
+
+struct Params {
+    View in[2], out[2];   // queries, keys
+    int heads[2];
+    const uint64_t* freqs;
+    const void* positions;  // (B, N) int32 or int64, or null
+    int64_t pos_sb;         // elements between the batches' positions (0: shared)
+    const int32_t* lens;    // (B), or null
+    int wide;               // positions are int64
+    int64_t n;
+    int d, rot, interleaved;
+    int tiles;              // position tiles of a sequence
+    int head_tiles, heads_per_thread;
+    float factor;
+    float sign;             // -1 turns the angle round (gradient)
+};
+
+__device__ __forceinline__ int64_t position_of(const Params& p, int b, int64_t i)
+{
+    if (p.positions) {
+        const int64_t at = b * p.pos_sb + i;
+        return p.wide ? static_cast<const int64_t*>(p.positions)[at] : (int64_t) static_cast<const int32_t*>(p.positions)[at];
+    }
+    return (p.lens ? (int64_t)p.lens[b] - p.n : 0) + i;
+}
+
+// cos and sin of the angle of one pair.
+__device__ __forceinline__ void turn(int64_t pos, uint64_t freq, float factor, float sign, float& c, float& s)
+{
+    const uint64_t a = (uint64_t)pos * freq;
+    sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &s, &c);
+    c *= factor;
+    s *= factor * sign;
+}
+
+__device__ __forceinline__ uint4 ld16(const __nv_bfloat16* p)
+{
+    uint4 r;  // not .nc: an output may be its input
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+
+__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Pairs split over two words: word a holds two pairs' first channels, b their second ones.
+__device__ __forceinline__ void turn_half(uint32_t& a, uint32_t& b, float c0, float s0, float c1, float s1)
+{
+    const float a0 = lo(a), a1 = hi(a), b0 = lo(b), b1 = hi(b);
+    a = ptx::pack_bf16x2(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
+    b = ptx::pack_bf16x2(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
+}
+
+// A pair within one word.
+__device__ __forceinline__ void turn_word(uint32_t& w, float c, float s)
+{
+    const float a = lo(w), b = hi(w);
+    w = ptx::pack_bf16x2(a * c - b * s, b * c + a * s);
+}
+
+// VEC: units of two 16-byte vectors (every vector wholly turned or wholly
+// passed through, rows and strides 16-byte aligned).  Otherwise a unit is one
+// pair, in 2-byte accesses: odd rotated sizes and strides.
+// Block (units, positions, head lanes).
+template <bool VEC>
+__global__ void __launch_bounds__(THREADS) fa_rope_kernel(const Params p)
+{
+    ptx::griddep_wait();  // a programmatic dependent: the inputs are complete
+    ptx::griddep_launch_dependents();
+    unsigned blk = blockIdx.x;
+    const int ht = blk % p.head_tiles;
+    blk /= p.head_tiles;
+    const int64_t i = (int64_t)(blk % p.tiles) * blockDim.y + threadIdx.y;
+    const int b = blk / p.tiles;
+    if (i >= p.n) return;
+    const int64_t pos = position_of(p, b, i);
+    const int u = threadIdx.x;
+    const int total = p.heads[0] + p.heads[1];
+    const int h0 = ht * p.heads_per_thread * blockDim.z + threadIdx.z;
+    const int h1 = min(total, (ht + 1) * p.heads_per_thread * (int)blockDim.z);
+
+    // The unit's two places (channels) and its pairs' first index; pass: not turned.
+    constexpr int W = VEC ? 8 : 1;
+    const int turned = p.rot / (2 * W);  // units of whole pairs (VEC, interleaved: maybe one half unit more)
+    int ca, cb, f0;
+    bool pass_a = false, pass_b = false;
+    if (!p.interleaved && u < turned) {
+        ca = u * W;
+        cb = p.rot / 2 + u * W;
+        f0 = u * W;
+    } else {
+        ca = u * 2 * W;
+        cb = ca + W;
+        f0 = u * W;
+        pass_a = ca >= p.rot;
+        pass_b = cb >= p.rot;
+    }
+    const bool have_b = cb < p.d;
+    float c[W], s[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+        c[e] = 1.f;
+        s[e] = 0.f;
+        if (f0 + e < p.rot / 2 && !pass_a) turn(pos, p.freqs[f0 + e], p.factor, p.sign, c[e], s[e]);
+    }
+    const bool split = !p.interleaved;  // pairs lie across the two places
+
+    for (int h = h0; h < h1; h += U * (int)blockDim.z) {
+        const __nv_bfloat16* src[U];
+        __nv_bfloat16* dst[U];
+        bool ok[U];
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+            const int hh = h + e * (int)blockDim.z;
+            ok[e] = hh < h1;
+            const int t = hh >= p.heads[0];
+            const int64_t hl = t ? hh - p.heads[0] : hh;
+            src[e] = p.in[t].p + b * p.in[t].sb + hl * p.in[t].sh + i * p.in[t].sn;
+            dst[e] = p.out[t].p + b * p.out[t].sb + hl * p.out[t].sh + i * p.out[t].sn;
+        }
+        if constexpr (VEC) {
+            uint4 va[U], vb[U];
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+                if (ok[e]) va[e] = ld16(src[e] + ca);
+                if (ok[e] && have_b) vb[e] = ld16(src[e] + cb);
+            }
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+                if (!ok[e]) continue;
+                if (split) {
+                    if (!pass_a) {
+                        turn_half(va[e].x, vb[e].x, c[0], s[0], c[1], s[1]);
+                        turn_half(va[e].y, vb[e].y, c[2], s[2], c[3], s[3]);
+                        turn_half(va[e].z, vb[e].z, c[4], s[4], c[5], s[5]);
+                        turn_half(va[e].w, vb[e].w, c[6], s[6], c[7], s[7]);
+                    }
+                } else {
+                    if (!pass_a) {
+                        turn_word(va[e].x, c[0], s[0]);
+                        turn_word(va[e].y, c[1], s[1]);
+                        turn_word(va[e].z, c[2], s[2]);
+                        turn_word(va[e].w, c[3], s[3]);
+                    }
+                    if (!pass_b) {
+                        turn_word(vb[e].x, c[4], s[4]);
+                        turn_word(vb[e].y, c[5], s[5]);
+                        turn_word(vb[e].z, c[6], s[6]);
+                        turn_word(vb[e].w, c[7], s[7]);
+                    }
+                }
+                ptx::st_global_v4(dst[e] + ca, va[e].x, va[e].y, va[e].z, va[e].w);
+                if (have_b) ptx::st_global_v4(dst[e] + cb, vb[e].x, vb[e].y, vb[e].z, vb[e].w);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+                if (!ok[e]) continue;
+                const __nv_bfloat16 xa = src[e][ca], xb = src[e][cb];
+                if (pass_a) {
+                    dst[e][ca] = xa;
+                    dst[e][cb] = xb;
+                } else {
+                    const float a = __bfloat162float(xa), bb = __bfloat162float(xb);
+                    dst[e][ca] = __float2bfloat16_rn(a * c[0] - bb * s[0]);
+                    dst[e][cb] = __float2bfloat16_rn(bb * c[0] + a * s[0]);
+                }
+            }
+        }
+    }
+}
+
+}  // namespace rope
+}  // namespace fa
