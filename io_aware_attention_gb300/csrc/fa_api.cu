@@ -623,12 +623,6 @@ QRows qcache_rows(int64_t group, int64_t Nq)
     return r;
 }
 
-template <int D, int NT>
-size_t qcache_decode_smem(int64_t B)
-{
-    return (size_t)(2 * fa::qc::WARPS * fa::qc::Partial<D, 8 * NT>::FLOATS + B + 1) * 4;
-}
-
 size_t qcache_part_bytes(int64_t Dp, int nt) { return (size_t)(8 * nt) * (size_t)(Dp + 2) * 4; }
 
 // Blocks of the decode kernel: one an SM, no more than there can be pages.
@@ -656,11 +650,12 @@ fa_status allow_smem(K kernel, size_t bytes, std::atomic<int>* done, int dev)
 template <int D, int NT>
 fa_status launch_qcache_decode(const fa::qc::DecParams& p, int64_t blocks, int dev, cudaStream_t st)
 {
+    using Y = fa::qc::DecLayout<D, NT>;
     static std::atomic<int> done[MAX_DEVICES];
-    const fa_status as = allow_smem(fa::qc::fa_qcache_decode_kernel<D, NT>, qcache_decode_smem<D, NT>(fa::qc::MAX_B), done, dev);
+    const fa_status as = allow_smem(fa::qc::fa_qcache_decode_kernel<D, NT>, (size_t)Y::bytes(fa::qc::MAX_B), done, dev);
     if (as != FA_OK) return as;
-    if (launch_pdl(fa::qc::fa_qcache_decode_kernel<D, NT>, dim3((unsigned)blocks), dim3(fa::qc::THREADS),
-                   qcache_decode_smem<D, NT>(p.B), st, p) != cudaSuccess ||
+    if (launch_pdl(fa::qc::fa_qcache_decode_kernel<D, NT>, dim3((unsigned)blocks), dim3(Y::THREADS),
+                   (size_t)Y::bytes(p.B), st, p) != cudaSuccess ||
         launch_pdl(fa::qc::fa_qcache_combine_kernel<D, NT>, dim3((unsigned)blocks, 8 * NT), dim3(256), 0, st, p) !=
             cudaSuccess)
         return FA_ERR_CUDA;
@@ -668,10 +663,14 @@ fa_status launch_qcache_decode(const fa::qc::DecParams& p, int64_t blocks, int d
 }
 
 template <int D, int NT>
-fa_status launch_qcache_weights(const fa::qc::DecParams& p, int64_t blocks, cudaStream_t st)
+fa_status launch_qcache_weights(const fa::qc::DecParams& p, int64_t blocks, int dev, cudaStream_t st)
 {
-    return launch_pdl(fa::qc::fa_qcache_weights_kernel<D, NT>, dim3((unsigned)blocks), dim3(fa::qc::THREADS),
-                      (size_t)(p.B + 1) * 4, st, p) == cudaSuccess
+    using Y = fa::qc::WeightLayout<D>;
+    static std::atomic<int> done[MAX_DEVICES];
+    const fa_status as = allow_smem(fa::qc::fa_qcache_weights_kernel<D, NT>, (size_t)Y::bytes(fa::qc::MAX_B), done, dev);
+    if (as != FA_OK) return as;
+    return launch_pdl(fa::qc::fa_qcache_weights_kernel<D, NT>, dim3((unsigned)blocks), dim3(Y::THREADS),
+                      (size_t)Y::bytes(p.B), st, p) == cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
 }
@@ -1247,6 +1246,8 @@ fa_status fa_qcache_decode(const void* q, const void* pool, int64_t num_pages, c
     p.num_pages = (int)num_pages;
     p.causal = causal;
     p.scale_log2 = (float)((double)scale * 1.4426950408889634074 * (double)k_scale);
+    p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    p.debug_skip = g_debug_skip_k.load(std::memory_order_relaxed);
     p.v_scale = v_scale;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (Dp == 128)
@@ -1298,11 +1299,13 @@ fa_status fa_qcache_weights(const void* q, const float* lse, const void* pool, i
     p.num_pages = (int)num_pages;
     p.causal = causal;
     p.scale_log2 = (float)((double)scale * 1.4426950408889634074 * (double)k_scale);
+    p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    p.debug_skip = g_debug_skip_k.load(std::memory_order_relaxed);
     const int64_t blocks = std::min<int64_t>((int64_t)info.sms * 2, B * Hkv * max_pages);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (padded_head_size(d) == 128)
-        return r.nt == 1 ? launch_qcache_weights<128, 1>(p, blocks, st) : launch_qcache_weights<128, 2>(p, blocks, st);
-    return r.nt == 1 ? launch_qcache_weights<64, 1>(p, blocks, st) : launch_qcache_weights<64, 2>(p, blocks, st);
+        return r.nt == 1 ? launch_qcache_weights<128, 1>(p, blocks, dev, st) : launch_qcache_weights<128, 2>(p, blocks, dev, st);
+    return r.nt == 1 ? launch_qcache_weights<64, 1>(p, blocks, dev, st) : launch_qcache_weights<64, 2>(p, blocks, dev, st);
 }
 
 fa_status fa_qcache_evict(void* pool, int64_t num_pages, const int32_t* table, int64_t max_pages, const int32_t* lens,

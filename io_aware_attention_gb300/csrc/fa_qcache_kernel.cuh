@@ -424,19 +424,19 @@ struct DecParams {
     int d, max_pages, num_pages, causal;
     float scale_log2;             // scale * log2(e) * k_scale
     float v_scale;
+    uint64_t wait_limit_ns;
+    int debug_skip;               // test hook: block 0's first warp never copies this one of its pages (-1: off)
     const float* lse_in;          // weights: (B, H, nq)
     const float* w_in;            // (B, hkv, w_len)
     float* w_out;
     int64_t w_len;
 };
 
-constexpr int WARPS = 8;
-constexpr int THREADS = WARPS * 32;
-
 // A probability is held as 2^(x - max + SHIFT) in fp16 (11 bits): 1 becomes
 // 2^15, within fp16's range, and weights down to 2^-29 of the largest keep
 // full precision, so that a long cache of small weights is not rounded away.
 constexpr float SHIFT = 15.0f;
+constexpr uint32_t WAIT_CODE = 900;  // fa_check_device_status's wait code of the cache kernels' copies
 
 template <int NBYTES>
 struct Chunk {  // a lane's share of a row: 16 or 8 bytes
@@ -580,12 +580,11 @@ struct State {
         }
     }
 
-    __device__ __forceinline__ void add_page(const uint8_t* blk, const Rows<D, NT>& rows, int page)
+    // Takes a page's scores in: the running maxima and sums, and the
+    // probabilities as the B operand (keys 2t, 2t + 1 and 2t + 8, 2t + 9 of row g).
+    __device__ __forceinline__ void add_scores(float (&s)[4][NT][4], const Rows<D, NT>& rows, int page, uint32_t (&pb)[4][NT][2])
     {
-        using L = Block<D>;
-        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        float s[4][NT][4];
-        page_scores<D, NT>(blk, rows, s);
+        const int lane = threadIdx.x & 31, g = lane >> 2;
         const int key0 = page * PAGE;
         const bool whole = key0 + PAGE <= rows.min_lim;  // every row sees every key
         bool rises = false;
@@ -629,7 +628,6 @@ struct State {
                 }
             }
         }
-        uint32_t pb[4][NT][2];  // probabilities as the B operand: keys 2t, 2t + 1 (and + 8) of row g
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float top[2];
@@ -649,8 +647,18 @@ struct State {
                 pb[r][nt][1] = transpose8x8(pack_h2(s[r][nt][2], s[r][nt][3]));
             }
         }
-        // O^T += V^T P^T: a scale belongs to a key and a block of channels,
-        // so it multiplies the operand (exactly), two keys at a time.
+    }
+
+    // O^T += V^T P^T: a scale belongs to a key and a block of channels, so it
+    // multiplies the operand (exactly), two keys at a time.  vblk: the V half
+    // of a page's block.
+    __device__ __forceinline__ void add_values(const uint8_t* vblk, const Rows<D, NT>& rows, int page, const uint32_t (&pb)[4][NT][2])
+    {
+        using L = Block<D>;
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const uint8_t* const blk = vblk - L::VC;
+        const int key0 = page * PAGE;
+        const bool whole = key0 + PAGE <= rows.len;
         const int b = g * (D / 8) / 16;
         Chunk<16> sc;
         sc.load(blk + L::VS + (t * L::NB + b) * 16);
@@ -708,6 +716,145 @@ __device__ __forceinline__ float natural_lse(float m, float l)
     return l > 0.f || !(l == l) ? (m + ptx::lg2(l) - SHIFT) * LN2 : -INFINITY;
 }
 
+// Shared memory of the decode kernel: a ring of half pages for each warp, one
+// partial result for each (its first piece; its last one takes the ring's
+// place when the ring is done), and the page counts' prefix sums.
+// One block an SM.  At up to 8 rows 12 warps of 3 halves (9 KB in flight a
+// warp, 110 KB an SM, twice what the copy latency needs); at more, 8 warps,
+// since a warp's accumulators take twice the registers.
+template <int D, int NT>
+struct DecLayout {
+    static constexpr int WARPS = NT == 1 ? 12 : 8;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int SLOTS = D == 128 ? 3 : 6;
+    static constexpr int HALF = 36 * D;
+    static constexpr int PART = Partial<D, 8 * NT>::FLOATS * 4;
+    static constexpr int RING = SLOTS * HALF;
+    static constexpr int PREFIX = WARPS * (RING + PART);
+    static_assert(PART <= RING && HALF % 16 == 0 && PART % 16 == 0, "layout");
+    static constexpr int bytes(int B) { return PREFIX + (B + 1) * 4; }
+    static_assert(bytes(MAX_B) + 2048 <= 232448, "shared memory");
+    static __device__ __forceinline__ int ring(int warp) { return warp * RING; }
+    static __device__ __forceinline__ float* partial(uint8_t* smem, int slot)
+    {
+        return reinterpret_cast<float*>(slot % 2 ? smem + ring(slot / 2) : smem + WARPS * RING + slot / 2 * PART);
+    }
+};
+
+// A unit as a warp needs it.
+struct Place {
+    int seg, page, pages, blk;  // blk: the page's block in the pool, -1: no such page
+};
+
+// A warp's copies of its run of pages into its ring.  SLOTS halves (K, then V;
+// or K alone) are in flight; the warp waits for one, reads it and refills its
+// slot.  The places of 32 units are looked up at once, one a lane, the next
+// 32 ahead of their use.
+template <int D, int SLOTS, bool WITH_V>
+struct Feed {
+    static constexpr int HALF = 36 * D, PER = WITH_V ? 2 : 1;
+    const DecParams& p;
+    const Work& work;
+    uint8_t* ring;
+    uint32_t bar;
+    int x1, base;             // end of the run; first unit of `now`
+    int next_unit, next_half; // what is copied next
+    int fill, use;            // slots
+    uint32_t parity;
+    int flying;
+    Place now, ahead;         // this lane's unit of the current 32 and of the next
+
+    __device__ __forceinline__ Place look(int x)
+    {
+        Place q{-1, 0, 1, -1};
+        if (x < x1) {
+            const Work::Unit u = work.at(x);
+            q.seg = u.b * work.hr + u.hr;
+            q.page = u.page;
+            q.pages = u.pages;
+            const int id = page_of(p.table, p.max_pages, p.num_pages, u.b, u.page);
+            if (id < 0) atomicOr(&g_status, STATUS_BAD_PAGE);
+            else q.blk = id * p.hkv + u.hr / (work.hr / p.hkv);
+        }
+        return q;
+    }
+    __device__ __forceinline__ Feed(uint8_t* ring_, uint32_t bar_, const DecParams& p_, const Work& work_, int x0, int x1_)
+        : p(p_), work(work_), ring(ring_), bar(bar_), x1(x1_), base(x0), next_unit(x0), next_half(0), fill(0), use(0),
+          parity(0), flying(0)
+    {
+        const int lane = threadIdx.x & 31;
+        now = look(base + lane);
+        ahead = x1 - x0 > 32 ? look(base + 32 + lane) : Place{-1, 0, 1, -1};
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) issue();
+    }
+    // Starts the next copy, if one is left.
+    __device__ __forceinline__ void issue()
+    {
+        if (next_unit >= x1) return;
+        const int i = next_unit - base;
+        const int a = __shfl_sync(0xffffffffu, now.blk, i & 31), b = __shfl_sync(0xffffffffu, ahead.blk, i & 31);
+        const int blk = max(0, i < 32 ? a : b);  // a page that does not exist: any block, not used
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(bar + 8 * fill, HALF);
+            if (!(p.debug_skip == i && base == 0 && blockIdx.x == 0))
+                ptx::bulk_load(ptx::smem_addr(ring) + fill * HALF,
+                               p.pool + (int64_t)blk * Block<D>::BYTES + (WITH_V ? next_half * HALF : 0), HALF, bar + 8 * fill);
+        }
+        fill = fill + 1 == SLOTS ? 0 : fill + 1;
+        ++flying;
+        if (++next_half == PER) {
+            next_half = 0;
+            ++next_unit;
+        }
+    }
+    __device__ __forceinline__ Place place(int x)
+    {
+        if (x - base == 32) {
+            now = ahead;
+            base += 32;
+            ahead = x1 - base > 32 ? look(base + 32 + (int)(threadIdx.x & 31)) : Place{-1, 0, 1, -1};
+        }
+        const int i = x - base;
+        Place q;
+        q.seg = __shfl_sync(0xffffffffu, now.seg, i);
+        q.page = __shfl_sync(0xffffffffu, now.page, i);
+        q.pages = __shfl_sync(0xffffffffu, now.pages, i);
+        q.blk = __shfl_sync(0xffffffffu, now.blk, i);
+        return q;
+    }
+    // The oldest half in flight, or null when the wait gave up.
+    __device__ __forceinline__ const uint8_t* wait(volatile uint32_t* abort_flag)
+    {
+        const bool ok = wait_bar(bar + 8 * use, parity, p.wait_limit_ns, abort_flag, WAIT_CODE);
+        return __all_sync(0xffffffffu, ok) ? ring + use * HALF : nullptr;
+    }
+    // The warp has read it: refill its slot.
+    __device__ __forceinline__ void next()
+    {
+        __syncwarp();
+        if (++use == SLOTS) {
+            use = 0;
+            parity ^= 1u;
+        }
+        --flying;
+        issue();
+    }
+    // Copies still in flight after a wait gave up must land before the block leaves.
+    __device__ __forceinline__ void drain(volatile uint32_t* abort_flag)
+    {
+        for (; flying > 0; --flying) {
+            drain_bar(bar + 8 * use, parity, p.wait_limit_ns, abort_flag, WAIT_CODE);
+            if (++use == SLOTS) {
+                use = 0;
+                parity ^= 1u;
+            }
+        }
+        __syncwarp();
+    }
+};
+
 // Decode.  Block c takes units [c T / G, (c + 1) T / G) of the T pages, and its
 // warps equal runs of those.  A segment (all pages of one sequence, kv head
 // and row block) that lies within a warp's run is written out at once; the
@@ -715,20 +862,25 @@ __device__ __forceinline__ float natural_lse(float m, float l)
 // warps' pieces of a segment; pieces of segments that cross blocks go to the
 // workspace (two a block at most) for the combine kernel.
 template <int D, int NT>
-__global__ void __launch_bounds__(THREADS, 1) fa_qcache_decode_kernel(const DecParams p)
+__global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode_kernel(const DecParams p)
 {
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    constexpr int R = 8 * NT;
+    using Y = DecLayout<D, NT>;
+    constexpr int R = 8 * NT, WARPS = Y::WARPS, THREADS = Y::THREADS;
     using PS = Partial<D, R>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    float* const slots = reinterpret_cast<float*>(smem);             // 2 * WARPS partial results
-    int* const prefix = reinterpret_cast<int*>(slots + 2 * WARPS * PS::FLOATS);
+    extern __shared__ __align__(128) uint8_t smem[];
+    int* const prefix = reinterpret_cast<int*>(smem + Y::PREFIX);
     __shared__ int scratch[WARPS];
+    __shared__ __align__(8) uint64_t bars[WARPS * Y::SLOTS];
+    __shared__ uint32_t abort_flag;
     __shared__ int slot_seg[2 * WARPS];   // segment of each slot, or -1
     __shared__ int slot_ends[2 * WARPS];  // bit 0: the segment begins in it, bit 1: ends
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     if (tid < 2 * WARPS) slot_seg[tid] = -1;
+    if (tid < WARPS * Y::SLOTS) ptx::mbar_init(ptx::smem_addr(&bars[tid]), 1);
+    if (tid == 0) abort_flag = 0;
+    ptx::fence_barrier_init();
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     page_prefix<THREADS>(p.lens, p.B, p.max_pages, prefix, scratch);
     Work work{prefix, p.B, p.hkv * p.rb};
 
@@ -782,7 +934,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_qcache_decode_kernel(const DecP
                 return;
             }
             const int at = warp * 2 + slot++;
-            float* const f = slots + at * PS::FLOATS;
+            float* const f = Y::partial(smem, at);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -801,36 +953,34 @@ __global__ void __launch_bounds__(THREADS, 1) fa_qcache_decode_kernel(const DecP
                 slot_ends[at] = begins | (ends << 1);
             }
         };
-        for (int base = x0; base < x1; base += 32) {
-            // The next 32 units' places, one a lane.
-            int my_seg = 0, my_page = 0, my_pages = 0, my_blk = -1;
-            if (base + lane < x1) {
-                const Work::Unit u = work.at(base + lane);
-                my_seg = u.b * work.hr + u.hr;
-                my_page = u.page;
-                my_pages = u.pages;
-                const int id = page_of(p.table, p.max_pages, p.num_pages, u.b, u.page);
-                if (id < 0) atomicOr(&g_status, STATUS_BAD_PAGE);
-                else my_blk = id * p.hkv + u.hr / p.rb;
+        // Copies run ahead of the arithmetic by the ring's slots: K and V halves
+        // of the pages in turn, each slot refilled as soon as the warp has read it.
+        Feed<D, Y::SLOTS, true> feed(smem + Y::ring(warp), ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
+        for (int x = x0; x < x1; ++x) {
+            const Place u = feed.place(x);
+            if (u.seg != seg) {
+                if (seg >= 0) finish();
+                seg = u.seg;
+                begins = u.page == 0;
+                seg_pages = u.pages;
+                const int b = seg / work.hr;
+                rows.load(p, b, seg - b * work.hr, length_of(p.lens, b, p.max_pages));
+                st.clear();
             }
-            const int n = min(32, x1 - base);
-            for (int i = 0; i < n; ++i) {
-                const int s = __shfl_sync(0xffffffffu, my_seg, i);
-                const int page = __shfl_sync(0xffffffffu, my_page, i);
-                const int blk = __shfl_sync(0xffffffffu, my_blk, i);
-                if (s != seg) {
-                    if (seg >= 0) finish();
-                    seg = s;
-                    begins = page == 0;
-                    seg_pages = __shfl_sync(0xffffffffu, my_pages, i);
-                    const int b = s / work.hr;
-                    rows.load(p, b, s - b * work.hr, length_of(p.lens, b, p.max_pages));
-                    st.clear();
-                }
-                last_page = page;
-                if (blk >= 0) st.add_page(p.pool + (int64_t)blk * Block<D>::BYTES, rows, page);
-            }
+            last_page = u.page;
+            float s[4][NT][4];
+            uint32_t pb[4][NT][2];
+            const uint8_t* blk = feed.wait(&abort_flag);
+            if (!blk) break;
+            page_scores<D, NT>(blk, rows, s);
+            feed.next();
+            if (u.blk >= 0) st.add_scores(s, rows, u.page, pb);
+            blk = feed.wait(&abort_flag);
+            if (!blk) break;
+            if (u.blk >= 0) st.add_values(blk, rows, u.page, pb);
+            feed.next();
         }
+        feed.drain(&abort_flag);
         finish();
     }
     __syncthreads();
@@ -859,11 +1009,11 @@ __global__ void __launch_bounds__(THREADS, 1) fa_qcache_decode_kernel(const DecP
             const int r = e / (D / 2), c = e % (D / 2) * 2;
             float mx = -INFINITY;
             for (int k = a; k <= z; ++k)
-                if (slot_seg[k] >= 0) mx = fmaxf(mx, slots[k * PS::FLOATS + PS::m(r)]);
+                if (slot_seg[k] >= 0) mx = fmaxf(mx, Y::partial(smem, k)[PS::m(r)]);
             float x = 0.f, y = 0.f, l = 0.f;
             for (int k = a; k <= z; ++k) {
                 if (slot_seg[k] < 0) continue;
-                const float* const f = slots + k * PS::FLOATS;
+                const float* const f = Y::partial(smem, k);
                 const float mk = f[PS::m(r)];
                 const float wk = mk == -INFINITY ? 0.f : ptx::ex2(mk - mx);
                 const float2 v = *reinterpret_cast<const float2*>(f + PS::o(r) + c);
@@ -953,15 +1103,32 @@ __global__ void __launch_bounds__(256) fa_qcache_combine_kernel(const DecParams 
 // w_out[key] = w_in[key] + sum over the rows of the key's kv head of
 // exp(scale q.k - lse): the attention weight that the rows gave each key,
 // from the logsumexps that decode returned.  Only K is read.
+template <int D>
+struct WeightLayout {
+    static constexpr int WARPS = 8, THREADS = WARPS * 32;
+    static constexpr int SLOTS = D == 128 ? 2 : 4;
+    static constexpr int RING = SLOTS * 36 * D;
+    static constexpr int PREFIX = WARPS * RING;
+    static constexpr int bytes(int B) { return PREFIX + (B + 1) * 4; }
+    static_assert(2 * (bytes(MAX_B) + 2048) <= 232448, "shared memory of two blocks an SM");
+};
+
 template <int D, int NT>
-__global__ void __launch_bounds__(THREADS) fa_qcache_weights_kernel(const DecParams p)
+__global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights_kernel(const DecParams p)
 {
+    using Y = WeightLayout<D>;
+    constexpr int WARPS = Y::WARPS, THREADS = Y::THREADS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    int* const prefix = reinterpret_cast<int*>(smem + Y::PREFIX);
+    __shared__ int scratch[WARPS];
+    __shared__ __align__(8) uint64_t bars[WARPS * Y::SLOTS];
+    __shared__ uint32_t abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    if (tid < WARPS * Y::SLOTS) ptx::mbar_init(ptx::smem_addr(&bars[tid]), 1);
+    if (tid == 0) abort_flag = 0;
+    ptx::fence_barrier_init();
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    extern __shared__ __align__(16) uint8_t smem[];
-    int* const prefix = reinterpret_cast<int*>(smem);
-    __shared__ int scratch[WARPS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     page_prefix<THREADS>(p.lens, p.B, p.max_pages, prefix, scratch);
     // One unit is a page of a kv head: all its row blocks, so that every key's weight is one warp's.
     Work work{prefix, p.B, p.hkv};
@@ -980,18 +1147,19 @@ __global__ void __launch_bounds__(THREADS) fa_qcache_weights_kernel(const DecPar
     Rows<D, NT> rows;
     float off[NT][2];
     int have = -1;  // segment (with row block) whose rows are loaded
+    Feed<D, Y::SLOTS, false> feed(smem + warp * Y::RING, ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
     for (int x = x0; x < x1; ++x) {
-        const Work::Unit u = work.at(x);
-        const int id = page_of(p.table, p.max_pages, p.num_pages, u.b, u.page);
-        const int len = length_of(p.lens, u.b, p.max_pages);
-        if (id < 0 && lane == 0) atomicOr(&g_status, STATUS_BAD_PAGE);
+        const Place u = feed.place(x);
+        const int b = u.seg / p.hkv, h = u.seg - b * p.hkv;
+        const uint8_t* const blk = feed.wait(&abort_flag);
+        if (!blk) break;
         float sum[8] = {};
         for (int rbi = 0; rbi < p.rb; ++rbi) {
-            const int seg = (u.b * p.hkv + u.hr) * p.rb + rbi;
+            const int seg = u.seg * p.rb + rbi;
             if (seg != have) {
                 have = seg;
-                rows.load(p, u.b, u.hr * p.rb + rbi, len);
-                const int64_t row0 = ((int64_t)u.b * p.hkv + u.hr) * p.rows;
+                rows.load(p, b, h * p.rb + rbi, length_of(p.lens, b, p.max_pages));
+                const int64_t row0 = (int64_t)u.seg * p.rows;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1002,9 +1170,9 @@ __global__ void __launch_bounds__(THREADS) fa_qcache_weights_kernel(const DecPar
                         off[nt][j] = e == -INFINITY ? -INFINITY : -e * 1.4426950408889634f;
                     }
             }
-            if (id < 0) continue;
+            if (u.blk < 0) continue;
             float s[4][NT][4];
-            page_scores<D, NT>(p.pool + ((int64_t)id * p.hkv + u.hr) * Block<D>::BYTES, rows, s);
+            page_scores<D, NT>(blk, rows, s);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -1018,18 +1186,20 @@ __global__ void __launch_bounds__(THREADS) fa_qcache_weights_kernel(const DecPar
                                 sum[2 * r + half] += ptx::ex2(fmaf(s[r][nt][2 * half + j], rows.sc[nt][j], off[nt][j]));
                 }
         }
+        feed.next();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
             sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
         }
-        const int64_t at = ((int64_t)u.b * p.hkv + u.hr) * p.w_len;
+        const int64_t at = (int64_t)u.seg * p.w_len;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int64_t key = (int64_t)u.page * PAGE + 8 * e + g;
-            if (e / 2 == t && key < len && key < p.w_len) p.w_out[at + key] = p.w_in[at + key] + sum[e];
+            if (e / 2 == t && key < rows.len && key < p.w_len) p.w_out[at + key] = p.w_in[at + key] + sum[e];
         }
     }
+    feed.drain(&abort_flag);
 }
 
 // ----------------------------------------------------------------- eviction
