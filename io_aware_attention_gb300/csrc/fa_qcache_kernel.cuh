@@ -111,6 +111,14 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// As mma from zero sums.
+__device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // ----------------------------------------------------------------- rounding
 
 // A scale for 16 channels from their largest magnitude: amax / (6 scale) in
@@ -379,25 +387,36 @@ __device__ __forceinline__ int length_of(const int32_t* lens, int b, int max_pag
 }
 
 // prefix[0 .. B] by a block of NTHREADS threads (scratch: one int per warp).
+// Up to 32 sequences every warp computes them all and waits for no other.
 template <int NTHREADS>
 __device__ __forceinline__ void page_prefix(const int32_t* lens, int B, int max_pages, int* prefix, int* scratch)
 {
     constexpr int W = NTHREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int base = 0;
-    if (tid == 0) prefix[0] = 0;
-    for (int b0 = 0; b0 < B; b0 += NTHREADS) {
-        const int b = b0 + tid;
+    auto scan = [&](int b) {
         int v = b < B ? (length_of(lens, b, max_pages) + PAGE - 1) / PAGE : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int n = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o) v += n;
         }
+        return v;
+    };
+    if (B <= 32) {
+        const int v = scan(lane);
+        if (lane == 0) prefix[0] = 0;
+        if (lane < B) prefix[lane + 1] = v;
+        __syncwarp();
+        return;
+    }
+    int base = 0;
+    if (tid == 0) prefix[0] = 0;
+    for (int b0 = 0; b0 < B; b0 += NTHREADS) {
+        const int b = b0 + tid, v = scan(b);
         if (lane == 31) scratch[warp] = v;
         __syncthreads();
         int before = base, all = base;
-#pragma unroll
+#pragma unroll 4
         for (int w = 0; w < W; ++w) {
             const int n = scratch[w];
             if (w < warp) before += n;
@@ -407,7 +426,16 @@ __device__ __forceinline__ void page_prefix(const int32_t* lens, int B, int max_
         base = all;
         __syncthreads();
     }
-    __syncthreads();
+}
+
+// Brings the small tensors of a call to L2, every block a share, before the
+// work that this launch depends on has ended: their later reads, which
+// follow one another, then cost an L2 access each instead of a DRAM one.
+__device__ __forceinline__ void prefetch_l2(const void* p, int64_t bytes)
+{
+    const char* const c = static_cast<const char*>(p);
+    for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 128; i < bytes; i += (int64_t)gridDim.x * blockDim.x * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(c + i));
 }
 
 // ------------------------------------------------------------------- decode
@@ -453,8 +481,14 @@ struct Chunk {  // a lane's share of a row: 16 or 8 bytes
     }
 };
 
-__device__ __forceinline__ uint32_t dup_lo(uint32_t h2) { return __byte_perm(h2, h2, 0x1010); }
-__device__ __forceinline__ uint32_t dup_hi(uint32_t h2) { return __byte_perm(h2, h2, 0x3232); }
+// a * (half `HI` of f, twice): the multiply reads either half of its operand.
+template <int HI>
+__device__ __forceinline__ uint32_t hmul2_by(uint32_t a, uint32_t f)
+{
+    const __half2 x = *reinterpret_cast<const __half2*>(&a), y = *reinterpret_cast<const __half2*>(&f);
+    const __half2 r = __hmul2(x, HI ? __high2half2(y) : __low2half2(y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 // Query rows of one (sequence, kv head, row block), as the B operand of the
 // score product, and what a lane needs of them: lane (g, t) = (lane / 4,
@@ -470,24 +504,39 @@ struct Rows {
     int lim[NT][2];
     int len, min_lim;
 
-    __device__ __forceinline__ void load(const DecParams& p, int b, int hr, int len_)
+    // The rows' raw entries: issued before a warp's first copies, so that they
+    // do not wait behind them.
+    struct Raw {
+        uint4 w[NT][D / 32];
+    };
+    static __device__ __forceinline__ void fetch(Raw& raw, const DecParams& p, int b, int hr)
     {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const int h = hr / p.rb, r0 = (hr - h * p.rb) * (8 * NT);
         const int64_t row0 = ((int64_t)b * p.hkv + h) * p.rows;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = r0 + nt * 8 + g;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+                const int c = D / 4 * t + 8 * e;
+                raw.w[nt][e] = make_uint4(0, 0, 0, 0);
+                if (row < p.rows && c < p.d) raw.w[nt][e] = *reinterpret_cast<const uint4*>(p.q + (row0 + row) * p.d + c);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void load(const Raw& raw, const DecParams& p, int hr, int len_)
+    {
+        const int lane = threadIdx.x & 31, t = lane & 3;
+        const int r0 = hr % p.rb * (8 * NT);
         len = len_;
         min_lim = p.causal ? len - p.nq + 1 : len;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = r0 + nt * 8 + g;
             float f[D / 4];
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) {
-                uint4 w = make_uint4(0, 0, 0, 0);
-                const int c = D / 4 * t + 8 * e;
-                if (row < p.rows && c < p.d) w = *reinterpret_cast<const uint4*>(p.q + (row0 + row) * p.d + c);
-                unpack8(w, f + 8 * e);
-            }
+            for (int e = 0; e < D / 32; ++e) unpack8(raw.w[nt][e], f + 8 * e);
             float am = 0.f;
 #pragma unroll
             for (int e = 0; e < D / 4; ++e) am = fmaxf(am, fabsf(f[e]));
@@ -528,30 +577,24 @@ __device__ __forceinline__ void page_scores(const uint8_t* blk, const Rows<D, NT
         Chunk<D / 8> k0, k1;
         k0.load(blk + L::kcode(16 * r + g) + t * (D / 8));
         k1.load(blk + L::kcode(16 * r + 8 + g) + t * (D / 8));
-        uint32_t s0[L::P], s1[L::P];  // scales of the lane's channel blocks, rows g and g + 8
-        if constexpr (D == 128) {
-            const uint32_t a = e4m3x2(sc.w[r]), b = e4m3x2(sc.w[r] >> 16);
-            s0[0] = dup_lo(a), s0[1] = dup_hi(a);
-            s1[0] = dup_lo(b), s1[1] = dup_hi(b);
-        } else {
-            const uint32_t a = e4m3x2(sc.w[r / 2] >> (16 * (r % 2)));
-            s0[0] = dup_lo(a);
-            s1[0] = dup_hi(a);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[r][nt][e] = 0.f;
+        // Scales: at D = 128 those of rows g and g + 8, each of the lane's two
+        // channel blocks; at D = 64 one of each row.
+        const uint32_t f0 = e4m3x2(D == 128 ? sc.w[r] : sc.w[r / 2] >> (16 * (r % 2)));
+        const uint32_t f1 = D == 128 ? e4m3x2(sc.w[r] >> 16) : f0;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
             const uint32_t w0 = k0.w[c / 2], w1 = k1.w[c / 2];
-            const uint32_t f0 = s0[c / 4], f1 = s1[c / 4];
-            const uint32_t a0 = hmul2(c % 2 ? e2m1x2<2>(w0) : e2m1x2<0>(w0), f0);
-            const uint32_t a1 = hmul2(c % 2 ? e2m1x2<2>(w1) : e2m1x2<0>(w1), f1);
-            const uint32_t a2 = hmul2(c % 2 ? e2m1x2<3>(w0) : e2m1x2<1>(w0), f0);
-            const uint32_t a3 = hmul2(c % 2 ? e2m1x2<3>(w1) : e2m1x2<1>(w1), f1);
+            auto by0 = [&](uint32_t a) { return D == 128 && c >= 4 ? hmul2_by<1>(a, f0) : hmul2_by<0>(a, f0); };
+            auto by1 = [&](uint32_t a) { return D == 64 || c >= 4 ? hmul2_by<1>(a, f1) : hmul2_by<0>(a, f1); };
+            const uint32_t a0 = by0(c % 2 ? e2m1x2<2>(w0) : e2m1x2<0>(w0));
+            const uint32_t a1 = by1(c % 2 ? e2m1x2<2>(w1) : e2m1x2<0>(w1));
+            const uint32_t a2 = by0(c % 2 ? e2m1x2<3>(w0) : e2m1x2<1>(w0));
+            const uint32_t a3 = by1(c % 2 ? e2m1x2<3>(w1) : e2m1x2<1>(w1));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma(s[r][nt], a0, a1, a2, a3, rows.q[nt][c][0], rows.q[nt][c][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+                if (c == 0) mma_zero(s[r][nt], a0, a1, a2, a3, rows.q[nt][c][0], rows.q[nt][c][1]);
+                else mma(s[r][nt], a0, a1, a2, a3, rows.q[nt][c][0], rows.q[nt][c][1]);
+            }
         }
     }
 }
@@ -602,7 +645,7 @@ struct State {
                 }
                 float x = fmaxf(s[0][nt][j], s[0][nt][2 + j]);
 #pragma unroll
-                for (int r = 1; r < 4; ++r) x = fmaxf(x, fmaxf(s[r][nt][j], s[r][nt][2 + j]));
+                for (int r = 1; r < 4; ++r) x = ptx::fmax3(x, s[r][nt][j], s[r][nt][2 + j]);
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -633,19 +676,28 @@ struct State {
             float top[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) top[j] = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
+            // Pairs of columns in packed fp32 arithmetic.
+            const uint64_t neg = ptx::f2_pack(-top[0], -top[1]), sc = ptx::f2_pack(rows.sc[nt][0], rows.sc[nt][1]);
+            const uint64_t shift = ptx::f2_pack(SHIFT, SHIFT);
+            uint64_t sum = ptx::f2_pack(l[nt][0], l[nt][1]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = s[r][nt][e];
-                    float pr = ptx::ex2(fmaf(x - top[e & 1], rows.sc[nt][e & 1], SHIFT));
-                    if (!whole && x == -INFINITY) pr = 0.f;
-                    l[nt][e & 1] += pr;
-                    s[r][nt][e] = pr;
+                for (int e = 0; e < 4; e += 2) {
+                    float x0 = s[r][nt][e], x1 = s[r][nt][e + 1], p0, p1;
+                    ptx::f2_unpack(ptx::f2_fma(ptx::f2_add(ptx::f2_pack(x0, x1), neg), sc, shift), p0, p1);
+                    p0 = ptx::ex2(p0);
+                    p1 = ptx::ex2(p1);
+                    if (!whole && x0 == -INFINITY) p0 = 0.f;
+                    if (!whole && x1 == -INFINITY) p1 = 0.f;
+                    sum = ptx::f2_add(sum, ptx::f2_pack(p0, p1));
+                    s[r][nt][e] = p0;
+                    s[r][nt][e + 1] = p1;
                 }
                 pb[r][nt][0] = transpose8x8(pack_h2(s[r][nt][0], s[r][nt][1]));
                 pb[r][nt][1] = transpose8x8(pack_h2(s[r][nt][2], s[r][nt][3]));
             }
+            ptx::f2_unpack(sum, l[nt][0], l[nt][1]);
         }
     }
 
@@ -784,9 +836,13 @@ struct Feed {
     {
         const int lane = threadIdx.x & 31;
         now = look(base + lane);
-        ahead = x1 - x0 > 32 ? look(base + 32 + lane) : Place{-1, 0, 1, -1};
-#pragma unroll
+        ahead = Place{-1, 0, 1, -1};
+    }
+    __device__ __forceinline__ void begin()
+    {
+#pragma unroll 1
         for (int i = 0; i < SLOTS; ++i) issue();
+        if (x1 - base > 32) ahead = look(base + 32 + (int)(threadIdx.x & 31));
     }
     // Starts the next copy, if one is left.
     __device__ __forceinline__ void issue()
@@ -816,12 +872,22 @@ struct Feed {
             base += 32;
             ahead = x1 - base > 32 ? look(base + 32 + (int)(threadIdx.x & 31)) : Place{-1, 0, 1, -1};
         }
+        return peek(x);
+    }
+    // The place of unit x, at most one 32 ahead of the last that place() gave.
+    __device__ __forceinline__ Place peek(int x) const
+    {
         const int i = x - base;
+        if (i >= 32) return given(ahead, i - 32);
+        return given(now, i);
+    }
+    static __device__ __forceinline__ Place given(const Place& of, int i)
+    {
         Place q;
-        q.seg = __shfl_sync(0xffffffffu, now.seg, i);
-        q.page = __shfl_sync(0xffffffffu, now.page, i);
-        q.pages = __shfl_sync(0xffffffffu, now.pages, i);
-        q.blk = __shfl_sync(0xffffffffu, now.blk, i);
+        q.seg = __shfl_sync(0xffffffffu, of.seg, i);
+        q.page = __shfl_sync(0xffffffffu, of.page, i);
+        q.pages = __shfl_sync(0xffffffffu, of.pages, i);
+        q.blk = __shfl_sync(0xffffffffu, of.blk, i);
         return q;
     }
     // The oldest half in flight, or null when the wait gave up.
@@ -871,14 +937,22 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
     int* const prefix = reinterpret_cast<int*>(smem + Y::PREFIX);
     __shared__ int scratch[WARPS];
     __shared__ __align__(8) uint64_t bars[WARPS * Y::SLOTS];
-    __shared__ uint32_t abort_flag;
-    __shared__ int slot_seg[2 * WARPS];   // segment of each slot, or -1
-    __shared__ int slot_ends[2 * WARPS];  // bit 0: the segment begins in it, bit 1: ends
+    __shared__ uint32_t abort_flags[WARPS];
+    __shared__ int slot_seg[32];                 // segment of each slot, or -1
+    __shared__ int slot_ends[2 * WARPS];         // bit 0: the segment begins in it, bit 1: ends
+    __shared__ float slot_weight[2 * WARPS][R];  // of each slot's row in the joined one
+    __shared__ float joined_m[R], joined_l[R];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    if (tid < 2 * WARPS) slot_seg[tid] = -1;
-    if (tid < WARPS * Y::SLOTS) ptx::mbar_init(ptx::smem_addr(&bars[tid]), 1);
-    if (tid == 0) abort_flag = 0;
+    static_assert(2 * WARPS <= 32, "a lane a slot");
+    if (lane < Y::SLOTS) ptx::mbar_init(ptx::smem_addr(&bars[warp * Y::SLOTS + lane]), 1);
+    if (lane < 2) slot_seg[warp * 2 + lane] = -1;
+    if (warp == 0 && lane >= 2 * WARPS) slot_seg[lane] = -1;
+    if (lane == 0) abort_flags[warp] = 0;
+    volatile uint32_t* const abort_flag = &abort_flags[warp];
     ptx::fence_barrier_init();
+    __syncwarp();
+    prefetch_l2(p.table, (int64_t)p.B * p.max_pages * 4);
+    prefetch_l2(p.q, (int64_t)p.B * p.hkv * p.rows * p.d * 2);
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     page_prefix<THREADS>(p.lens, p.B, p.max_pages, prefix, scratch);
@@ -956,81 +1030,88 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
         // Copies run ahead of the arithmetic by the ring's slots: K and V halves
         // of the pages in turn, each slot refilled as soon as the warp has read it.
         Feed<D, Y::SLOTS, true> feed(smem + Y::ring(warp), ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
+        typename Rows<D, NT>::Raw raw;
         for (int x = x0; x < x1; ++x) {
             const Place u = feed.place(x);
             if (u.seg != seg) {
+                const int b = u.seg / work.hr, hr = u.seg - b * work.hr;
+                rows.fetch(raw, p, b, hr);
                 if (seg >= 0) finish();
+                else feed.begin();
                 seg = u.seg;
                 begins = u.page == 0;
                 seg_pages = u.pages;
-                const int b = seg / work.hr;
-                rows.load(p, b, seg - b * work.hr, length_of(p.lens, b, p.max_pages));
+                rows.load(raw, p, hr, length_of(p.lens, b, p.max_pages));
                 st.clear();
             }
             last_page = u.page;
             float s[4][NT][4];
             uint32_t pb[4][NT][2];
-            const uint8_t* blk = feed.wait(&abort_flag);
+            const uint8_t* blk = feed.wait(abort_flag);
             if (!blk) break;
             page_scores<D, NT>(blk, rows, s);
             feed.next();
             if (u.blk >= 0) st.add_scores(s, rows, u.page, pb);
-            blk = feed.wait(&abort_flag);
+            blk = feed.wait(abort_flag);
             if (!blk) break;
             if (u.blk >= 0) st.add_values(blk, rows, u.page, pb);
             feed.next();
         }
-        feed.drain(&abort_flag);
+        feed.drain(abort_flag);
         finish();
     }
     __syncthreads();
 
-    // Join the warps' pieces.
+    // Join the warps' pieces: runs of slots of one segment.
     if (tid == 0) p.desc[2 * cta] = -1;
-    int a = 0;
-    while (a < 2 * WARPS) {
-        const int seg = slot_seg[a];
-        if (seg < 0) {
-            ++a;
-            continue;
-        }
-        int z = a;  // last slot of the run
-        for (int e = a + 1; e < 2 * WARPS; ++e) {
-            if (slot_seg[e] < 0) continue;
-            if (slot_seg[e] != seg) break;
-            z = e;
-        }
+    const int my_seg = slot_seg[lane];
+    uint32_t left = __ballot_sync(0xffffffffu, my_seg >= 0);
+    while (left) {
+        const int a = __ffs(left) - 1, seg = __shfl_sync(0xffffffffu, my_seg, a);
+        const uint32_t run = left & __ballot_sync(0xffffffffu, my_seg == seg);
+        const int z = 31 - __clz(run);
+        left &= ~run;
         const bool begins = slot_ends[a] & 1, ends = slot_ends[z] & 2;
         const int b = seg / work.hr, hr = seg - b * work.hr, h = hr / p.rb;
         const int r0 = (hr - h * p.rb) * R;
         const int64_t row0 = ((int64_t)b * p.hkv + h) * p.rows;
         float* const part = p.ws + ((int64_t)cta * 2 + (begins ? 1 : 0)) * PS::FLOATS;
+        // Each row's maximum, sum and slots' weights: a warp a row, a lane a slot.
+        for (int r = warp; r < R; r += WARPS) {
+            const bool mine = run >> lane & 1u;
+            const float m = mine ? Y::partial(smem, lane)[PS::m(r)] : -INFINITY;
+            float mx = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float w = m == -INFINITY ? 0.f : ptx::ex2(m - mx);
+            float l = mine ? w * Y::partial(smem, lane)[PS::l(r)] : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (mine) slot_weight[lane][r] = w;
+            if (lane == 0) joined_m[r] = mx, joined_l[r] = l;
+        }
+        __syncthreads();
         for (int e = tid; e < R * (D / 2); e += THREADS) {
             const int r = e / (D / 2), c = e % (D / 2) * 2;
-            float mx = -INFINITY;
-            for (int k = a; k <= z; ++k)
-                if (slot_seg[k] >= 0) mx = fmaxf(mx, Y::partial(smem, k)[PS::m(r)]);
-            float x = 0.f, y = 0.f, l = 0.f;
-            for (int k = a; k <= z; ++k) {
-                if (slot_seg[k] < 0) continue;
-                const float* const f = Y::partial(smem, k);
-                const float mk = f[PS::m(r)];
-                const float wk = mk == -INFINITY ? 0.f : ptx::ex2(mk - mx);
-                const float2 v = *reinterpret_cast<const float2*>(f + PS::o(r) + c);
-                x = fmaf(v.x, wk, x);
-                y = fmaf(v.y, wk, y);
-                l = fmaf(f[PS::l(r)], wk, l);
+            float x = 0.f, y = 0.f;
+            for (uint32_t k = run; k; k &= k - 1) {
+                const int slot_ = __ffs(k) - 1;
+                const float w = slot_weight[slot_][r];
+                const float2 v = *reinterpret_cast<const float2*>(Y::partial(smem, slot_) + PS::o(r) + c);
+                x = fmaf(v.x, w, x);
+                y = fmaf(v.y, w, y);
             }
+            const float l = joined_l[r];
             if (begins && ends) {
                 if (r0 + r >= p.rows) continue;
                 const float f = l == 0.f ? 0.f : p.v_scale / l;
                 if (c < p.d)
                     *reinterpret_cast<uint32_t*>(p.o + (row0 + r0 + r) * p.d + c) = ptx::pack_bf16x2(x * f, y * f);
-                if (c == 0) p.lse[row0 + r0 + r] = natural_lse(mx, l);
+                if (c == 0) p.lse[row0 + r0 + r] = natural_lse(joined_m[r], l);
             } else {
                 *reinterpret_cast<float2*>(part + PS::o(r) + c) = make_float2(x, y);
                 if (c == 0) {
-                    part[PS::m(r)] = mx;
+                    part[PS::m(r)] = joined_m[r];
                     part[PS::l(r)] = l;
                 }
             }
@@ -1041,7 +1122,7 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
             p.desc[2 * cta] = seg;
             p.desc[2 * cta + 1] = (int)(((int64_t)(x + 1) * G - 1) / T);
         }
-        a = z + 1;
+        if (left) __syncthreads();
     }
 }
 
@@ -1122,11 +1203,16 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
     int* const prefix = reinterpret_cast<int*>(smem + Y::PREFIX);
     __shared__ int scratch[WARPS];
     __shared__ __align__(8) uint64_t bars[WARPS * Y::SLOTS];
-    __shared__ uint32_t abort_flag;
+    __shared__ uint32_t abort_flags[WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    if (tid < WARPS * Y::SLOTS) ptx::mbar_init(ptx::smem_addr(&bars[tid]), 1);
-    if (tid == 0) abort_flag = 0;
+    if (lane < Y::SLOTS) ptx::mbar_init(ptx::smem_addr(&bars[warp * Y::SLOTS + lane]), 1);
+    if (lane == 0) abort_flags[warp] = 0;
+    volatile uint32_t* const abort_flag = &abort_flags[warp];
     ptx::fence_barrier_init();
+    __syncwarp();
+    prefetch_l2(p.table, (int64_t)p.B * p.max_pages * 4);
+    prefetch_l2(p.q, (int64_t)p.B * p.hkv * p.rows * p.d * 2);
+    prefetch_l2(p.lse_in, (int64_t)p.B * p.hkv * p.rows * 4);
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     page_prefix<THREADS>(p.lens, p.B, p.max_pages, prefix, scratch);
@@ -1148,17 +1234,34 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
     float off[NT][2];
     int have = -1;  // segment (with row block) whose rows are loaded
     Feed<D, Y::SLOTS, false> feed(smem + warp * Y::RING, ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
+    feed.begin();
+    typename Rows<D, NT>::Raw raw;
+    // The weights that a lane adds to, of the unit after the current one: keys 16t + g and 16t + 8 + g of its page.
+    auto weights_at = [&](const Place& u) { return (int64_t)u.seg * p.w_len + (int64_t)u.page * PAGE; };
+    float w_next[2] = {};
+    auto fetch_weights = [&](const Place& u) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = 16 * t + 8 * i + g;
+            w_next[i] = (int64_t)u.page * PAGE + k < p.w_len ? p.w_in[weights_at(u) + k] : 0.f;
+        }
+    };
+    Place u = feed.place(x0);
+    fetch_weights(u);
     for (int x = x0; x < x1; ++x) {
-        const Place u = feed.place(x);
+        const float w_now[2] = {w_next[0], w_next[1]};
+        const Place after = x + 1 < x1 ? feed.peek(x + 1) : u;
+        if (x + 1 < x1) fetch_weights(after);
         const int b = u.seg / p.hkv, h = u.seg - b * p.hkv;
-        const uint8_t* const blk = feed.wait(&abort_flag);
+        const uint8_t* const blk = feed.wait(abort_flag);
         if (!blk) break;
         float sum[8] = {};
         for (int rbi = 0; rbi < p.rb; ++rbi) {
             const int seg = u.seg * p.rb + rbi;
             if (seg != have) {
                 have = seg;
-                rows.load(p, b, h * p.rb + rbi, length_of(p.lens, b, p.max_pages));
+                rows.fetch(raw, p, b, h * p.rb + rbi);
+                rows.load(raw, p, h * p.rb + rbi, length_of(p.lens, b, p.max_pages));
                 const int64_t row0 = (int64_t)u.seg * p.rows;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -1192,14 +1295,14 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
             sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
             sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
         }
-        const int64_t at = (int64_t)u.seg * p.w_len;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int64_t key = (int64_t)u.page * PAGE + 8 * e + g;
-            if (e / 2 == t && key < rows.len && key < p.w_len) p.w_out[at + key] = p.w_in[at + key] + sum[e];
+            const int k = 8 * e + g, key = u.page * PAGE + k;
+            if (e / 2 == t && key < rows.len && key < p.w_len) p.w_out[weights_at(u) + k] = w_now[e % 2] + sum[e];
         }
+        if (x + 1 < x1) u = feed.place(x + 1);
     }
-    feed.drain(&abort_flag);
+    feed.drain(abort_flag);
 }
 
 // ----------------------------------------------------------------- eviction
