@@ -52,6 +52,7 @@ one pass over its tensors (a few microseconds of host time per call).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -473,58 +474,75 @@ def _strides(t):
 def _check_int32(name, t, shape, dev):
     import torch
 
-    if not t.is_cuda or t.get_device() != dev or t.dtype != torch.int32 or not t.is_contiguous():
+    if t.get_device() != dev or t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA int32 tensor on cuda:{dev}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _check_rope(q, k, freqs, positions, lens, layout):
+    """Checks of everything but the results; returns (device, B, H, Hk, N, d)."""
+    import torch
+
+    if layout != "half" and layout != "interleaved":
+        raise ValueError(f"unknown layout {layout!r}")
+    _check_rows("q", q)
+    dev = q.get_device()
+    B, H, N, d = q.shape
+    Hk = 0
+    if k is not None:
+        _check_rows("k", k, dev)
+        Bk, Hk, Nk, dk = k.shape
+        if Bk != B or Nk != N or dk != d:
+            raise ValueError(f"k must be (B, Hk, N, d) like q: {tuple(q.shape)} {tuple(k.shape)}")
+    if freqs.get_device() != dev or freqs.dtype is not torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous CUDA int64 vector (see rope_frequencies)")
+    if positions is not None:
+        if positions.get_device() != dev or positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError("positions must be a CUDA int32 or int64 tensor")
+        if tuple(positions.shape) not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions must be (N,) or (B, N), the positions of a sequence adjoining")
+    if lens is not None:
+        _check_int32("lens", lens, (B,), dev)
+    return dev, B, H, Hk, N, d
+
+
+def _rope_call(q, k, q_out, k_out, freqs, positions, lens, layout, factor, inverse, stream, sizes):
+    dev, B, H, Hk, N, d = sizes
+    pos_ptr, pos_bytes, pos_stride = 0, 0, 0
+    if positions is not None:
+        pos_ptr, pos_bytes = positions.data_ptr(), positions.element_size()
+        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    if k is None:
+        kp, ks, kop, kos = 0, None, 0, None
+    else:
+        kp, ks, kop, kos = k.data_ptr(), _strides(k), k_out.data_ptr(), _strides(k_out)
+    rc = library().fa_rope(q.data_ptr(), _strides(q), kp, ks, q_out.data_ptr(), _strides(q_out), kop, kos, B, H, Hk, N,
+                           d, freqs.data_ptr(), 2 * freqs.numel(), layout == "interleaved", factor, bool(inverse),
+                           pos_ptr, pos_bytes, pos_stride, 0 if lens is None else lens.data_ptr(),
+                           _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_rope")
+    return q_out, k_out
 
 
 def rope_into(q, k, q_out, k_out, freqs, positions=None, lens=None, layout: str = "half", factor: float = 1.0,
               inverse: bool = False, stream=None):
     """:func:`rope` into caller-provided tensors of q's and k's shapes (each
     may be its own input; strided views are fine)."""
-    import torch
-
-    if layout not in ("half", "interleaved"):
-        raise ValueError(f"unknown layout {layout!r}")
-    _check_rows("q", q)
-    dev = q.get_device()
+    sizes = _check_rope(q, k, freqs, positions, lens, layout)
+    dev = sizes[0]
     _check_rows("q_out", q_out, dev)
     if q_out.shape != q.shape:
         raise ValueError("q_out must have the shape of q")
-    B, H, N, d = q.shape
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
-    Hk = 0
     if k is not None:
-        _check_rows("k", k, dev)
         _check_rows("k_out", k_out, dev)
-        if k_out.shape != k.shape or (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
-            raise ValueError(f"k must be (B, Hk, N, d) like q, and k_out like k: {tuple(q.shape)} {tuple(k.shape)}")
-        Hk = k.shape[1]
-    if not freqs.is_cuda or freqs.get_device() != dev or freqs.dtype != torch.int64 or freqs.dim() != 1 \
-            or not freqs.is_contiguous():
-        raise ValueError("freqs must be a contiguous CUDA int64 vector (see rope_frequencies)")
-    pos_ptr, pos_bytes, pos_stride = 0, 0, 0
-    if positions is not None:
-        if not positions.is_cuda or positions.get_device() != dev or positions.dtype not in (torch.int32, torch.int64):
-            raise ValueError("positions must be a CUDA int32 or int64 tensor")
-        if tuple(positions.shape) not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
-            raise ValueError("positions must be (N,) or (B, N), the positions of a sequence adjoining")
-        pos_ptr, pos_bytes = positions.data_ptr(), positions.element_size()
-        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    if lens is not None:
-        _check_int32("lens", lens, (B,), dev)
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
     _on_current_device(dev)
-    rc = library().fa_rope(q.data_ptr(), _strides(q), 0 if k is None else k.data_ptr(),
-                           None if k is None else _strides(k), q_out.data_ptr(), _strides(q_out),
-                           0 if k is None else k_out.data_ptr(), None if k is None else _strides(k_out), B, H, Hk, N,
-                           d, freqs.data_ptr(), 2 * freqs.numel(), int(layout == "interleaved"), float(factor),
-                           int(bool(inverse)), pos_ptr, pos_bytes, pos_stride,
-                           0 if lens is None else lens.data_ptr(), _stream_handle(stream, dev))
-    if rc != 0:
-        raise FaError(rc, "fa_rope")
-    return q_out, k_out
+    return _rope_call(q, k, q_out, k_out, freqs, positions, lens, layout, factor, inverse, stream, sizes)
 
 
 def rope(q, k, freqs, positions=None, lens=None, layout: str = "half", factor: float = 1.0, inverse: bool = False,
@@ -537,11 +555,14 @@ def rope(q, k, freqs, positions=None, lens=None, layout: str = "half", factor: f
     projection) are taken as they are."""
     import torch
 
-    _check_rows("q", q)
-    with torch.cuda.device(q.device):
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        return rope_into(q, k, q_out, k_out, freqs, positions, lens, layout, factor, inverse, stream)
+    sizes = _check_rope(q, k, freqs, positions, lens, layout)
+    dev = sizes[0]
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return rope(q, k, freqs, positions, lens, layout, factor, inverse, stream)
+    q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+    return _rope_call(q, k, q_out, k_out, freqs, positions, lens, layout, factor, inverse, stream, sizes)
 
 
 def rope_bwd(dq, dk, freqs, positions=None, lens=None, layout: str = "half", factor: float = 1.0, stream=None):
@@ -568,18 +589,20 @@ def _check_qcache(pool, table, lens, d):
     """The cache's tensors; returns (device, B, num_pages, Hkv, max_pages)."""
     import torch
 
-    if not pool.is_cuda or pool.dtype != torch.uint8 or pool.dim() != 3 or not pool.is_contiguous():
-        raise ValueError("pool must be a contiguous CUDA uint8 (pages, Hkv, bytes) tensor (see qcache_pool)")
-    if d is not None and pool.shape[2] != 72 * (64 if d <= 64 else 128):
-        raise ValueError(f"pool was made for another head size than {d}")
-    if pool.shape[2] not in (72 * 64, 72 * 128):
-        raise ValueError("pool's blocks must hold 72 * 64 or 72 * 128 bytes")
     dev = pool.get_device()
+    if dev < 0 or pool.dtype is not torch.uint8 or pool.dim() != 3 or not pool.is_contiguous():
+        raise ValueError("pool must be a contiguous CUDA uint8 (pages, Hkv, bytes) tensor (see qcache_pool)")
+    num_pages, Hkv, block = pool.shape
+    if d is not None and block != (4608 if d <= 64 else 9216):
+        raise ValueError(f"pool was made for another head size than {d}")
+    if block != 4608 and block != 9216:
+        raise ValueError("pool's blocks must hold 72 * 64 or 72 * 128 bytes")
     if table.dim() != 2:
         raise ValueError("table must be (B, max_pages)")
     _check_int32("table", table, None, dev)
-    _check_int32("lens", lens, (table.shape[0],), dev)
-    return dev, table.shape[0], pool.shape[0], pool.shape[1], table.shape[1]
+    B, max_pages = table.shape
+    _check_int32("lens", lens, (B,), dev)
+    return dev, B, num_pages, Hkv, max_pages
 
 
 def qcache_append(k, v, pool, table, lens, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
@@ -587,16 +610,16 @@ def qcache_append(k, v, pool, table, lens, k_scale: float = 1.0, v_scale: float 
     sequence: row i becomes key lens[b] - N + i (rows of negative position are
     padding).  lens counts the new keys already."""
     _check_rows("k", k)
-    _check_rows("v", v)
     B, Hkv, N, d = k.shape
     dev, Bc, num_pages, Hp, max_pages = _check_qcache(pool, table, lens, d)
-    if v.shape != k.shape or Bc != B or Hp != Hkv or k.get_device() != dev or v.get_device() != dev:
+    _check_rows("v", v, dev)
+    if v.shape != k.shape or Bc != B or Hp != Hkv or k.get_device() != dev:
         raise ValueError(f"k and v must be (B, Hkv, N, d) of the cache's batch, heads and device: {tuple(k.shape)} "
                          f"{tuple(v.shape)}")
     _on_current_device(dev)
-    rc = library().fa_qcache_append(k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), B, Hkv, N, d,
-                                    float(k_scale), float(v_scale), pool.data_ptr(), num_pages, table.data_ptr(),
-                                    max_pages, lens.data_ptr(), _stream_handle(stream, dev))
+    rc = library().fa_qcache_append(k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), B, Hkv, N, d, k_scale,
+                                    v_scale, pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
+                                    _stream_handle(stream, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_append")
 
@@ -610,21 +633,24 @@ def qcache_read(pool, table, lens, n: int, d: int, newest: bool = False, k_scale
     dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, d)
     if n < 1:
         raise ValueError("n must be positive")
-    with torch.cuda.device(dev):
-        k = torch.empty((B, Hkv, n, d), dtype=torch.bfloat16, device=pool.device)
-        v = torch.empty_like(k)
-        rc = library().fa_qcache_read(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
-                                      k.data_ptr(), v.data_ptr(), B, Hkv, n, d, int(bool(newest)), float(k_scale),
-                                      float(v_scale), _stream_handle(stream, dev))
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return qcache_read(pool, table, lens, n, d, newest, k_scale, v_scale, stream)
+    k = torch.empty((B, Hkv, n, d), dtype=torch.bfloat16, device=pool.device)
+    v = torch.empty((B, Hkv, n, d), dtype=torch.bfloat16, device=pool.device)
+    rc = library().fa_qcache_read(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
+                                  k.data_ptr(), v.data_ptr(), B, Hkv, n, d, bool(newest), k_scale, v_scale,
+                                  _stream_handle(stream, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_read")
     return k, v
 
 
 def _check_qcache_query(q, pool, table, lens):
+    """Checks of a call with queries; returns (device, num_pages, Hkv, max_pages)."""
     import torch
 
-    if not q.is_cuda or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.dim() != 4:
+    if not q.is_cuda or q.dtype is not torch.bfloat16 or not q.is_contiguous() or q.dim() != 4:
         raise ValueError("q must be a contiguous CUDA bf16 (B, H, Nq, d) tensor")
     B, H, Nq, d = q.shape
     dev, Bc, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, d)
@@ -643,6 +669,26 @@ def qcache_decode_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, d: int, max
     return int(out.value)
 
 
+@functools.lru_cache(maxsize=256)
+def _qcache_workspace(dev, B, H, Hkv, Nq, d, max_pages):
+    """The workspace size on device dev (the current one), a function of the sizes alone."""
+    return qcache_decode_workspace_bytes(B, H, Hkv, Nq, d, max_pages)
+
+
+def _qcache_decode_call(q, pool, table, lens, o, lse, workspace, causal, scale, k_scale, v_scale, stream, sizes):
+    dev, num_pages, Hkv, max_pages = sizes
+    B, H, Nq, d = q.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    rc = library().fa_qcache_decode(q.data_ptr(), pool.data_ptr(), num_pages, table.data_ptr(), max_pages,
+                                    lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, d, bool(causal),
+                                    scale, k_scale, v_scale, workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_qcache_decode")
+    return o, lse
+
+
 def qcache_decode_into(q, pool, table, lens, o, lse, workspace, causal: bool = False, scale: float | None = None,
                        k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
     """:func:`qcache_decode` into caller-provided o (bf16, like q), lse (fp32,
@@ -650,23 +696,14 @@ def qcache_decode_into(q, pool, table, lens, o, lse, workspace, causal: bool = F
     qcache_decode_workspace_bytes bytes)."""
     import torch
 
-    dev, num_pages, Hkv, max_pages = _check_qcache_query(q, pool, table, lens)
-    B, H, Nq, d = q.shape
+    sizes = _check_qcache_query(q, pool, table, lens)
+    dev = sizes[0]
     _check_out("o", o, q.shape, torch.bfloat16, q.device)
-    _check_out("lse", lse, (B, H, Nq), torch.float32, q.device)
+    _check_out("lse", lse, q.shape[:3], torch.float32, q.device)
     if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     _on_current_device(dev)
-    rc = library().fa_qcache_decode(q.data_ptr(), pool.data_ptr(), num_pages, table.data_ptr(), max_pages,
-                                    lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, d,
-                                    int(bool(causal)), float(scale), float(k_scale), float(v_scale),
-                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                    _stream_handle(stream, dev))
-    if rc != 0:
-        raise FaError(rc, "fa_qcache_decode")
-    return o, lse
+    return _qcache_decode_call(q, pool, table, lens, o, lse, workspace, causal, scale, k_scale, v_scale, stream, sizes)
 
 
 def qcache_decode(q, pool, table, lens, causal: bool = False, scale: float | None = None, k_scale: float = 1.0,
@@ -677,13 +714,17 @@ def qcache_decode(q, pool, table, lens, causal: bool = False, scale: float | Non
     (B, H, Nq) fp32)``; a query that sees no key gives 0 and -inf."""
     import torch
 
-    dev, _, Hkv, max_pages = _check_qcache_query(q, pool, table, lens)
+    sizes = _check_qcache_query(q, pool, table, lens)
+    dev, _, Hkv, max_pages = sizes
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return qcache_decode(q, pool, table, lens, causal, scale, k_scale, v_scale, stream)
     B, H, Nq, d = q.shape
-    with torch.cuda.device(dev):
-        ws = torch.empty(qcache_decode_workspace_bytes(B, H, Hkv, Nq, d, max_pages), dtype=torch.uint8, device=q.device)
-        o = torch.empty_like(q)
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-        return qcache_decode_into(q, pool, table, lens, o, lse, ws, causal, scale, k_scale, v_scale, stream)
+    on = q.device
+    ws = torch.empty(_qcache_workspace(dev, B, H, Hkv, Nq, d, max_pages), dtype=torch.uint8, device=on)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=on)
+    return _qcache_decode_call(q, pool, table, lens, o, lse, ws, causal, scale, k_scale, v_scale, stream, sizes)
 
 
 def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, scale: float | None = None,
@@ -695,6 +736,9 @@ def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, sca
     import torch
 
     dev, num_pages, Hkv, max_pages = _check_qcache_query(q, pool, table, lens)
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return qcache_weights(q, lse, pool, table, lens, weights, causal, scale, k_scale, out, stream)
     B, H, Nq, d = q.shape
     _check_out("lse", lse, (B, H, Nq), torch.float32, q.device)
     if weights.dim() != 3:
@@ -702,15 +746,14 @@ def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, sca
     _check_out("weights", weights, (B, Hkv, weights.shape[2]), torch.float32, q.device)
     if out is not None:
         _check_out("out", out, weights.shape, torch.float32, q.device)
+    else:
+        out = torch.empty_like(weights)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty_like(weights)
-        rc = library().fa_qcache_weights(q.data_ptr(), lse.data_ptr(), pool.data_ptr(), num_pages, table.data_ptr(),
-                                         max_pages, lens.data_ptr(), weights.data_ptr(), out.data_ptr(),
-                                         weights.shape[2], B, H, Hkv, Nq, d, int(bool(causal)), float(scale),
-                                         float(k_scale), _stream_handle(stream, dev))
+    rc = library().fa_qcache_weights(q.data_ptr(), lse.data_ptr(), pool.data_ptr(), num_pages, table.data_ptr(),
+                                     max_pages, lens.data_ptr(), weights.data_ptr(), out.data_ptr(),
+                                     weights.shape[2], B, H, Hkv, Nq, d, bool(causal), scale, k_scale,
+                                     _stream_handle(stream, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_weights")
     return out
@@ -727,6 +770,9 @@ def qcache_evict(pool, table, lens, weights, keep: int, sink: int = 0, recent: i
     import torch
 
     dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, None)
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return qcache_evict(pool, table, lens, weights, keep, sink, recent, table_out, stream)
     if weights.dim() != 3:
         raise ValueError("weights must be (B, Hkv, W)")
     _check_out("weights", weights, (B, Hkv, weights.shape[2]), torch.float32, pool.device)
@@ -737,14 +783,13 @@ def qcache_evict(pool, table, lens, weights, keep: int, sink: int = 0, recent: i
     _check_int32("table_out", table_out, None, dev)
     if keep < 1 or sink < 0 or recent < 0 or sink + recent > keep:
         raise ValueError("keep must be positive, sink and recent not negative and together at most keep")
-    with torch.cuda.device(dev):
-        kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=pool.device)
-        lens_out = torch.empty_like(lens)
-        weights_out = torch.empty_like(weights)
-        rc = library().fa_qcache_evict(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
-                                       table_out.data_ptr(), table_out.shape[1], weights.data_ptr(),
-                                       weights_out.data_ptr(), weights.shape[2], kept.data_ptr(), lens_out.data_ptr(),
-                                       B, Hkv, pool.shape[2] // 72, keep, sink, recent, _stream_handle(stream, dev))
+    kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=pool.device)
+    lens_out = torch.empty_like(lens)
+    weights_out = torch.empty_like(weights)
+    rc = library().fa_qcache_evict(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
+                                   table_out.data_ptr(), table_out.shape[1], weights.data_ptr(),
+                                   weights_out.data_ptr(), weights.shape[2], kept.data_ptr(), lens_out.data_ptr(), B,
+                                   Hkv, pool.shape[2] // 72, keep, sink, recent, _stream_handle(stream, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_evict")
     return kept, lens_out, weights_out
