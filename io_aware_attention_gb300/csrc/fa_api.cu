@@ -675,6 +675,53 @@ fa_status launch_qcache_weights(const fa::qc::DecParams& p, int64_t blocks, int 
                : FA_ERR_CUDA;
 }
 
+// Launches `kernel` like launch_pdl, in clusters of `cluster` blocks along x.
+template <typename... KParams, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KParams...), dim3 grid, dim3 block, size_t smem, int cluster,
+                            cudaStream_t st, Args&&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <int C>
+fa_status launch_qcache_select(const fa::qc::EvictParams& p, int64_t Hkv, int64_t B, int dev, cudaStream_t st)
+{
+    static std::atomic<int> done[MAX_DEVICES];
+    const fa_status as = allow_smem(fa::qc::fa_qcache_select_kernel<C>, (size_t)fa::qc::SEL_SMEM, done, dev);
+    if (as != FA_OK) return as;
+    return launch_clusters(fa::qc::fa_qcache_select_kernel<C>, dim3((unsigned)(Hkv * C), (unsigned)B),
+                           dim3(fa::qc::SEL_THREADS), (size_t)fa::qc::SEL_SMEM, C, st, p) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
+template <int D>
+fa_status launch_qcache_move(const fa::qc::EvictParams& p, int64_t Hkv, int64_t B, int dev, cudaStream_t st)
+{
+    static std::atomic<int> done[MAX_DEVICES];
+    constexpr size_t bytes = (size_t)fa::qc::MOVE_PAGES * fa::qc::Block<D>::BYTES;
+    const fa_status as = allow_smem(fa::qc::fa_qcache_move_kernel<D>, bytes, done, dev);
+    if (as != FA_OK) return as;
+    return launch_clusters(fa::qc::fa_qcache_move_kernel<D>, dim3((unsigned)(Hkv * fa::qc::MOVE_C), (unsigned)B),
+                           dim3(fa::qc::MOVE_THREADS), bytes, fa::qc::MOVE_C, st, p) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
 // What decode and weights share: the query side.
 fa_status qcache_query_check(const void* q, int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t max_pages,
                              int causal, float scale, float k_scale)
@@ -1363,14 +1410,13 @@ fa_status fa_qcache_evict(void* pool, int64_t num_pages, const int32_t* table, i
     p.sink = (int)sink;
     p.recent = (int)recent;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const dim3 grid((unsigned)Hkv, (unsigned)B);
-    if (launch_pdl(fa::qc::fa_qcache_select_kernel, grid, dim3(fa::qc::SEL_THREADS), 0, st, p) != cudaSuccess)
-        return FA_ERR_CUDA;
-    const cudaError_t e =
-        padded_head_size(d) == 128
-            ? launch_pdl(fa::qc::fa_qcache_move_kernel<128>, grid, dim3(fa::qc::ROW_THREADS), 0, st, p)
-            : launch_pdl(fa::qc::fa_qcache_move_kernel<64>, grid, dim3(fa::qc::ROW_THREADS), 0, st, p);
-    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    // A cluster of 8 blocks a head where heads are long: its barriers cost more
+    // than they save below some thousands of keys.
+    const bool wide = max_pages * fa::qc::PAGE > 4096;
+    const fa_status ss = wide ? launch_qcache_select<8>(p, Hkv, B, dev, st) : launch_qcache_select<1>(p, Hkv, B, dev, st);
+    if (ss != FA_OK) return ss;
+    return padded_head_size(d) == 128 ? launch_qcache_move<128>(p, Hkv, B, dev, st)
+                                      : launch_qcache_move<64>(p, Hkv, B, dev, st);
 }
 
 fa_status fa_check_device_status(fa_stream_t stream, uint32_t* where)

@@ -285,62 +285,102 @@ __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float s)
     return ptx::pack_bf16x2(f.x * s, f.y * s);
 }
 
-// Read: rows first .. first + N - 1 of every sequence as bf16 (rounded once:
-// the stored value times the tensor's scale); rows where no key is are zero.
-// Block (tile of 64 rows, kv head, sequence).
+// 32 consecutive bytes of global memory in one store (or two of 16).
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&w)[8], bool aligned)
+{
+    if (aligned)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    else {
+        ptx::st_global_v4(p, w[0], w[1], w[2], w[3]);
+        ptx::st_global_v4(static_cast<char*>(p) + 16, w[4], w[5], w[6], w[7]);
+    }
+}
+
+// Read: rows 0 .. N - 1 (or the newest N) of every sequence as bf16 (rounded
+// once: the stored value times the tensor's scale); rows where no key is are
+// zero.  Block (tile of 64 rows, kv head, sequence): the rows' pages are looked
+// up once, then a thread takes a channel block of some rows with all its loads
+// in flight before the first is used.
 template <int D>
 __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_read_kernel(const RowParams p)
 {
+    using L = Block<D>;
+    constexpr int STEP = ROW_THREADS / L::NB, PER = PAGE / STEP;  // rows apart, rows of a thread
+    __shared__ int src_blk[PAGE], src_row[PAGE];
+    const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    using L = Block<D>;
-    const int b = blockIdx.z, h = blockIdx.y;
-    const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.max_pages * PAGE);
-    const int64_t shift = p.newest ? (int64_t)p.lens[b] - p.n : 0;
     const int64_t i0 = (int64_t)blockIdx.x * PAGE;
     const int rows = (int)min(p.n - i0, (int64_t)PAGE);
-    const int64_t out0 = (((int64_t)b * p.hkv + h) * p.n + i0) * p.d;
-    for (int t = threadIdx.x; t < rows * L::NB; t += ROW_THREADS) {
-        const int r = t / L::NB, c = t % L::NB;
-        if (c * 16 >= p.d) continue;
-        const int64_t pos = i0 + r + shift;
-        uint32_t kw[8] = {}, vw[8] = {};
-        if (pos >= 0 && pos < len) {
+    if (tid < PAGE) {
+        const int given = p.lens[b];
+        const int64_t len = min((int64_t)max(given, 0), (int64_t)p.max_pages * PAGE);
+        const int64_t pos = i0 + tid + (p.newest ? (int64_t)given - p.n : 0);
+        int blk = -1;
+        if (tid < rows && pos >= 0 && pos < len) {
             const int id = page_of(p.table, p.max_pages, p.num_pages, b, (int)(pos / PAGE));
-            if (id < 0) {
-                atomicOr(&g_status, STATUS_BAD_PAGE);
-            } else {
-                const int x = (int)(pos % PAGE);
-                const uint8_t* const blk = p.pool + ((int64_t)id * p.hkv + h) * L::BYTES;
-                const uint2 kc = *reinterpret_cast<const uint2*>(blk + L::kcode(x) + c * 8);
-                const float ks = scale_value(blk[L::kscale(x, c)]) * p.k_scale;
-                const uint4 vc = *reinterpret_cast<const uint4*>(blk + L::vcode(x) + c * 16);
-                const float vs = scale_value(blk[L::vscale(x, c)]) * p.v_scale;
-                kw[0] = scaled_bf16x2(e2m1x2<0>(kc.x), ks);
-                kw[1] = scaled_bf16x2(e2m1x2<1>(kc.x), ks);
-                kw[2] = scaled_bf16x2(e2m1x2<2>(kc.x), ks);
-                kw[3] = scaled_bf16x2(e2m1x2<3>(kc.x), ks);
-                kw[4] = scaled_bf16x2(e2m1x2<0>(kc.y), ks);
-                kw[5] = scaled_bf16x2(e2m1x2<1>(kc.y), ks);
-                kw[6] = scaled_bf16x2(e2m1x2<2>(kc.y), ks);
-                kw[7] = scaled_bf16x2(e2m1x2<3>(kc.y), ks);
-                const uint32_t v4[4] = {vc.x, vc.y, vc.z, vc.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {  // 4 channels' bytes: this key's nibbles, packed two to a byte
-                    const uint32_t n = (x % 2 ? v4[i] >> 4 : v4[i]) & 0x0F0F0F0Fu;
-                    const uint32_t two = n | (n >> 4);  // bytes 0 and 2 hold channels (0, 1) and (2, 3)
-                    vw[2 * i] = scaled_bf16x2(e2m1x2<0>(two), vs);
-                    vw[2 * i + 1] = scaled_bf16x2(e2m1x2<2>(two), vs);
-                }
-            }
+            if (id >= 0) blk = id * p.hkv + h;
+            else atomicOr(&g_status, STATUS_BAD_PAGE);
         }
-        __nv_bfloat16* const ko = p.ko + out0 + (int64_t)r * p.d + c * 16;
-        __nv_bfloat16* const vo = p.vo + out0 + (int64_t)r * p.d + c * 16;
-        ptx::st_global_v4(ko, kw[0], kw[1], kw[2], kw[3]);
-        ptx::st_global_v4(vo, vw[0], vw[1], vw[2], vw[3]);
+        src_blk[tid] = blk;
+        src_row[tid] = (int)(pos & (PAGE - 1));
+    }
+    __syncthreads();
+    const int c = tid % L::NB, r0 = tid / L::NB;
+    if (c * 16 >= p.d) return;
+    uint2 kc[PER];
+    uint4 vc[PER];
+    uint8_t ksc[PER], vsc[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int r = r0 + i * STEP;
+        kc[i] = make_uint2(0, 0);
+        vc[i] = make_uint4(0, 0, 0, 0);
+        ksc[i] = vsc[i] = 0;
+        if (src_blk[r] >= 0) {
+            const uint8_t* const blk = p.pool + (int64_t)src_blk[r] * L::BYTES;
+            const int x = src_row[r];
+            kc[i] = __ldg(reinterpret_cast<const uint2*>(blk + L::kcode(x) + c * 8));
+            vc[i] = __ldg(reinterpret_cast<const uint4*>(blk + L::vcode(x) + c * 16));
+            ksc[i] = __ldg(blk + L::kscale(x, c));
+            vsc[i] = __ldg(blk + L::vscale(x, c));
+        }
+    }
+    const int64_t out0 = (((int64_t)b * p.hkv + h) * p.n + i0) * p.d + c * 16;
+    const bool aligned = p.d % 16 == 0 && ((reinterpret_cast<uintptr_t>(p.ko) | reinterpret_cast<uintptr_t>(p.vo)) & 31u) == 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int r = r0 + i * STEP;
+        if (r >= rows) break;
+        const float ks = scale_value(ksc[i]) * p.k_scale, vs = scale_value(vsc[i]) * p.v_scale;
+        uint32_t kw[8], vw[8];
+        kw[0] = scaled_bf16x2(e2m1x2<0>(kc[i].x), ks);
+        kw[1] = scaled_bf16x2(e2m1x2<1>(kc[i].x), ks);
+        kw[2] = scaled_bf16x2(e2m1x2<2>(kc[i].x), ks);
+        kw[3] = scaled_bf16x2(e2m1x2<3>(kc[i].x), ks);
+        kw[4] = scaled_bf16x2(e2m1x2<0>(kc[i].y), ks);
+        kw[5] = scaled_bf16x2(e2m1x2<1>(kc[i].y), ks);
+        kw[6] = scaled_bf16x2(e2m1x2<2>(kc[i].y), ks);
+        kw[7] = scaled_bf16x2(e2m1x2<3>(kc[i].y), ks);
+        const uint32_t v4[4] = {vc[i].x, vc[i].y, vc[i].z, vc[i].w};
+        const int nibble = src_row[r] % 2 * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // 4 channels' bytes: this key's nibbles, packed two to a byte
+            const uint32_t n = v4[e] >> nibble & 0x0F0F0F0Fu;
+            const uint32_t two = n | (n >> 4);  // bytes 0 and 2 hold channels (0, 1) and (2, 3)
+            vw[2 * e] = scaled_bf16x2(e2m1x2<0>(two), vs);
+            vw[2 * e + 1] = scaled_bf16x2(e2m1x2<2>(two), vs);
+        }
+        __nv_bfloat16* const ko = p.ko + out0 + (int64_t)r * p.d;
+        __nv_bfloat16* const vo = p.vo + out0 + (int64_t)r * p.d;
         if (c * 16 + 8 < p.d) {
-            ptx::st_global_v4(ko + 8, kw[4], kw[5], kw[6], kw[7]);
-            ptx::st_global_v4(vo + 8, vw[4], vw[5], vw[6], vw[7]);
+            st_global_32(ko, kw, aligned);
+            st_global_32(vo, vw, aligned);
+        } else {
+            ptx::st_global_v4(ko, kw[0], kw[1], kw[2], kw[3]);
+            ptx::st_global_v4(vo, vw[0], vw[1], vw[2], vw[3]);
         }
     }
 }
@@ -478,6 +518,11 @@ struct Chunk {  // a lane's share of a row: 16 or 8 bytes
             const uint2 v = *reinterpret_cast<const uint2*>(p);
             w[0] = v.x, w[1] = v.y;
         }
+    }
+    __device__ __forceinline__ void store(uint8_t* p) const
+    {
+        if constexpr (NBYTES == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     }
 };
 
@@ -1327,18 +1372,55 @@ __device__ __forceinline__ uint32_t order_of(float w)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int SEL_THREADS = 1024;
+// Thread-block clusters: the C blocks of one kv head of one sequence.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Reads an int of block `rank`'s shared memory.
+__device__ __forceinline__ int cluster_read(const int* mine, int rank)
+{
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_addr(mine)), "r"(rank));
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
 
-// Chooses the keys that stay, one block a kv head of a sequence: the first
-// `sink`, the last `recent`, and of those between the keep - sink - recent
-// with the largest weights (of equal weights the lowest places), found by
-// radix selection: four histograms of 8 bits of order_of, largest digit
-// first, give the smallest weight that stays and how many of that weight do.
+constexpr int SEL_THREADS = 512;
+constexpr int SEL_BINS = 256;
+// Weights that a block keeps in shared memory over its passes (the rest are
+// read again): a cluster of 8 holds 65536 of a head.  49 KB a block, so that 4 fit an SM.
+constexpr int SEL_HELD = 8192;
+constexpr int SEL_SMEM = SEL_HELD * 4;
+
+// Chooses the keys that stay: the first `sink`, the last `recent`, and of those
+// between the keep - sink - recent with the largest weights (of equal weights
+// the lowest places), found by radix selection: four histograms of 8 bits of
+// order_of, largest digit first, give the smallest weight that stays and how
+// many of that weight do.  (Digits of 11 bits need a pass less, but a block
+// then reads 16384 counts of the others a pass: 109 us against 32 for 64 heads
+// of 32768 keys.)  A cluster of C blocks shares a kv
+// head of a sequence, each block a run of the places and each warp a run of
+// its block's; the histograms and the counts before a block's run are read
+// from the other blocks' shared memory, so the result does not depend on
+// timing.
+template <int C>
 __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const EvictParams p)
 {
+    constexpr int W = SEL_THREADS / 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint32_t* const held = reinterpret_cast<uint32_t*>(smem);
+    __shared__ int hist[2][SEL_BINS];  // two, in turn: one is read by the cluster while the other is cleared
+    __shared__ int found[2];
+    __shared__ int sums[W];
+    __shared__ int counts[2];          // this block's larger and equal ones
+    __shared__ int warp_gt[W], warp_eq[W];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = C > 1 ? blockIdx.x % C : 0, h = blockIdx.x / C, b = blockIdx.y;
+    for (int e = tid; e < 2 * SEL_BINS; e += SEL_THREADS) (&hist[0][0])[e] = 0;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t bh = (int64_t)b * p.hkv + h;
     const int len = length_of(p.lens, b, p.max_pages);
     const int count = min(len, p.keep);
@@ -1350,166 +1432,226 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
         kept[at] = x;
         if (at < p.w_len) wo[at] = weight(x);
     };
-    if (h == 0 && tid == 0) {
+    const int all = C * SEL_THREADS, me = rank * SEL_THREADS + tid;
+    if (h == 0 && me == 0) {
         p.lens_out[b] = count;
         if (p.lens[b] > p.max_pages * (int64_t)PAGE) atomicOr(&g_status, STATUS_BAD_PAGE);
     }
-    for (int64_t e = count + tid; e < p.w_len; e += SEL_THREADS) wo[e] = 0.f;
-    for (int e = count + tid; e < p.keep; e += SEL_THREADS) kept[e] = -1;
+    for (int64_t e = count + me; e < p.w_len; e += all) wo[e] = 0.f;
+    for (int e = count + me; e < p.keep; e += all) kept[e] = -1;
     if (len <= p.keep) {
-        for (int e = tid; e < len; e += SEL_THREADS) put(e, e);
+        for (int e = me; e < len; e += all) put(e, e);
         return;
     }
     const int first = p.sink, last = len - p.recent;  // the choice lies between
-    for (int e = tid; e < p.sink; e += SEL_THREADS) put(e, e);
-    for (int e = tid; e < p.recent; e += SEL_THREADS) put(p.keep - p.recent + e, last + e);
+    for (int e = me; e < p.sink; e += all) put(e, e);
+    for (int e = me; e < p.recent; e += all) put(p.keep - p.recent + e, last + e);
     int need = p.keep - p.sink - p.recent;
-    if (need == 0) return;
+    if (need == 0) return;  // (the whole cluster)
 
-    __shared__ int hist[256];
-    __shared__ int found[2];
-    __shared__ int sums[SEL_THREADS / 32];
+    // This block's run of places, and each of its threads' view of their order.
+    const int n = last - first;
+    const int lo = first + (int)((int64_t)n * rank / C), hi = first + (int)((int64_t)n * (rank + 1) / C), size = hi - lo;
+    auto order = [&](int e) { return e < SEL_HELD ? held[e] : order_of(weight(lo + e)); };
+    for (int e0 = tid; e0 < min(size, SEL_HELD); e0 += 8 * SEL_THREADS) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = e0 + i * SEL_THREADS < size ? weight(lo + e0 + i * SEL_THREADS) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e0 + i * SEL_THREADS < min(size, SEL_HELD)) held[e0 + i * SEL_THREADS] = order_of(x[i]);
+    }
+    __syncthreads();
+
     uint32_t prefix = 0, mask = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int e = first + tid; e < last; e += SEL_THREADS) {
-            const uint32_t u = order_of(weight(e));
-            if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1);
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        int* const mine = hist[pass & 1];
+#pragma unroll 4
+        for (int e = tid; e < size; e += SEL_THREADS) {
+            const uint32_t u = order(e);
+            if ((u & mask) == prefix) atomicAdd(&mine[u >> shift & 255u], 1);
         }
-        __syncthreads();
-        if (warp == 0) {
-            // Lane l holds digits 255 - 8l down to 248 - 8l.
-            int c[8], sum = 0;
+        if constexpr (C > 1) cluster_sync();
+        else __syncthreads();
+        // A pair of threads a digit, from the largest down, half of the blocks each.
+        const int digit = 255 - tid / 2;
+        int c = 0;
+        if constexpr (C > 1) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
-            int upto = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int n = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += n;
-            }
-            int above = upto - sum;
-            if (above < need && need <= upto) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (above < need && need <= above + c[i]) {
-                        found[0] = 255 - 8 * lane - i;
-                        found[1] = need - above;
-                    }
-                    above += c[i];
-                }
-            }
+            for (int k = 0; k < C / 2; ++k) c += cluster_read(&mine[digit], tid % 2 * (C / 2) + k);
+        } else {
+            c = tid % 2 ? 0 : mine[digit];
         }
+        c += __shfl_xor_sync(0xffffffffu, c, 1);
+        int upto = tid % 2 ? 0 : c;  // sums over the digits, each once
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        int before = 0;
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            if (k < warp) before += sums[k];
+        const int above = before + upto - c;
+        if (tid % 2 == 0 && above < need && need <= above + c) {
+            found[0] = digit;
+            found[1] = need - above;
+        }
+        // The other histogram is read by no block any more: all have passed this pass's cluster barrier.
+        for (int e = tid; e < SEL_BINS; e += SEL_THREADS) hist[~pass & 1][e] = 0;
         __syncthreads();
         prefix |= (uint32_t)found[0] << shift;
         mask |= 255u << shift;
         need = found[1];
-        __syncthreads();
     }
-    // Everything above `prefix` stays, and the first `need` equal to it.
-    int base = 0;  // larger ones so far (low half), equal ones (high half) in separate counts
-    int base_eq = 0;
-    for (int e0 = first; e0 < last; e0 += SEL_THREADS) {
-        const int e = e0 + tid;
-        uint32_t u = 0;
-        bool gt = false, eq = false;
-        if (e < last) {
-            u = order_of(weight(e));
-            gt = u > prefix;
-            eq = u == prefix;
+    // Everything above `prefix` stays, and the first `need` equal to it.  Each
+    // warp counts its run, then places it.
+    const int wlo = (int)((int64_t)size * warp / W), whi = (int)((int64_t)size * (warp + 1) / W);
+    int gt = 0, eq = 0;
+#pragma unroll 4
+    for (int e = wlo + lane; e < whi; e += 32) {
+        const uint32_t u = order(e);
+        gt += u > prefix;
+        eq += u == prefix;
+    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) warp_gt[warp] = gt, warp_eq[warp] = eq;
+    __syncthreads();
+    if (tid < 2) {
+        int v = 0;
+        for (int k = 0; k < W; ++k) v += tid ? warp_eq[k] : warp_gt[k];
+        counts[tid] = v;
+    }
+    int base = 0, base_eq = 0;
+    if constexpr (C > 1) {
+        cluster_sync();
+        for (int k = 0; k < rank; ++k) {
+            base += cluster_read(&counts[0], k);
+            base_eq += cluster_read(&counts[1], k);
         }
-        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) sums[warp] = __popc(mg) | (__popc(me) << 16);
-        __syncthreads();
-        int before = 0, all = 0;
-        {
-            int v = sums[lane];
-            int upto = v;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int n = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += n;
-            }
-            all = __shfl_sync(0xffffffffu, upto, 31);
-            before = __shfl_sync(0xffffffffu, upto - v, warp);
-        }
+    }
+    for (int k = 0; k < warp; ++k) {
+        base += warp_gt[k];
+        base_eq += warp_eq[k];
+    }
+    for (int e0 = wlo; e0 < whi; e0 += 32) {
+        const int e = e0 + lane;
+        const uint32_t u = e < whi ? order(e) : 0u;
+        const bool is_gt = e < whi && u > prefix, is_eq = e < whi && u == prefix;
+        const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me_ = __ballot_sync(0xffffffffu, is_eq);
         const uint32_t below = (1u << lane) - 1u;
-        const int ng = base + (before & 0xffff) + __popc(mg & below);
-        const int ne = base_eq + (before >> 16) + __popc(me & below);
-        if (gt || (eq && ne < need)) put(p.sink + ng + min(ne, need), e);
-        base += all & 0xffff;
-        base_eq += all >> 16;
-        __syncthreads();
+        const int ng = base + __popc(mg & below), ne = base_eq + __popc(me_ & below);
+        if (is_gt || (is_eq && ne < need)) put(p.sink + ng + min(ne, need), lo + e);
+        base += __popc(mg);
+        base_eq += __popc(me_);
     }
+    if constexpr (C > 1) cluster_sync();  // no block leaves while its shared memory may be read
 }
 
-// Moves the kept rows to the front, a page of the destination at a time, one
-// block a kv head of a sequence.  The destination's pages may be the
-// sequence's own: row j comes from place kept[j] >= j, so writing a page
-// overwrites no row that a later page still needs, and the page is read
-// whole into shared memory before it is written.
+// Moves the kept rows to the front.  A cluster of MOVE_C blocks shares a kv
+// head of a sequence; in a round each block gathers up to MOVE_PAGES pages of
+// the destination into shared memory, the cluster meets, and all write.  The
+// destination's pages may be the sequence's own: row j comes from place
+// kept[j] >= j, so what a round writes no later round reads, and what it
+// overwrites has been read by then (its own and earlier rounds' rows).
+constexpr int MOVE_C = 8, MOVE_PAGES = 4, MOVE_THREADS = 256;
+
 template <int D>
-__global__ void __launch_bounds__(ROW_THREADS) fa_qcache_move_kernel(const EvictParams p)
+__global__ void __launch_bounds__(MOVE_THREADS) fa_qcache_move_kernel(const EvictParams p)
 {
+    using L = Block<D>;
+    constexpr int ROWS = MOVE_PAGES * PAGE;
+    static_assert(ROWS == MOVE_THREADS, "a thread looks up a row");
+    extern __shared__ __align__(16) uint8_t smem[];  // MOVE_PAGES blocks
+    __shared__ int src_blk[ROWS], src_row[ROWS];
+    __shared__ int out_blk[MOVE_PAGES];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    using L = Block<D>;
-    __shared__ __align__(16) uint8_t buf[L::BYTES];
-    __shared__ int src[PAGE];
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int rank = blockIdx.x % MOVE_C, h = blockIdx.x / MOVE_C, b = blockIdx.y, tid = threadIdx.x;
     const int64_t bh = (int64_t)b * p.hkv + h;
-    const int count = min(length_of(p.lens, b, p.max_pages), p.keep);
-    auto block = [&](int id) { return p.pool + ((int64_t)id * p.hkv + h) * L::BYTES; };
-    for (int x0 = 0; x0 < count; x0 += PAGE) {
-        const int out = page_of(p.table_out, p.max_pages_out, p.num_pages, b, x0 / PAGE);
-        if (tid < PAGE) src[tid] = x0 + tid < count ? p.kept[bh * p.keep + x0 + tid] : -1;
-        __syncthreads();
-        for (int t = tid; t < PAGE * L::NB; t += ROW_THREADS) {
-            const int x = t / L::NB, c = t % L::NB;
-            uint2 code = make_uint2(0, 0);
-            uint8_t sc = 0;
-            if (src[x] >= 0) {
-                const int id = page_of(p.table, p.max_pages, p.num_pages, b, src[x] / PAGE);
-                if (id >= 0) {
-                    const uint8_t* const blk = block(id);
-                    code = *reinterpret_cast<const uint2*>(blk + L::kcode(src[x] % PAGE) + c * 8);
-                    sc = blk[L::kscale(src[x] % PAGE, c)];
-                } else {
-                    atomicOr(&g_status, STATUS_BAD_PAGE);
-                }
+    const int len = length_of(p.lens, b, p.max_pages), count = min(len, p.keep);
+    if (len <= p.keep && p.table_out == p.table) return;  // (the whole cluster) nothing moves
+    const int pages = (count + PAGE - 1) / PAGE;
+    // Pages of the block in a round: rank, rank + 8, ... of the round's 32.
+    for (int r0 = 0; r0 < pages; r0 += MOVE_C * MOVE_PAGES) {
+        {
+            const int page = r0 + rank + MOVE_C * (tid / PAGE), x = page * PAGE + tid % PAGE;
+            int blk = -1, row = 0;
+            if (x < count) {
+                const int s = p.kept[bh * p.keep + x];
+                const int id = page_of(p.table, p.max_pages, p.num_pages, b, s / PAGE);
+                if (id >= 0) blk = id * p.hkv + h, row = s % PAGE;
+                else atomicOr(&g_status, STATUS_BAD_PAGE);
             }
-            *reinterpret_cast<uint2*>(buf + L::kcode(x) + c * 8) = code;
-            buf[L::kscale(x, c)] = sc;
+            src_blk[tid] = blk;
+            src_row[tid] = row;
+            if (tid % PAGE == 0) {
+                int out = -1;
+                if (page < pages) {
+                    const int id = page_of(p.table_out, p.max_pages_out, p.num_pages, b, page);
+                    if (id >= 0) out = id * p.hkv + h;
+                    else atomicOr(&g_status, STATUS_BAD_PAGE);
+                }
+                out_blk[tid / PAGE] = out;
+            }
         }
-        for (int t = tid; t < PAGE / 2 * L::NB; t += ROW_THREADS) {
-            const int j = t / L::NB, c = t % L::NB;
-            uint32_t w[4] = {0, 0, 0, 0};
+        __syncthreads();
+        auto block = [&](int i) { return p.pool + (int64_t)i * L::BYTES; };
+        // K: a quarter of a row and its scales to a thread.
+#pragma unroll 4
+        for (int i = tid; i < ROWS * 4; i += MOVE_THREADS) {
+            const int r = i / 4, t = i % 4, x = r % PAGE;
+            Chunk<D / 8> code;
+            uint16_t sc = 0;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) code.w[k] = 0;
+            if (src_blk[r] >= 0) {
+                const uint8_t* const blk = block(src_blk[r]);
+                code.load(blk + L::kcode(src_row[r]) + t * (D / 8));
+                const uint8_t* const at = blk + L::kscale(src_row[r], t * L::P);
+                sc = D == 128 ? *reinterpret_cast<const uint16_t*>(at) : *at;
+            }
+            uint8_t* const buf = smem + r / PAGE * L::BYTES;
+            code.store(buf + L::kcode(x) + t * (D / 8));
+            if (D == 128) *reinterpret_cast<uint16_t*>(buf + L::kscale(x, t * L::P)) = sc;
+            else buf[L::kscale(x, t)] = (uint8_t)sc;
+        }
+        // V: a channel block of two rows to a thread.
+#pragma unroll 4
+        for (int i = tid; i < ROWS / 2 * L::NB; i += MOVE_THREADS) {
+            const int j = i / L::NB, c = i % L::NB;
+            uint4 v[2];
+            uint8_t sc[2];
 #pragma unroll
             for (int odd = 0; odd < 2; ++odd) {
-                const int s = src[2 * j + odd];
-                uint8_t sc = 0;
-                const int id = s >= 0 ? page_of(p.table, p.max_pages, p.num_pages, b, s / PAGE) : -1;
-                if (id >= 0) {
-                    const uint8_t* const blk = block(id);
-                    const uint4 v = *reinterpret_cast<const uint4*>(blk + L::vcode(s % PAGE) + c * 16);
-                    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] |= ((s % 2 ? a[i] >> 4 : a[i]) & 0x0F0F0F0Fu) << (4 * odd);
-                    sc = blk[L::vscale(s % PAGE, c)];
+                const int r = 2 * j + odd;
+                v[odd] = make_uint4(0, 0, 0, 0);
+                sc[odd] = 0;
+                if (src_blk[r] >= 0) {
+                    const uint8_t* const blk = block(src_blk[r]);
+                    v[odd] = *reinterpret_cast<const uint4*>(blk + L::vcode(src_row[r]) + c * 16);
+                    sc[odd] = blk[L::vscale(src_row[r], c)];
                 }
-                buf[L::vscale(2 * j + odd, c)] = sc;
             }
-            *reinterpret_cast<uint4*>(buf + L::vcode(2 * j) + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            const int s0 = src_row[2 * j] % 2 * 4, s1 = src_row[2 * j + 1] % 2 * 4, x = 2 * j % PAGE;
+            auto both = [&](uint32_t a, uint32_t e) { return (a >> s0 & 0x0F0F0F0Fu) | (e >> s1 & 0x0F0F0F0Fu) << 4; };
+            uint8_t* const buf = smem + 2 * j / PAGE * L::BYTES;
+            *reinterpret_cast<uint4*>(buf + L::vcode(x) + c * 16) =
+                make_uint4(both(v[0].x, v[1].x), both(v[0].y, v[1].y), both(v[0].z, v[1].z), both(v[0].w, v[1].w));
+            *reinterpret_cast<uint16_t*>(buf + L::vscale(x, c)) = (uint16_t)(sc[0] | sc[1] << 8);
         }
-        __syncthreads();
-        if (out >= 0) {
-            uint4* const to = reinterpret_cast<uint4*>(block(out));
-            for (int t = tid; t < L::BYTES / 16; t += ROW_THREADS) to[t] = reinterpret_cast<const uint4*>(buf)[t];
-        } else if (tid == 0) {
-            atomicOr(&g_status, STATUS_BAD_PAGE);
+        cluster_sync();  // every block's rows are read
+        for (int i = tid; i < MOVE_PAGES * L::BYTES / 16; i += MOVE_THREADS) {
+            const int q = i / (L::BYTES / 16), at = i % (L::BYTES / 16);
+            if (out_blk[q] >= 0) reinterpret_cast<uint4*>(block(out_blk[q]))[at] = reinterpret_cast<const uint4*>(smem)[i];
         }
-        __syncthreads();  // the page's writes before later pages' reads, and buf's reads before its next writes
+        __syncthreads();  // out_blk and smem are free
     }
 }
 
