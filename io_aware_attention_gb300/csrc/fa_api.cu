@@ -1103,15 +1103,11 @@ fa_status fa_rope(const void* q, const int64_t* q_strides, const void* k, const 
     const int64_t units = !vec ? d / 2 : interleaved ? (d + 15) / 16 : rot / 16 + (d - rot + 15) / 16;
     const int64_t room = fa::rope::THREADS / units;
     const int64_t ny = std::min<int64_t>(N, room), nz = std::max<int64_t>(1, std::min<int64_t>(room / ny, Hq + Hk));
-    // Heads a thread walks with its angles: more spread them over more
-    // heads, fewer give more threads.
     const int64_t total = Hq + Hk, tiles = (N + ny - 1) / ny;
-    const int64_t per = std::min<int64_t>((total + nz - 1) / nz, 2 * fa::rope::U);
-    const int64_t head_tiles = (total + nz * per - 1) / (nz * per);
+    const int64_t head_tiles = (total + nz * fa::rope::U - 1) / (nz * fa::rope::U);
     if (tiles > INT32_MAX || B * head_tiles > INT32_MAX / tiles) return FA_ERR_INVALID_ARG;
     p.tiles = (int)tiles;
     p.head_tiles = (int)head_tiles;
-    p.heads_per_thread = (int)per;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const dim3 block((unsigned)units, (unsigned)ny, (unsigned)nz);
     return vec ? launch_rope<true>(p, block, B * tiles * head_tiles, st)

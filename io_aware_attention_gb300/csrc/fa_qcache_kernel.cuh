@@ -138,16 +138,16 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
 }
 
 // Two quotients x / (e4m3 * scale) as e2m1, to nearest, halves to even,
-// magnitudes above 6 to 6: `lo` in the low nibble.  inv is the reciprocal in
+// magnitudes above 6 to 6: `lo` in the low nibble.  An inv is a reciprocal in
 // fp32, which puts a quotient that is half way between two codes up to 2^-23
 // off it (bf16 inputs meet exact halves often); adding and subtracting
 // 1.5 * 2^9 rounds to a multiple of 2^-14 first, which brings those back and
 // moves no other: a quotient of an 8-bit and a 4-bit significand that is not
 // half way differs from there by 2^-10 at least.
-__device__ __forceinline__ uint32_t codes2(float lo, float hi, float inv)
+__device__ __forceinline__ uint32_t codes2(float lo, float hi, float inv_lo, float inv_hi)
 {
     constexpr float C = 768.0f;
-    const float a = __fadd_rn(__fmaf_rn(lo, inv, C), -C), b = __fadd_rn(__fmaf_rn(hi, inv, C), -C);
+    const float a = __fadd_rn(__fmaf_rn(lo, inv_lo, C), -C), b = __fadd_rn(__fmaf_rn(hi, inv_hi, C), -C);
     uint32_t r;
     asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b32 %0, {t, t, t, t};\n\t}" : "=r"(r) : "f"(b), "f"(a));
     return r & 0xFFu;
@@ -178,14 +178,20 @@ struct RowParams {
 };
 
 // The 16 channels of block b of row p (d of them exist), zeros past d or when !have.
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, int b, int d, bool have, float (&f)[16])
-{
-    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-    if (have && b * 16 < d) w0 = *reinterpret_cast<const uint4*>(p + b * 16);
-    if (have && b * 16 + 8 < d) w1 = *reinterpret_cast<const uint4*>(p + b * 16 + 8);
-    unpack8(w0, f);
-    unpack8(w1, f + 8);
-}
+struct Raw16 {
+    uint4 w0, w1;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int b, int d, bool have)
+    {
+        w0 = w1 = make_uint4(0, 0, 0, 0);
+        if (have && b * 16 < d) w0 = __ldg(reinterpret_cast<const uint4*>(p + b * 16));
+        if (have && b * 16 + 8 < d) w1 = __ldg(reinterpret_cast<const uint4*>(p + b * 16 + 8));
+    }
+    __device__ __forceinline__ void unpack(float (&f)[16]) const
+    {
+        unpack8(w0, f);
+        unpack8(w1, f + 8);
+    }
+};
 
 __device__ __forceinline__ float amax16(const float (&f)[16])
 {
@@ -234,49 +240,61 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const Row
     uint8_t* const blk = p.pool + ((int64_t)id * p.hkv + h) * L::BYTES;
     const __nv_bfloat16* const kr = p.k + b * p.ksb + h * p.ksh + (page0 * PAGE + shift) * p.ksn;
     const __nv_bfloat16* const vr = p.v + b * p.vsb + h * p.vsh + (page0 * PAGE + shift) * p.vsn;
-    for (int t = threadIdx.x; t < (x1 - x0) * L::NB; t += ROW_THREADS) {
-        const int x = x0 + t / L::NB, c = t % L::NB;
+    // A channel block of some key rows and of one pair of value rows to a
+    // thread, all its loads in flight before the first is used.
+    constexpr int STEP = ROW_THREADS / L::NB, PER = PAGE / STEP;
+    const int c = threadIdx.x % L::NB, r0 = threadIdx.x / L::NB;
+    const bool pair = r0 < PAGE / 2;
+    const bool even = pair && 2 * r0 >= x0 && 2 * r0 < x1, odd = pair && 2 * r0 + 1 >= x0 && 2 * r0 + 1 < x1;
+    Raw16 kr_[PER], vr_[2];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int x = r0 + i * STEP;
+        kr_[i].load(kr + x * p.ksn, c, p.d, x >= x0 && x < x1);
+    }
+    vr_[0].load(vr + 2 * r0 * p.vsn, c, p.d, even);
+    vr_[1].load(vr + (2 * r0 + 1) * p.vsn, c, p.d, odd);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int x = r0 + i * STEP;
+        if (x < x0 || x >= x1) continue;
         float f[16];
-        load16(kr + x * p.ksn, c, p.d, true, f);
+        kr_[i].unpack(f);
         const uint32_t sb = scale_byte(amax16(f), p.k_six);
         const float s = scale_value(sb) * p.k_scale;
         const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
         uint32_t w[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i / 4] |= codes2(f[2 * i], f[2 * i + 1], inv) << (8 * (i % 4));
+        for (int e = 0; e < 8; ++e) w[e / 4] |= codes2(f[2 * e], f[2 * e + 1], inv, inv) << (8 * (e % 4));
         *reinterpret_cast<uint2*>(blk + L::kcode(x) + c * 8) = make_uint2(w[0], w[1]);
         blk[L::kscale(x, c)] = (uint8_t)sb;
     }
-    const int j0 = x0 / 2, j1 = (x1 + 1) / 2;
-    for (int t = threadIdx.x; t < (j1 - j0) * L::NB; t += ROW_THREADS) {
-        const int j = j0 + t / L::NB, c = t % L::NB;
-        const bool even = 2 * j >= x0, odd = 2 * j + 1 < x1;
-        float f[16], g[16];
-        load16(vr + 2 * j * p.vsn, c, p.d, even, f);
-        load16(vr + (2 * j + 1) * p.vsn, c, p.d, odd, g);
-        const uint32_t sf = scale_byte(amax16(f), p.v_six), sg = scale_byte(amax16(g), p.v_six);
-        const float vf = scale_value(sf) * p.v_scale, vg = scale_value(sg) * p.v_scale;
-        const float nf = vf > 0.f ? __frcp_rn(vf) : 0.f, ng = vg > 0.f ? __frcp_rn(vg) : 0.f;
-        uint32_t w[4] = {0, 0, 0, 0};
+    if (!even && !odd) return;
+    float f[16], g[16];
+    vr_[0].unpack(f);
+    vr_[1].unpack(g);
+    const uint32_t sf = scale_byte(amax16(f), p.v_six), sg = scale_byte(amax16(g), p.v_six);
+    const float vf = scale_value(sf) * p.v_scale, vg = scale_value(sg) * p.v_scale;
+    const float nf = vf > 0.f ? __frcp_rn(vf) : 0.f, ng = vg > 0.f ? __frcp_rn(vg) : 0.f;
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {  // channels 2i, 2i + 1 of both keys
-            const uint32_t a = codes2(f[2 * i], f[2 * i + 1], nf), e = codes2(g[2 * i], g[2 * i + 1], ng);
-            const uint32_t two = (a & 15u) | ((e & 15u) << 4) | ((a >> 4) << 8) | ((e >> 4) << 12);
-            w[i / 2] |= two << (16 * (i % 2));
-        }
-        uint4* const at = reinterpret_cast<uint4*>(blk + L::vcode(2 * j) + c * 16);
-        if (!(even && odd)) {
-            const uint4 old = *at;
-            const uint32_t mine = even ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
-            w[0] = (w[0] & mine) | (old.x & ~mine);
-            w[1] = (w[1] & mine) | (old.y & ~mine);
-            w[2] = (w[2] & mine) | (old.z & ~mine);
-            w[3] = (w[3] & mine) | (old.w & ~mine);
-        }
+    for (int i = 0; i < 16; ++i)  // channel i of both keys
+        w[i / 4] |= codes2(f[i], g[i], nf, ng) << (8 * (i % 4));
+    uint4* const at = reinterpret_cast<uint4*>(blk + L::vcode(2 * r0) + c * 16);
+    if (!(even && odd)) {
+        const uint4 old = *at;
+        const uint32_t mine = even ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
+        w[0] = (w[0] & mine) | (old.x & ~mine);
+        w[1] = (w[1] & mine) | (old.y & ~mine);
+        w[2] = (w[2] & mine) | (old.z & ~mine);
+        w[3] = (w[3] & mine) | (old.w & ~mine);
         *at = make_uint4(w[0], w[1], w[2], w[3]);
-        if (even) blk[L::vscale(2 * j, c)] = (uint8_t)sf;
-        if (odd) blk[L::vscale(2 * j + 1, c)] = (uint8_t)sg;
+        if (even) blk[L::vscale(2 * r0, c)] = (uint8_t)sf;
+        else blk[L::vscale(2 * r0 + 1, c)] = (uint8_t)sg;
+        return;
     }
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint16_t*>(blk + L::vscale(2 * r0, c)) = (uint16_t)(sf | sg << 8);
 }
 
 __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float s)
@@ -1409,7 +1427,7 @@ template <int C>
 __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const EvictParams p)
 {
     constexpr int W = SEL_THREADS / 32;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     uint32_t* const held = reinterpret_cast<uint32_t*>(smem);
     __shared__ int hist[2][SEL_BINS];  // two, in turn: one is read by the cluster while the other is cleared
     __shared__ int found[2];
@@ -1568,7 +1586,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) fa_qcache_move_kernel(const Evic
     using L = Block<D>;
     constexpr int ROWS = MOVE_PAGES * PAGE;
     static_assert(ROWS == MOVE_THREADS, "a thread looks up a row");
-    extern __shared__ __align__(16) uint8_t smem[];  // MOVE_PAGES blocks
+    extern __shared__ __align__(128) uint8_t smem[];  // MOVE_PAGES blocks
     __shared__ int src_blk[ROWS], src_row[ROWS];
     __shared__ int out_blk[MOVE_PAGES];
     ptx::griddep_wait();

@@ -17,8 +17,11 @@
 //
 // The work is bound by memory: 4 bytes moved per element against 3 flops.  A
 // thread owns one unit of channels (two 16-byte vectors holding 8 whole
-// pairs) of one position, computes its 8 angles once, and walks heads with
-// them, U heads' loads in flight.  Queries and keys go in one launch.
+// pairs) of one position and U = 4 heads, whose loads are in flight while it
+// computes the 8 angles that they share.  Queries and keys go in one launch.
+// Measured at B8 H32 + 32 N4096 d128 (a forward and a gradient, 2.15 GB): 341 us,
+// 6293 GB/s, 0.93 of the measured copy bandwidth; with 8 heads a thread 353 us,
+// with 2 heads in flight 404 us (too few bytes in flight).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -48,7 +51,7 @@ struct Params {
     int64_t n;
     int d, rot, interleaved;
     int tiles;              // position tiles of a sequence
-    int head_tiles, heads_per_thread;
+    int head_tiles;         // groups of U * blockDim.z heads
     float factor;
     float sign;             // -1 turns the angle round (gradient)
 };
@@ -113,11 +116,7 @@ __global__ void __launch_bounds__(THREADS) fa_rope_kernel(const Params p)
     const int64_t i = (int64_t)(blk % p.tiles) * blockDim.y + threadIdx.y;
     const int b = blk / p.tiles;
     if (i >= p.n) return;
-    const int64_t pos = position_of(p, b, i);
     const int u = threadIdx.x;
-    const int total = p.heads[0] + p.heads[1];
-    const int h0 = ht * p.heads_per_thread * blockDim.z + threadIdx.z;
-    const int h1 = min(total, (ht + 1) * p.heads_per_thread * (int)blockDim.z);
 
     // The unit's two places (channels) and its pairs' first index; pass: not turned.
     constexpr int W = VEC ? 8 : 1;
@@ -136,6 +135,27 @@ __global__ void __launch_bounds__(THREADS) fa_rope_kernel(const Params p)
         pass_b = cb >= p.rot;
     }
     const bool have_b = cb < p.d;
+
+    // The thread's heads: where they are, and (VEC) their vectors, in flight
+    // while the angles are computed.
+    const __nv_bfloat16* src[U];
+    __nv_bfloat16* dst[U];
+    uint4 va[U], vb[U];
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+        const int h = (ht * U + e) * (int)blockDim.z + threadIdx.z;
+        src[e] = nullptr;
+        if (h >= p.heads[0] + p.heads[1]) continue;
+        const int t = h >= p.heads[0];
+        const int64_t hl = t ? h - p.heads[0] : h;
+        src[e] = p.in[t].p + b * p.in[t].sb + hl * p.in[t].sh + i * p.in[t].sn;
+        dst[e] = p.out[t].p + b * p.out[t].sb + hl * p.out[t].sh + i * p.out[t].sn;
+        if constexpr (VEC) {
+            va[e] = ld16(src[e] + ca);
+            if (have_b) vb[e] = ld16(src[e] + cb);
+        }
+    }
+    const int64_t pos = position_of(p, b, i);
     float c[W], s[W];
 #pragma unroll
     for (int e = 0; e < W; ++e) {
@@ -143,68 +163,42 @@ __global__ void __launch_bounds__(THREADS) fa_rope_kernel(const Params p)
         s[e] = 0.f;
         if (f0 + e < p.rot / 2 && !pass_a) turn(pos, p.freqs[f0 + e], p.factor, p.sign, c[e], s[e]);
     }
-    const bool split = !p.interleaved;  // pairs lie across the two places
-
-    for (int h = h0; h < h1; h += U * (int)blockDim.z) {
-        const __nv_bfloat16* src[U];
-        __nv_bfloat16* dst[U];
-        bool ok[U];
 #pragma unroll
-        for (int e = 0; e < U; ++e) {
-            const int hh = h + e * (int)blockDim.z;
-            ok[e] = hh < h1;
-            const int t = hh >= p.heads[0];
-            const int64_t hl = t ? hh - p.heads[0] : hh;
-            src[e] = p.in[t].p + b * p.in[t].sb + hl * p.in[t].sh + i * p.in[t].sn;
-            dst[e] = p.out[t].p + b * p.out[t].sb + hl * p.out[t].sh + i * p.out[t].sn;
-        }
+    for (int e = 0; e < U; ++e) {
+        if (!src[e]) continue;
         if constexpr (VEC) {
-            uint4 va[U], vb[U];
-#pragma unroll
-            for (int e = 0; e < U; ++e) {
-                if (ok[e]) va[e] = ld16(src[e] + ca);
-                if (ok[e] && have_b) vb[e] = ld16(src[e] + cb);
-            }
-#pragma unroll
-            for (int e = 0; e < U; ++e) {
-                if (!ok[e]) continue;
-                if (split) {
-                    if (!pass_a) {
-                        turn_half(va[e].x, vb[e].x, c[0], s[0], c[1], s[1]);
-                        turn_half(va[e].y, vb[e].y, c[2], s[2], c[3], s[3]);
-                        turn_half(va[e].z, vb[e].z, c[4], s[4], c[5], s[5]);
-                        turn_half(va[e].w, vb[e].w, c[6], s[6], c[7], s[7]);
-                    }
-                } else {
-                    if (!pass_a) {
-                        turn_word(va[e].x, c[0], s[0]);
-                        turn_word(va[e].y, c[1], s[1]);
-                        turn_word(va[e].z, c[2], s[2]);
-                        turn_word(va[e].w, c[3], s[3]);
-                    }
-                    if (!pass_b) {
-                        turn_word(vb[e].x, c[4], s[4]);
-                        turn_word(vb[e].y, c[5], s[5]);
-                        turn_word(vb[e].z, c[6], s[6]);
-                        turn_word(vb[e].w, c[7], s[7]);
-                    }
+            if (!p.interleaved) {  // pairs lie across the two places
+                if (!pass_a) {
+                    turn_half(va[e].x, vb[e].x, c[0], s[0], c[1], s[1]);
+                    turn_half(va[e].y, vb[e].y, c[2], s[2], c[3], s[3]);
+                    turn_half(va[e].z, vb[e].z, c[4], s[4], c[5], s[5]);
+                    turn_half(va[e].w, vb[e].w, c[6], s[6], c[7], s[7]);
                 }
-                ptx::st_global_v4(dst[e] + ca, va[e].x, va[e].y, va[e].z, va[e].w);
-                if (have_b) ptx::st_global_v4(dst[e] + cb, vb[e].x, vb[e].y, vb[e].z, vb[e].w);
+            } else {
+                if (!pass_a) {
+                    turn_word(va[e].x, c[0], s[0]);
+                    turn_word(va[e].y, c[1], s[1]);
+                    turn_word(va[e].z, c[2], s[2]);
+                    turn_word(va[e].w, c[3], s[3]);
+                }
+                if (!pass_b) {
+                    turn_word(vb[e].x, c[4], s[4]);
+                    turn_word(vb[e].y, c[5], s[5]);
+                    turn_word(vb[e].z, c[6], s[6]);
+                    turn_word(vb[e].w, c[7], s[7]);
+                }
             }
+            ptx::st_global_v4(dst[e] + ca, va[e].x, va[e].y, va[e].z, va[e].w);
+            if (have_b) ptx::st_global_v4(dst[e] + cb, vb[e].x, vb[e].y, vb[e].z, vb[e].w);
         } else {
-#pragma unroll
-            for (int e = 0; e < U; ++e) {
-                if (!ok[e]) continue;
-                const __nv_bfloat16 xa = src[e][ca], xb = src[e][cb];
-                if (pass_a) {
-                    dst[e][ca] = xa;
-                    dst[e][cb] = xb;
-                } else {
-                    const float a = __bfloat162float(xa), bb = __bfloat162float(xb);
-                    dst[e][ca] = __float2bfloat16_rn(a * c[0] - bb * s[0]);
-                    dst[e][cb] = __float2bfloat16_rn(bb * c[0] + a * s[0]);
-                }
+            const __nv_bfloat16 xa = src[e][ca], xb = src[e][cb];
+            if (pass_a) {
+                dst[e][ca] = xa;
+                dst[e][cb] = xb;
+            } else {
+                const float a = __bfloat162float(xa), bb = __bfloat162float(xb);
+                dst[e][ca] = __float2bfloat16_rn(a * c[0] - bb * s[0]);
+                dst[e][cb] = __float2bfloat16_rn(bb * c[0] + a * s[0]);
             }
         }
     }
