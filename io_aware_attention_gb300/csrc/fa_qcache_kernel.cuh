@@ -575,7 +575,7 @@ struct Rows {
     static __device__ __forceinline__ void fetch(Raw& raw, const DecParams& p, int b, int hr)
     {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const int h = hr / p.rb, r0 = (hr - h * p.rb) * (8 * NT);
+        const int h = p.rb == 1 ? hr : hr / p.rb, r0 = (hr - h * p.rb) * (8 * NT);
         const int64_t row0 = ((int64_t)b * p.hkv + h) * p.rows;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -592,7 +592,7 @@ struct Rows {
     __device__ __forceinline__ void load(const Raw& raw, const DecParams& p, int hr, int len_)
     {
         const int lane = threadIdx.x & 31, t = lane & 3;
-        const int r0 = hr % p.rb * (8 * NT);
+        const int r0 = p.rb == 1 ? 0 : hr % p.rb * (8 * NT);
         len = len_;
         min_lim = p.causal ? len - p.nq + 1 : len;
 #pragma unroll
@@ -618,7 +618,7 @@ struct Rows {
             for (int j = 0; j < 2; ++j) {
                 sc[nt][j] = __shfl_sync(0xffffffffu, down, (2 * t + j) * 4);
                 const int r = r0 + nt * 8 + 2 * t + j;
-                lim[nt][j] = p.causal && r < p.rows ? len - p.nq + r % p.nq + 1 : len;
+                lim[nt][j] = p.causal && r < p.rows ? len - p.nq + (p.nq == 1 ? 0 : r % p.nq) + 1 : len;
             }
         }
     }
@@ -826,6 +826,18 @@ struct Partial {
     static __device__ __forceinline__ int l(int row) { return R * D + R + row; }
 };
 
+// The same in shared memory, as the warps write it: pairs of channels by rows,
+// a pair's rows adjoining and one place left free, which spreads a store of
+// the lanes (8 pairs by 4 rows) over the banks.
+template <int D, int R>
+struct Piece {
+    static constexpr int FLOATS = D * (R + 1) + 2 * R;
+    // Channels D/8 g + 2c and the next.
+    static __device__ __forceinline__ int o(int g, int c, int row) { return ((c * 8 + g) * (R + 1) + row) * 2; }
+    static __device__ __forceinline__ int m(int row) { return D * (R + 1) + row; }
+    static __device__ __forceinline__ int l(int row) { return D * (R + 1) + R + row; }
+};
+
 __device__ __forceinline__ float natural_lse(float m, float l)
 {
     return l > 0.f || !(l == l) ? (m + ptx::lg2(l) - SHIFT) * LN2 : -INFINITY;
@@ -834,16 +846,16 @@ __device__ __forceinline__ float natural_lse(float m, float l)
 // Shared memory of the decode kernel: a ring of half pages for each warp, one
 // partial result for each (its first piece; its last one takes the ring's
 // place when the ring is done), and the page counts' prefix sums.
-// One block an SM.  At up to 8 rows 12 warps of 3 halves (9 KB in flight a
-// warp, 110 KB an SM, twice what the copy latency needs); at more, 8 warps,
-// since a warp's accumulators take twice the registers.
+// One block an SM, of as many warps as registers and shared memory allow: a
+// warp's chain through a page (scores, maximum, exponentials, transposes,
+// products) is long, and it takes 12 to keep the SM's pipes fed.
 template <int D, int NT>
 struct DecLayout {
-    static constexpr int WARPS = NT == 1 ? 12 : 8;
+    static constexpr int WARPS = D == 128 && NT == 2 ? 8 : 12;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int SLOTS = D == 128 ? 3 : 6;
     static constexpr int HALF = 36 * D;
-    static constexpr int PART = Partial<D, 8 * NT>::FLOATS * 4;
+    static constexpr int PART = Piece<D, 8 * NT>::FLOATS * 4;
     static constexpr int RING = SLOTS * HALF;
     static constexpr int PREFIX = WARPS * (RING + PART);
     static_assert(PART <= RING && HALF % 16 == 0 && PART % 16 == 0, "layout");
@@ -877,6 +889,7 @@ struct Feed {
     int fill, use;            // slots
     uint32_t parity;
     int flying;
+    bool due;                 // `ahead` is to be looked up
     Place now, ahead;         // this lane's unit of the current 32 and of the next
 
     __device__ __forceinline__ Place look(int x)
@@ -889,23 +902,23 @@ struct Feed {
             q.pages = u.pages;
             const int id = page_of(p.table, p.max_pages, p.num_pages, u.b, u.page);
             if (id < 0) atomicOr(&g_status, STATUS_BAD_PAGE);
-            else q.blk = id * p.hkv + u.hr / (work.hr / p.hkv);
+            else q.blk = id * p.hkv + (work.hr == p.hkv ? u.hr : u.hr / p.rb);
         }
         return q;
     }
     __device__ __forceinline__ Feed(uint8_t* ring_, uint32_t bar_, const DecParams& p_, const Work& work_, int x0, int x1_)
         : p(p_), work(work_), ring(ring_), bar(bar_), x1(x1_), base(x0), next_unit(x0), next_half(0), fill(0), use(0),
-          parity(0), flying(0)
+          parity(0), flying(0), due(false)
     {
         const int lane = threadIdx.x & 31;
         now = look(base + lane);
         ahead = Place{-1, 0, 1, -1};
+        due = x1 - base > 32;
     }
     __device__ __forceinline__ void begin()
     {
 #pragma unroll 1
         for (int i = 0; i < SLOTS; ++i) issue();
-        if (x1 - base > 32) ahead = look(base + 32 + (int)(threadIdx.x & 31));
     }
     // Starts the next copy, if one is left.
     __device__ __forceinline__ void issue()
@@ -933,7 +946,11 @@ struct Feed {
         if (x - base == 32) {
             now = ahead;
             base += 32;
-            ahead = x1 - base > 32 ? look(base + 32 + (int)(threadIdx.x & 31)) : Place{-1, 0, 1, -1};
+            due = x1 - base > 32;
+        }
+        if (due && x - base >= 4) {  // well before the copies need it, and not among a segment's first steps
+            due = false;
+            ahead = look(base + 32 + (int)(threadIdx.x & 31));
         }
         return peek(x);
     }
@@ -996,6 +1013,7 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
     using Y = DecLayout<D, NT>;
     constexpr int R = 8 * NT, WARPS = Y::WARPS, THREADS = Y::THREADS;
     using PS = Partial<D, R>;
+    using PC = Piece<D, R>;
     extern __shared__ __align__(128) uint8_t smem[];
     int* const prefix = reinterpret_cast<int*>(smem + Y::PREFIX);
     __shared__ int scratch[WARPS];
@@ -1079,10 +1097,10 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
                     const int row = nt * 8 + 2 * t + j;
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c)
-                        *reinterpret_cast<float2*>(f + PS::o(row) + g * (D / 8) + 2 * c) = make_float2(st.o[c][nt][j], st.o[c][nt][2 + j]);
+                        *reinterpret_cast<float2*>(f + PC::o(g, c, row)) = make_float2(st.o[c][nt][j], st.o[c][nt][2 + j]);
                     if (g == 0) {
-                        f[PS::m(row)] = st.m[nt][j];
-                        f[PS::l(row)] = st.l[nt][j];
+                        f[PC::m(row)] = st.m[nt][j];
+                        f[PC::l(row)] = st.l[nt][j];
                     }
                 }
             if (lane == 0) {
@@ -1142,12 +1160,12 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
         // Each row's maximum, sum and slots' weights: a warp a row, a lane a slot.
         for (int r = warp; r < R; r += WARPS) {
             const bool mine = run >> lane & 1u;
-            const float m = mine ? Y::partial(smem, lane)[PS::m(r)] : -INFINITY;
+            const float m = mine ? Y::partial(smem, lane)[PC::m(r)] : -INFINITY;
             float mx = m;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const float w = m == -INFINITY ? 0.f : ptx::ex2(m - mx);
-            float l = mine ? w * Y::partial(smem, lane)[PS::l(r)] : 0.f;
+            float l = mine ? w * Y::partial(smem, lane)[PC::l(r)] : 0.f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             if (mine) slot_weight[lane][r] = w;
@@ -1160,7 +1178,7 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
             for (uint32_t k = run; k; k &= k - 1) {
                 const int slot_ = __ffs(k) - 1;
                 const float w = slot_weight[slot_][r];
-                const float2 v = *reinterpret_cast<const float2*>(Y::partial(smem, slot_) + PS::o(r) + c);
+                const float2 v = *reinterpret_cast<const float2*>(Y::partial(smem, slot_) + PC::o(c / (D / 8), c % (D / 8) / 2, r));
                 x = fmaf(v.x, w, x);
                 y = fmaf(v.y, w, y);
             }
