@@ -1406,10 +1406,10 @@ fa_status fa_qcache_evict(void* pool, int64_t num_pages, const int32_t* table, i
     p.sink = (int)sink;
     p.recent = (int)recent;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // A cluster of 8 blocks a head where heads are long: its barriers cost more
+    // A cluster of 4 blocks a head where heads are long: its barriers cost more
     // than they save below some thousands of keys.
     const bool wide = max_pages * fa::qc::PAGE > 4096;
-    const fa_status ss = wide ? launch_qcache_select<8>(p, Hkv, B, dev, st) : launch_qcache_select<1>(p, Hkv, B, dev, st);
+    const fa_status ss = wide ? launch_qcache_select<4>(p, Hkv, B, dev, st) : launch_qcache_select<1>(p, Hkv, B, dev, st);
     if (ss != FA_OK) return ss;
     return padded_head_size(d) == 128 ? launch_qcache_move<128>(p, Hkv, B, dev, st)
                                       : launch_qcache_move<64>(p, Hkv, B, dev, st);

@@ -868,11 +868,6 @@ struct DecLayout {
     }
 };
 
-// A unit as a warp needs it.
-struct Place {
-    int seg, page, pages, blk;  // blk: the page's block in the pool, -1: no such page
-};
-
 // A warp's copies of its run of pages into its ring.  SLOTS halves (K, then V;
 // or K alone) are in flight; the warp waits for one, reads it and refills its
 // slot.  The places of 32 units are looked up at once, one a lane, the next
@@ -890,29 +885,30 @@ struct Feed {
     uint32_t parity;
     int flying;
     bool due;                 // `ahead` is to be looked up
-    Place now, ahead;         // this lane's unit of the current 32 and of the next
+    // This lane's unit of the current 32 and of the next: its segment, and the
+    // page's block in the pool (-1 where the table's entry is none of its pages).
+    int now_seg, now_blk, ahead_seg, ahead_blk;
+    int first_page;           // of the run's first unit (a later unit's page follows from its segment's first)
+    const uint8_t* src;       // the block that is being copied
 
-    __device__ __forceinline__ Place look(int x)
+    __device__ __forceinline__ int look(int x, int& seg, int& blk) const
     {
-        Place q{-1, 0, 1, -1};
-        if (x < x1) {
-            const Work::Unit u = work.at(x);
-            q.seg = u.b * work.hr + u.hr;
-            q.page = u.page;
-            q.pages = u.pages;
-            const int id = page_of(p.table, p.max_pages, p.num_pages, u.b, u.page);
-            if (id < 0) atomicOr(&g_status, STATUS_BAD_PAGE);
-            else q.blk = id * p.hkv + (work.hr == p.hkv ? u.hr : u.hr / p.rb);
-        }
-        return q;
+        seg = blk = -1;
+        if (x >= x1) return 0;
+        const Work::Unit u = work.at(x);
+        seg = u.b * work.hr + u.hr;
+        const int id = page_of(p.table, p.max_pages, p.num_pages, u.b, u.page);
+        if (id < 0) atomicOr(&g_status, STATUS_BAD_PAGE);
+        else blk = id * p.hkv + (work.hr == p.hkv ? u.hr : u.hr / p.rb);
+        return u.page;
     }
     __device__ __forceinline__ Feed(uint8_t* ring_, uint32_t bar_, const DecParams& p_, const Work& work_, int x0, int x1_)
         : p(p_), work(work_), ring(ring_), bar(bar_), x1(x1_), base(x0), next_unit(x0), next_half(0), fill(0), use(0),
-          parity(0), flying(0), due(false)
+          parity(0), flying(0), src(nullptr)
     {
         const int lane = threadIdx.x & 31;
-        now = look(base + lane);
-        ahead = Place{-1, 0, 1, -1};
+        first_page = __shfl_sync(0xffffffffu, look(base + lane, now_seg, now_blk), 0);
+        ahead_seg = ahead_blk = -1;
         due = x1 - base > 32;
     }
     __device__ __forceinline__ void begin()
@@ -925,14 +921,15 @@ struct Feed {
     {
         if (next_unit >= x1) return;
         const int i = next_unit - base;
-        const int a = __shfl_sync(0xffffffffu, now.blk, i & 31), b = __shfl_sync(0xffffffffu, ahead.blk, i & 31);
-        const int blk = max(0, i < 32 ? a : b);  // a page that does not exist: any block, not used
+        if (next_half == 0) {
+            const int blk = i < 32 ? __shfl_sync(0xffffffffu, now_blk, i) : __shfl_sync(0xffffffffu, ahead_blk, i - 32);
+            src = p.pool + (int64_t)max(0, blk) * Block<D>::BYTES;  // a page that does not exist: any block, not used
+        }
         const int lane = threadIdx.x & 31;
         if (lane == 0) {
             ptx::mbar_arrive_expect_tx(bar + 8 * fill, HALF);
             if (!(p.debug_skip == i && base == 0 && blockIdx.x == 0))
-                ptx::bulk_load(ptx::smem_addr(ring) + fill * HALF,
-                               p.pool + (int64_t)blk * Block<D>::BYTES + (WITH_V ? next_half * HALF : 0), HALF, bar + 8 * fill);
+                ptx::bulk_load(ptx::smem_addr(ring) + fill * HALF, src + (WITH_V ? next_half * HALF : 0), HALF, bar + 8 * fill);
         }
         fill = fill + 1 == SLOTS ? 0 : fill + 1;
         ++flying;
@@ -941,34 +938,21 @@ struct Feed {
             ++next_unit;
         }
     }
-    __device__ __forceinline__ Place place(int x)
+    // The segment of unit x, the units in turn; `there`: its page exists.
+    __device__ __forceinline__ int place(int x, bool& there)
     {
         if (x - base == 32) {
-            now = ahead;
+            now_seg = ahead_seg;
+            now_blk = ahead_blk;
             base += 32;
             due = x1 - base > 32;
         }
-        if (due && x - base >= 4) {  // well before the copies need it, and not among a segment's first steps
+        if (due && x - base >= 4) {  // well before the copies need it, and not among a run's first steps
             due = false;
-            ahead = look(base + 32 + (int)(threadIdx.x & 31));
+            look(base + 32 + (int)(threadIdx.x & 31), ahead_seg, ahead_blk);
         }
-        return peek(x);
-    }
-    // The place of unit x, at most one 32 ahead of the last that place() gave.
-    __device__ __forceinline__ Place peek(int x) const
-    {
-        const int i = x - base;
-        if (i >= 32) return given(ahead, i - 32);
-        return given(now, i);
-    }
-    static __device__ __forceinline__ Place given(const Place& of, int i)
-    {
-        Place q;
-        q.seg = __shfl_sync(0xffffffffu, of.seg, i);
-        q.page = __shfl_sync(0xffffffffu, of.page, i);
-        q.pages = __shfl_sync(0xffffffffu, of.pages, i);
-        q.blk = __shfl_sync(0xffffffffu, of.blk, i);
-        return q;
+        there = __shfl_sync(0xffffffffu, now_blk, x - base) >= 0;
+        return __shfl_sync(0xffffffffu, now_seg, x - base);
     }
     // The oldest half in flight, or null when the wait gave up.
     __device__ __forceinline__ const uint8_t* wait(volatile uint32_t* abort_flag)
@@ -1062,10 +1046,10 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
         const int x0 = lo + (int)((int64_t)(hi - lo) * warp / nw), x1 = lo + (int)((int64_t)(hi - lo) * (warp + 1) / nw);
         Rows<D, NT> rows;
         State<D, NT> st;
-        int seg = -1, begins = 0, last_page = 0, seg_pages = 0;
+        int seg = -1, begins = 0, page = 0;
         auto finish = [&] {
             st.close(rows);
-            const int ends = last_page == seg_pages - 1;
+            const int ends = (page + 1) * PAGE >= rows.len;
             if (begins && ends) {
                 const int b = seg / work.hr, hr = seg - b * work.hr, h = hr / p.rb;
                 const int r0 = (hr - h * p.rb) * R;
@@ -1113,29 +1097,34 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
         Feed<D, Y::SLOTS, true> feed(smem + Y::ring(warp), ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
         typename Rows<D, NT>::Raw raw;
         for (int x = x0; x < x1; ++x) {
-            const Place u = feed.place(x);
-            if (u.seg != seg) {
-                const int b = u.seg / work.hr, hr = u.seg - b * work.hr;
+            bool there;
+            const int next_seg = feed.place(x, there);
+            ++page;
+            if (next_seg != seg) {
+                const int b = next_seg / work.hr, hr = next_seg - b * work.hr;
                 rows.fetch(raw, p, b, hr);
-                if (seg >= 0) finish();
-                else feed.begin();
-                seg = u.seg;
-                begins = u.page == 0;
-                seg_pages = u.pages;
+                if (seg >= 0) {
+                    --page;
+                    finish();
+                } else {
+                    feed.begin();
+                }
+                page = seg < 0 ? feed.first_page : 0;
+                seg = next_seg;
+                begins = page == 0;
                 rows.load(raw, p, hr, length_of(p.lens, b, p.max_pages));
                 st.clear();
             }
-            last_page = u.page;
             float s[4][NT][4];
             uint32_t pb[4][NT][2];
             const uint8_t* blk = feed.wait(abort_flag);
             if (!blk) break;
             page_scores<D, NT>(blk, rows, s);
             feed.next();
-            if (u.blk >= 0) st.add_scores(s, rows, u.page, pb);
+            if (there) st.add_scores(s, rows, page, pb);
             blk = feed.wait(abort_flag);
             if (!blk) break;
-            if (u.blk >= 0) st.add_values(blk, rows, u.page, pb);
+            if (there) st.add_values(blk, rows, page, pb);
             feed.next();
         }
         feed.drain(abort_flag);
@@ -1312,76 +1301,97 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
     if (me >= G) return;
     const int x0 = (int)((int64_t)me * T / G), x1 = (int)((int64_t)(me + 1) * T / G);
     Rows<D, NT> rows;
-    float off[NT][2];
-    int have = -1;  // segment (with row block) whose rows are loaded
+    uint64_t off[NT], sc[NT];  // of the lane's two columns: scores' factors, and -lse in base 2
+    int have = -1;             // segment (with row block) whose rows are loaded
     Feed<D, Y::SLOTS, false> feed(smem + warp * Y::RING, ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
     feed.begin();
     typename Rows<D, NT>::Raw raw;
-    // The weights that a lane adds to, of the unit after the current one: keys 16t + g and 16t + 8 + g of its page.
-    auto weights_at = [&](const Place& u) { return (int64_t)u.seg * p.w_len + (int64_t)u.page * PAGE; };
-    float w_next[2] = {};
-    auto fetch_weights = [&](const Place& u) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k = 16 * t + 8 * i + g;
-            w_next[i] = (int64_t)u.page * PAGE + k < p.w_len ? p.w_in[weights_at(u) + k] : 0.f;
-        }
+    bool there;
+    int seg = feed.place(x0, there), page = feed.first_page;
+    // A lane's part of the weights: keys 16t + g and 16t + 8 + g of a page,
+    // fetched while the page before is worked on.
+    auto weights_at = [&](int seg_, int page_) { return (int64_t)seg_ * p.w_len + page_ * PAGE + 16 * t + g; };
+    float w_next[2] = {0.f, 0.f};
+    auto fetch_weights = [&](int seg_, int page_) {
+        const float* const w = p.w_in + weights_at(seg_, page_);
+        const int64_t left = p.w_len - (page_ * PAGE + 16 * t + g);
+        if (left > 0) w_next[0] = w[0];
+        if (left > 8) w_next[1] = w[8];
     };
-    Place u = feed.place(x0);
-    fetch_weights(u);
+    fetch_weights(seg, page);
     for (int x = x0; x < x1; ++x) {
         const float w_now[2] = {w_next[0], w_next[1]};
-        const Place after = x + 1 < x1 ? feed.peek(x + 1) : u;
-        if (x + 1 < x1) fetch_weights(after);
-        const int b = u.seg / p.hkv, h = u.seg - b * p.hkv;
+        bool there_next = false;
+        int seg_next = seg, page_next = page;
+        if (x + 1 < x1) {
+            seg_next = feed.place(x + 1, there_next);
+            page_next = seg_next == seg ? page + 1 : 0;
+            fetch_weights(seg_next, page_next);
+        }
         const uint8_t* const blk = feed.wait(abort_flag);
         if (!blk) break;
         float sum[8] = {};
         for (int rbi = 0; rbi < p.rb; ++rbi) {
-            const int seg = u.seg * p.rb + rbi;
-            if (seg != have) {
-                have = seg;
-                rows.fetch(raw, p, b, h * p.rb + rbi);
-                rows.load(raw, p, h * p.rb + rbi, length_of(p.lens, b, p.max_pages));
-                const int64_t row0 = (int64_t)u.seg * p.rows;
+            if (seg * p.rb + rbi != have) {
+                have = seg * p.rb + rbi;
+                const int b = seg / p.hkv, hr = (seg - b * p.hkv) * p.rb + rbi;
+                rows.fetch(raw, p, b, hr);
+                rows.load(raw, p, hr, length_of(p.lens, b, p.max_pages));
+                const float* const lse = p.lse_in + (int64_t)seg * p.rows;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    float e[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int r = rbi * 8 * NT + nt * 8 + 2 * t + j;
-                        const float e = r < p.rows ? p.lse_in[row0 + r] : -INFINITY;
-                        // A row that saw nothing (or is none) gives nothing.
-                        off[nt][j] = e == -INFINITY ? -INFINITY : -e * 1.4426950408889634f;
+                        // A row that saw nothing (or is none) gives nothing: 2^-inf.
+                        const float v = r < p.rows ? lse[r] : -INFINITY;
+                        e[j] = v == -INFINITY ? v : -v * 1.4426950408889634f;
                     }
+                    off[nt] = ptx::f2_pack(e[0], e[1]);
+                    sc[nt] = ptx::f2_pack(rows.sc[nt][0], rows.sc[nt][1]);
+                }
             }
-            if (u.blk < 0) continue;
+            if (!there) continue;
             float s[4][NT][4];
             page_scores<D, NT>(blk, rows, s);
+            const bool whole = (page + 1) * PAGE <= rows.min_lim;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int key = u.page * PAGE + 16 * r + 8 * half + g;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            if (key < rows.lim[nt][j] && off[nt][j] != -INFINITY)
-                                sum[2 * r + half] += ptx::ex2(fmaf(s[r][nt][2 * half + j], rows.sc[nt][j], off[nt][j]));
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float x0_, x1_;
+                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[r][nt][2 * half], s[r][nt][2 * half + 1]), sc[nt], off[nt]), x0_, x1_);
+                        if (!whole) {
+                            const int key = page * PAGE + 16 * r + 8 * half + g;
+                            if (key >= rows.lim[nt][0]) x0_ = -INFINITY;
+                            if (key >= rows.lim[nt][1]) x1_ = -INFINITY;
+                        }
+                        sum[2 * r + half] += ptx::ex2(x0_) + ptx::ex2(x1_);
+                    }
                 }
         }
         feed.next();
+        // Sums over the four lanes that share a key's columns, each lane ending
+        // with the two keys it writes: half of the keys change hands, then half
+        // of those left.
+        const bool up2 = t & 2, up1 = t & 1;
+        float four[4], two[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
-            sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
-        }
+        for (int e = 0; e < 4; ++e)
+            four[e] = (up2 ? sum[4 + e] : sum[e]) + __shfl_xor_sync(0xffffffffu, up2 ? sum[e] : sum[4 + e], 2);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int k = 8 * e + g, key = u.page * PAGE + k;
-            if (e / 2 == t && key < rows.len && key < p.w_len) p.w_out[weights_at(u) + k] = w_now[e % 2] + sum[e];
-        }
-        if (x + 1 < x1) u = feed.place(x + 1);
+        for (int e = 0; e < 2; ++e)
+            two[e] = (up1 ? four[2 + e] : four[e]) + __shfl_xor_sync(0xffffffffu, up1 ? four[e] : four[2 + e], 1);
+        float* const w = p.w_out + weights_at(seg, page);
+        const int64_t left = min((int64_t)rows.len, p.w_len) - (page * PAGE + 16 * t + g);
+        if (left > 0) w[0] = w_now[0] + two[0];
+        if (left > 8) w[8] = w_now[1] + two[1];
+        seg = seg_next;
+        page = page_next;
+        there = there_next;
     }
     feed.drain(abort_flag);
 }
@@ -1426,7 +1436,7 @@ __device__ __forceinline__ int cluster_read(const int* mine, int rank)
 constexpr int SEL_THREADS = 512;
 constexpr int SEL_BINS = 256;
 // Weights that a block keeps in shared memory over its passes (the rest are
-// read again): a cluster of 8 holds 65536 of a head.  49 KB a block, so that 4 fit an SM.
+// read again): a cluster of 4 holds 32768 of a head.  49 KB a block, so that 4 fit an SM.
 constexpr int SEL_HELD = 8192;
 constexpr int SEL_SMEM = SEL_HELD * 4;
 
@@ -1435,8 +1445,8 @@ constexpr int SEL_SMEM = SEL_HELD * 4;
 // the lowest places), found by radix selection: four histograms of 8 bits of
 // order_of, largest digit first, give the smallest weight that stays and how
 // many of that weight do.  (Digits of 11 bits need a pass less, but a block
-// then reads 16384 counts of the others a pass: 109 us against 32 for 64 heads
-// of 32768 keys.)  A cluster of C blocks shares a kv
+// then reads 8 times as many counts of the others: 109 us against 32 for 64
+// heads of 32768 keys in clusters of 8; clusters of 4 take 27, of 2 take 32.)  A cluster of C blocks shares a kv
 // head of a sequence, each block a run of the places and each warp a run of
 // its block's; the histograms and the counts before a block's run are read
 // from the other blocks' shared memory, so the result does not depend on
