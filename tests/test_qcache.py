@@ -523,3 +523,111 @@ def test_evict_with_narrow_weights_and_refusals():
             fa.qcache_evict(*cache, w, **kw)
     with pytest.raises(fa.FaError):  # no room for the kept keys
         fa.qcache_evict(*cache, w, 150, table_out=torch.zeros((1, 1), dtype=torch.int32, device="cuda"))
+
+
+# ------------------------------------------------------------ sizes and failures
+
+@gpu
+def test_offsets_beyond_32_bits():
+    """Pages whose bytes lie past 4 GB in the pool: append, read, decode, weights and eviction find them."""
+    d, Hkv, pages, n = 128, 1, 480000, 200
+    pool = torch.empty((pages, Hkv, 9216), dtype=torch.uint8, device="cuda")
+    assert pool.numel() > 2 ** 32
+    table = torch.tensor([[pages - 1, 5, pages - 2, 233017], [pages - 3, 466034, 7, pages - 4]], dtype=torch.int32)
+    lens = torch.tensor([n, n + 50], dtype=torch.int32)
+    k, v = rand((2, Hkv, n, d), 1), rand((2, Hkv, n, d), 2)
+    low = torch.empty((8, Hkv, 9216), dtype=torch.uint8, device="cuda")  # the same keys in a small pool
+    low_table = torch.arange(8, dtype=torch.int32).reshape(2, 4)
+    q = rand((2, 4, 1, d), 3).cuda()
+    out = []
+    for p, t in ((pool, table), (low, low_table)):
+        p[t.flatten().long().cuda()] = 0
+        td, ld = dev(t, lens)
+        fa.qcache_append(*dev(k, v), p, td, ld)
+        o, lse = fa.qcache_decode(q, p, td, ld)
+        w = fa.qcache_weights(q, lse, p, td, ld, torch.zeros((2, Hkv, 256), device="cuda"))
+        kept, new, w2 = fa.qcache_evict(p, td, ld, w, 90, sink=2, recent=10)
+        out.append([o, lse, w, kept, new, w2, *fa.qcache_read(p, td, new, 90, d)])
+    torch.cuda.synchronize()
+    assert fa.check_device_status() == 0
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    assert (out[0][3] >= 0).all() and torch.isfinite(out[0][1]).all()
+
+
+@gpu
+@pytest.mark.parametrize("B", [33, 257, 2048])
+def test_many_sequences(B):
+    """Batches past a warp, a block and up to the limit, with empty sequences among them; one more is refused."""
+    d, Hkv, H = 64, 1, 2
+    g = np.random.default_rng(B)
+    lens = [int(x) for x in g.integers(0, 130, B)]
+    lens[0], lens[-1] = 0, 129
+    cache = ref.make_cache(lens, Hkv, d, seed=B)
+    q = rand((B, H, 1, d), B)
+    o, lse = fa.qcache_decode(q.cuda(), *dev(*cache), scale=0.2)
+    check_attention(o, lse, q, cache, False, 0.2, f"B{B}")
+    w = fa.qcache_weights(q.cuda(), lse, *dev(*cache), torch.zeros((B, Hkv, 130), device="cuda"), scale=0.2)
+    rows = torch.tensor([H if n else 0 for n in lens], dtype=torch.float64)
+    assert ((w.double().sum(-1)[:, 0].cpu() - rows).abs() <= 1e-4).all()
+    if B == 2048:
+        more = torch.zeros((B + 1, 3), dtype=torch.int32, device="cuda")
+        with pytest.raises(fa.FaError):
+            fa.qcache_decode(rand((B + 1, H, 1, d), 1).cuda(), cache[0].cuda(), more, more[:, 0].contiguous())
+
+
+@gpu
+@pytest.mark.parametrize("call", ["decode", "weights"])
+def test_a_wait_that_runs_out_is_reported_and_recoverable(call):
+    """A copy that is never made (test hook): the wait gives up after its limit, the status says so, and the
+    next call is right.  No fault, trap or hang is involved."""
+    d, lens = 128, [1000, 200]
+    cache = ref.make_cache(lens, 2, d, seed=3)
+    q = rand((2, 4, 1, d), 1)
+    dc = dev(*cache)
+    o, lse = fa.qcache_decode(q.cuda(), *dc)
+    zero = torch.zeros((2, 2, 1000), device="cuda")
+    w = fa.qcache_weights(q.cuda(), lse, *dc, zero)
+    assert fa.check_device_status() == 0
+    fa.set_wait_limit_ns(20_000_000)  # 20 ms
+    fa.debug_skip_k_tile(0)
+    try:
+        if call == "decode":
+            fa.qcache_decode(q.cuda(), *dc)
+        else:
+            fa.qcache_weights(q.cuda(), lse, *dc, zero)
+        torch.cuda.synchronize()
+        assert fa.check_device_status() == 4  # FA_ERR_TIMEOUT
+    finally:
+        fa.debug_skip_k_tile(-1)
+        fa.set_wait_limit_ns(0)
+    assert fa.check_device_status() == 0
+    o2, lse2 = fa.qcache_decode(q.cuda(), *dc)
+    w2 = fa.qcache_weights(q.cuda(), lse, *dc, zero)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(w, w2)
+    check_attention(o2, lse2, q, cache, False, 1 / math.sqrt(d))
+
+
+@gpu
+def test_results_do_not_depend_on_timing():
+    d = 128
+    lens = [5000, 17, 0, 900, 2500]
+    cache = dev(*ref.make_cache(lens, 2, d, seed=9))
+    q = rand((5, 16, 1, d), 2).cuda()
+    first = None
+    for _ in range(10):
+        o, lse = fa.qcache_decode(q, *cache)
+        w = fa.qcache_weights(q, lse, *cache, torch.zeros((5, 2, 5000), device="cuda"))
+        kept, new, w2 = fa.qcache_evict(cache[0].clone(), cache[1], cache[2], w, 300, sink=1, recent=9)
+        if first is None:
+            first = (o, lse, w, kept, new, w2)
+        assert all(torch.equal(a, b) for a, b in zip(first, (o, lse, w, kept, new, w2)))
+
+
+@gpu
+def test_evict_longer_heads_than_shared_memory_holds():
+    """A head whose weights are read again in each pass, with many equal ones around the border."""
+    n = 50000
+    g = torch.Generator().manual_seed(1)
+    w = torch.randint(0, 40, (1, 1, n), generator=g).float() * 0.25
+    check_evict([n], 1, 64, 20000, 3, 100, w, True)
