@@ -1423,6 +1423,9 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same in two halves, ordering no memory: for leaving shared memory that others read.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 // Reads an int of block `rank`'s shared memory.
 __device__ __forceinline__ int cluster_read(const int* mine, int rank)
 {
@@ -1465,6 +1468,7 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = C > 1 ? blockIdx.x % C : 0, h = blockIdx.x / C, b = blockIdx.y;
     for (int e = tid; e < 2 * SEL_BINS; e += SEL_THREADS) (&hist[0][0])[e] = 0;
+    if (tid < 2) counts[tid] = 0;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int64_t bh = (int64_t)b * p.hkv + h;
@@ -1474,26 +1478,31 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
     float* const wo = p.w_out + bh * p.w_len;
     int32_t* const kept = p.kept + bh * p.keep;
     auto weight = [&](int x) { return x < p.w_len ? w[x] : 0.f; };
-    auto put = [&](int at, int x) {
+    auto put = [&](int at, int x, float v) {
         kept[at] = x;
-        if (at < p.w_len) wo[at] = weight(x);
+        if (at < p.w_len) wo[at] = v;
+    };
+    // The weight that order_of made u of (NaN and the zeros, whose bits it does not keep, are read again).
+    auto weight_of = [&](uint32_t u, int x) {
+        return u == 0u || u == 0x80000000u ? weight(x) : __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
     };
     const int all = C * SEL_THREADS, me = rank * SEL_THREADS + tid;
     if (h == 0 && me == 0) {
         p.lens_out[b] = count;
         if (p.lens[b] > p.max_pages * (int64_t)PAGE) atomicOr(&g_status, STATUS_BAD_PAGE);
     }
-    for (int64_t e = count + me; e < p.w_len; e += all) wo[e] = 0.f;
-    for (int e = count + me; e < p.keep; e += all) kept[e] = -1;
-    if (len <= p.keep) {
-        for (int e = me; e < len; e += all) put(e, e);
-        return;
-    }
+    const bool cut = len > p.keep;
     const int first = p.sink, last = len - p.recent;  // the choice lies between
-    for (int e = me; e < p.sink; e += all) put(e, e);
-    for (int e = me; e < p.recent; e += all) put(p.keep - p.recent + e, last + e);
     int need = p.keep - p.sink - p.recent;
-    if (need == 0) return;  // (the whole cluster)
+    // What needs no choice, written last: a barrier would wait for the stores.
+    auto rest = [&] {
+        for (int64_t e = count + me; e < p.w_len; e += all) wo[e] = 0.f;
+        for (int e = count + me; e < p.keep; e += all) kept[e] = -1;
+        for (int e = me; e < (cut ? p.sink : len); e += all) put(e, e, weight(e));
+        if (!cut) return;
+        for (int e = me; e < p.recent; e += all) put(p.keep - p.recent + e, last + e, weight(last + e));
+    };
+    if (cut && need > 0) {  // (the whole cluster)
 
     // This block's run of places, and each of its threads' view of their order.
     const int n = last - first;
@@ -1514,11 +1523,12 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
         int* const mine = hist[pass & 1];
-#pragma unroll 4
-        for (int e = tid; e < size; e += SEL_THREADS) {
-            const uint32_t u = order(e);
+        auto add = [&](uint32_t u) {
             if ((u & mask) == prefix) atomicAdd(&mine[u >> shift & 255u], 1);
-        }
+        };
+#pragma unroll 4
+        for (int e = tid; e < min(size, SEL_HELD); e += SEL_THREADS) add(held[e]);
+        for (int e = SEL_HELD + tid; e < size; e += SEL_THREADS) add(order_of(weight(lo + e)));
         if constexpr (C > 1) cluster_sync();
         else __syncthreads();
         // A pair of threads a digit, from the largest down, half of the blocks each.
@@ -1567,13 +1577,12 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
     }
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) warp_gt[warp] = gt, warp_eq[warp] = eq;
-    __syncthreads();
-    if (tid < 2) {
-        int v = 0;
-        for (int k = 0; k < W; ++k) v += tid ? warp_eq[k] : warp_gt[k];
-        counts[tid] = v;
+    if (lane == 0) {
+        warp_gt[warp] = gt, warp_eq[warp] = eq;
+        atomicAdd(&counts[0], gt);
+        atomicAdd(&counts[1], eq);
     }
+    __syncthreads();
     int base = 0, base_eq = 0;
     if constexpr (C > 1) {
         cluster_sync();
@@ -1593,11 +1602,16 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
         const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me_ = __ballot_sync(0xffffffffu, is_eq);
         const uint32_t below = (1u << lane) - 1u;
         const int ng = base + __popc(mg & below), ne = base_eq + __popc(me_ & below);
-        if (is_gt || (is_eq && ne < need)) put(p.sink + ng + min(ne, need), lo + e);
+        if (is_gt || (is_eq && ne < need)) put(p.sink + ng + min(ne, need), lo + e, weight_of(u, lo + e));
         base += __popc(mg);
         base_eq += __popc(me_);
     }
-    if constexpr (C > 1) cluster_sync();  // no block leaves while its shared memory may be read
+    if constexpr (C > 1) cluster_arrive_relaxed();
+    }
+    rest();
+    if constexpr (C > 1) {  // no block leaves while its shared memory may be read
+        if (cut && p.keep - p.sink - p.recent > 0) cluster_wait();
+    }
 }
 
 // Moves the kept rows to the front.  A cluster of MOVE_C blocks shares a kv
