@@ -698,13 +698,14 @@ cudaError_t launch_clusters(void (*kernel)(KParams...), dim3 grid, dim3 block, s
 }
 
 template <int C>
-fa_status launch_qcache_select(const fa::qc::EvictParams& p, int64_t Hkv, int64_t B, int dev, cudaStream_t st)
+fa_status launch_qcache_select(fa::qc::EvictParams p, int64_t Hkv, int64_t B, int dev, cudaStream_t st)
 {
     static std::atomic<int> done[MAX_DEVICES];
-    const fa_status as = allow_smem(fa::qc::fa_qcache_select_kernel<C>, (size_t)fa::qc::SEL_SMEM, done, dev);
+    const fa_status as = allow_smem(fa::qc::fa_qcache_select_kernel<C>, (size_t)fa::qc::SEL_HELD_MOST * 4, done, dev);
     if (as != FA_OK) return as;
+    p.held = (int)std::min<int64_t>(((int64_t)p.max_pages * fa::qc::PAGE + C - 1) / C, fa::qc::SEL_HELD_MOST);
     return launch_clusters(fa::qc::fa_qcache_select_kernel<C>, dim3((unsigned)(Hkv * C), (unsigned)B),
-                           dim3(fa::qc::SEL_THREADS), (size_t)fa::qc::SEL_SMEM, C, st, p) == cudaSuccess
+                           dim3(fa::qc::SEL_THREADS), (size_t)p.held * 4, C, st, p) == cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
 }
@@ -716,8 +717,8 @@ fa_status launch_qcache_move(const fa::qc::EvictParams& p, int64_t Hkv, int64_t 
     constexpr size_t bytes = (size_t)fa::qc::MOVE_PAGES * fa::qc::Block<D>::BYTES;
     const fa_status as = allow_smem(fa::qc::fa_qcache_move_kernel<D>, bytes, done, dev);
     if (as != FA_OK) return as;
-    return launch_clusters(fa::qc::fa_qcache_move_kernel<D>, dim3((unsigned)(Hkv * fa::qc::MOVE_C), (unsigned)B),
-                           dim3(fa::qc::MOVE_THREADS), bytes, fa::qc::MOVE_C, st, p) == cudaSuccess
+    return launch_clusters(fa::qc::fa_qcache_move_kernel<D>, dim3((unsigned)(Hkv * p.move_blocks), (unsigned)B),
+                           dim3(fa::qc::MOVE_THREADS), bytes, p.move_blocks, st, p) == cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
 }
@@ -1406,11 +1407,22 @@ fa_status fa_qcache_evict(void* pool, int64_t num_pages, const int32_t* table, i
     p.sink = (int)sink;
     p.recent = (int)recent;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // A cluster of 4 blocks a head where heads are long: its barriers cost more
-    // than they save below some thousands of keys.
-    const bool wide = max_pages * fa::qc::PAGE > 4096;
+    // A cluster of 4 blocks a head pays where heads are long and few; one block
+    // a head where they fill the SMs anyway.  Whole call in us, cluster against
+    // one block, cutting 64-channel heads back to 64 keys: 8 heads of 2048 keys
+    // 10.4 / 9.2, of 8192 11.5 / 13.8; 64 heads of 8192 20.5 / 16.4, of 32768
+    // 30.0 / 35.4; 256 heads of 16384 51.8 / 33.6, of 65536 112 / 330.
+    const int64_t heads = B * Hkv, most = max_pages * fa::qc::PAGE;
+    const bool wide = most > (heads * 4 <= info.sms ? 4096 : heads <= info.sms ? 16384 : 32768);
     const fa_status ss = wide ? launch_qcache_select<4>(p, Hkv, B, dev, st) : launch_qcache_select<1>(p, Hkv, B, dev, st);
     if (ss != FA_OK) return ss;
+    // Blocks of a head's move: one for each kept page, at most 8, and where there
+    // are heads enough one for every 4 pages.
+    const int64_t pages = std::min(need, max_pages);
+    int blocks = 1;
+    while (blocks < 8 && blocks < pages) blocks *= 2;
+    while (blocks > 1 && heads * blocks > 4 * info.sms && blocks / 2 * fa::qc::MOVE_PAGES >= pages) blocks /= 2;
+    p.move_blocks = blocks;
     return padded_head_size(d) == 128 ? launch_qcache_move<128>(p, Hkv, B, dev, st)
                                       : launch_qcache_move<64>(p, Hkv, B, dev, st);
 }

@@ -1407,6 +1407,8 @@ struct EvictParams {
     int64_t w_len;
     int hkv, max_pages, max_pages_out, num_pages;
     int keep, sink, recent;
+    int held;            // weights a block of the selection keeps in shared memory
+    int move_blocks;     // blocks of a head's move (a cluster)
 };
 
 // Floats in the order of their values as unsigned integers: equal values
@@ -1438,10 +1440,9 @@ __device__ __forceinline__ int cluster_read(const int* mine, int rank)
 
 constexpr int SEL_THREADS = 512;
 constexpr int SEL_BINS = 256;
-// Weights that a block keeps in shared memory over its passes (the rest are
-// read again): a cluster of 4 holds 32768 of a head.  49 KB a block, so that 4 fit an SM.
-constexpr int SEL_HELD = 8192;
-constexpr int SEL_SMEM = SEL_HELD * 4;
+// Weights that a block keeps in shared memory over its passes, at most (the
+// rest are read again).
+constexpr int SEL_HELD_MOST = 32768;
 
 // Chooses the keys that stay: the first `sink`, the last `recent`, and of those
 // between the keep - sink - recent with the largest weights (of equal weights
@@ -1507,14 +1508,14 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
     // This block's run of places, and each of its threads' view of their order.
     const int n = last - first;
     const int lo = first + (int)((int64_t)n * rank / C), hi = first + (int)((int64_t)n * (rank + 1) / C), size = hi - lo;
-    auto order = [&](int e) { return e < SEL_HELD ? held[e] : order_of(weight(lo + e)); };
-    for (int e0 = tid; e0 < min(size, SEL_HELD); e0 += 8 * SEL_THREADS) {
+    auto order = [&](int e) { return e < p.held ? held[e] : order_of(weight(lo + e)); };
+    for (int e0 = tid; e0 < min(size, p.held); e0 += 8 * SEL_THREADS) {
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = e0 + i * SEL_THREADS < size ? weight(lo + e0 + i * SEL_THREADS) : 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (e0 + i * SEL_THREADS < min(size, SEL_HELD)) held[e0 + i * SEL_THREADS] = order_of(x[i]);
+            if (e0 + i * SEL_THREADS < min(size, p.held)) held[e0 + i * SEL_THREADS] = order_of(x[i]);
     }
     __syncthreads();
 
@@ -1527,8 +1528,8 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
             if ((u & mask) == prefix) atomicAdd(&mine[u >> shift & 255u], 1);
         };
 #pragma unroll 4
-        for (int e = tid; e < min(size, SEL_HELD); e += SEL_THREADS) add(held[e]);
-        for (int e = SEL_HELD + tid; e < size; e += SEL_THREADS) add(order_of(weight(lo + e)));
+        for (int e = tid; e < min(size, p.held); e += SEL_THREADS) add(held[e]);
+        for (int e = p.held + tid; e < size; e += SEL_THREADS) add(order_of(weight(lo + e)));
         if constexpr (C > 1) cluster_sync();
         else __syncthreads();
         // A pair of threads a digit, from the largest down, half of the blocks each.
@@ -1614,13 +1615,13 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
     }
 }
 
-// Moves the kept rows to the front.  A cluster of MOVE_C blocks shares a kv
+// Moves the kept rows to the front.  A cluster of up to 8 blocks shares a kv
 // head of a sequence; in a round each block gathers up to MOVE_PAGES pages of
 // the destination into shared memory, the cluster meets, and all write.  The
 // destination's pages may be the sequence's own: row j comes from place
 // kept[j] >= j, so what a round writes no later round reads, and what it
 // overwrites has been read by then (its own and earlier rounds' rows).
-constexpr int MOVE_C = 8, MOVE_PAGES = 4, MOVE_THREADS = 256;
+constexpr int MOVE_PAGES = 4, MOVE_THREADS = 256;
 
 template <int D>
 __global__ void __launch_bounds__(MOVE_THREADS) fa_qcache_move_kernel(const EvictParams p)
@@ -1633,15 +1634,15 @@ __global__ void __launch_bounds__(MOVE_THREADS) fa_qcache_move_kernel(const Evic
     __shared__ int out_blk[MOVE_PAGES];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int rank = blockIdx.x % MOVE_C, h = blockIdx.x / MOVE_C, b = blockIdx.y, tid = threadIdx.x;
+    const int blocks = p.move_blocks, rank = blockIdx.x % blocks, h = blockIdx.x / blocks, b = blockIdx.y, tid = threadIdx.x;
     const int64_t bh = (int64_t)b * p.hkv + h;
     const int len = length_of(p.lens, b, p.max_pages), count = min(len, p.keep);
     if (len <= p.keep && p.table_out == p.table) return;  // (the whole cluster) nothing moves
     const int pages = (count + PAGE - 1) / PAGE;
-    // Pages of the block in a round: rank, rank + 8, ... of the round's 32.
-    for (int r0 = 0; r0 < pages; r0 += MOVE_C * MOVE_PAGES) {
+    // Pages of the block in a round: rank, rank + blocks, ... of the round's.
+    for (int r0 = 0; r0 < pages; r0 += blocks * MOVE_PAGES) {
         {
-            const int page = r0 + rank + MOVE_C * (tid / PAGE), x = page * PAGE + tid % PAGE;
+            const int page = r0 + rank + blocks * (tid / PAGE), x = page * PAGE + tid % PAGE;
             int blk = -1, row = 0;
             if (x < count) {
                 const int s = p.kept[bh * p.keep + x];
