@@ -1096,6 +1096,7 @@ fa_status fa_rope(const void* q, const int64_t* q_strides, const void* k, const 
     p.d = (int)d;
     p.rot = (int)rot;
     p.interleaved = interleaved;
+    p.stream = (double)B * (double)(Hq + Hk) * (double)N * (double)d * 2.0 > (double)info.l2;
     p.factor = factor;
     p.sign = inverse ? -1.0f : 1.0f;
     // Whole 16-byte vectors turn together when the halves (or the end of the

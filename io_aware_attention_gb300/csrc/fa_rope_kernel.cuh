@@ -12,16 +12,18 @@
 // 2^-64 of a turn), so t * f_i modulo one turn is the low 64 bits of one
 // integer product: no reduction, and no position is too far (an fp32 product
 // t * f_i is off by 0.03 rad at t = 10^6).  The top 32 bits, read as a signed
-// fraction of half a turn, go to sincospif: the angle is then within 2^-32 of
-// a turn plus the fraction's rounding to fp32 (2^-24 relative).
+// fraction of half a turn, become the angle: within 2^-32 of a turn, and
+// 2^-24 of itself by its rounding to fp32.
 //
 // The work is bound by memory: 4 bytes moved per element against 3 flops.  A
 // thread owns one unit of channels (two 16-byte vectors holding 8 whole
 // pairs) of one position and U = 4 heads, whose loads are in flight while it
 // computes the 8 angles that they share.  Queries and keys go in one launch.
-// Measured at B8 H32 + 32 N4096 d128 (a forward and a gradient, 2.15 GB): 341 us,
-// 6293 GB/s, 0.93 of the measured copy bandwidth; with 8 heads a thread 353 us,
-// with 2 heads in flight 404 us (too few bytes in flight).
+// Measured at B8 H32 + 32 N4096 d128 (a forward and a gradient, 2.15 GB): 318 us,
+// 6758 GB/s, 1.00 of the measured copy bandwidth.  What brought it there: 4
+// blocks an SM instead of 3 (349 -> 328 us; 5 spill, 409 us) and, for results
+// larger than L2, streaming stores (328 -> 318 us); with 2 heads in flight 404
+// us, with the angles computed before the loads 383 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -52,6 +54,7 @@ struct Params {
     int d, rot, interleaved;
     int tiles;              // position tiles of a sequence
     int head_tiles;         // groups of U * blockDim.z heads
+    int stream;
     float factor;
     float sign;             // -1 turns the angle round (gradient)
 };
@@ -65,13 +68,16 @@ __device__ __forceinline__ int64_t position_of(const Params& p, int b, int64_t i
     return (p.lens ? (int64_t)p.lens[b] - p.n : 0) + i;
 }
 
-// cos and sin of the angle of one pair.
+// cos and sin of the angle of one pair.  The special-function unit's are good to
+// 2^-21 on [-pi, pi], far inside the result's rounding to bf16, and 8 pairs take
+// a tenth of the instructions that sincospif does (which were 4 in 10 of the
+// kernel's).
 __device__ __forceinline__ void turn(int64_t pos, uint64_t freq, float factor, float sign, float& c, float& s)
 {
     const uint64_t a = (uint64_t)pos * freq;
-    sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &s, &c);
-    c *= factor;
-    s *= factor * sign;
+    const float x = (float)(int32_t)(a >> 32) * (0x1p-31f * 3.14159265358979f);
+    c = __cosf(x) * factor;
+    s = __sinf(x) * (factor * sign);
 }
 
 __device__ __forceinline__ uint4 ld16(const __nv_bfloat16* p)
@@ -83,15 +89,28 @@ __device__ __forceinline__ uint4 ld16(const __nv_bfloat16* p)
     return r;
 }
 
+// stream: the results are larger than L2 and will not be found there by the next reader.
+__device__ __forceinline__ void st16(__nv_bfloat16* p, const uint4& v, int stream)
+{
+    if (stream)
+        asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    else
+        ptx::st_global_v4(p, v.x, v.y, v.z, v.w);
+}
+
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Pairs split over two words: word a holds two pairs' first channels, b their second ones.
-__device__ __forceinline__ void turn_half(uint32_t& a, uint32_t& b, float c0, float s0, float c1, float s1)
+// Pairs split over two words: word a holds two pairs' first channels, b their
+// second ones; c, s: the two pairs' cosines and sines.
+__device__ __forceinline__ void turn_half(uint32_t& a, uint32_t& b, uint64_t c, uint64_t s, uint64_t minus_s)
 {
-    const float a0 = lo(a), a1 = hi(a), b0 = lo(b), b1 = hi(b);
-    a = ptx::pack_bf16x2(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
-    b = ptx::pack_bf16x2(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
+    const uint64_t x = ptx::f2_pack(lo(a), hi(a)), y = ptx::f2_pack(lo(b), hi(b));
+    float u, v;
+    ptx::f2_unpack(ptx::f2_fma(y, minus_s, ptx::f2_mul(x, c)), u, v);
+    a = ptx::pack_bf16x2(u, v);
+    ptx::f2_unpack(ptx::f2_fma(x, s, ptx::f2_mul(y, c)), u, v);
+    b = ptx::pack_bf16x2(u, v);
 }
 
 // A pair within one word.
@@ -106,7 +125,7 @@ __device__ __forceinline__ void turn_word(uint32_t& w, float c, float s)
 // pair, in 2-byte accesses: odd rotated sizes and strides.
 // Block (units, positions, head lanes).
 template <bool VEC>
-__global__ void __launch_bounds__(THREADS) fa_rope_kernel(const Params p)
+__global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
 {
     ptx::griddep_wait();  // a programmatic dependent: the inputs are complete
     ptx::griddep_launch_dependents();
@@ -169,10 +188,13 @@ __global__ void __launch_bounds__(THREADS) fa_rope_kernel(const Params p)
         if constexpr (VEC) {
             if (!p.interleaved) {  // pairs lie across the two places
                 if (!pass_a) {
-                    turn_half(va[e].x, vb[e].x, c[0], s[0], c[1], s[1]);
-                    turn_half(va[e].y, vb[e].y, c[2], s[2], c[3], s[3]);
-                    turn_half(va[e].z, vb[e].z, c[4], s[4], c[5], s[5]);
-                    turn_half(va[e].w, vb[e].w, c[6], s[6], c[7], s[7]);
+                    auto two = [&](uint32_t& x, uint32_t& y, int k) {
+                        turn_half(x, y, ptx::f2_pack(c[k], c[k + 1]), ptx::f2_pack(s[k], s[k + 1]), ptx::f2_pack(-s[k], -s[k + 1]));
+                    };
+                    two(va[e].x, vb[e].x, 0);
+                    two(va[e].y, vb[e].y, 2);
+                    two(va[e].z, vb[e].z, 4);
+                    two(va[e].w, vb[e].w, 6);
                 }
             } else {
                 if (!pass_a) {
@@ -188,8 +210,8 @@ __global__ void __launch_bounds__(THREADS) fa_rope_kernel(const Params p)
                     turn_word(vb[e].w, c[7], s[7]);
                 }
             }
-            ptx::st_global_v4(dst[e] + ca, va[e].x, va[e].y, va[e].z, va[e].w);
-            if (have_b) ptx::st_global_v4(dst[e] + cb, vb[e].x, vb[e].y, vb[e].z, vb[e].w);
+            st16(dst[e] + ca, va[e], p.stream);
+            if (have_b) st16(dst[e] + cb, vb[e], p.stream);
         } else {
             const __nv_bfloat16 xa = src[e][ca], xb = src[e][cb];
             if (pass_a) {

@@ -1,10 +1,10 @@
 """Rotary positions (fa_rope) and their gradient against the formula in 64 bits.
 
 Tolerance: results are rounded to bf16 once (2^-8 of the result), and before
-that carry fp32 errors: two products and a sum of terms |a cos| and |b sin|,
-cosine and sine good to 2^-22, a fraction of a half turn rounded to 24 bits
-(2^-24 half turns, so 2^-22 in the angle): together below 2^-20 of
-factor * (|a| + |b|).
+that carry fp32 errors: cosine and sine good to 2^-21.1 (what CUDA documents for
+__sinf and __cosf on [-pi, pi]), an angle of at most pi rounded twice to 24 bits
+(2 pi 2^-25 = 2^-22.3), and the roundings of two products and a sum (3 * 2^-24 =
+2^-22.4): 0.45 + 0.20 + 0.18 = 0.83 of 2^-20 times factor * (|a| + |b|).
 """
 import math
 
