@@ -1664,48 +1664,63 @@ __global__ void __launch_bounds__(MOVE_THREADS) fa_qcache_move_kernel(const Evic
         }
         __syncthreads();
         auto block = [&](int i) { return p.pool + (int64_t)i * L::BYTES; };
+        // All of a thread's loads before its first store.
         // K: a quarter of a row and its scales to a thread.
-#pragma unroll 4
-        for (int i = tid; i < ROWS * 4; i += MOVE_THREADS) {
-            const int r = i / 4, t = i % 4, x = r % PAGE;
-            Chunk<D / 8> code;
-            uint16_t sc = 0;
+        constexpr int NK = ROWS * 4 / MOVE_THREADS, NV = ROWS / 2 * L::NB / MOVE_THREADS;
+        {
+            Chunk<D / 8> code[NK];
+            uint16_t sc[NK];
+            const int t = tid % 4;
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) code.w[k] = 0;
-            if (src_blk[r] >= 0) {
-                const uint8_t* const blk = block(src_blk[r]);
-                code.load(blk + L::kcode(src_row[r]) + t * (D / 8));
-                const uint8_t* const at = blk + L::kscale(src_row[r], t * L::P);
-                sc = D == 128 ? *reinterpret_cast<const uint16_t*>(at) : *at;
-            }
-            uint8_t* const buf = smem + r / PAGE * L::BYTES;
-            code.store(buf + L::kcode(x) + t * (D / 8));
-            if (D == 128) *reinterpret_cast<uint16_t*>(buf + L::kscale(x, t * L::P)) = sc;
-            else buf[L::kscale(x, t)] = (uint8_t)sc;
-        }
-        // V: a channel block of two rows to a thread.
-#pragma unroll 4
-        for (int i = tid; i < ROWS / 2 * L::NB; i += MOVE_THREADS) {
-            const int j = i / L::NB, c = i % L::NB;
-            uint4 v[2];
-            uint8_t sc[2];
+            for (int i = 0; i < NK; ++i) {
+                const int r = (i * MOVE_THREADS + tid) / 4, from = src_blk[r], x = src_row[r];
+                sc[i] = 0;
 #pragma unroll
-            for (int odd = 0; odd < 2; ++odd) {
-                const int r = 2 * j + odd;
-                v[odd] = make_uint4(0, 0, 0, 0);
-                sc[odd] = 0;
-                if (src_blk[r] >= 0) {
-                    const uint8_t* const blk = block(src_blk[r]);
-                    v[odd] = *reinterpret_cast<const uint4*>(blk + L::vcode(src_row[r]) + c * 16);
-                    sc[odd] = blk[L::vscale(src_row[r], c)];
+                for (int k = 0; k < D / 32; ++k) code[i].w[k] = 0;
+                if (from >= 0) {
+                    const uint8_t* const blk = block(from);
+                    code[i].load(blk + L::kcode(x) + t * (D / 8));
+                    const uint8_t* const at = blk + L::kscale(x, t * L::P);
+                    sc[i] = D == 128 ? *reinterpret_cast<const uint16_t*>(at) : *at;
                 }
             }
-            const int s0 = src_row[2 * j] % 2 * 4, s1 = src_row[2 * j + 1] % 2 * 4, x = 2 * j % PAGE;
-            auto both = [&](uint32_t a, uint32_t e) { return (a >> s0 & 0x0F0F0F0Fu) | (e >> s1 & 0x0F0F0F0Fu) << 4; };
-            uint8_t* const buf = smem + 2 * j / PAGE * L::BYTES;
-            *reinterpret_cast<uint4*>(buf + L::vcode(x) + c * 16) =
-                make_uint4(both(v[0].x, v[1].x), both(v[0].y, v[1].y), both(v[0].z, v[1].z), both(v[0].w, v[1].w));
-            *reinterpret_cast<uint16_t*>(buf + L::vscale(x, c)) = (uint16_t)(sc[0] | sc[1] << 8);
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                const int r = (i * MOVE_THREADS + tid) / 4, x = r % PAGE;
+                uint8_t* const buf = smem + r / PAGE * L::BYTES;
+                code[i].store(buf + L::kcode(x) + t * (D / 8));
+                if (D == 128) *reinterpret_cast<uint16_t*>(buf + L::kscale(x, t * L::P)) = sc[i];
+                else buf[L::kscale(x, t)] = (uint8_t)sc[i];
+            }
+        }
+        // V: a channel block of two rows to a thread.
+        {
+            uint4 v[NV][2];
+            uint8_t sc[NV][2];
+            const int c = tid % L::NB;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int odd = 0; odd < 2; ++odd) {
+                    const int r = 2 * ((i * MOVE_THREADS + tid) / L::NB) + odd, from = src_blk[r], x = src_row[r];
+                    v[i][odd] = make_uint4(0, 0, 0, 0);
+                    sc[i][odd] = 0;
+                    if (from >= 0) {
+                        const uint8_t* const blk = block(from);
+                        v[i][odd] = *reinterpret_cast<const uint4*>(blk + L::vcode(x) + c * 16);
+                        sc[i][odd] = blk[L::vscale(x, c)];
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int r = 2 * ((i * MOVE_THREADS + tid) / L::NB), x = r % PAGE;
+                const int s0 = src_row[r] % 2 * 4, s1 = src_row[r + 1] % 2 * 4;
+                auto both = [&](uint32_t a, uint32_t e) { return (a >> s0 & 0x0F0F0F0Fu) | (e >> s1 & 0x0F0F0F0Fu) << 4; };
+                const uint4 &a = v[i][0], &e = v[i][1];
+                uint8_t* const buf = smem + r / PAGE * L::BYTES;
+                *reinterpret_cast<uint4*>(buf + L::vcode(x) + c * 16) = make_uint4(both(a.x, e.x), both(a.y, e.y), both(a.z, e.z), both(a.w, e.w));
+                *reinterpret_cast<uint16_t*>(buf + L::vscale(x, c)) = (uint16_t)(sc[i][0] | sc[i][1] << 8);
+            }
         }
         cluster_sync();  // every block's rows are read
         for (int i = tid; i < MOVE_PAGES * L::BYTES / 16; i += MOVE_THREADS) {
