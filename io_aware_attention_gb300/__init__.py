@@ -560,8 +560,8 @@ def rope(q, k, freqs, positions=None, lens=None, layout: str = "half", factor: f
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return rope(q, k, freqs, positions, lens, layout, factor, inverse, stream)
-    q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+    q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    k_out = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
     return _rope_call(q, k, q_out, k_out, freqs, positions, lens, layout, factor, inverse, stream, sizes)
 
 
@@ -637,7 +637,7 @@ def qcache_read(pool, table, lens, n: int, d: int, newest: bool = False, k_scale
         with torch.cuda.device(dev):
             return qcache_read(pool, table, lens, n, d, newest, k_scale, v_scale, stream)
     k = torch.empty((B, Hkv, n, d), dtype=torch.bfloat16, device=pool.device)
-    v = torch.empty((B, Hkv, n, d), dtype=torch.bfloat16, device=pool.device)
+    v = torch.empty_like(k)
     rc = library().fa_qcache_read(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
                                   k.data_ptr(), v.data_ptr(), B, Hkv, n, d, bool(newest), k_scale, v_scale,
                                   _stream_handle(stream, dev))
@@ -740,10 +740,12 @@ def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, sca
         with torch.cuda.device(dev):
             return qcache_weights(q, lse, pool, table, lens, weights, causal, scale, k_scale, out, stream)
     B, H, Nq, d = q.shape
-    _check_out("lse", lse, (B, H, Nq), torch.float32, q.device)
+    if not _fast_ok(dev, (B, H, Nq), torch.float32, lse):
+        _check_out("lse", lse, (B, H, Nq), torch.float32, q.device)
     if weights.dim() != 3:
         raise ValueError("weights must be (B, Hkv, W)")
-    _check_out("weights", weights, (B, Hkv, weights.shape[2]), torch.float32, q.device)
+    if not _fast_ok(dev, (B, Hkv, weights.shape[2]), torch.float32, weights):
+        _check_out("weights", weights, (B, Hkv, weights.shape[2]), torch.float32, q.device)
     if out is not None:
         _check_out("out", out, weights.shape, torch.float32, q.device)
     else:
@@ -775,7 +777,8 @@ def qcache_evict(pool, table, lens, weights, keep: int, sink: int = 0, recent: i
             return qcache_evict(pool, table, lens, weights, keep, sink, recent, table_out, stream)
     if weights.dim() != 3:
         raise ValueError("weights must be (B, Hkv, W)")
-    _check_out("weights", weights, (B, Hkv, weights.shape[2]), torch.float32, pool.device)
+    if not _fast_ok(dev, (B, Hkv, weights.shape[2]), torch.float32, weights):
+        _check_out("weights", weights, (B, Hkv, weights.shape[2]), torch.float32, pool.device)
     if table_out is None:
         table_out = table
     elif table_out.dim() != 2 or table_out.shape[0] != B:

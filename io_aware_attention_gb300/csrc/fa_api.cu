@@ -656,8 +656,8 @@ fa_status launch_qcache_decode(const fa::qc::DecParams& p, int64_t blocks, int d
     if (as != FA_OK) return as;
     if (launch_pdl(fa::qc::fa_qcache_decode_kernel<D, NT>, dim3((unsigned)blocks), dim3(Y::THREADS),
                    (size_t)Y::bytes(p.B), st, p) != cudaSuccess ||
-        launch_pdl(fa::qc::fa_qcache_combine_kernel<D, NT>, dim3((unsigned)blocks, 8 * NT), dim3(256), 0, st, p) !=
-            cudaSuccess)
+        launch_pdl(fa::qc::fa_qcache_combine_kernel<D, NT>,
+                   dim3((unsigned)blocks, (unsigned)std::min(p.rows, 8 * NT)), dim3(256), 0, st, p) != cudaSuccess)
         return FA_ERR_CUDA;
     return FA_OK;
 }
