@@ -7,7 +7,8 @@
 // against bf16's 2, and decode, bound by reading the cache, can run 3.6 times
 // as fast.  The product e2m1 * e4m3 has at most 6 significant bits and lies
 // between 2^-10 and 2688, so it is exact in fp16: the tensor cores' operands
-// are the stored values, not roundings of them.
+// are the stored values, not roundings of them.  (Measured: 2.9 times the bf16
+// cache's speed at 8 x 32 heads x 32768 keys.)
 //
 // A page holds PAGE = 64 keys of one kv head in one block of 72 * D bytes,
 // D = 64 or 128 stored channels (smaller head sizes are padded with zeros).
@@ -216,6 +217,10 @@ constexpr int ROW_THREADS = 256;
 // position are padding and go nowhere.  A byte of V holds two keys: where
 // only one of them is new, the other nibble is kept.  One block writes all
 // of a page's new rows, so no two blocks share a byte.
+//
+// Bound by memory for prompts (4d bytes read and 9d/8 written a key), by its
+// launch for single keys.  Appending and reading back 4 x 8 heads x up to 4096
+// keys at d = 128: 25.5 us, about half of it here; 64 x 8 heads x 1 key: 6.2 us.
 template <int D>
 __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const RowParams p)
 {
@@ -320,7 +325,9 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&w)[8], bo
 // once: the stored value times the tensor's scale); rows where no key is are
 // zero.  Block (tile of 64 rows, kv head, sequence): the rows' pages are looked
 // up once, then a thread takes a channel block of some rows with all its loads
-// in flight before the first is used.
+// in flight before the first is used.  Bound by memory: 64 heads x 4096 rows at
+// d = 128 (38 MB read, 134 MB written) in 26 us, 6.6 TB/s; row by row, each
+// load waited for, it took 38.
 template <int D>
 __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_read_kernel(const RowParams p)
 {
@@ -991,6 +998,14 @@ struct Feed {
 // pieces of others go to shared memory, where the block joins neighbouring
 // warps' pieces of a segment; pieces of segments that cross blocks go to the
 // workspace (two a block at most) for the combine kernel.
+//
+// Bound by reading the cache: 8 x 32 heads x 32768 keys at d = 128 (1.21 GB) in
+// 207 us with the combine kernel, 5819 GB/s, 0.86 of the measured copy
+// bandwidth; the same attention over a bf16 cache takes 590 us.  In the loop a
+// page (9216 bytes) takes an SM 430 cycles where the copy bandwidth alone gives
+// about 400; the conversions (280 a page, 2 a clock) need 140 of them, the fp16
+// multiplies 128 and the products 128, on pipes of their own.  The rest is the
+// start (lengths, page table, query rows: 8 us) and the join.
 template <int D, int NT>
 __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode_kernel(const DecParams p)
 {
@@ -1253,7 +1268,12 @@ __global__ void __launch_bounds__(256) fa_qcache_combine_kernel(const DecParams 
 
 // w_out[key] = w_in[key] + sum over the rows of the key's kv head of
 // exp(scale q.k - lse): the attention weight that the rows gave each key,
-// from the logsumexps that decode returned.  Only K is read.
+// from the logsumexps that decode returned.  Only K is read.  Two blocks of 8
+// warps an SM, a page a warp as in decode, but every unit is a page of a kv head
+// with all its query rows, so a key's sum is one warp's and needs no atomics.
+// 8 x 8 heads x 30000 to 32768 keys, 8 rows each, d = 128 (161 MB): 36.9 us, 0.65
+// of the measured copy bandwidth; 5 us are the start, the rest is bound by
+// instructions (about 700 a page with the warp's start spread over 13 pages).
 template <int D>
 struct WeightLayout {
     static constexpr int WARPS = 8, THREADS = WARPS * 32;
@@ -1448,13 +1468,15 @@ constexpr int SEL_HELD_MOST = 32768;
 // between the keep - sink - recent with the largest weights (of equal weights
 // the lowest places), found by radix selection: four histograms of 8 bits of
 // order_of, largest digit first, give the smallest weight that stays and how
-// many of that weight do.  (Digits of 11 bits need a pass less, but a block
-// then reads 8 times as many counts of the others: 109 us against 32 for 64
-// heads of 32768 keys in clusters of 8; clusters of 4 take 27, of 2 take 32.)  A cluster of C blocks shares a kv
-// head of a sequence, each block a run of the places and each warp a run of
-// its block's; the histograms and the counts before a block's run are read
-// from the other blocks' shared memory, so the result does not depend on
-// timing.
+// many of that weight do.  A cluster of C blocks shares a kv head of a
+// sequence, each block a run of the places and each warp a run of its block's;
+// the histograms and the counts before a block's run are read from the other
+// blocks' shared memory, so the result does not depend on timing.
+//
+// Bound by latency: a pass is a sweep over the block's weights, a cluster
+// barrier and a look at 256 counts, about 2.5 us.  64 heads of 32768 keys: 22 us
+// in clusters of 4 (of 8 and of 2, 5 us more).  Three digits of 11 bits need a
+// pass less but 8 times as many counts of the other blocks: 109 us.
 template <int C>
 __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const EvictParams p)
 {
@@ -1504,110 +1526,109 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
         for (int e = me; e < p.recent; e += all) put(p.keep - p.recent + e, last + e, weight(last + e));
     };
     if (cut && need > 0) {  // (the whole cluster)
-
-    // This block's run of places, and each of its threads' view of their order.
-    const int n = last - first;
-    const int lo = first + (int)((int64_t)n * rank / C), hi = first + (int)((int64_t)n * (rank + 1) / C), size = hi - lo;
-    auto order = [&](int e) { return e < p.held ? held[e] : order_of(weight(lo + e)); };
-    for (int e0 = tid; e0 < min(size, p.held); e0 += 8 * SEL_THREADS) {
-        float x[8];
+        // This block's run of places, and each of its threads' view of their order.
+        const int n = last - first;
+        const int lo = first + (int)((int64_t)n * rank / C), hi = first + (int)((int64_t)n * (rank + 1) / C), size = hi - lo;
+        auto order = [&](int e) { return e < p.held ? held[e] : order_of(weight(lo + e)); };
+        for (int e0 = tid; e0 < min(size, p.held); e0 += 8 * SEL_THREADS) {
+            float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = e0 + i * SEL_THREADS < size ? weight(lo + e0 + i * SEL_THREADS) : 0.f;
+            for (int i = 0; i < 8; ++i) x[i] = e0 + i * SEL_THREADS < size ? weight(lo + e0 + i * SEL_THREADS) : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (e0 + i * SEL_THREADS < min(size, p.held)) held[e0 + i * SEL_THREADS] = order_of(x[i]);
-    }
-    __syncthreads();
+            for (int i = 0; i < 8; ++i)
+                if (e0 + i * SEL_THREADS < min(size, p.held)) held[e0 + i * SEL_THREADS] = order_of(x[i]);
+        }
+        __syncthreads();
 
-    uint32_t prefix = 0, mask = 0;
+        uint32_t prefix = 0, mask = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        int* const mine = hist[pass & 1];
-        auto add = [&](uint32_t u) {
-            if ((u & mask) == prefix) atomicAdd(&mine[u >> shift & 255u], 1);
-        };
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            int* const mine = hist[pass & 1];
+            auto add = [&](uint32_t u) {
+                if ((u & mask) == prefix) atomicAdd(&mine[u >> shift & 255u], 1);
+            };
 #pragma unroll 4
-        for (int e = tid; e < min(size, p.held); e += SEL_THREADS) add(held[e]);
-        for (int e = p.held + tid; e < size; e += SEL_THREADS) add(order_of(weight(lo + e)));
-        if constexpr (C > 1) cluster_sync();
-        else __syncthreads();
-        // A pair of threads a digit, from the largest down, half of the blocks each.
-        const int digit = 255 - tid / 2;
-        int c = 0;
+            for (int e = tid; e < min(size, p.held); e += SEL_THREADS) add(held[e]);
+            for (int e = p.held + tid; e < size; e += SEL_THREADS) add(order_of(weight(lo + e)));
+            if constexpr (C > 1) cluster_sync();
+            else __syncthreads();
+            // A pair of threads a digit, from the largest down, half of the blocks each.
+            const int digit = 255 - tid / 2;
+            int c = 0;
+            if constexpr (C > 1) {
+#pragma unroll
+                for (int k = 0; k < C / 2; ++k) c += cluster_read(&mine[digit], tid % 2 * (C / 2) + k);
+            } else {
+                c = tid % 2 ? 0 : mine[digit];
+            }
+            c += __shfl_xor_sync(0xffffffffu, c, 1);
+            int upto = tid % 2 ? 0 : c;  // sums over the digits, each once
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            if (lane == 31) sums[warp] = upto;
+            __syncthreads();
+            int before = 0;
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+                if (k < warp) before += sums[k];
+            const int above = before + upto - c;
+            if (tid % 2 == 0 && above < need && need <= above + c) {
+                found[0] = digit;
+                found[1] = need - above;
+            }
+            // The other histogram is read by no block any more: all have passed this pass's cluster barrier.
+            for (int e = tid; e < SEL_BINS; e += SEL_THREADS) hist[~pass & 1][e] = 0;
+            __syncthreads();
+            prefix |= (uint32_t)found[0] << shift;
+            mask |= 255u << shift;
+            need = found[1];
+        }
+        // Everything above `prefix` stays, and the first `need` equal to it.  Each
+        // warp counts its run, then places it.
+        const int wlo = (int)((int64_t)size * warp / W), whi = (int)((int64_t)size * (warp + 1) / W);
+        int gt = 0, eq = 0;
+#pragma unroll 4
+        for (int e = wlo + lane; e < whi; e += 32) {
+            const uint32_t u = order(e);
+            gt += u > prefix;
+            eq += u == prefix;
+        }
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        eq = __reduce_add_sync(0xffffffffu, eq);
+        if (lane == 0) {
+            warp_gt[warp] = gt, warp_eq[warp] = eq;
+            atomicAdd(&counts[0], gt);
+            atomicAdd(&counts[1], eq);
+        }
+        __syncthreads();
+        int base = 0, base_eq = 0;
         if constexpr (C > 1) {
-#pragma unroll
-            for (int k = 0; k < C / 2; ++k) c += cluster_read(&mine[digit], tid % 2 * (C / 2) + k);
-        } else {
-            c = tid % 2 ? 0 : mine[digit];
+            cluster_sync();
+            for (int k = 0; k < rank; ++k) {
+                base += cluster_read(&counts[0], k);
+                base_eq += cluster_read(&counts[1], k);
+            }
         }
-        c += __shfl_xor_sync(0xffffffffu, c, 1);
-        int upto = tid % 2 ? 0 : c;  // sums over the digits, each once
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
+        for (int k = 0; k < warp; ++k) {
+            base += warp_gt[k];
+            base_eq += warp_eq[k];
         }
-        if (lane == 31) sums[warp] = upto;
-        __syncthreads();
-        int before = 0;
-#pragma unroll
-        for (int k = 0; k < W; ++k)
-            if (k < warp) before += sums[k];
-        const int above = before + upto - c;
-        if (tid % 2 == 0 && above < need && need <= above + c) {
-            found[0] = digit;
-            found[1] = need - above;
+        for (int e0 = wlo; e0 < whi; e0 += 32) {
+            const int e = e0 + lane;
+            const uint32_t u = e < whi ? order(e) : 0u;
+            const bool is_gt = e < whi && u > prefix, is_eq = e < whi && u == prefix;
+            const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me_ = __ballot_sync(0xffffffffu, is_eq);
+            const uint32_t below = (1u << lane) - 1u;
+            const int ng = base + __popc(mg & below), ne = base_eq + __popc(me_ & below);
+            if (is_gt || (is_eq && ne < need)) put(p.sink + ng + min(ne, need), lo + e, weight_of(u, lo + e));
+            base += __popc(mg);
+            base_eq += __popc(me_);
         }
-        // The other histogram is read by no block any more: all have passed this pass's cluster barrier.
-        for (int e = tid; e < SEL_BINS; e += SEL_THREADS) hist[~pass & 1][e] = 0;
-        __syncthreads();
-        prefix |= (uint32_t)found[0] << shift;
-        mask |= 255u << shift;
-        need = found[1];
-    }
-    // Everything above `prefix` stays, and the first `need` equal to it.  Each
-    // warp counts its run, then places it.
-    const int wlo = (int)((int64_t)size * warp / W), whi = (int)((int64_t)size * (warp + 1) / W);
-    int gt = 0, eq = 0;
-#pragma unroll 4
-    for (int e = wlo + lane; e < whi; e += 32) {
-        const uint32_t u = order(e);
-        gt += u > prefix;
-        eq += u == prefix;
-    }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) {
-        warp_gt[warp] = gt, warp_eq[warp] = eq;
-        atomicAdd(&counts[0], gt);
-        atomicAdd(&counts[1], eq);
-    }
-    __syncthreads();
-    int base = 0, base_eq = 0;
-    if constexpr (C > 1) {
-        cluster_sync();
-        for (int k = 0; k < rank; ++k) {
-            base += cluster_read(&counts[0], k);
-            base_eq += cluster_read(&counts[1], k);
-        }
-    }
-    for (int k = 0; k < warp; ++k) {
-        base += warp_gt[k];
-        base_eq += warp_eq[k];
-    }
-    for (int e0 = wlo; e0 < whi; e0 += 32) {
-        const int e = e0 + lane;
-        const uint32_t u = e < whi ? order(e) : 0u;
-        const bool is_gt = e < whi && u > prefix, is_eq = e < whi && u == prefix;
-        const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me_ = __ballot_sync(0xffffffffu, is_eq);
-        const uint32_t below = (1u << lane) - 1u;
-        const int ng = base + __popc(mg & below), ne = base_eq + __popc(me_ & below);
-        if (is_gt || (is_eq && ne < need)) put(p.sink + ng + min(ne, need), lo + e, weight_of(u, lo + e));
-        base += __popc(mg);
-        base_eq += __popc(me_);
-    }
-    if constexpr (C > 1) cluster_arrive_relaxed();
+        if constexpr (C > 1) cluster_arrive_relaxed();
     }
     rest();
     if constexpr (C > 1) {  // no block leaves while its shared memory may be read
@@ -1621,6 +1642,8 @@ __global__ void __launch_bounds__(SEL_THREADS) fa_qcache_select_kernel(const Evi
 // destination's pages may be the sequence's own: row j comes from place
 // kept[j] >= j, so what a round writes no later round reads, and what it
 // overwrites has been read by then (its own and earlier rounds' rows).
+// Bound by memory: a row touches 384 bytes of sectors for its 144; 64 heads cut
+// to 4096 of 32768 keys (d = 128, 100 MB of sectors read, 38 MB written) in 25 us.
 constexpr int MOVE_PAGES = 4, MOVE_THREADS = 256;
 
 template <int D>
