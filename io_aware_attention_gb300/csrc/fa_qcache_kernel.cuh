@@ -446,10 +446,8 @@ struct Work {
 };
 
 // A sequence's length, at most what its page table holds.
-__device__ __forceinline__ int length_of(const int32_t* lens, int b, int max_pages)
-{
-    return (int)min((int64_t)max(lens[b], 0), (int64_t)max_pages * PAGE);
-}
+__device__ __forceinline__ int clamp_length(int len, int max_pages) { return (int)min((int64_t)max(len, 0), (int64_t)max_pages * PAGE); }
+__device__ __forceinline__ int length_of(const int32_t* lens, int b, int max_pages) { return clamp_length(lens[b], max_pages); }
 
 // prefix[0 .. B] by a block of NTHREADS threads (scratch: one int per warp).
 // Up to 32 sequences every warp computes them all and waits for no other.
@@ -578,12 +576,14 @@ struct Rows {
     // do not wait behind them.
     struct Raw {
         uint4 w[NT][D / 32];
+        int len;
     };
     static __device__ __forceinline__ void fetch(Raw& raw, const DecParams& p, int b, int hr)
     {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const int h = p.rb == 1 ? hr : hr / p.rb, r0 = (hr - h * p.rb) * (8 * NT);
         const int64_t row0 = ((int64_t)b * p.hkv + h) * p.rows;
+        raw.len = p.lens[b];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = r0 + nt * 8 + g;
@@ -596,11 +596,11 @@ struct Rows {
         }
     }
 
-    __device__ __forceinline__ void load(const Raw& raw, const DecParams& p, int hr, int len_)
+    __device__ __forceinline__ void load(const Raw& raw, const DecParams& p, int hr)
     {
         const int lane = threadIdx.x & 31, t = lane & 3;
         const int r0 = p.rb == 1 ? 0 : hr % p.rb * (8 * NT);
-        len = len_;
+        len = clamp_length(raw.len, p.max_pages);
         min_lim = p.causal ? len - p.nq + 1 : len;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -893,21 +893,31 @@ struct Feed {
     int flying;
     bool due;                 // `ahead` is to be looked up
     // This lane's unit of the current 32 and of the next: its segment, and the
-    // page's block in the pool (-1 where the table's entry is none of its pages).
+    // page's block in the pool (-1 where the table's entry is none of its pages;
+    // until begin(), the entry itself, so that nothing waits for it yet).
     int now_seg, now_blk, ahead_seg, ahead_blk;
     int first_page;           // of the run's first unit (a later unit's page follows from its segment's first)
     const uint8_t* src;       // the block that is being copied
 
-    __device__ __forceinline__ int look(int x, int& seg, int& blk) const
+    // The segment and page of unit x, and the page table's entry.
+    __device__ __forceinline__ int look(int x, int& seg, int& id) const
     {
-        seg = blk = -1;
+        seg = id = -1;
         if (x >= x1) return 0;
         const Work::Unit u = work.at(x);
         seg = u.b * work.hr + u.hr;
-        const int id = page_of(p.table, p.max_pages, p.num_pages, u.b, u.page);
-        if (id < 0) atomicOr(&g_status, STATUS_BAD_PAGE);
-        else blk = id * p.hkv + (work.hr == p.hkv ? u.hr : u.hr / p.rb);
+        id = p.table[(int64_t)u.b * p.max_pages + u.page];
         return u.page;
+    }
+    __device__ __forceinline__ int block_of(int seg, int id) const
+    {
+        if (seg < 0) return -1;
+        if ((unsigned)id >= (unsigned)p.num_pages) {
+            atomicOr(&g_status, STATUS_BAD_PAGE);
+            return -1;
+        }
+        const int hr = seg % work.hr;
+        return id * p.hkv + (work.hr == p.hkv ? hr : hr / p.rb);
     }
     __device__ __forceinline__ Feed(uint8_t* ring_, uint32_t bar_, const DecParams& p_, const Work& work_, int x0, int x1_)
         : p(p_), work(work_), ring(ring_), bar(bar_), x1(x1_), base(x0), next_unit(x0), next_half(0), fill(0), use(0),
@@ -918,8 +928,10 @@ struct Feed {
         ahead_seg = ahead_blk = -1;
         due = x1 - base > 32;
     }
+    // Starts the first copies.
     __device__ __forceinline__ void begin()
     {
+        now_blk = block_of(now_seg, now_blk);
 #pragma unroll 1
         for (int i = 0; i < SLOTS; ++i) issue();
     }
@@ -945,8 +957,8 @@ struct Feed {
             ++next_unit;
         }
     }
-    // The segment of unit x, the units in turn; `there`: its page exists.
-    __device__ __forceinline__ int place(int x, bool& there)
+    // The segment of unit x, the units in turn.
+    __device__ __forceinline__ int place(int x)
     {
         if (x - base == 32) {
             now_seg = ahead_seg;
@@ -957,10 +969,12 @@ struct Feed {
         if (due && x - base >= 4) {  // well before the copies need it, and not among a run's first steps
             due = false;
             look(base + 32 + (int)(threadIdx.x & 31), ahead_seg, ahead_blk);
+            ahead_blk = block_of(ahead_seg, ahead_blk);
         }
-        there = __shfl_sync(0xffffffffu, now_blk, x - base) >= 0;
         return __shfl_sync(0xffffffffu, now_seg, x - base);
     }
+    // Whether the page of the unit that place() gave last exists.
+    __device__ __forceinline__ bool there(int x) const { return __shfl_sync(0xffffffffu, now_blk, x - base) >= 0; }
     // The oldest half in flight, or null when the wait gave up.
     __device__ __forceinline__ const uint8_t* wait(volatile uint32_t* abort_flag)
     {
@@ -1112,8 +1126,7 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
         Feed<D, Y::SLOTS, true> feed(smem + Y::ring(warp), ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
         typename Rows<D, NT>::Raw raw;
         for (int x = x0; x < x1; ++x) {
-            bool there;
-            const int next_seg = feed.place(x, there);
+            const int next_seg = feed.place(x);
             ++page;
             if (next_seg != seg) {
                 const int b = next_seg / work.hr, hr = next_seg - b * work.hr;
@@ -1127,9 +1140,10 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
                 page = seg < 0 ? feed.first_page : 0;
                 seg = next_seg;
                 begins = page == 0;
-                rows.load(raw, p, hr, length_of(p.lens, b, p.max_pages));
+                rows.load(raw, p, hr);
                 st.clear();
             }
+            const bool there = feed.there(x);
             float s[4][NT][4];
             uint32_t pb[4][NT][2];
             const uint8_t* blk = feed.wait(abort_flag);
@@ -1324,10 +1338,8 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
     uint64_t off[NT], sc[NT];  // of the lane's two columns: scores' factors, and -lse in base 2
     int have = -1;             // segment (with row block) whose rows are loaded
     Feed<D, Y::SLOTS, false> feed(smem + warp * Y::RING, ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
-    feed.begin();
     typename Rows<D, NT>::Raw raw;
-    bool there;
-    int seg = feed.place(x0, there), page = feed.first_page;
+    int seg = feed.place(x0), page = feed.first_page;
     // A lane's part of the weights: keys 16t + g and 16t + 8 + g of a page,
     // fetched while the page before is worked on.
     auto weights_at = [&](int seg_, int page_) { return (int64_t)seg_ * p.w_len + page_ * PAGE + 16 * t + g; };
@@ -1339,12 +1351,15 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
         if (left > 8) w_next[1] = w[8];
     };
     fetch_weights(seg, page);
+    feed.begin();
+    bool there = feed.there(x0);
     for (int x = x0; x < x1; ++x) {
         const float w_now[2] = {w_next[0], w_next[1]};
         bool there_next = false;
         int seg_next = seg, page_next = page;
         if (x + 1 < x1) {
-            seg_next = feed.place(x + 1, there_next);
+            seg_next = feed.place(x + 1);
+            there_next = feed.there(x + 1);
             page_next = seg_next == seg ? page + 1 : 0;
             fetch_weights(seg_next, page_next);
         }
@@ -1356,7 +1371,7 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
                 have = seg * p.rb + rbi;
                 const int b = seg / p.hkv, hr = (seg - b * p.hkv) * p.rb + rbi;
                 rows.fetch(raw, p, b, hr);
-                rows.load(raw, p, hr, length_of(p.lens, b, p.max_pages));
+                rows.load(raw, p, hr);
                 const float* const lse = p.lse_in + (int64_t)seg * p.rows;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
