@@ -80,22 +80,32 @@ __device__ __forceinline__ void turn(int64_t pos, uint64_t freq, float factor, f
     s = __sinf(x) * (factor * sign);
 }
 
-__device__ __forceinline__ uint4 ld16(const __nv_bfloat16* p)
+// W elements.  Not .nc: an output may be its input.
+template <int W, int N>
+__device__ __forceinline__ void ld(uint32_t (&r)[N], const __nv_bfloat16* p)
 {
-    uint4 r;  // not .nc: an output may be its input
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
+    if constexpr (W == 8)
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
+    else if constexpr (W == 2)
+        r[0] = *reinterpret_cast<const uint32_t*>(p);
+    else
+        r[0] = *reinterpret_cast<const unsigned short*>(p);
 }
 
 // stream: the results are larger than L2 and will not be found there by the next reader.
-__device__ __forceinline__ void st16(__nv_bfloat16* p, const uint4& v, int stream)
+template <int W, int N>
+__device__ __forceinline__ void st(__nv_bfloat16* p, const uint32_t (&r)[N], int stream)
 {
-    if (stream)
-        asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-    else
-        ptx::st_global_v4(p, v.x, v.y, v.z, v.w);
+    if constexpr (W == 8) {
+        if (stream)
+            asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+        else
+            ptx::st_global_v4(p, r[0], r[1], r[2], r[3]);
+    } else if constexpr (W == 2) {
+        *reinterpret_cast<uint32_t*>(p) = r[0];
+    } else {
+        *reinterpret_cast<unsigned short*>(p) = (unsigned short)r[0];
+    }
 }
 
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -120,11 +130,11 @@ __device__ __forceinline__ void turn_word(uint32_t& w, float c, float s)
     w = ptx::pack_bf16x2(a * c - b * s, b * c + a * s);
 }
 
-// VEC: units of two 16-byte vectors (every vector wholly turned or wholly
-// passed through, rows and strides 16-byte aligned).  Otherwise a unit is one
-// pair, in 2-byte accesses: odd rotated sizes and strides.
-// Block (units, positions, head lanes).
-template <bool VEC>
+// W = 8: units of two 16-byte vectors (every vector wholly turned or wholly
+// passed through, rows and strides 16-byte aligned).  W = 2 and 1 do the same in
+// two 4-byte and two 2-byte accesses, for turned parts and strides that 16
+// bytes do not divide.  Block (units, positions, head lanes).
+template <int W>
 __global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
 {
     ptx::griddep_wait();  // a programmatic dependent: the inputs are complete
@@ -138,8 +148,7 @@ __global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
     const int u = threadIdx.x;
 
     // The unit's two places (channels) and its pairs' first index; pass: not turned.
-    constexpr int W = VEC ? 8 : 1;
-    const int turned = p.rot / (2 * W);  // units of whole pairs (VEC, interleaved: maybe one half unit more)
+    const int turned = p.rot / (2 * W);  // units of whole pairs (interleaved: maybe one half unit more)
     int ca, cb, f0;
     bool pass_a = false, pass_b = false;
     if (!p.interleaved && u < turned) {
@@ -155,11 +164,12 @@ __global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
     }
     const bool have_b = cb < p.d;
 
-    // The thread's heads: where they are, and (VEC) their vectors, in flight
-    // while the angles are computed.
+    // The thread's heads: where they are, and their vectors, in flight while the
+    // angles are computed.
+    constexpr int WORDS = W / 2 > 0 ? W / 2 : 1;
     const __nv_bfloat16* src[U];
     __nv_bfloat16* dst[U];
-    uint4 va[U], vb[U];
+    uint32_t va[U][WORDS], vb[U][WORDS];
 #pragma unroll
     for (int e = 0; e < U; ++e) {
         const int h = (ht * U + e) * (int)blockDim.z + threadIdx.z;
@@ -169,10 +179,8 @@ __global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
         const int64_t hl = t ? h - p.heads[0] : h;
         src[e] = p.in[t].p + b * p.in[t].sb + hl * p.in[t].sh + i * p.in[t].sn;
         dst[e] = p.out[t].p + b * p.out[t].sb + hl * p.out[t].sh + i * p.out[t].sn;
-        if constexpr (VEC) {
-            va[e] = ld16(src[e] + ca);
-            if (have_b) vb[e] = ld16(src[e] + cb);
-        }
+        ld<W>(va[e], src[e] + ca);
+        if (have_b) ld<W>(vb[e], src[e] + cb);
     }
     const int64_t pos = position_of(p, b, i);
     float c[W], s[W];
@@ -185,44 +193,28 @@ __global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
 #pragma unroll
     for (int e = 0; e < U; ++e) {
         if (!src[e]) continue;
-        if constexpr (VEC) {
-            if (!p.interleaved) {  // pairs lie across the two places
-                if (!pass_a) {
-                    auto two = [&](uint32_t& x, uint32_t& y, int k) {
-                        turn_half(x, y, ptx::f2_pack(c[k], c[k + 1]), ptx::f2_pack(s[k], s[k + 1]), ptx::f2_pack(-s[k], -s[k + 1]));
-                    };
-                    two(va[e].x, vb[e].x, 0);
-                    two(va[e].y, vb[e].y, 2);
-                    two(va[e].z, vb[e].z, 4);
-                    two(va[e].w, vb[e].w, 6);
-                }
-            } else {
-                if (!pass_a) {
-                    turn_word(va[e].x, c[0], s[0]);
-                    turn_word(va[e].y, c[1], s[1]);
-                    turn_word(va[e].z, c[2], s[2]);
-                    turn_word(va[e].w, c[3], s[3]);
-                }
-                if (!pass_b) {
-                    turn_word(vb[e].x, c[4], s[4]);
-                    turn_word(vb[e].y, c[5], s[5]);
-                    turn_word(vb[e].z, c[6], s[6]);
-                    turn_word(vb[e].w, c[7], s[7]);
-                }
+        if constexpr (W == 1) {
+            if (!pass_a) {
+                const float a = lo(va[e][0]), bb = lo(vb[e][0]);
+                va[e][0] = ptx::pack_bf16x2(a * c[0] - bb * s[0], 0.f);
+                vb[e][0] = ptx::pack_bf16x2(bb * c[0] + a * s[0], 0.f);
             }
-            st16(dst[e] + ca, va[e], p.stream);
-            if (have_b) st16(dst[e] + cb, vb[e], p.stream);
+        } else if (!p.interleaved) {  // pairs lie across the two places
+            if (!pass_a) {
+#pragma unroll
+                for (int k = 0; k < WORDS; ++k)
+                    turn_half(va[e][k], vb[e][k], ptx::f2_pack(c[2 * k], c[2 * k + 1]), ptx::f2_pack(s[2 * k], s[2 * k + 1]),
+                              ptx::f2_pack(-s[2 * k], -s[2 * k + 1]));
+            }
         } else {
-            const __nv_bfloat16 xa = src[e][ca], xb = src[e][cb];
-            if (pass_a) {
-                dst[e][ca] = xa;
-                dst[e][cb] = xb;
-            } else {
-                const float a = __bfloat162float(xa), bb = __bfloat162float(xb);
-                dst[e][ca] = __float2bfloat16_rn(a * c[0] - bb * s[0]);
-                dst[e][cb] = __float2bfloat16_rn(bb * c[0] + a * s[0]);
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k) {
+                if (!pass_a) turn_word(va[e][k], c[k], s[k]);
+                if (!pass_b) turn_word(vb[e][k], c[WORDS + k], s[WORDS + k]);
             }
         }
+        st<W>(dst[e] + ca, va[e], p.stream);
+        if (have_b) st<W>(dst[e] + cb, vb[e], p.stream);
     }
 }
 

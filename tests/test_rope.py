@@ -84,7 +84,7 @@ def test_bad_frequencies_are_refused(kw):
 @gpu
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("d, rot", [(128, 128), (64, 64), (128, 32), (80, 40), (80, 48), (96, 96), (72, 72), (8, 8), (8, 2),
-                                    (128, 126), (40, 24), (24, 16)])
+                                    (128, 126), (40, 24), (24, 16), (80, 36), (80, 38)])
 @pytest.mark.parametrize("B, H, Hk, N", [(1, 1, 1, 1), (2, 5, 3, 37), (3, 16, 2, 130)])
 def test_rope_and_gradient(layout, d, rot, B, H, Hk, N):
     inv = [10000.0 ** (-2 * i / rot) for i in range(rot // 2)]
@@ -171,11 +171,12 @@ def test_unaligned_rows_and_repeated_inputs():
     """Rows that start off 16 bytes, and an input expanded over heads (stride 0)."""
     B, H, N, d = 2, 3, 17, 64
     f, _ = fa.rope_frequencies(d)
-    buf = rand((B * H * N * d + 3,), 7).cuda()
-    q = buf[3:].view(B, H, N, d)
-    got, _ = fa.rope(q, None, f)
-    want, _ = fa.rope(q.clone(), None, f)
-    assert torch.equal(got, want)
+    for off in (1, 2, 3, 4):
+        buf = rand((B * H * N * d + off,), 7).cuda()
+        q = buf[off:].view(B, H, N, d)
+        got, _ = fa.rope(q, None, f)
+        want, _ = fa.rope(q.clone(), None, f)
+        assert torch.equal(got, want)
     one = rand((B, 1, N, d), 8).cuda()
     got, _ = fa.rope(one.expand(B, H, N, d), None, f)
     want, _ = fa.rope(one.expand(B, H, N, d).contiguous(), None, f)
