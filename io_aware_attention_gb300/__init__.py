@@ -518,7 +518,7 @@ def _rope_call(q, k, q_out, k_out, freqs, positions, lens, layout, factor, inver
     else:
         kp, ks, kop, kos = k.data_ptr(), _strides(k), k_out.data_ptr(), _strides(k_out)
     rc = library().fa_rope(q.data_ptr(), _strides(q), kp, ks, q_out.data_ptr(), _strides(q_out), kop, kos, B, H, Hk, N,
-                           d, freqs.data_ptr(), 2 * freqs.numel(), layout == "interleaved", factor, bool(inverse),
+                           d, freqs.data_ptr(), 2 * freqs.numel(), layout == "interleaved", float(factor), bool(inverse),
                            pos_ptr, pos_bytes, pos_stride, 0 if lens is None else lens.data_ptr(),
                            _stream_handle(stream, dev))
     if rc != 0:
@@ -617,8 +617,8 @@ def qcache_append(k, v, pool, table, lens, k_scale: float = 1.0, v_scale: float 
         raise ValueError(f"k and v must be (B, Hkv, N, d) of the cache's batch, heads and device: {tuple(k.shape)} "
                          f"{tuple(v.shape)}")
     _on_current_device(dev)
-    rc = library().fa_qcache_append(k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), B, Hkv, N, d, k_scale,
-                                    v_scale, pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
+    rc = library().fa_qcache_append(k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), B, Hkv, N, d,
+                                    float(k_scale), float(v_scale), pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
                                     _stream_handle(stream, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_append")
@@ -631,6 +631,7 @@ def qcache_read(pool, table, lens, n: int, d: int, newest: bool = False, k_scale
     import torch
 
     dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, d)
+    n = int(n)
     if n < 1:
         raise ValueError("n must be positive")
     if torch.cuda.current_device() != dev:
@@ -639,7 +640,7 @@ def qcache_read(pool, table, lens, n: int, d: int, newest: bool = False, k_scale
     k = torch.empty((B, Hkv, n, d), dtype=torch.bfloat16, device=pool.device)
     v = torch.empty_like(k)
     rc = library().fa_qcache_read(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
-                                  k.data_ptr(), v.data_ptr(), B, Hkv, n, d, bool(newest), k_scale, v_scale,
+                                  k.data_ptr(), v.data_ptr(), B, Hkv, n, d, bool(newest), float(k_scale), float(v_scale),
                                   _stream_handle(stream, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_read")
@@ -682,7 +683,7 @@ def _qcache_decode_call(q, pool, table, lens, o, lse, workspace, causal, scale, 
         scale = 1.0 / math.sqrt(d)
     rc = library().fa_qcache_decode(q.data_ptr(), pool.data_ptr(), num_pages, table.data_ptr(), max_pages,
                                     lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, d, bool(causal),
-                                    scale, k_scale, v_scale, workspace.data_ptr(),
+                                    float(scale), float(k_scale), float(v_scale), workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_decode")
@@ -754,7 +755,8 @@ def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, sca
         scale = 1.0 / math.sqrt(d)
     rc = library().fa_qcache_weights(q.data_ptr(), lse.data_ptr(), pool.data_ptr(), num_pages, table.data_ptr(),
                                      max_pages, lens.data_ptr(), weights.data_ptr(), out.data_ptr(),
-                                     weights.shape[2], B, H, Hkv, Nq, d, bool(causal), scale, k_scale,
+                                     weights.shape[2], B, H, Hkv, Nq, d, bool(causal), float(scale),
+                                     float(k_scale),
                                      _stream_handle(stream, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_weights")
@@ -784,6 +786,7 @@ def qcache_evict(pool, table, lens, weights, keep: int, sink: int = 0, recent: i
     elif table_out.dim() != 2 or table_out.shape[0] != B:
         raise ValueError("table_out must be (B, max_pages_out)")
     _check_int32("table_out", table_out, None, dev)
+    keep, sink, recent = int(keep), int(sink), int(recent)
     if keep < 1 or sink < 0 or recent < 0 or sink + recent > keep:
         raise ValueError("keep must be positive, sink and recent not negative and together at most keep")
     kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=pool.device)

@@ -493,9 +493,11 @@ __device__ __forceinline__ void page_prefix(const int32_t* lens, int B, int max_
 
 // Brings the small tensors of a call to L2, every block a share, before the
 // work that this launch depends on has ended: their later reads, which
-// follow one another, then cost an L2 access each instead of a DRAM one.
+// follow one another, then cost an L2 access each instead of a DRAM one.  A
+// page table with room for far more than its sequences hold is left alone.
 __device__ __forceinline__ void prefetch_l2(const void* p, int64_t bytes)
 {
+    if (bytes > (1 << 20)) return;
     const char* const c = static_cast<const char*>(p);
     for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 128; i < bytes; i += (int64_t)gridDim.x * blockDim.x * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(c + i));

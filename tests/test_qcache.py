@@ -631,3 +631,41 @@ def test_evict_longer_heads_than_shared_memory_holds():
     g = torch.Generator().manual_seed(1)
     w = torch.randint(0, 40, (1, 1, n), generator=g).float() * 0.25
     check_evict([n], 1, 64, 20000, 3, 100, w, True)
+
+
+@gpu
+def test_numbers_of_any_kind():
+    """numpy's numbers are taken as Python's are."""
+    d = 64
+    cache = dev(*ref.make_cache([100], 2, d, seed=1))
+    q = rand((1, 2, 1, d), 1).cuda()
+    o, lse = fa.qcache_decode(q, *cache, scale=0.125)
+    o2, lse2 = fa.qcache_decode(q, *cache, scale=np.float32(0.125), k_scale=np.float32(1), v_scale=np.float64(1), causal=np.bool_(False))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    w = torch.zeros((1, 2, 128), device="cuda")
+    w = fa.qcache_weights(q, lse, *cache, w, scale=np.float32(0.125), k_scale=np.float32(1))
+    k, v = fa.qcache_read(*cache, np.int64(10), d, k_scale=np.float32(1))
+    assert k.shape == (1, 2, 10, d)
+    kept, _, _ = fa.qcache_evict(*cache, w, np.int32(10), sink=np.int64(1), recent=np.int64(2))
+    assert kept.shape == (1, 2, 10)
+    f, _ = fa.rope_frequencies(d)
+    a, _ = fa.rope(q, None, f, factor=np.float32(1.5))
+    b, _ = fa.rope(q, None, f, factor=1.5)
+    assert torch.equal(a, b)
+
+
+@gpu
+def test_a_page_table_with_much_more_room_than_keys():
+    """Only the entries that hold keys are read: the rest of a 16 MB table is out of range everywhere."""
+    d, lens = 64, [70, 3]
+    pool, table, lens_t = ref.make_cache(lens, 2, d, seed=4)
+    wide = torch.full((2, 2_000_000), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    q = rand((2, 4, 1, d), 2).cuda()
+    a = fa.qcache_decode(q, *dev(pool, table, lens_t))
+    b = fa.qcache_decode(q, *dev(pool, wide, lens_t))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and fa.check_device_status() == 0
+    w = [fa.qcache_weights(q, a[1], *dev(pool, t, lens_t), torch.zeros((2, 2, 70), device="cuda")) for t in (table, wide)]
+    assert torch.equal(*w)
+    r = [fa.qcache_evict(*dev(pool, t, lens_t), w[0], 30) for t in (table, wide)]
+    assert torch.equal(r[0][0], r[1][0]) and torch.equal(r[0][2], r[1][2]) and fa.check_device_status() == 0
