@@ -1037,7 +1037,6 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
     __shared__ int slot_seg[32];                 // segment of each slot, or -1
     __shared__ int slot_ends[2 * WARPS];         // bit 0: the segment begins in it, bit 1: ends
     __shared__ float slot_weight[2 * WARPS][R];  // of each slot's row in the joined one
-    __shared__ float joined_m[R], joined_l[R];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     static_assert(2 * WARPS <= 32, "a lane a slot");
     if (lane < Y::SLOTS) ptx::mbar_init(ptx::smem_addr(&bars[warp * Y::SLOTS + lane]), 1);
@@ -1163,13 +1162,35 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
     }
     __syncthreads();
 
-    // Join the warps' pieces: runs of slots of one segment.
+    // Join the warps' pieces: runs of slots of one segment.  First every run's
+    // maxima, sums and slots' weights, a warp a row and a lane a slot (the run's
+    // first slot takes the joined maximum and sum), then the outputs.
     if (tid == 0) p.desc[2 * cta] = -1;
     const int my_seg = slot_seg[lane];
-    uint32_t left = __ballot_sync(0xffffffffu, my_seg >= 0);
-    while (left) {
+    const uint32_t used = __ballot_sync(0xffffffffu, my_seg >= 0);
+    for (uint32_t left = used; left;) {
+        const int a = __ffs(left) - 1;
+        const uint32_t run = used & __ballot_sync(0xffffffffu, my_seg == __shfl_sync(0xffffffffu, my_seg, a));
+        left &= ~run;
+        const bool mine = run >> lane & 1u;
+        for (int r = warp; r < R; r += WARPS) {
+            float* const f = Y::partial(smem, mine ? lane : a);
+            const float m = mine ? f[PC::m(r)] : -INFINITY;
+            float l = mine ? f[PC::l(r)] : 0.f, mx = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float w = m == -INFINITY ? 0.f : ptx::ex2(m - mx);
+            l = mine ? w * l : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (mine) slot_weight[lane][r] = w;
+            if (lane == a) f[PC::m(r)] = mx, f[PC::l(r)] = l;
+        }
+    }
+    __syncthreads();
+    for (uint32_t left = used; left;) {
         const int a = __ffs(left) - 1, seg = __shfl_sync(0xffffffffu, my_seg, a);
-        const uint32_t run = left & __ballot_sync(0xffffffffu, my_seg == seg);
+        const uint32_t run = used & __ballot_sync(0xffffffffu, my_seg == seg);
         const int z = 31 - __clz(run);
         left &= ~run;
         const bool begins = slot_ends[a] & 1, ends = slot_ends[z] & 2;
@@ -1177,21 +1198,7 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
         const int r0 = (hr - h * p.rb) * R;
         const int64_t row0 = ((int64_t)b * p.hkv + h) * p.rows;
         float* const part = p.ws + ((int64_t)cta * 2 + (begins ? 1 : 0)) * PS::FLOATS;
-        // Each row's maximum, sum and slots' weights: a warp a row, a lane a slot.
-        for (int r = warp; r < R; r += WARPS) {
-            const bool mine = run >> lane & 1u;
-            const float m = mine ? Y::partial(smem, lane)[PC::m(r)] : -INFINITY;
-            float mx = m;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float w = m == -INFINITY ? 0.f : ptx::ex2(m - mx);
-            float l = mine ? w * Y::partial(smem, lane)[PC::l(r)] : 0.f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (mine) slot_weight[lane][r] = w;
-            if (lane == 0) joined_m[r] = mx, joined_l[r] = l;
-        }
-        __syncthreads();
+        const float* const joined = Y::partial(smem, a);
         for (int e = tid; e < R * (D / 2); e += THREADS) {
             const int r = e / (D / 2), c = e % (D / 2) * 2;
             float x = 0.f, y = 0.f;
@@ -1202,17 +1209,17 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
                 x = fmaf(v.x, w, x);
                 y = fmaf(v.y, w, y);
             }
-            const float l = joined_l[r];
+            const float l = joined[PC::l(r)];
             if (begins && ends) {
                 if (r0 + r >= p.rows) continue;
                 const float f = l == 0.f ? 0.f : p.v_scale / l;
                 if (c < p.d)
                     *reinterpret_cast<uint32_t*>(p.o + (row0 + r0 + r) * p.d + c) = ptx::pack_bf16x2(x * f, y * f);
-                if (c == 0) p.lse[row0 + r0 + r] = natural_lse(joined_m[r], l);
+                if (c == 0) p.lse[row0 + r0 + r] = natural_lse(joined[PC::m(r)], l);
             } else {
                 *reinterpret_cast<float2*>(part + PS::o(r) + c) = make_float2(x, y);
                 if (c == 0) {
-                    part[PS::m(r)] = joined_m[r];
+                    part[PS::m(r)] = joined[PC::m(r)];
                     part[PS::l(r)] = l;
                 }
             }
@@ -1223,7 +1230,6 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
             p.desc[2 * cta] = seg;
             p.desc[2 * cta + 1] = (int)(((int64_t)(x + 1) * G - 1) / T);
         }
-        if (left) __syncthreads();
     }
 }
 
