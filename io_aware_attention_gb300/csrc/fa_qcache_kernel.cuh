@@ -1037,6 +1037,14 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
     __shared__ int slot_seg[32];                 // segment of each slot, or -1
     __shared__ int slot_ends[2 * WARPS];         // bit 0: the segment begins in it, bit 1: ends
     __shared__ float slot_weight[2 * WARPS][R];  // of each slot's row in the joined one
+    struct Run {
+        uint32_t mask;    // its slots
+        int begins, ends; // whether the segment does in this block
+        int rows;         // query rows from its row block's first
+        int64_t row;      // that one, of all
+    };
+    __shared__ Run runs[2 * WARPS];
+    __shared__ int run_count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     static_assert(2 * WARPS <= 32, "a lane a slot");
     if (lane < Y::SLOTS) ptx::mbar_init(ptx::smem_addr(&bars[warp * Y::SLOTS + lane]), 1);
@@ -1162,73 +1170,91 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
     }
     __syncthreads();
 
-    // Join the warps' pieces: runs of slots of one segment.  First every run's
-    // maxima, sums and slots' weights, a warp a row and a lane a slot (the run's
-    // first slot takes the joined maximum and sum), then the outputs.
-    if (tid == 0) p.desc[2 * cta] = -1;
-    const int my_seg = slot_seg[lane];
-    const uint32_t used = __ballot_sync(0xffffffffu, my_seg >= 0);
-    for (uint32_t left = used; left;) {
-        const int a = __ffs(left) - 1;
-        const uint32_t run = used & __ballot_sync(0xffffffffu, my_seg == __shfl_sync(0xffffffffu, my_seg, a));
-        left &= ~run;
-        const bool mine = run >> lane & 1u;
-        for (int r = warp; r < R; r += WARPS) {
-            float* const f = Y::partial(smem, mine ? lane : a);
-            const float m = mine ? f[PC::m(r)] : -INFINITY;
-            float l = mine ? f[PC::l(r)] : 0.f, mx = m;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float w = m == -INFINITY ? 0.f : ptx::ex2(m - mx);
-            l = mine ? w * l : 0.f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (mine) slot_weight[lane][r] = w;
-            if (lane == a) f[PC::m(r)] = mx, f[PC::l(r)] = l;
+    // Join the warps' pieces: runs of slots of one segment.  A lane a slot finds
+    // the runs, a thread a run's row weighs its slots (the first one takes the
+    // joined maximum and sum), a thread four channels of a row adds them up.
+    if (warp == 0) {
+        const int seg = slot_seg[lane];
+        const uint32_t mask = __match_any_sync(0xffffffffu, seg);
+        const int a = __ffs(mask) - 1, z = 31 - __clz(mask);
+        const bool leads = seg >= 0 && a == lane;
+        const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+        if (lane == 0) {
+            run_count = __popc(leaders);
+            p.desc[2 * cta] = -1;
+        }
+        __syncwarp();
+        if (leads) {
+            Run& run = runs[__popc(leaders & ((1u << lane) - 1u))];
+            const int b = seg / work.hr, hr = seg - b * work.hr, h = p.rb == 1 ? hr : hr / p.rb;
+            run.mask = mask;
+            run.begins = slot_ends[a] & 1;
+            run.ends = slot_ends[z] & 2;
+            run.row = ((int64_t)b * p.hkv + h) * p.rows + (hr - h * p.rb) * R;
+            run.rows = p.rows - (hr - h * p.rb) * R;
+            if (run.begins && !run.ends) {
+                // The block that holds the segment's last unit x: the c with c T / G <= x < (c + 1) T / G.
+                const int x = prefix[b] * work.hr + (hr + 1) * (prefix[b + 1] - prefix[b]) - 1;
+                p.desc[2 * cta] = seg;
+                p.desc[2 * cta + 1] = (int)(((int64_t)(x + 1) * G - 1) / T);
+            }
         }
     }
     __syncthreads();
-    for (uint32_t left = used; left;) {
-        const int a = __ffs(left) - 1, seg = __shfl_sync(0xffffffffu, my_seg, a);
-        const uint32_t run = used & __ballot_sync(0xffffffffu, my_seg == seg);
-        const int z = 31 - __clz(run);
-        left &= ~run;
-        const bool begins = slot_ends[a] & 1, ends = slot_ends[z] & 2;
-        const int b = seg / work.hr, hr = seg - b * work.hr, h = hr / p.rb;
-        const int r0 = (hr - h * p.rb) * R;
-        const int64_t row0 = ((int64_t)b * p.hkv + h) * p.rows;
-        float* const part = p.ws + ((int64_t)cta * 2 + (begins ? 1 : 0)) * PS::FLOATS;
-        const float* const joined = Y::partial(smem, a);
-        for (int e = tid; e < R * (D / 2); e += THREADS) {
-            const int r = e / (D / 2), c = e % (D / 2) * 2;
-            float x = 0.f, y = 0.f;
-            for (uint32_t k = run; k; k &= k - 1) {
-                const int slot_ = __ffs(k) - 1;
-                const float w = slot_weight[slot_][r];
-                const float2 v = *reinterpret_cast<const float2*>(Y::partial(smem, slot_) + PC::o(c / (D / 8), c % (D / 8) / 2, r));
-                x = fmaf(v.x, w, x);
-                y = fmaf(v.y, w, y);
+    const int n_runs = run_count;
+    for (int e = tid; e < n_runs * R; e += THREADS) {
+        const uint32_t mask = runs[e / R].mask;
+        const int r = e % R, a = __ffs(mask) - 1, z = 31 - __clz(mask);
+        float mx = -INFINITY, l = 0.f;
+#pragma unroll 4
+        for (int k = a; k <= z; ++k)
+            if (mask >> k & 1u) mx = fmaxf(mx, Y::partial(smem, k)[PC::m(r)]);
+#pragma unroll 4
+        for (int k = a; k <= z; ++k)
+            if (mask >> k & 1u) {
+                const float* const f = Y::partial(smem, k);
+                const float m = f[PC::m(r)], w = m == -INFINITY ? 0.f : ptx::ex2(m - mx);
+                slot_weight[k][r] = w;
+                l = fmaf(w, f[PC::l(r)], l);
             }
-            const float l = joined[PC::l(r)];
-            if (begins && ends) {
-                if (r0 + r >= p.rows) continue;
-                const float f = l == 0.f ? 0.f : p.v_scale / l;
-                if (c < p.d)
-                    *reinterpret_cast<uint32_t*>(p.o + (row0 + r0 + r) * p.d + c) = ptx::pack_bf16x2(x * f, y * f);
-                if (c == 0) p.lse[row0 + r0 + r] = natural_lse(joined[PC::m(r)], l);
-            } else {
-                *reinterpret_cast<float2*>(part + PS::o(r) + c) = make_float2(x, y);
-                if (c == 0) {
-                    part[PS::m(r)] = joined[PC::m(r)];
-                    part[PS::l(r)] = l;
-                }
+        float* const f = Y::partial(smem, a);
+        f[PC::m(r)] = mx;
+        f[PC::l(r)] = l;
+    }
+    __syncthreads();
+    constexpr int QUADS = R * D / 4;
+    for (int e = tid; e < n_runs * QUADS; e += THREADS) {
+        const Run run = runs[e / QUADS];
+        const int r = e % QUADS / (D / 4), c = e % (D / 4) * 4;
+        if (r >= run.rows) continue;
+        const int a = __ffs(run.mask) - 1, z = 31 - __clz(run.mask);
+        const int at = PC::o(c / (D / 8), c % (D / 8) / 2, r), next = PC::o(c / (D / 8), c % (D / 8) / 2 + 1, r);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = a; k <= z; ++k)
+            if (run.mask >> k & 1u) {
+                const float* const f = Y::partial(smem, k);
+                const float w = slot_weight[k][r];
+                const float2 u = *reinterpret_cast<const float2*>(f + at), v = *reinterpret_cast<const float2*>(f + next);
+                s.x = fmaf(u.x, w, s.x);
+                s.y = fmaf(u.y, w, s.y);
+                s.z = fmaf(v.x, w, s.z);
+                s.w = fmaf(v.y, w, s.w);
             }
-        }
-        if (begins && !ends && tid == 0) {
-            // The block that holds the segment's last unit x: the c with c T / G <= x < (c + 1) T / G.
-            const int x = prefix[b] * work.hr + (hr + 1) * (prefix[b + 1] - prefix[b]) - 1;
-            p.desc[2 * cta] = seg;
-            p.desc[2 * cta + 1] = (int)(((int64_t)(x + 1) * G - 1) / T);
+        const float m = Y::partial(smem, a)[PC::m(r)], l = Y::partial(smem, a)[PC::l(r)];
+        if (run.begins && run.ends) {
+            const float f = l == 0.f ? 0.f : p.v_scale / l;
+            if (c < p.d)
+                *reinterpret_cast<uint2*>(p.o + (run.row + r) * p.d + c) =
+                    make_uint2(ptx::pack_bf16x2(s.x * f, s.y * f), ptx::pack_bf16x2(s.z * f, s.w * f));
+            if (c == 0) p.lse[run.row + r] = natural_lse(m, l);
+        } else {
+            float* const part = p.ws + ((int64_t)cta * 2 + (run.begins ? 1 : 0)) * PS::FLOATS;
+            *reinterpret_cast<float4*>(part + PS::o(r) + c) = s;
+            if (c == 0) {
+                part[PS::m(r)] = m;
+                part[PS::l(r)] = l;
+            }
         }
     }
 }

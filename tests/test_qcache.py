@@ -556,10 +556,11 @@ def test_offsets_beyond_32_bits():
 
 
 @gpu
-@pytest.mark.parametrize("B", [33, 257, 2048])
-def test_many_sequences(B):
-    """Batches past a warp, a block and up to the limit, with empty sequences among them; one more is refused."""
-    d, Hkv, H = 64, 1, 2
+@pytest.mark.parametrize("B, d, H", [(33, 64, 2), (257, 64, 2), (2048, 64, 2), (2048, 128, 2), (2048, 64, 9), (2048, 128, 9)])
+def test_many_sequences(B, d, H):
+    """Batches past a warp, a block and up to the limit (with the shared memory of every kernel instance), with
+    empty sequences among them; one more is refused."""
+    Hkv = 1
     g = np.random.default_rng(B)
     lens = [int(x) for x in g.integers(0, 130, B)]
     lens[0], lens[-1] = 0, 129
