@@ -930,28 +930,34 @@ struct Feed {
         ahead_seg = ahead_blk = -1;
         due = x1 - base > 32;
     }
-    // Starts the first copies.
+    // Starts the first copies, a lane a slot.
     __device__ __forceinline__ void begin()
     {
         now_blk = block_of(now_seg, now_blk);
-#pragma unroll 1
-        for (int i = 0; i < SLOTS; ++i) issue();
+        const int lane = threadIdx.x & 31;
+        const int blk = __shfl_sync(0xffffffffu, now_blk, lane / PER);
+        flying = min(SLOTS, (x1 - base) * PER);
+        if (lane < flying) copy(lane, lane / PER, lane % PER, source(blk));
+        fill = flying == SLOTS ? 0 : flying;
+        next_unit = base + flying / PER;
+        next_half = flying % PER;
+        if (next_half != 0) src = source(__shfl_sync(0xffffffffu, now_blk, next_unit - base));
+    }
+    // A page's block; any block for a page that does not exist (it is not used).
+    __device__ __forceinline__ const uint8_t* source(int blk) const { return p.pool + (int64_t)max(0, blk) * Block<D>::BYTES; }
+    __device__ __forceinline__ void copy(int slot, int unit, int half, const uint8_t* from) const
+    {
+        ptx::mbar_arrive_expect_tx(bar + 8 * slot, HALF);
+        if (!(p.debug_skip == unit && base == 0 && blockIdx.x == 0))
+            ptx::bulk_load(ptx::smem_addr(ring) + slot * HALF, from + (WITH_V ? half * HALF : 0), HALF, bar + 8 * slot);
     }
     // Starts the next copy, if one is left.
     __device__ __forceinline__ void issue()
     {
         if (next_unit >= x1) return;
         const int i = next_unit - base;
-        if (next_half == 0) {
-            const int blk = i < 32 ? __shfl_sync(0xffffffffu, now_blk, i) : __shfl_sync(0xffffffffu, ahead_blk, i - 32);
-            src = p.pool + (int64_t)max(0, blk) * Block<D>::BYTES;  // a page that does not exist: any block, not used
-        }
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(bar + 8 * fill, HALF);
-            if (!(p.debug_skip == i && base == 0 && blockIdx.x == 0))
-                ptx::bulk_load(ptx::smem_addr(ring) + fill * HALF, src + (WITH_V ? next_half * HALF : 0), HALF, bar + 8 * fill);
-        }
+        if (next_half == 0) src = source(i < 32 ? __shfl_sync(0xffffffffu, now_blk, i) : __shfl_sync(0xffffffffu, ahead_blk, i - 32));
+        if ((threadIdx.x & 31) == 0) copy(fill, i, next_half, src);
         fill = fill + 1 == SLOTS ? 0 : fill + 1;
         ++flying;
         if (++next_half == PER) {
