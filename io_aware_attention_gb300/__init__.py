@@ -555,14 +555,17 @@ def rope(q, k, freqs, positions=None, lens=None, layout: str = "half", factor: f
     projection) are taken as they are."""
     import torch
 
+    if stream is not None:  # the results belong to the stream that writes them
+        with torch.cuda.stream(stream):
+            return rope(q, k, freqs, positions, lens, layout, factor, inverse)
     sizes = _check_rope(q, k, freqs, positions, lens, layout)
     dev = sizes[0]
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            return rope(q, k, freqs, positions, lens, layout, factor, inverse, stream)
+            return rope(q, k, freqs, positions, lens, layout, factor, inverse)
     q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     k_out = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
-    return _rope_call(q, k, q_out, k_out, freqs, positions, lens, layout, factor, inverse, stream, sizes)
+    return _rope_call(q, k, q_out, k_out, freqs, positions, lens, layout, factor, inverse, None, sizes)
 
 
 def rope_bwd(dq, dk, freqs, positions=None, lens=None, layout: str = "half", factor: float = 1.0, stream=None):
@@ -630,18 +633,21 @@ def qcache_read(pool, table, lens, n: int, d: int, newest: bool = False, k_scale
     (B, Hkv, n, d); rows where no key is are zero."""
     import torch
 
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qcache_read(pool, table, lens, n, d, newest, k_scale, v_scale)
     dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, d)
     n = int(n)
     if n < 1:
         raise ValueError("n must be positive")
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            return qcache_read(pool, table, lens, n, d, newest, k_scale, v_scale, stream)
+            return qcache_read(pool, table, lens, n, d, newest, k_scale, v_scale)
     k = torch.empty((B, Hkv, n, d), dtype=torch.bfloat16, device=pool.device)
     v = torch.empty_like(k)
     rc = library().fa_qcache_read(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
                                   k.data_ptr(), v.data_ptr(), B, Hkv, n, d, bool(newest), float(k_scale), float(v_scale),
-                                  _stream_handle(stream, dev))
+                                  _stream_handle(None, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_read")
     return k, v
@@ -715,17 +721,20 @@ def qcache_decode(q, pool, table, lens, causal: bool = False, scale: float | Non
     (B, H, Nq) fp32)``; a query that sees no key gives 0 and -inf."""
     import torch
 
+    if stream is not None:  # the workspace and the results belong to the stream that writes them
+        with torch.cuda.stream(stream):
+            return qcache_decode(q, pool, table, lens, causal, scale, k_scale, v_scale)
     sizes = _check_qcache_query(q, pool, table, lens)
     dev, _, Hkv, max_pages = sizes
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            return qcache_decode(q, pool, table, lens, causal, scale, k_scale, v_scale, stream)
+            return qcache_decode(q, pool, table, lens, causal, scale, k_scale, v_scale)
     B, H, Nq, d = q.shape
     on = q.device
     ws = torch.empty(_qcache_workspace(dev, B, H, Hkv, Nq, d, max_pages), dtype=torch.uint8, device=on)
     o = torch.empty_like(q)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=on)
-    return _qcache_decode_call(q, pool, table, lens, o, lse, ws, causal, scale, k_scale, v_scale, stream, sizes)
+    return _qcache_decode_call(q, pool, table, lens, o, lse, ws, causal, scale, k_scale, v_scale, None, sizes)
 
 
 def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, scale: float | None = None,
@@ -736,10 +745,13 @@ def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, sca
     ``out`` may be weights itself."""
     import torch
 
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qcache_weights(q, lse, pool, table, lens, weights, causal, scale, k_scale, out)
     dev, num_pages, Hkv, max_pages = _check_qcache_query(q, pool, table, lens)
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            return qcache_weights(q, lse, pool, table, lens, weights, causal, scale, k_scale, out, stream)
+            return qcache_weights(q, lse, pool, table, lens, weights, causal, scale, k_scale, out)
     B, H, Nq, d = q.shape
     if not _fast_ok(dev, (B, H, Nq), torch.float32, lse):
         _check_out("lse", lse, (B, H, Nq), torch.float32, q.device)
@@ -756,8 +768,7 @@ def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, sca
     rc = library().fa_qcache_weights(q.data_ptr(), lse.data_ptr(), pool.data_ptr(), num_pages, table.data_ptr(),
                                      max_pages, lens.data_ptr(), weights.data_ptr(), out.data_ptr(),
                                      weights.shape[2], B, H, Hkv, Nq, d, bool(causal), float(scale),
-                                     float(k_scale),
-                                     _stream_handle(stream, dev))
+                                     float(k_scale), _stream_handle(None, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_weights")
     return out
@@ -773,10 +784,13 @@ def qcache_evict(pool, table, lens, weights, keep: int, sink: int = 0, recent: i
     new places, 0 after them (like weights)."""
     import torch
 
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qcache_evict(pool, table, lens, weights, keep, sink, recent, table_out)
     dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, None)
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            return qcache_evict(pool, table, lens, weights, keep, sink, recent, table_out, stream)
+            return qcache_evict(pool, table, lens, weights, keep, sink, recent, table_out)
     if weights.dim() != 3:
         raise ValueError("weights must be (B, Hkv, W)")
     if not _fast_ok(dev, (B, Hkv, weights.shape[2]), torch.float32, weights):
@@ -795,7 +809,7 @@ def qcache_evict(pool, table, lens, weights, keep: int, sink: int = 0, recent: i
     rc = library().fa_qcache_evict(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
                                    table_out.data_ptr(), table_out.shape[1], weights.data_ptr(),
                                    weights_out.data_ptr(), weights.shape[2], kept.data_ptr(), lens_out.data_ptr(), B,
-                                   Hkv, pool.shape[2] // 72, keep, sink, recent, _stream_handle(stream, dev))
+                                   Hkv, pool.shape[2] // 72, keep, sink, recent, _stream_handle(None, dev))
     if rc != 0:
         raise FaError(rc, "fa_qcache_evict")
     return kept, lens_out, weights_out

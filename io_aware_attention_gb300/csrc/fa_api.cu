@@ -1130,8 +1130,8 @@ fa_status fa_qcache_append(const void* k, const int64_t* k_strides, const void* 
     if (!k || !v) return FA_ERR_INVALID_ARG;
     const fa_status cs = qcache_check(pool, num_pages, table, max_pages, lens, B, Hkv, d);
     if (cs != FA_OK) return cs;
-    if (N < 1 || N > INT32_MAX / 2 || !scale_ok(k_scale) || !scale_ok(v_scale) || !scale_ok(6.0f * k_scale) ||
-        !scale_ok(6.0f * v_scale))
+    if (N < 1 || N > INT32_MAX / 2 || !scale_ok(k_scale) || !scale_ok(v_scale) || !scale_ok((float)(1.0 / (6.0 * (double)k_scale))) ||
+        !scale_ok((float)(1.0 / (6.0 * (double)v_scale))))
         return FA_ERR_INVALID_ARG;
     const int64_t LIM = (int64_t)1 << 59;
     if (B * Hkv > LIM / N || B * Hkv * N > LIM / d) return FA_ERR_INVALID_ARG;
@@ -1173,8 +1173,8 @@ fa_status fa_qcache_append(const void* k, const int64_t* k_strides, const void* 
     p.num_pages = (int)num_pages;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    p.k_six = 6.0f * k_scale;
-    p.v_six = 6.0f * v_scale;
+    p.k_inv_six = (float)(1.0 / (6.0 * (double)k_scale));
+    p.v_inv_six = (float)(1.0 / (6.0 * (double)v_scale));
     // Pages that N keys can touch, wherever they begin.
     const int64_t pages = std::min<int64_t>((N - 1 + fa::qc::PAGE - 1) / fa::qc::PAGE + 1, max_pages);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -122,14 +122,18 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1
 
 // ----------------------------------------------------------------- rounding
 
-// A scale for 16 channels from their largest magnitude: amax / (6 scale) in
-// e4m3, to nearest (halves to even), at most 448.  Returns its byte.
-__device__ __forceinline__ uint32_t scale_byte(float amax, float six)
+// Scales for two blocks of 16 channels from their largest magnitudes:
+// amax / (6 scale) in e4m3, to nearest (halves to even), at most 448.  Returns
+// their bytes, lo first.  The quotient (by a reciprocal, within 2^-23) is rounded to
+// 17 bits first, which brings exact halves back and moves no other across one:
+// the quotient of bf16's 8-bit significand that is not half way between two e4m3
+// values differs from there by 2^-8 of itself.
+__device__ __forceinline__ uint32_t scale_bytes(float amax_lo, float amax_hi, float inv_six)
 {
-    const float t = fminf(__fdiv_rn(amax, six), 448.0f);
+    auto quotient = [&](float amax) { return __uint_as_float((__float_as_uint(amax * inv_six) + 0x40u) & 0xFFFFFF80u); };
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(t));
-    return r & 0xFFu;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(quotient(amax_hi)), "f"(quotient(amax_lo)));
+    return r;
 }
 
 __device__ __forceinline__ float scale_value(uint32_t byte)
@@ -138,17 +142,26 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
     return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
 }
 
+// The reciprocal of a block's scale, to 2^-23 (0 for a scale of 0).
+__device__ __forceinline__ float reciprocal(float s)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return s > 0.f ? r : 0.f;
+}
+
 // Two quotients x / (e4m3 * scale) as e2m1, to nearest, halves to even,
-// magnitudes above 6 to 6: `lo` in the low nibble.  An inv is a reciprocal in
-// fp32, which puts a quotient that is half way between two codes up to 2^-23
-// off it (bf16 inputs meet exact halves often); adding and subtracting
-// 1.5 * 2^9 rounds to a multiple of 2^-14 first, which brings those back and
-// moves no other: a quotient of an 8-bit and a 4-bit significand that is not
-// half way differs from there by 2^-10 at least.
-__device__ __forceinline__ uint32_t codes2(float lo, float hi, float inv_lo, float inv_hi)
+// magnitudes above 6 to 6: the first in the low nibble.  x and the reciprocals
+// come as pairs.  A product with a reciprocal lies up to 2^-22 off a quotient
+// that is half way between two codes (bf16 inputs meet exact halves often);
+// adding and subtracting 1.5 * 2^9 rounds to a multiple of 2^-14 first, which
+// brings those back and moves no other: a quotient of an 8-bit and a 4-bit
+// significand that is not half way differs from there by 2^-10 at least.
+__device__ __forceinline__ uint32_t codes2(uint64_t x, uint64_t inv)
 {
     constexpr float C = 768.0f;
-    const float a = __fadd_rn(__fmaf_rn(lo, inv_lo, C), -C), b = __fadd_rn(__fmaf_rn(hi, inv_hi, C), -C);
+    float a, b;
+    ptx::f2_unpack(ptx::f2_add(ptx::f2_fma(x, inv, ptx::f2_pack(C, C)), ptx::f2_pack(-C, -C)), a, b);
     uint32_t r;
     asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b32 %0, {t, t, t, t};\n\t}" : "=r"(r) : "f"(b), "f"(a));
     return r & 0xFFu;
@@ -175,7 +188,7 @@ struct RowParams {
     int64_t n;
     int hkv, d, max_pages, num_pages, tiles;
     int newest;                    // row i is position lens - N + i (else i)
-    float k_scale, v_scale, k_six, v_six;
+    float k_scale, v_scale, k_inv_six, v_inv_six;  // 1 / (6 scale)
 };
 
 // The 16 channels of block b of row p (d of them exist), zeros past d or when !have.
@@ -192,15 +205,16 @@ struct Raw16 {
         unpack8(w0, f);
         unpack8(w1, f + 8);
     }
-};
-
-__device__ __forceinline__ float amax16(const float (&f)[16])
-{
-    float m = 0.f;
+    // The largest magnitude (NaN does not count).
+    __device__ __forceinline__ float amax() const
+    {
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
-    return m;
-}
+        for (int i = 0; i < 8; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7FFF7FFFu));
+        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    }
+};
 
 // The page of position x of sequence b, or -1 (and the status bit).
 __device__ __forceinline__ int page_of(const int32_t* table, int max_pages, int num_pages, int b, int slot)
@@ -220,7 +234,7 @@ constexpr int ROW_THREADS = 256;
 //
 // Bound by memory for prompts (4d bytes read and 9d/8 written a key), by its
 // launch for single keys.  Appending and reading back 4 x 8 heads x up to 4096
-// keys at d = 128: 25.5 us, about half of it here; 64 x 8 heads x 1 key: 6.2 us.
+// keys at d = 128: 24.8 us, about half of it here; 64 x 8 heads x 1 key: 6.2 us.
 template <int D>
 __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const RowParams p)
 {
@@ -265,12 +279,12 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const Row
         if (x < x0 || x >= x1) continue;
         float f[16];
         kr_[i].unpack(f);
-        const uint32_t sb = scale_byte(amax16(f), p.k_six);
-        const float s = scale_value(sb) * p.k_scale;
-        const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+        const uint32_t sb = scale_bytes(kr_[i].amax(), 0.f, p.k_inv_six) & 0xFFu;
+        const float inv = reciprocal(scale_value(sb) * p.k_scale);
         uint32_t w[2] = {0, 0};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e / 4] |= codes2(f[2 * e], f[2 * e + 1], inv, inv) << (8 * (e % 4));
+        for (int e = 0; e < 8; ++e)
+            w[e / 4] |= codes2(ptx::f2_pack(f[2 * e], f[2 * e + 1]), ptx::f2_pack(inv, inv)) << (8 * (e % 4));
         *reinterpret_cast<uint2*>(blk + L::kcode(x) + c * 8) = make_uint2(w[0], w[1]);
         blk[L::kscale(x, c)] = (uint8_t)sb;
     }
@@ -278,13 +292,12 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const Row
     float f[16], g[16];
     vr_[0].unpack(f);
     vr_[1].unpack(g);
-    const uint32_t sf = scale_byte(amax16(f), p.v_six), sg = scale_byte(amax16(g), p.v_six);
-    const float vf = scale_value(sf) * p.v_scale, vg = scale_value(sg) * p.v_scale;
-    const float nf = vf > 0.f ? __frcp_rn(vf) : 0.f, ng = vg > 0.f ? __frcp_rn(vg) : 0.f;
+    const uint32_t both = scale_bytes(vr_[0].amax(), vr_[1].amax(), p.v_inv_six), sf = both & 0xFFu, sg = both >> 8;
+    const uint64_t inv = ptx::f2_pack(reciprocal(scale_value(sf) * p.v_scale), reciprocal(scale_value(sg) * p.v_scale));
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 16; ++i)  // channel i of both keys
-        w[i / 4] |= codes2(f[i], g[i], nf, ng) << (8 * (i % 4));
+        w[i / 4] |= codes2(ptx::f2_pack(f[i], g[i]), inv) << (8 * (i % 4));
     uint4* const at = reinterpret_cast<uint4*>(blk + L::vcode(2 * r0) + c * 16);
     if (!(even && odd)) {
         const uint4 old = *at;
@@ -299,7 +312,7 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const Row
         return;
     }
     *at = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint16_t*>(blk + L::vscale(2 * r0, c)) = (uint16_t)(sf | sg << 8);
+    *reinterpret_cast<uint16_t*>(blk + L::vscale(2 * r0, c)) = (uint16_t)both;
 }
 
 __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float s)

@@ -177,3 +177,39 @@ def test_lengths_and_tables_are_read_when_the_call_runs():
         assert torch.equal(o, a) and torch.equal(lse, b), new
         check_attention(o, lse, q.cpu(), (pool, table, lens), False, 1 / math.sqrt(d), str(new))
     assert fa.check_device_status() == 0
+
+
+def test_an_explicit_stream():
+    """stream= runs the call, and gives its workspace and results, on that stream: while the current stream is busy
+    and reuses the memory it frees, the results stay right."""
+    B, H, Hkv, d, n = 2, 8, 2, 128, 300
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    pool = fa.qcache_pool(B * 8, Hkv, d)
+    table = torch.arange(B * 8, dtype=torch.int32, device="cuda").reshape(B, 8)
+    q, k, v = rand((B, H, 1, d), 1), rand((B, Hkv, n, d), 2), rand((B, Hkv, n, d), 3)
+    freqs, _ = fa.rope_frequencies(d)
+    zero = torch.zeros((B, Hkv, 512), device="cuda")
+    table_out = table[:, 4:].contiguous()
+
+    def calls(stream):
+        q2, _ = fa.rope(q, None, freqs, lens=lens, stream=stream)
+        fa.qcache_append(k, v, pool, table, lens, stream=stream)
+        o, lse = fa.qcache_decode(q2, pool, table, lens, stream=stream)
+        w = fa.qcache_weights(q2, lse, pool, table, lens, zero, stream=stream)
+        kept, new, w2 = fa.qcache_evict(pool, table, lens, w, 100, table_out=table_out, stream=stream)
+        return [q2, o, lse, w, kept, new, w2, *fa.qcache_read(pool, table_out, new, 100, d, stream=stream)]
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        a = torch.randn((2048, 2048), device="cuda")
+        for _ in range(10):  # keeps the current stream busy, allocating and freeing
+            a = (a @ a).clamp(-1, 1)
+        got = calls(side)
+        junk = [torch.full_like(t, 7) for t in got]
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+        del junk
+    assert fa.check_device_status() == 0
