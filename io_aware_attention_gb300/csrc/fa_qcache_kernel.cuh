@@ -650,37 +650,47 @@ struct Rows {
 // product, so that few rows waste no tensor work.  Lane (g, t) of s[r][nt]
 // holds keys 16r + g (entries 0, 1) and 16r + 8 + g (2, 3) against rows 2t and
 // 2t + 1.  blk: a page's block in shared or global memory.
-template <int D, int NT>
+template <int D, int NT, int TOGETHER>
 __device__ __forceinline__ void page_scores(const uint8_t* blk, const Rows<D, NT>& rows, float (&s)[4][NT][4])
 {
     using L = Block<D>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     Chunk<8 * L::P> sc;
     sc.load(blk + L::KS + lane * (8 * L::P));
+    // TOGETHER groups of 16 keys at a time: a product waits for the one before it
+    // on the same sums, and another group's fill the wait.
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        Chunk<D / 8> k0, k1;
-        k0.load(blk + L::kcode(16 * r + g) + t * (D / 8));
-        k1.load(blk + L::kcode(16 * r + 8 + g) + t * (D / 8));
-        // Scales: at D = 128 those of rows g and g + 8, each of the lane's two
-        // channel blocks; at D = 64 one of each row.
-        const uint32_t f0 = e4m3x2(D == 128 ? sc.w[r] : sc.w[r / 2] >> (16 * (r % 2)));
-        const uint32_t f1 = D == 128 ? e4m3x2(sc.w[r] >> 16) : f0;
+    for (int r0 = 0; r0 < 4; r0 += TOGETHER) {
+        Chunk<D / 8> k[TOGETHER][2];
+        uint32_t f[TOGETHER][2];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            const uint32_t w0 = k0.w[c / 2], w1 = k1.w[c / 2];
-            auto by0 = [&](uint32_t a) { return D == 128 && c >= 4 ? hmul2_by<1>(a, f0) : hmul2_by<0>(a, f0); };
-            auto by1 = [&](uint32_t a) { return D == 64 || c >= 4 ? hmul2_by<1>(a, f1) : hmul2_by<0>(a, f1); };
-            const uint32_t a0 = by0(c % 2 ? e2m1x2<2>(w0) : e2m1x2<0>(w0));
-            const uint32_t a1 = by1(c % 2 ? e2m1x2<2>(w1) : e2m1x2<0>(w1));
-            const uint32_t a2 = by0(c % 2 ? e2m1x2<3>(w0) : e2m1x2<1>(w0));
-            const uint32_t a3 = by1(c % 2 ? e2m1x2<3>(w1) : e2m1x2<1>(w1));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (c == 0) mma_zero(s[r][nt], a0, a1, a2, a3, rows.q[nt][c][0], rows.q[nt][c][1]);
-                else mma(s[r][nt], a0, a1, a2, a3, rows.q[nt][c][0], rows.q[nt][c][1]);
-            }
+        for (int i = 0; i < TOGETHER; ++i) {
+            const int r = r0 + i;
+            k[i][0].load(blk + L::kcode(16 * r + g) + t * (D / 8));
+            k[i][1].load(blk + L::kcode(16 * r + 8 + g) + t * (D / 8));
+            // Scales: at D = 128 those of rows g and g + 8, each of the lane's two
+            // channel blocks; at D = 64 one of each row.
+            f[i][0] = e4m3x2(D == 128 ? sc.w[r] : sc.w[r / 2] >> (16 * (r % 2)));
+            f[i][1] = D == 128 ? e4m3x2(sc.w[r] >> 16) : f[i][0];
         }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int i = 0; i < TOGETHER; ++i) {
+                const uint32_t w0 = k[i][0].w[c / 2], w1 = k[i][1].w[c / 2];
+                auto by0 = [&](uint32_t a) { return D == 128 && c >= 4 ? hmul2_by<1>(a, f[i][0]) : hmul2_by<0>(a, f[i][0]); };
+                auto by1 = [&](uint32_t a) { return D == 64 || c >= 4 ? hmul2_by<1>(a, f[i][1]) : hmul2_by<0>(a, f[i][1]); };
+                const uint32_t a0 = by0(c % 2 ? e2m1x2<2>(w0) : e2m1x2<0>(w0));
+                const uint32_t a1 = by1(c % 2 ? e2m1x2<2>(w1) : e2m1x2<0>(w1));
+                const uint32_t a2 = by0(c % 2 ? e2m1x2<3>(w0) : e2m1x2<1>(w0));
+                const uint32_t a3 = by1(c % 2 ? e2m1x2<3>(w1) : e2m1x2<1>(w1));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float(&d)[4] = s[r0 + i][nt];
+                    if (c == 0) mma_zero(d, a0, a1, a2, a3, rows.q[nt][c][0], rows.q[nt][c][1]);
+                    else mma(d, a0, a1, a2, a3, rows.q[nt][c][0], rows.q[nt][c][1]);
+                }
+            }
     }
 }
 
@@ -1176,7 +1186,7 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
             uint32_t pb[4][NT][2];
             const uint8_t* blk = feed.wait(abort_flag);
             if (!blk) break;
-            page_scores<D, NT>(blk, rows, s);
+            page_scores<D, NT, 1>(blk, rows, s);
             feed.next();
             if (there) st.add_scores(s, rows, page, pb);
             blk = feed.wait(abort_flag);
@@ -1338,7 +1348,7 @@ __global__ void __launch_bounds__(256) fa_qcache_combine_kernel(const DecParams 
 // from the logsumexps that decode returned.  Only K is read.  Two blocks of 8
 // warps an SM, a page a warp as in decode, but every unit is a page of a kv head
 // with all its query rows, so a key's sum is one warp's and needs no atomics.
-// 8 x 8 heads x 30000 to 32768 keys, 8 rows each, d = 128 (161 MB): 36.9 us, 0.65
+// 8 x 8 heads x 30000 to 32768 keys, 8 rows each, d = 128 (161 MB): 35.3 us, 0.68
 // of the measured copy bandwidth; 5 us are the start, the rest is bound by
 // instructions (about 700 a page with the warp's start spread over 13 pages).
 template <int D>
@@ -1442,7 +1452,9 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
             }
             if (!there) continue;
             float s[4][NT][4];
-            page_scores<D, NT>(blk, rows, s);
+            // (8 x 8 heads x 32768 keys, 8 rows: 35.3 us with two groups together, 36.9 with one; decode and more
+            // rows have products of their own to fill the waits and lose registers.)
+            page_scores<D, NT, NT == 1 ? 2 : 1>(blk, rows, s);
             const bool whole = (page + 1) * PAGE <= rows.min_lim;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
