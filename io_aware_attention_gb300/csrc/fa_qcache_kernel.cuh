@@ -886,8 +886,11 @@ template <int D, int NT>
 struct DecLayout {
     static constexpr int WARPS = D == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 16 : 12);
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int SLOTS = D == 128 ? 3 : NT == 1 ? 4 : 6;
-    static constexpr int HALF = 36 * D;
+    // A slot holds half a page (K or V) at 128 channels and a whole one at 64:
+    // copies of 4608 bytes either way.
+    static constexpr int SLOTS = D == 128 || NT == 2 ? 3 : 2;
+    static constexpr bool WHOLE = D == 64;
+    static constexpr int HALF = 36 * 128;
     static constexpr int PART = Piece<D, 8 * NT>::FLOATS * 4;
     static constexpr int RING = SLOTS * HALF;
     static constexpr int PREFIX = WARPS * (RING + PART);
@@ -902,12 +905,12 @@ struct DecLayout {
 };
 
 // A warp's copies of its run of pages into its ring.  SLOTS halves (K, then V;
-// or K alone) are in flight; the warp waits for one, reads it and refills its
+// or K alone; or WHOLE pages) are in flight; the warp waits for one, reads it and refills its
 // slot.  The places of 32 units are looked up at once, one a lane, the next
 // 32 ahead of their use.
-template <int D, int SLOTS, bool WITH_V>
+template <int D, int SLOTS, bool WITH_V, bool WHOLE>
 struct Feed {
-    static constexpr int HALF = 36 * D, PER = WITH_V ? 2 : 1;
+    static constexpr int HALF = WHOLE ? 72 * D : 36 * D, PER = WITH_V && !WHOLE ? 2 : 1;
     const DecParams& p;
     const Work& work;
     uint8_t* ring;
@@ -973,7 +976,7 @@ struct Feed {
     {
         ptx::mbar_arrive_expect_tx(bar + 8 * slot, HALF);
         if (!(p.debug_skip == unit && base == 0 && blockIdx.x == 0))
-            ptx::bulk_load(ptx::smem_addr(ring) + slot * HALF, from + (WITH_V ? half * HALF : 0), HALF, bar + 8 * slot);
+            ptx::bulk_load(ptx::smem_addr(ring) + slot * HALF, from + (PER == 2 ? half * HALF : 0), HALF, bar + 8 * slot);
     }
     // Starts the next copy, if one is left.
     __device__ __forceinline__ void issue()
@@ -1162,7 +1165,7 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
         };
         // Copies run ahead of the arithmetic by the ring's slots: K and V halves
         // of the pages in turn, each slot refilled as soon as the warp has read it.
-        Feed<D, Y::SLOTS, true> feed(smem + Y::ring(warp), ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
+        Feed<D, Y::SLOTS, true, Y::WHOLE> feed(smem + Y::ring(warp), ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
         typename Rows<D, NT>::Raw raw;
         for (int x = x0; x < x1; ++x) {
             const int next_seg = feed.place(x);
@@ -1188,10 +1191,14 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
             const uint8_t* blk = feed.wait(abort_flag);
             if (!blk) break;
             page_scores<D, NT, 1>(blk, rows, s);
-            feed.next();
+            if constexpr (!Y::WHOLE) feed.next();
             if (there) st.add_scores(s, rows, page, pb);
-            blk = feed.wait(abort_flag);
-            if (!blk) break;
+            if constexpr (Y::WHOLE) {
+                blk += Block<D>::VC;
+            } else {
+                blk = feed.wait(abort_flag);
+                if (!blk) break;
+            }
             if (there) st.add_values(blk, rows, page, pb);
             feed.next();
         }
@@ -1401,7 +1408,7 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
     Rows<D, NT> rows;
     uint64_t off[NT], sc[NT];  // of the lane's two columns: scores' factors, and -lse in base 2
     int have = -1;             // segment (with row block) whose rows are loaded
-    Feed<D, Y::SLOTS, false> feed(smem + warp * Y::RING, ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
+    Feed<D, Y::SLOTS, false, false> feed(smem + warp * Y::RING, ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
     typename Rows<D, NT>::Raw raw;
     int seg = feed.place(x0), page = feed.first_page;
     // A lane's part of the weights: keys 16t + g and 16t + 8 + g of a page,
