@@ -948,12 +948,17 @@ struct Feed {
         const int hr = seg % work.hr;
         return id * p.hkv + (work.hr == p.hkv ? hr : hr / p.rb);
     }
-    __device__ __forceinline__ Feed(uint8_t* ring_, uint32_t bar_, const DecParams& p_, const Work& work_, int x0, int x1_)
-        : p(p_), work(work_), ring(ring_), bar(bar_), x1(x1_), base(x0), next_unit(x0), next_half(0), fill(0), use(0),
-          parity(0), flying(0), src(nullptr)
+    __device__ __forceinline__ Feed(uint8_t* ring_, uint32_t bar_, const DecParams& p_, const Work& work_)
+        : p(p_), work(work_), ring(ring_), bar(bar_), fill(0), use(0), parity(0), flying(0), src(nullptr)
     {
-        const int lane = threadIdx.x & 31;
-        first_page = __shfl_sync(0xffffffffu, look(base + lane, now_seg, now_blk), 0);
+    }
+    // Takes up units x0 .. x1_ - 1 (nothing is in flight).
+    __device__ __forceinline__ void start(int x0, int x1_)
+    {
+        x1 = x1_;
+        base = next_unit = x0;
+        next_half = 0;
+        first_page = __shfl_sync(0xffffffffu, look(base + (int)(threadIdx.x & 31), now_seg, now_blk), 0);
         ahead_seg = ahead_blk = -1;
         due = x1 - base > 32;
     }
@@ -964,8 +969,8 @@ struct Feed {
         const int lane = threadIdx.x & 31;
         const int blk = __shfl_sync(0xffffffffu, now_blk, lane / PER);
         flying = min(SLOTS, (x1 - base) * PER);
-        if (lane < flying) copy(lane, lane / PER, lane % PER, source(blk));
-        fill = flying == SLOTS ? 0 : flying;
+        if (lane < flying) copy(fill + lane < SLOTS ? fill + lane : fill + lane - SLOTS, lane / PER, lane % PER, source(blk));
+        fill = fill + flying < SLOTS ? fill + flying : fill + flying - SLOTS;
         next_unit = base + flying / PER;
         next_half = flying % PER;
         if (next_half != 0) src = source(__shfl_sync(0xffffffffu, now_blk, next_unit - base));
@@ -1165,7 +1170,8 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
         };
         // Copies run ahead of the arithmetic by the ring's slots: K and V halves
         // of the pages in turn, each slot refilled as soon as the warp has read it.
-        Feed<D, Y::SLOTS, true, Y::WHOLE> feed(smem + Y::ring(warp), ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
+        Feed<D, Y::SLOTS, true, Y::WHOLE> feed(smem + Y::ring(warp), ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work);
+        feed.start(x0, x1);
         typename Rows<D, NT>::Raw raw;
         for (int x = x0; x < x1; ++x) {
             const int next_seg = feed.place(x);
@@ -1408,98 +1414,117 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
     Rows<D, NT> rows;
     uint64_t off[NT], sc[NT];  // of the lane's two columns: scores' factors, and -lse in base 2
     int have = -1;             // segment (with row block) whose rows are loaded
-    Feed<D, Y::SLOTS, false, false> feed(smem + warp * Y::RING, ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work, x0, x1);
+    Feed<D, Y::SLOTS, false, false> feed(smem + warp * Y::RING, ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work);
     typename Rows<D, NT>::Raw raw;
-    int seg = feed.place(x0), page = feed.first_page;
     // A lane's part of the weights: keys 16t + g and 16t + 8 + g of a page,
     // fetched while the page before is worked on.
     auto weights_at = [&](int seg_, int page_) { return (int64_t)seg_ * p.w_len + page_ * PAGE + 16 * t + g; };
     float w_next[2] = {0.f, 0.f};
-    auto fetch_weights = [&](int seg_, int page_) {
-        const float* const w = p.w_in + weights_at(seg_, page_);
+    auto fetch_weights = [&](int rbi, int seg_, int page_) {
+        const float* const w = (rbi == 0 ? p.w_in : p.w_out) + weights_at(seg_, page_);
         const int64_t left = p.w_len - (page_ * PAGE + 16 * t + g);
         if (left > 0) w_next[0] = w[0];
         if (left > 8) w_next[1] = w[8];
     };
-    fetch_weights(seg, page);
-    feed.begin();
-    bool there = feed.there(x0);
-    for (int x = x0; x < x1; ++x) {
-        const float w_now[2] = {w_next[0], w_next[1]};
-        bool there_next = false;
-        int seg_next = seg, page_next = page;
-        if (x + 1 < x1) {
-            seg_next = feed.place(x + 1);
-            there_next = feed.there(x + 1);
-            page_next = seg_next == seg ? page + 1 : 0;
-            fetch_weights(seg_next, page_next);
+    // With one row block the warp goes through its run once.  With more, it goes
+    // through one segment's pages once a row block, adding to what the last time
+    // wrote (its own lanes did): a row block's query rows stay in registers.
+    bool ok = true;
+    for (int xa = x0, xb; ok && xa < x1; xa = xb) {
+        xb = x1;
+        if (p.rb > 1) {
+            const Work::Unit u = work.at(xa);
+            xb = min(x1, xa + u.pages - u.page);
         }
-        const uint8_t* const blk = feed.wait(abort_flag);
-        if (!blk) break;
-        float sum[8] = {};
-        for (int rbi = 0; rbi < p.rb; ++rbi) {
-            if (seg * p.rb + rbi != have) {
-                have = seg * p.rb + rbi;
-                const int b = seg / p.hkv, hr = (seg - b * p.hkv) * p.rb + rbi;
-                rows.fetch(raw, p, b, hr);
-                rows.load(raw, p, hr);
-                const float* const lse = p.lse_in + (int64_t)seg * p.rows;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float e[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int r = rbi * 8 * NT + nt * 8 + 2 * t + j;
-                        // A row that saw nothing (or is none) gives nothing: 2^-inf.
-                        const float v = r < p.rows ? lse[r] : -INFINITY;
-                        e[j] = v == -INFINITY ? v : -v * 1.4426950408889634f;
-                    }
-                    off[nt] = ptx::f2_pack(e[0], e[1]);
-                    sc[nt] = ptx::f2_pack(rows.sc[nt][0], rows.sc[nt][1]);
+        for (int rbi = 0; ok && rbi < p.rb; ++rbi) {
+            feed.start(xa, xb);
+            int seg = feed.place(xa), page = feed.first_page;
+            fetch_weights(rbi, seg, page);
+            feed.begin();
+            bool there = feed.there(xa);
+            for (int x = xa; x < xb; ++x) {
+                const float w_now[2] = {w_next[0], w_next[1]};
+                bool there_next = false;
+                int seg_next = seg, page_next = page;
+                if (x + 1 < xb) {
+                    seg_next = feed.place(x + 1);
+                    there_next = feed.there(x + 1);
+                    page_next = seg_next == seg ? page + 1 : 0;
+                    fetch_weights(rbi, seg_next, page_next);
                 }
-            }
-            if (!there) continue;
-            float s[4][NT][4];
-            // (8 x 8 heads x 32768 keys, 8 rows: 35.3 us with two groups together, 36.9 with one; decode and more
-            // rows have products of their own to fill the waits and lose registers.)
-            page_scores<D, NT, NT == 1 ? 2 : 1>(blk, rows, s);
-            const bool whole = (page + 1) * PAGE <= rows.min_lim;
+                if (seg * p.rb + rbi != have) {
+                    have = seg * p.rb + rbi;
+                    const int b = seg / p.hkv, hr = (seg - b * p.hkv) * p.rb + rbi;
+                    rows.fetch(raw, p, b, hr);
+                    const float* const lse = p.lse_in + (int64_t)seg * p.rows;
+                    float e[NT][2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                        for (int j = 0; j < 2; ++j) {
+                            const int r = rbi * 8 * NT + nt * 8 + 2 * t + j;
+                            // A row that saw nothing (or is none) gives nothing: 2^-inf.
+                            e[nt][j] = r < p.rows ? lse[r] : -INFINITY;
+                        }
+                    rows.load(raw, p, hr);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float x0_, x1_;
-                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[r][nt][2 * half], s[r][nt][2 * half + 1]), sc[nt], off[nt]), x0_, x1_);
-                        if (!whole) {
-                            const int key = page * PAGE + 16 * r + 8 * half + g;
-                            if (key >= rows.lim[nt][0]) x0_ = -INFINITY;
-                            if (key >= rows.lim[nt][1]) x1_ = -INFINITY;
-                        }
-                        sum[2 * r + half] += ptx::ex2(x0_) + ptx::ex2(x1_);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) e[nt][j] = e[nt][j] == -INFINITY ? e[nt][j] : -e[nt][j] * 1.4426950408889634f;
+                        off[nt] = ptx::f2_pack(e[nt][0], e[nt][1]);
+                        sc[nt] = ptx::f2_pack(rows.sc[nt][0], rows.sc[nt][1]);
                     }
                 }
+                const uint8_t* const blk = feed.wait(abort_flag);
+                if (!blk) {
+                    ok = false;
+                    break;
+                }
+                float sum[8] = {};
+                if (there) {
+                    // (8 x 8 heads x 32768 keys, 8 rows: 35.3 us with two groups together, 36.9 with one; decode and
+                    // more rows have products of their own to fill the waits and lose registers.)
+                    float s[4][NT][4];
+                    page_scores<D, NT, NT == 1 ? 2 : 1>(blk, rows, s);
+                    const bool whole = (page + 1) * PAGE <= rows.min_lim;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float x0_, x1_;
+                                ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[r][nt][2 * half], s[r][nt][2 * half + 1]), sc[nt], off[nt]), x0_, x1_);
+                                if (!whole) {
+                                    const int key = page * PAGE + 16 * r + 8 * half + g;
+                                    if (key >= rows.lim[nt][0]) x0_ = -INFINITY;
+                                    if (key >= rows.lim[nt][1]) x1_ = -INFINITY;
+                                }
+                                sum[2 * r + half] += ptx::ex2(x0_) + ptx::ex2(x1_);
+                            }
+                        }
+                }
+                feed.next();
+                // Sums over the four lanes that share a key's columns, each lane ending
+                // with the two keys it writes: half of the keys change hands, then half
+                // of those left.
+                const bool up2 = t & 2, up1 = t & 1;
+                float four[4], two[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    four[e] = (up2 ? sum[4 + e] : sum[e]) + __shfl_xor_sync(0xffffffffu, up2 ? sum[e] : sum[4 + e], 2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    two[e] = (up1 ? four[2 + e] : four[e]) + __shfl_xor_sync(0xffffffffu, up1 ? four[e] : four[2 + e], 1);
+                float* const w = p.w_out + weights_at(seg, page);
+                const int64_t left = min((int64_t)rows.len, p.w_len) - (page * PAGE + 16 * t + g);
+                if (left > 0) w[0] = w_now[0] + two[0];
+                if (left > 8) w[8] = w_now[1] + two[1];
+                seg = seg_next;
+                page = page_next;
+                there = there_next;
+            }
         }
-        feed.next();
-        // Sums over the four lanes that share a key's columns, each lane ending
-        // with the two keys it writes: half of the keys change hands, then half
-        // of those left.
-        const bool up2 = t & 2, up1 = t & 1;
-        float four[4], two[2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            four[e] = (up2 ? sum[4 + e] : sum[e]) + __shfl_xor_sync(0xffffffffu, up2 ? sum[e] : sum[4 + e], 2);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            two[e] = (up1 ? four[2 + e] : four[e]) + __shfl_xor_sync(0xffffffffu, up1 ? four[e] : four[2 + e], 1);
-        float* const w = p.w_out + weights_at(seg, page);
-        const int64_t left = min((int64_t)rows.len, p.w_len) - (page * PAGE + 16 * t + g);
-        if (left > 0) w[0] = w_now[0] + two[0];
-        if (left > 8) w[8] = w_now[1] + two[1];
-        seg = seg_next;
-        page = page_next;
-        there = there_next;
     }
     feed.drain(abort_flag);
 }
