@@ -1054,12 +1054,12 @@ struct Feed {
 // workspace (two a block at most) for the combine kernel.
 //
 // Bound by reading the cache: 8 x 32 heads x 32768 keys at d = 128 (1.21 GB) in
-// 207 us with the combine kernel, 5819 GB/s, 0.86 of the measured copy
+// 206 us with the combine kernel, 5870 GB/s, 0.87 of the measured copy
 // bandwidth; the same attention over a bf16 cache takes 590 us.  In the loop a
 // page (9216 bytes) takes an SM 430 cycles where the copy bandwidth alone gives
 // about 400; the conversions (280 a page, 2 a clock) need 140 of them, the fp16
 // multiplies 128 and the products 128, on pipes of their own.  The rest is the
-// start (lengths, page table, query rows: 8 us) and the join.
+// start (lengths, page table, query rows: 7 us) and the join.
 template <int D, int NT>
 __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode_kernel(const DecParams p)
 {
@@ -1362,7 +1362,7 @@ __global__ void __launch_bounds__(256) fa_qcache_combine_kernel(const DecParams 
 // from the logsumexps that decode returned.  Only K is read.  Two blocks of 8
 // warps an SM, a page a warp as in decode, but every unit is a page of a kv head
 // with all its query rows, so a key's sum is one warp's and needs no atomics.
-// 8 x 8 heads x 30000 to 32768 keys, 8 rows each, d = 128 (161 MB): 35.3 us, 0.68
+// 8 x 8 heads x 30000 to 32768 keys, 8 rows each, d = 128 (161 MB): 34.5 us, 0.69
 // of the measured copy bandwidth; 5 us are the start, the rest is bound by
 // instructions (about 700 a page with the warp's start spread over 13 pages).
 template <int D>

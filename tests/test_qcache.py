@@ -670,3 +670,63 @@ def test_a_page_table_with_much_more_room_than_keys():
     assert torch.equal(*w)
     r = [fa.qcache_evict(*dev(pool, t, lens_t), w[0], 30) for t in (table, wide)]
     assert torch.equal(r[0][0], r[1][0]) and torch.equal(r[0][2], r[1][2]) and fa.check_device_status() == 0
+
+
+@gpu
+def test_sequences_that_share_pages():
+    """A common prefix held once: sequences whose tables begin with the same pages read, attend, gather weights and
+    are cut back (into pages of their own) as if each held a copy; appending goes to their own last pages."""
+    d, Hkv, n = 64, 2, [200, 170, 200]
+    pool, table, lens = ref.make_cache([200, 0, 0], Hkv, d, seed=5, max_pages=4, spare=20)
+    free = [p for p in range(len(pool)) if p not in set(table[0].tolist())]
+    own = torch.tensor(free[:12], dtype=torch.int32).reshape(3, 4)
+    shared = table[0].repeat(3, 1)
+    shared[:, 2:] = own[:, :2]          # the first 128 keys are common
+    for b in range(3):                  # copies of the rest
+        pool[shared[b, 2].long()], pool[shared[b, 3].long()] = pool[table[0, 2].long()], pool[table[0, 3].long()]
+    lens = torch.tensor(n, dtype=torch.int32)
+    k, v = rand((3, Hkv, 20, d), 1), rand((3, Hkv, 20, d), 2)
+    q = rand((3, 4, 1, d), 3).cuda()
+    pd, td, ld = dev(pool, shared, lens)
+    fa.qcache_append(*dev(k, v), pd, td, ld)
+    ks, vs = ref.unpack(pd, td, ld, d)
+    for b in range(3):
+        assert np.array_equal(ks[b][:, :128], ks[0][:, :128])
+        code, byte = ref.quantise(k[b].double().numpy())
+        assert np.array_equal(ks[b][:, n[b] - 20:], ref.value(code, byte)[..., :d])
+    o, lse = fa.qcache_decode(q, pd, td, ld)
+    check_attention(o, lse, q.cpu(), (pd, td, ld), False, 1 / math.sqrt(d))
+    w = fa.qcache_weights(q, lse, pd, td, ld, torch.zeros((3, Hkv, 256), device="cuda"))
+    out = torch.tensor(free[12:18], dtype=torch.int32).reshape(3, 2).cuda()
+    kept, new, _ = fa.qcache_evict(pd, td, ld, w, 90, sink=3, recent=20, table_out=out)
+    k2, v2 = ref.unpack(pd, out, new, d)
+    assert fa.check_device_status() == 0
+    for b in range(3):
+        for h in range(Hkv):
+            src = choose(w[b, h].cpu().numpy(), n[b], 90, 3, 20)
+            assert kept[b, h].tolist() == src
+            assert np.array_equal(k2[b][h], ks[b][h][src]) and np.array_equal(v2[b][h], vs[b][h][src])
+
+
+@gpu
+@pytest.mark.parametrize("call", ["decode", "weights"])
+def test_many_rows_over_ragged_segments(call):
+    """40 and 64 query rows a kv head (several row blocks) over sequences that begin and end inside warps' runs."""
+    for d, H, Hkv, Nq, lens in ((64, 16, 2, 5, [700, 3, 0, 64, 1290]), (128, 8, 1, 8, [3000, 65, 1, 400])):
+        cache = ref.make_cache(lens, Hkv, d, seed=H)
+        q = rand((len(lens), H, Nq, d), 7)
+        dc = dev(*cache)
+        o, lse = fa.qcache_decode(q.cuda(), *dc, causal=True, scale=0.15)
+        if call == "decode":
+            check_attention(o, lse, q, cache, True, 0.15, f"{H * Nq // Hkv} rows")
+            continue
+        W = max(lens) + 1
+        before = torch.rand((len(lens), Hkv, W), generator=torch.Generator().manual_seed(2))
+        w = fa.qcache_weights(q.cuda(), lse, *dc, before.cuda(), causal=True, scale=0.15)
+        same = before.cuda()
+        fa.qcache_weights(q.cuda(), lse, *dc, same, causal=True, scale=0.15, out=same)
+        assert torch.equal(w, same)
+        ks, _ = ref.unpack(*cache, d)
+        w64, drive = ref.gathered(q, lse, ks, True, 0.15, W)
+        want = before.double().numpy() + w64
+        assert (np.abs(w.double().cpu().numpy() - want) <= 2.0 ** -18 * drive + 2.0 ** -20 * want).all()
