@@ -1305,6 +1305,9 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
 // Joins the pieces of the segment that begins in block blockIdx.x and ends in
 // a later one: its own second piece and the first pieces of the blocks after.
 // Every row is one block's; 8 groups of 32 threads take every eighth piece.
+// Bound by its launch and two round trips to L2 (about 3 us); one block of 1024
+// threads for all of a segment's rows saved 1 us where segments have two or
+// three pieces and cost 8 us for one sequence in 152 pieces.
 template <int D, int NT>
 __global__ void __launch_bounds__(256) fa_qcache_combine_kernel(const DecParams p)
 {
