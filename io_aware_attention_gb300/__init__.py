@@ -181,6 +181,15 @@ def _on_current_device(dev: int) -> None:
                          f"call under torch.cuda.device({dev})")
 
 
+def _cuda_device() -> int:
+    """The current CUDA device of this thread (torch.cuda.current_device without
+    its initialisation check: a CUDA tensor is at hand)."""
+    import torch
+
+    get = getattr(torch._C, "_cuda_getDevice", None)
+    return get() if get is not None else torch.cuda.current_device()
+
+
 def _fast_ok(dev: int, shape, dtype, *ts) -> bool:
     """One pass over tensors that must all be contiguous, of this dtype and
     shape, on CUDA device dev (the common case; any failure is reported by
@@ -560,7 +569,7 @@ def rope(q, k, freqs, positions=None, lens=None, layout: str = "half", factor: f
             return rope(q, k, freqs, positions, lens, layout, factor, inverse)
     sizes = _check_rope(q, k, freqs, positions, lens, layout)
     dev = sizes[0]
-    if torch.cuda.current_device() != dev:
+    if _cuda_device() != dev:
         with torch.cuda.device(dev):
             return rope(q, k, freqs, positions, lens, layout, factor, inverse)
     q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -640,7 +649,7 @@ def qcache_read(pool, table, lens, n: int, d: int, newest: bool = False, k_scale
     n = int(n)
     if n < 1:
         raise ValueError("n must be positive")
-    if torch.cuda.current_device() != dev:
+    if _cuda_device() != dev:
         with torch.cuda.device(dev):
             return qcache_read(pool, table, lens, n, d, newest, k_scale, v_scale)
     k = torch.empty((B, Hkv, n, d), dtype=torch.bfloat16, device=pool.device)
@@ -726,7 +735,7 @@ def qcache_decode(q, pool, table, lens, causal: bool = False, scale: float | Non
             return qcache_decode(q, pool, table, lens, causal, scale, k_scale, v_scale)
     sizes = _check_qcache_query(q, pool, table, lens)
     dev, _, Hkv, max_pages = sizes
-    if torch.cuda.current_device() != dev:
+    if _cuda_device() != dev:
         with torch.cuda.device(dev):
             return qcache_decode(q, pool, table, lens, causal, scale, k_scale, v_scale)
     B, H, Nq, d = q.shape
@@ -749,7 +758,7 @@ def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, sca
         with torch.cuda.stream(stream):
             return qcache_weights(q, lse, pool, table, lens, weights, causal, scale, k_scale, out)
     dev, num_pages, Hkv, max_pages = _check_qcache_query(q, pool, table, lens)
-    if torch.cuda.current_device() != dev:
+    if _cuda_device() != dev:
         with torch.cuda.device(dev):
             return qcache_weights(q, lse, pool, table, lens, weights, causal, scale, k_scale, out)
     B, H, Nq, d = q.shape
@@ -788,7 +797,7 @@ def qcache_evict(pool, table, lens, weights, keep: int, sink: int = 0, recent: i
         with torch.cuda.stream(stream):
             return qcache_evict(pool, table, lens, weights, keep, sink, recent, table_out)
     dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, None)
-    if torch.cuda.current_device() != dev:
+    if _cuda_device() != dev:
         with torch.cuda.device(dev):
             return qcache_evict(pool, table, lens, weights, keep, sink, recent, table_out)
     if weights.dim() != 3:
