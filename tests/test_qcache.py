@@ -730,3 +730,87 @@ def test_many_rows_over_ragged_segments(call):
         w64, drive = ref.gathered(q, lse, ks, True, 0.15, W)
         want = before.double().numpy() + w64
         assert (np.abs(w.double().cpu().numpy() - want) <= 2.0 ** -18 * drive + 2.0 ** -20 * want).all()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 40, 72])
+@pytest.mark.parametrize("H, Hkv, Nq", [(17, 1, 1), (8, 2, 8), (66, 2, 1), (64, 1, 1), (13, 1, 5), (65, 1, 2), (6, 2, 6)])
+def test_decode_of_more_rows_than_a_product_takes(H, Hkv, Nq, d):
+    """17 to 130 query rows a kv head, whole and partial row blocks, over sequences within a block, across
+    blocks, empty, and of one head in many blocks."""
+    for lens, causal in (([300, 0, 64, 1, 6000], True), ([20000], False), ([5, 129, 63], True)):
+        cache = ref.make_cache(lens, Hkv, d, seed=H + d)
+        q = rand((len(lens), H, Nq, d), H, 2.0)
+        o, lse = fa.qcache_decode(q.cuda(), *dev(*cache), causal=causal, scale=0.1)
+        torch.cuda.synchronize()
+        assert fa.check_device_status() == 0
+        check_attention(o, lse, q, cache, causal, 0.1, f"{H * Nq // Hkv} rows, {lens}")
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_skip_pages_out_of_range(d):
+    lens = [150, 64, 3000]
+    pool, table, lens_t = ref.make_cache(lens, 2, d, seed=6)
+    q = rand((3, 40, 1, d), 2)
+    t = table.clone()
+    t[0, 2], t[2, 46] = len(pool), -1
+    o, lse = fa.qcache_decode(q.cuda(), *dev(pool, t, lens_t), scale=0.1)
+    assert fa.check_device_status() == 1 and fa.check_device_status() == 0
+    check_attention(o, lse, q, (pool, table, torch.tensor([128, 64, 46 * 64], dtype=torch.int32)), False, 0.1)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_keep_to_their_own(d):
+    """Queries that are not finite reach their own rows alone; values that are not finite reach every row; the
+    result is the same each time, and the same rows give the same result among others."""
+    lens = [500, 1, 0, 4000]
+    pool, table, lens_t = ref.make_cache(lens, 1, d, seed=8)
+    q = rand((4, 36, 1, d), 5)
+    o, lse = fa.qcache_decode(q.cuda(), *dev(pool, table, lens_t), scale=0.1)
+    check_attention(o, lse, q, (pool, table, lens_t), False, 0.1)
+    for _ in range(5):
+        again = fa.qcache_decode(q.cuda(), *dev(pool, table, lens_t), scale=0.1)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    q2 = q.clone()
+    q2[0, 3, 0, 7], q2[3, 20, 0, 0] = float("nan"), float("inf")
+    o2, lse2 = fa.qcache_decode(q2.cuda(), *dev(pool, table, lens_t), scale=0.1)
+    ok = torch.ones((4, 36), dtype=torch.bool)
+    ok[0, 3] = ok[3, 20] = False
+    assert torch.equal(o2[ok.cuda()], o[ok.cuda()]) and torch.equal(lse2[ok.cuda()], lse[ok.cuda()])
+    assert not torch.isfinite(o2[0, 3]).any() and not torch.isfinite(o2[3, 20]).any()
+    few, few_lse = fa.qcache_decode(q[:, :8].contiguous().cuda(), *dev(pool, table, lens_t), scale=0.1)
+    check_attention(few, few_lse, q[:, :8], (pool, table, lens_t), False, 0.1)
+    x = rand((4, 1, 1, d), 1)
+    x[0, 0, 0, 3] = float("nan")
+    one = torch.tensor([501, 0, 0, 0], dtype=torch.int32)
+    p = pool.cuda()
+    fa.qcache_append(*dev(rand((4, 1, 1, d), 2), x), p, *dev(table, one))
+    o3, _ = fa.qcache_decode(q.cuda(), p, *dev(table, one), scale=0.1)
+    few3, _ = fa.qcache_decode(q[:, :8].contiguous().cuda(), p, *dev(table, one), scale=0.1)
+    assert torch.equal(torch.isfinite(o3[0, :8]), torch.isfinite(few3[0]))
+
+
+@gpu
+def test_a_wait_of_many_rows_that_runs_out():
+    """As above, with several row blocks a kv head."""
+    d, lens = 128, [3000, 200]
+    cache = ref.make_cache(lens, 2, d, seed=3)
+    q = rand((2, 80, 1, d), 1)
+    dc = dev(*cache)
+    o, lse = fa.qcache_decode(q.cuda(), *dc)
+    assert fa.check_device_status() == 0
+    fa.set_wait_limit_ns(20_000_000)  # 20 ms
+    fa.debug_skip_k_tile(0)
+    try:
+        fa.qcache_decode(q.cuda(), *dc)
+        torch.cuda.synchronize()
+        assert fa.check_device_status() == 4  # FA_ERR_TIMEOUT
+    finally:
+        fa.debug_skip_k_tile(-1)
+        fa.set_wait_limit_ns(0)
+    assert fa.check_device_status() == 0
+    o2, lse2 = fa.qcache_decode(q.cuda(), *dc)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    check_attention(o2, lse2, q, cache, False, 1 / math.sqrt(d))
