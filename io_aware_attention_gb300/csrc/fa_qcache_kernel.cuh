@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_read_kernel(const RowPa
     if (tid < PAGE) {
         const int given = p.lens[b];
         const int64_t len = min((int64_t)max(given, 0), (int64_t)p.max_pages * PAGE);
+        if (given > len && tid == 0 && h == 0 && blockIdx.x == 0) atomicOr(&g_status, STATUS_BAD_PAGE);
         const int64_t pos = i0 + tid + (p.newest ? (int64_t)given - p.n : 0);
         int blk = -1;
         if (tid < rows && pos >= 0 && pos < len) {

@@ -814,3 +814,16 @@ def test_a_wait_of_many_rows_that_runs_out():
     o2, lse2 = fa.qcache_decode(q.cuda(), *dc)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     check_attention(o2, lse2, q, cache, False, 1 / math.sqrt(d))
+
+
+@gpu
+@pytest.mark.parametrize("newest", [False, True])
+def test_read_reports_a_length_beyond_the_table(newest):
+    d = 64
+    pool, table, lens = ref.make_cache([150, 64], 2, d, seed=6)
+    long = torch.tensor([table.shape[1] * 64 + 1, 64], dtype=torch.int32)
+    want, _ = fa.qcache_read(*dev(pool, table, lens), 200, d, newest=newest)
+    assert fa.check_device_status() == 0
+    got, _ = fa.qcache_read(*dev(pool, table, long), 200, d, newest=newest)
+    assert fa.check_device_status() == 1 and fa.check_device_status() == 0
+    assert torch.equal(got[1], want[1])
