@@ -1777,7 +1777,8 @@ __global__ void __launch_bounds__(MOVE_THREADS) fa_qcache_move_kernel(const Evic
     const int blocks = p.move_blocks, rank = blockIdx.x % blocks, h = blockIdx.x / blocks, b = blockIdx.y, tid = threadIdx.x;
     const int64_t bh = (int64_t)b * p.hkv + h;
     const int len = length_of(p.lens, b, p.max_pages), count = min(len, p.keep);
-    if (len <= p.keep && p.table_out == p.table) return;  // (the whole cluster) nothing moves
+    // (The whole cluster.)  One table, rows of one pitch: nothing moves.
+    if (len <= p.keep && p.table_out == p.table && p.max_pages_out == p.max_pages) return;
     const int pages = (count + PAGE - 1) / PAGE;
     // Pages of the block in a round: rank, rank + blocks, ... of the round's.
     for (int r0 = 0; r0 < pages; r0 += blocks * MOVE_PAGES) {

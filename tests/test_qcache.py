@@ -827,3 +827,22 @@ def test_read_reports_a_length_beyond_the_table(newest):
     got, _ = fa.qcache_read(*dev(pool, table, long), 200, d, newest=newest)
     assert fa.check_device_status() == 1 and fa.check_device_status() == 0
     assert torch.equal(got[1], want[1])
+
+
+@gpu
+def test_evict_into_a_narrower_table_at_the_same_address():
+    """The destination's rows are entries of the table that hold no key: sequences of at most `keep` keys move too."""
+    d, lens, keep = 64, [100, 90], 100
+    pool, table, lens_t = ref.make_cache(lens, 2, d, seed=3, max_pages=4, spare=8)
+    free = [p for p in range(len(pool)) if p not in set(table[0, :2].tolist()) | set(table[1, :2].tolist())]
+    table[0, 2:] = torch.tensor(free[:2], dtype=torch.int32)
+    pd, td, ld = dev(pool, table, lens_t)
+    out = td.view(-1)[:4].view(2, 2)  # row 1 is row 0's spare entries
+    assert out.data_ptr() == td.data_ptr()
+    ks, vs = ref.unpack(pool, table, lens_t, d)
+    kept, new, _ = fa.qcache_evict(pd, td, ld, torch.rand((2, 2, 100), device="cuda"), keep, table_out=out)
+    assert fa.check_device_status() == 0 and new.tolist() == lens
+    k2, v2 = ref.unpack(pd, out, new, d)
+    for b in range(2):
+        assert np.array_equal(k2[b], ks[b]) and np.array_equal(v2[b], vs[b])
+        assert kept[b, 0, :lens[b]].tolist() == list(range(lens[b]))
