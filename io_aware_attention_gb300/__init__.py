@@ -170,6 +170,15 @@ def _stream_handle(stream, device: int | None = None):
     return int(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _under(stream, t):
+    """The context of a call on tensor t whose results belong to ``stream``."""
+    import torch
+
+    if t.is_cuda and stream.device.index != t.get_device():
+        raise ValueError(f"stream is on {stream.device} but the tensors are on cuda:{t.get_device()}")
+    return torch.cuda.stream(stream)
+
+
 def _on_current_device(dev: int) -> None:
     """The C entry points launch on the calling thread's current device, so
     the tensors must live there."""
@@ -565,7 +574,7 @@ def rope(q, k, freqs, positions=None, lens=None, layout: str = "half", factor: f
     import torch
 
     if stream is not None:  # the results belong to the stream that writes them
-        with torch.cuda.stream(stream):
+        with _under(stream, q):
             return rope(q, k, freqs, positions, lens, layout, factor, inverse)
     sizes = _check_rope(q, k, freqs, positions, lens, layout)
     dev = sizes[0]
@@ -643,7 +652,7 @@ def qcache_read(pool, table, lens, n: int, d: int, newest: bool = False, k_scale
     import torch
 
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, pool):
             return qcache_read(pool, table, lens, n, d, newest, k_scale, v_scale)
     dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, d)
     n = int(n)
@@ -731,7 +740,7 @@ def qcache_decode(q, pool, table, lens, causal: bool = False, scale: float | Non
     import torch
 
     if stream is not None:  # the workspace and the results belong to the stream that writes them
-        with torch.cuda.stream(stream):
+        with _under(stream, q):
             return qcache_decode(q, pool, table, lens, causal, scale, k_scale, v_scale)
     sizes = _check_qcache_query(q, pool, table, lens)
     dev, _, Hkv, max_pages = sizes
@@ -755,7 +764,7 @@ def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, sca
     import torch
 
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, q):
             return qcache_weights(q, lse, pool, table, lens, weights, causal, scale, k_scale, out)
     dev, num_pages, Hkv, max_pages = _check_qcache_query(q, pool, table, lens)
     if _cuda_device() != dev:
@@ -794,7 +803,7 @@ def qcache_evict(pool, table, lens, weights, keep: int, sink: int = 0, recent: i
     import torch
 
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _under(stream, pool):
             return qcache_evict(pool, table, lens, weights, keep, sink, recent, table_out)
     dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, None)
     if _cuda_device() != dev:

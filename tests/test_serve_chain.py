@@ -5,6 +5,7 @@ two streams at once, and against the forward kernel.
 """
 import math
 import threading
+import types
 
 import numpy as np
 import pytest
@@ -213,3 +214,18 @@ def test_an_explicit_stream():
         assert all(torch.equal(x, y) for x, y in zip(want, got))
         del junk
     assert fa.check_device_status() == 0
+
+
+def test_a_stream_of_another_device_is_refused():
+    """A stream that the tensors' device does not have is an error, not a call on some other stream."""
+    other = types.SimpleNamespace(device=torch.device("cuda", torch.cuda.current_device() + 1), cuda_stream=0)
+    pool, table = fa.qcache_pool(2, 1, 64), torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    lens, q = torch.ones(1, dtype=torch.int32, device="cuda"), rand((1, 1, 1, 64), 1)
+    w, lse = torch.zeros((1, 1, 64), device="cuda"), torch.zeros((1, 1, 1), device="cuda")
+    freqs, _ = fa.rope_frequencies(64)
+    for call in (lambda: fa.rope(q, None, freqs, stream=other), lambda: fa.qcache_read(pool, table, lens, 1, 64, stream=other),
+                 lambda: fa.qcache_decode(q, pool, table, lens, stream=other),
+                 lambda: fa.qcache_weights(q, lse, pool, table, lens, w, stream=other),
+                 lambda: fa.qcache_evict(pool, table, lens, w, 1, stream=other)):
+        with pytest.raises(ValueError, match="stream is on"):
+            call()
