@@ -647,14 +647,14 @@ fa_status allow_smem(K kernel, size_t bytes, std::atomic<int>* done, int dev)
     return FA_OK;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool FOLD>
 fa_status launch_qcache_decode(const fa::qc::DecParams& p, int64_t blocks, int dev, cudaStream_t st)
 {
     using Y = fa::qc::DecLayout<D, NT>;
     static std::atomic<int> done[MAX_DEVICES];
-    const fa_status as = allow_smem(fa::qc::fa_qcache_decode_kernel<D, NT>, (size_t)Y::bytes(fa::qc::MAX_B), done, dev);
+    const fa_status as = allow_smem(fa::qc::fa_qcache_decode_kernel<D, NT, FOLD>, (size_t)Y::bytes(fa::qc::MAX_B), done, dev);
     if (as != FA_OK) return as;
-    if (launch_pdl(fa::qc::fa_qcache_decode_kernel<D, NT>, dim3((unsigned)blocks), dim3(Y::THREADS),
+    if (launch_pdl(fa::qc::fa_qcache_decode_kernel<D, NT, FOLD>, dim3((unsigned)blocks), dim3(Y::THREADS),
                    (size_t)Y::bytes(p.B), st, p) != cudaSuccess ||
         launch_pdl(fa::qc::fa_qcache_combine_kernel<D, NT>,
                    dim3((unsigned)blocks, (unsigned)std::min(p.rows, 8 * NT)), dim3(256), 0, st, p) != cudaSuccess)
@@ -1302,8 +1302,12 @@ fa_status fa_qcache_decode(const void* q, const void* pool, int64_t num_pages, c
     p.v_scale = v_scale;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (Dp == 128)
-        return r.nt == 1 ? launch_qcache_decode<128, 1>(p, blocks, dev, st) : launch_qcache_decode<128, 2>(p, blocks, dev, st);
-    return r.nt == 1 ? launch_qcache_decode<64, 1>(p, blocks, dev, st) : launch_qcache_decode<64, 2>(p, blocks, dev, st);
+        return r.rows <= 4 ? launch_qcache_decode<128, 1, true>(p, blocks, dev, st)
+               : r.nt == 1 ? launch_qcache_decode<128, 1, false>(p, blocks, dev, st)
+                           : launch_qcache_decode<128, 2, false>(p, blocks, dev, st);
+    return r.rows <= 4 ? launch_qcache_decode<64, 1, true>(p, blocks, dev, st)
+           : r.nt == 1 ? launch_qcache_decode<64, 1, false>(p, blocks, dev, st)
+                       : launch_qcache_decode<64, 2, false>(p, blocks, dev, st);
 }
 
 fa_status fa_qcache_weights(const void* q, const float* lse, const void* pool, int64_t num_pages, const int32_t* table,

@@ -97,6 +97,13 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
     return r;
 }
 
+// What packing (lo, hi) as fp16 left of them, as fp16.
+__device__ __forceinline__ uint32_t rest_h2(float lo, float hi, uint32_t packed)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&packed));
+    return pack_h2(lo - f.x, hi - f.y);
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
 {
     uint32_t r;
@@ -539,9 +546,11 @@ struct DecParams {
     int64_t w_len;
 };
 
-// A probability is held as 2^(x - max + SHIFT) in fp16 (11 bits): 1 becomes
-// 2^15, within fp16's range, and weights down to 2^-29 of the largest keep
-// full precision, so that a long cache of small weights is not rounded away.
+// A probability 2^(x - max + SHIFT) is held as the sum of two fp16 numbers, its
+// rounding and what that left: 22 bits, fp32's own errors (one alone has 11, and
+// results that nearly cancel lost 2^-12 of sum p |v|).  1 becomes 2^15, within
+// fp16's range, and what lies below fp16's smallest steps is under 2^-40 of the
+// largest weight, so that a long cache of small weights is not rounded away.
 constexpr float SHIFT = 15.0f;
 constexpr uint32_t WAIT_CODE = 900;  // fa_check_device_status's wait code of the cache kernels' copies
 
@@ -580,9 +589,13 @@ __device__ __forceinline__ uint32_t hmul2_by(uint32_t a, uint32_t f)
 // 2t + 1 whose scores it gets, the factor to base-2 scores and the count of
 // keys they see.  Rows are scaled by a power of two so that their largest
 // entry lies in [2^14, 2^15): bf16 entries down to 2^-31 of it are exact in
-// fp16 whatever the row's size.
-template <int D, int NT>
+// fp16 whatever the row's size.  FOLD: at most 4 rows, and the tile's rows 4 to 7 are
+// rows 0 to 3 again (decode uses them for the second halves of probabilities).
+template <int D, int NT, bool FOLD = false>
 struct Rows {
+    static_assert(!FOLD || NT == 1, "one tile, folded");
+    // The query row of a tile's row.
+    static __device__ __forceinline__ int row_of(int r) { return FOLD ? r & 3 : r; }
     uint32_t q[NT][D / 16][2];
     float sc[NT][2];
     int lim[NT][2];
@@ -602,7 +615,7 @@ struct Rows {
         raw.len = p.lens[b];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = r0 + nt * 8 + g;
+            const int row = r0 + nt * 8 + row_of(g);
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
                 const int c = D / 4 * t + 8 * e;
@@ -640,7 +653,7 @@ struct Rows {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 sc[nt][j] = __shfl_sync(0xffffffffu, down, (2 * t + j) * 4);
-                const int r = r0 + nt * 8 + 2 * t + j;
+                const int r = r0 + nt * 8 + row_of(2 * t + j);
                 lim[nt][j] = p.causal && r < p.rows ? len - p.nq + (p.nq == 1 ? 0 : r % p.nq) + 1 : len;
             }
         }
@@ -651,8 +664,8 @@ struct Rows {
 // product, so that few rows waste no tensor work.  Lane (g, t) of s[r][nt]
 // holds keys 16r + g (entries 0, 1) and 16r + 8 + g (2, 3) against rows 2t and
 // 2t + 1.  blk: a page's block in shared or global memory.
-template <int D, int NT, int TOGETHER>
-__device__ __forceinline__ void page_scores(const uint8_t* blk, const Rows<D, NT>& rows, float (&s)[4][NT][4])
+template <int D, int NT, int TOGETHER, bool FOLD>
+__device__ __forceinline__ void page_scores(const uint8_t* blk, const Rows<D, NT, FOLD>& rows, float (&s)[4][NT][4])
 {
     using L = Block<D>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -698,8 +711,15 @@ __device__ __forceinline__ void page_scores(const uint8_t* blk, const Rows<D, NT
 // Running softmax of a warp over a segment's pages, O transposed: lane (g, t)
 // of o[m][nt] holds channels D/8 g + 2m (entries 0, 1) and D/8 g + 2m + 1
 // (2, 3) of rows 2t and 2t + 1.
-template <int D, int NT>
+//
+// A probability is two fp16 numbers, and so V meets two operands.  At most 4 rows
+// (FOLD) take one product for both: the tile's rows 0 to 3 carry the roundings, rows
+// 4 to 7 what those left, and close() adds them up.  (8 x 32 heads x 32768 keys, one
+// row, d = 128: 226 us with two products, 205 folded;
+// 48 x 4 heads x 0 to 5000 keys, 16 rows, d = 64, two products: 28.5 us.)
+template <int D, int NT, bool FOLD>
 struct State {
+    using R = Rows<D, NT, FOLD>;
     float o[D / 16][NT][4];
     // Largest unscaled score (differences to it are scaled, so that the
     // largest key's weight is 1 however large the scores are); this lane's
@@ -719,11 +739,18 @@ struct State {
         }
     }
 
-    // Takes a page's scores in: the running maxima and sums, and the
-    // probabilities as the B operand (keys 2t, 2t + 1 and 2t + 8, 2t + 9 of row g).
-    __device__ __forceinline__ void add_scores(float (&s)[4][NT][4], const Rows<D, NT>& rows, int page, uint32_t (&pb)[4][NT][2])
+    // A page's probabilities as B operands (keys 2t, 2t + 1 and 2t + 8, 2t + 9 of
+    // row g): their fp16 roundings, then what those left.
+    static constexpr int HALVES = FOLD ? 1 : 2;
+    struct Probs {
+        uint32_t w[4][NT][HALVES][2];
+    };
+
+    // Takes a page's scores in: the running maxima and sums, and the probabilities.
+    __device__ __forceinline__ void add_scores(float (&s)[4][NT][4], const R& rows, int page, Probs& pb)
     {
         const int lane = threadIdx.x & 31, g = lane >> 2;
+        const bool second = FOLD && (lane & 2);  // its columns carry the rests
         const int key0 = page * PAGE;
         const bool whole = key0 + PAGE <= rows.min_lim;  // every row sees every key
         bool rises = false;
@@ -790,8 +817,17 @@ struct State {
                     s[r][nt][e] = p0;
                     s[r][nt][e + 1] = p1;
                 }
-                pb[r][nt][0] = transpose8x8(pack_h2(s[r][nt][0], s[r][nt][1]));
-                pb[r][nt][1] = transpose8x8(pack_h2(s[r][nt][2], s[r][nt][3]));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float a = s[r][nt][2 * e], b = s[r][nt][2 * e + 1];
+                    const uint32_t h = pack_h2(a, b);
+                    if constexpr (FOLD) {
+                        pb.w[r][nt][0][e] = transpose8x8(second ? rest_h2(a, b, h) : h);
+                    } else {
+                        pb.w[r][nt][0][e] = transpose8x8(h);
+                        pb.w[r][nt][1][e] = transpose8x8(rest_h2(a, b, h));
+                    }
+                }
             }
             ptx::f2_unpack(sum, l[nt][0], l[nt][1]);
         }
@@ -800,7 +836,7 @@ struct State {
     // O^T += V^T P^T: a scale belongs to a key and a block of channels, so it
     // multiplies the operand (exactly), two keys at a time.  vblk: the V half
     // of a page's block.
-    __device__ __forceinline__ void add_values(const uint8_t* vblk, const Rows<D, NT>& rows, int page, const uint32_t (&pb)[4][NT][2])
+    __device__ __forceinline__ void add_values(const uint8_t* vblk, const R& rows, int page, const Probs& pb)
     {
         using L = Block<D>;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -829,15 +865,23 @@ struct State {
                 const uint32_t a2 = hmul2(c % 2 ? e2m1x2<2>(w1) : e2m1x2<0>(w1), f1);
                 const uint32_t a3 = hmul2(c % 2 ? e2m1x2<3>(w1) : e2m1x2<1>(w1), f1);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma(o[c][nt], a0, a1, a2, a3, pb[r][nt][0], pb[r][nt][1]);
+                for (int half = 0; half < HALVES; ++half)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma(o[c][nt], a0, a1, a2, a3, pb.w[r][nt][half][0], pb.w[r][nt][half][1]);
             }
         }
     }
 
     // The end of a segment: base-2 maxima, and the sums over the warp's lanes
     // that share a row.
-    __device__ __forceinline__ void close(const Rows<D, NT>& rows)
+    __device__ __forceinline__ void close(const R& rows)
     {
+        if constexpr (FOLD) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[c][0][e] += __shfl_xor_sync(0xffffffffu, o[c][0][e], 2);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1061,7 +1105,7 @@ struct Feed {
 // about 400; the conversions (280 a page, 2 a clock) need 140 of them, the fp16
 // multiplies 128 and the products 128, on pipes of their own.  The rest is the
 // start (lengths, page table, query rows: 7 us) and the join.
-template <int D, int NT>
+template <int D, int NT, bool FOLD>
 __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode_kernel(const DecParams p)
 {
     using Y = DecLayout<D, NT>;
@@ -1121,8 +1165,8 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
     int slot = 0;
     if (warp < nw) {
         const int x0 = lo + (int)((int64_t)(hi - lo) * warp / nw), x1 = lo + (int)((int64_t)(hi - lo) * (warp + 1) / nw);
-        Rows<D, NT> rows;
-        State<D, NT> st;
+        Rows<D, NT, FOLD> rows;
+        State<D, NT, FOLD> st;
         int seg = -1, begins = 0, page = 0;
         auto finish = [&] {
             st.close(rows);
@@ -1173,7 +1217,7 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
         // of the pages in turn, each slot refilled as soon as the warp has read it.
         Feed<D, Y::SLOTS, true, Y::WHOLE> feed(smem + Y::ring(warp), ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work);
         feed.start(x0, x1);
-        typename Rows<D, NT>::Raw raw;
+        typename Rows<D, NT, FOLD>::Raw raw;
         for (int x = x0; x < x1; ++x) {
             const int next_seg = feed.place(x);
             ++page;
@@ -1194,7 +1238,7 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
             }
             const bool there = feed.there(x);
             float s[4][NT][4];
-            uint32_t pb[4][NT][2];
+            typename State<D, NT, FOLD>::Probs pb;
             const uint8_t* blk = feed.wait(abort_flag);
             if (!blk) break;
             page_scores<D, NT, 1>(blk, rows, s);
