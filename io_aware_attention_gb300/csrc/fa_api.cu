@@ -1108,7 +1108,8 @@ fa_status fa_rope(const void* q, const int64_t* q_strides, const void* k, const 
     const int64_t w = fits(8) ? 8 : fits(2) ? 2 : 1;
     const int64_t units = interleaved ? (d + 2 * w - 1) / (2 * w) : rot / (2 * w) + (d - rot + 2 * w - 1) / (2 * w);
     const int64_t room = fa::rope::THREADS / units;
-    const int64_t ny = std::min<int64_t>(N, room), nz = std::max<int64_t>(1, std::min<int64_t>(room / ny, Hq + Hk));
+    // (A block's z is at most 64 on any device; ny <= THREADS is within y's 1024.)
+    const int64_t ny = std::min<int64_t>(N, room), nz = std::max<int64_t>(1, std::min<int64_t>({room / ny, Hq + Hk, 64}));
     const int64_t total = Hq + Hk, tiles = (N + ny - 1) / ny;
     const int64_t head_tiles = (total + nz * fa::rope::U - 1) / (nz * fa::rope::U);
     if (tiles > INT32_MAX || B * head_tiles > INT32_MAX / tiles) return FA_ERR_INVALID_ARG;
