@@ -557,19 +557,29 @@ struct RopeView {
     int64_t s[3], H;
 };
 
-// Whether two views may share a place.  Views of one buffer that interleave
-// row by row (the queries and keys of a fused projection) do not when each
-// position's heads stay within its row pitch.
+// Whether two views may share a place.  They cannot where their extents do not
+// meet, nor where some pitch keeps them apart: strides that are multiples of it
+// leave a place's remainder as it is, the others spread it over a run, and two runs
+// that do not meet on the pitch's circle hold no common place.  That lets through the
+// queries and keys of one buffer, by positions (a fused projection), by heads or by
+// batches, with one position or many; a stride over one element means nothing.
 bool may_overlap(const RopeView& x, const RopeView& y, int64_t B, int64_t N, int64_t d)
 {
     if (!overlaps(x.p, (size_t)extent(x.s, B, x.H, N, d) * 2, y.p, (size_t)extent(y.s, B, y.H, N, d) * 2)) return false;
-    const int64_t pitch = x.s[2];
-    if (pitch <= 0 || y.s[2] != pitch || x.s[0] % pitch || y.s[0] % pitch) return true;
     const int64_t bytes = (int64_t)(reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p));
     if (bytes % 2) return true;
-    const int64_t at = ((bytes / 2) % pitch + pitch) % pitch;
-    const int64_t nx = (x.H - 1) * x.s[1] + d, ny = (y.H - 1) * y.s[1] + d;
-    return !(nx <= at && at + ny <= pitch);
+    const RopeView* const v[2] = {&x, &y};
+    for (int k = 0; k < 6; ++k) {
+        const int64_t n[2][3] = {{B, x.H, N}, {B, y.H, N}}, pitch = v[k / 3]->s[k % 3];
+        if (pitch < 1 || n[k / 3][k % 3] == 1) continue;
+        int64_t run[2] = {d, d};
+        for (int i = 0; i < 2; ++i)
+            for (int j = 0; j < 3; ++j)
+                if (n[i][j] > 1 && v[i]->s[j] % pitch) run[i] += (n[i][j] - 1) * v[i]->s[j];
+        const int64_t at = ((bytes / 2) % pitch + pitch) % pitch;  // y's run after x's
+        if (run[0] <= at && run[1] <= pitch - at) return false;
+    }
+    return true;
 }
 
 template <int W>
