@@ -261,9 +261,11 @@ fa_status fa_bias_gelu_dropout(const void *x, const void *bias, const uint32_t *
  * at position t is turned by the angle t * f_i and scaled:
  *     a' = factor * (a cos(t f_i) - b sin(t f_i))
  *     b' = factor * (b cos(t f_i) + a sin(t f_i))
- * Channels from rot on are copied.  Angles are exact for any position: the
- * frequencies are 64-bit fractions of a turn, and position times frequency
- * modulo one turn is an integer product.  Results are rounded to bf16 once.
+ * Channels from rot on are copied.  The frequencies are 64-bit fractions of a
+ * turn, and position times frequency modulo one turn is an integer product,
+ * exact for any position: an angle's error is |t| times that of its frequency
+ * word (at most 2^-65 of a turn when rounded to nearest).  Cosine and sine are
+ * good to 2^-20 of themselves, however small.  Results are rounded to bf16 once.
  *
  * Arguments
  *   q, k       device pointers, bf16, (B, Hq, N, d) and (B, Hk, N, d); k may be

@@ -10,20 +10,22 @@
 //
 // Angles.  f_i comes as turns per position in 64-bit fixed point (units of
 // 2^-64 of a turn), so t * f_i modulo one turn is the low 64 bits of one
-// integer product: no reduction, and no position is too far (an fp32 product
-// t * f_i is off by 0.03 rad at t = 10^6).  The top 32 bits, read as a signed
-// fraction of half a turn, become the angle: within 2^-32 of a turn, and
-// 2^-24 of itself by its rounding to fp32.
+// integer product, exact for any position (an fp32 product t * f_i is off by 0.03
+// rad at t = 10^6); what remains is t times the word's own rounding.  The product
+// is taken to the nearest quarter turn and its distance from there becomes fp32,
+// so that cosine and sine come out to 2^-22 of themselves however small.
 //
 // The work is bound by memory: 4 bytes moved per element against 3 flops.  A
 // thread owns one unit of channels (two 16-byte vectors holding 8 whole
 // pairs) of one position and U = 4 heads, whose loads are in flight while it
 // computes the 8 angles that they share.  Queries and keys go in one launch.
 // Measured at B8 H32 + 32 N4096 d128 (a forward and a gradient, 2.15 GB): 318 us,
-// 6758 GB/s, 1.00 of the measured copy bandwidth.  What brought it there: 4
+// 6746 GB/s, 1.00 of the measured copy bandwidth.  What brought it there: 4
 // blocks an SM instead of 3 (349 -> 328 us; 5 spill, 409 us) and, for results
 // larger than L2, streaming stores (328 -> 318 us); with 2 heads in flight 404
-// us, with the angles computed before the loads 383 us.
+// us, with the angles computed before the loads 383 us.  Where the results go is
+// worked out after the angles: 64 registers hold no more beside the loads in flight
+// (worked out before, 19 words spill: 327 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -68,16 +70,43 @@ __device__ __forceinline__ int64_t position_of(const Params& p, int b, int64_t i
     return (p.lens ? (int64_t)p.lens[b] - p.n : 0) + i;
 }
 
-// cos and sin of the angle of one pair.  The special-function unit's are good to
-// 2^-21 on [-pi, pi], far inside the result's rounding to bf16, and 8 pairs take
-// a tenth of the instructions that sincospif does (which were 4 in 10 of the
-// kernel's).
-__device__ __forceinline__ void turn(int64_t pos, uint64_t freq, float factor, float sign, float& c, float& s)
+// The angle of a pair, from its nearest quarter turn: z in [-1, 1], in units of an
+// eighth of a turn, to fp32's rounding of itself, and the quarter.
+__device__ __forceinline__ void angle(int64_t pos, uint64_t freq, float& z, uint32_t& quarter)
 {
     const uint64_t a = (uint64_t)pos * freq;
-    const float x = (float)(int32_t)(a >> 32) * (0x1p-31f * 3.14159265358979f);
-    c = __cosf(x) * factor;
-    s = __sinf(x) * (factor * sign);
+    z = (float)(int64_t)(a << 2) * 0x1p-63f;
+    quarter = ((uint32_t)(a >> 32) + (1u << 29)) >> 30;
+}
+
+// Cosine and sine of an angle z of at most an eighth of a turn, by their power
+// series up to z^8 and z^9, which leave out at most 2^-25 and 2^-28 of the value: good
+// to fp32's rounding of themselves, however small they are.  (The special-function
+// unit's are good to 2^-21 of 1, which was 1 % of a slow pair's sine.)
+constexpr double EIGHTH = 0.78539816339744830962, E2 = EIGHTH * EIGHTH, E4 = E2 * E2;
+__device__ __forceinline__ void cos_sin(float z, float& c, float& s)
+{
+    const float w = z * z;
+    c = fmaf(w, (float)(E4 * E4 / 40320), (float)(-E4 * E2 / 720));
+    s = fmaf(w, (float)(EIGHTH * E4 * E4 / 362880), (float)(-EIGHTH * E4 * E2 / 5040));
+    c = fmaf(w, c, (float)(E4 / 24));
+    s = fmaf(w, s, (float)(EIGHTH * E4 / 120));
+    c = fmaf(w, c, (float)(-E2 / 2));
+    s = fmaf(w, s, (float)(-EIGHTH * E2 / 6));
+    c = fmaf(w, c, 1.0f);
+    s = z * fmaf(w, s, (float)EIGHTH);
+}
+
+// cos and sin of one pair's angle, scaled: those of its distance from the nearest
+// quarter turn, then turned by the quarters: (c, s), (-s, c), (-c, -s), (s, -c).
+__device__ __forceinline__ void turn(int64_t pos, uint64_t freq, float factor, float signed_factor, float& c, float& s)
+{
+    float z, x, y;
+    uint32_t quarter;
+    angle(pos, freq, z, quarter);
+    cos_sin(z, x, y);
+    c = (quarter & 1u ? y : x) * __uint_as_float(__float_as_uint(factor) ^ ((quarter + 1u) & 2u) << 30);
+    s = (quarter & 1u ? x : y) * __uint_as_float(__float_as_uint(signed_factor) ^ (quarter & 2u) << 30);
 }
 
 // W elements.  Not .nc: an output may be its input.
@@ -164,8 +193,7 @@ __global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
     }
     const bool have_b = cb < p.d;
 
-    // The thread's heads: where they are, and their vectors, in flight while the
-    // angles are computed.
+    // The vectors of the thread's heads, in flight while the angles are computed.
     constexpr int WORDS = W / 2 > 0 ? W / 2 : 1;
     const __nv_bfloat16* src[U];
     __nv_bfloat16* dst[U];
@@ -188,7 +216,7 @@ __global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
     for (int e = 0; e < W; ++e) {
         c[e] = 1.f;
         s[e] = 0.f;
-        if (f0 + e < p.rot / 2 && !pass_a) turn(pos, p.freqs[f0 + e], p.factor, p.sign, c[e], s[e]);
+        if (f0 + e < p.rot / 2 && !pass_a) turn(pos, p.freqs[f0 + e], p.factor, p.factor * p.sign, c[e], s[e]);
     }
 #pragma unroll
     for (int e = 0; e < U; ++e) {
