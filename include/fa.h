@@ -312,12 +312,12 @@ fa_status fa_rope(const void *q, const int64_t *q_strides, const void *k, const 
  *
  * A stored value is e2m1 * e4m3 * scale: a code of sign, two exponent bits and
  * one mantissa bit (0, .5, 1, 1.5, 2, 3, 4, 6), one e4m3 scale for 16 channels
- * of a row, and one fp32 scale a tensor (k_scale, v_scale: the same in every
- * call on a cache; with 1, blocks whose largest magnitude lies between 0.1 and
+ * of a row, and one fp32 scale a tensor (k_scale, v_scale: between 2^-60 and
+ * 2^60, the same in every call on a cache; with 1, blocks whose largest magnitude lies between 0.1 and
  * 2688 are held at full precision).  Rounding: the block's scale is the
  * largest magnitude / (6 * scale) to the nearest e4m3 (at most 448, 0 below
  * 2^-10), each code the nearest to value / (e4m3 * scale), halves to even,
- * magnitudes beyond 6 to 6.  Infinities are held as the largest value of their
+ * magnitudes beyond 6 to 6; both as if computed exactly, whatever the scale.  Infinities are held as the largest value of their
  * block, NaN as the largest positive one.
  *
  * Shared arguments
@@ -353,7 +353,7 @@ fa_status fa_rope(const void *q, const int64_t *q_strides, const void *k, const 
  *   k, v      device pointers, bf16, 16-byte aligned, (B, Hkv, N, d) with strides
  *             in elements (batch, head, position; multiples of 8), or NULL
  *             for contiguous.
- *   k_scale, v_scale  finite, > 0.
+ *   k_scale, v_scale  2^-60 to 2^60 (powers of two take the fewest instructions).
  * No two sequences of a call may append to one page.
  */
 fa_status fa_qcache_append(const void *k, const int64_t *k_strides, const void *v, const int64_t *v_strides,
@@ -388,7 +388,7 @@ fa_status fa_qcache_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, in
  *   q         device pointer, bf16, contiguous (B, H, Nq, d), 16-byte aligned;
  *             1 <= Nq <= 8, H a multiple of Hkv, B <= 2048.
  *   o         bf16 (B, H, Nq, d), lse fp32 (B, H, Nq): fully written.
- *   causal    0 or 1.  scale, k_scale, v_scale: finite, > 0.
+ *   causal    0 or 1.  scale: finite, > 0.
  *   workspace, workspace_bytes
  *             device scratch, 16-byte aligned, of at least
  *             fa_qcache_decode_workspace_bytes(...).  Nothing in it needs to

@@ -610,6 +610,10 @@ size_t qcache_block_bytes(int64_t d) { return (size_t)(72 * padded_head_size(d))
 
 bool scale_ok(float s) { return std::isfinite(s) && s > 0.0f; }
 
+// A tensor's scale: times any e4m3 scale its reciprocal is a normal number, and
+// so is a result's factor, scale / sum of probabilities.
+bool tensor_scale_ok(float s) { return s >= 0x1p-60f && s <= 0x1p60f; }
+
 // A written range of `n` bytes at p may overlap none of the cache's tensors.
 bool hits_cache(const void* p, size_t n, const void* pool, int64_t num_pages, int64_t Hkv, int64_t d,
                 const int32_t* table, int64_t max_pages, const int32_t* lens, int64_t B)
@@ -738,7 +742,7 @@ fa_status qcache_query_check(const void* q, int64_t B, int64_t H, int64_t Hkv, i
                              int causal, float scale, float k_scale)
 {
     if (!q) return FA_ERR_INVALID_ARG;
-    if (H < 1 || Nq < 1 || H % Hkv != 0 || (causal != 0 && causal != 1) || !scale_ok(scale) || !scale_ok(k_scale) ||
+    if (H < 1 || Nq < 1 || H % Hkv != 0 || (causal != 0 && causal != 1) || !scale_ok(scale) || !tensor_scale_ok(k_scale) ||
         !scale_ok((float)((double)scale * 1.4426950408889634074 * (double)k_scale)))
         return FA_ERR_INVALID_ARG;
     if (Nq > fa::qc::MAX_NQ || B > fa::qc::MAX_B) return FA_ERR_UNSUPPORTED;
@@ -1141,9 +1145,7 @@ fa_status fa_qcache_append(const void* k, const int64_t* k_strides, const void* 
     if (!k || !v) return FA_ERR_INVALID_ARG;
     const fa_status cs = qcache_check(pool, num_pages, table, max_pages, lens, B, Hkv, d);
     if (cs != FA_OK) return cs;
-    if (N < 1 || N > INT32_MAX / 2 || !scale_ok(k_scale) || !scale_ok(v_scale) || !scale_ok((float)(1.0 / (6.0 * (double)k_scale))) ||
-        !scale_ok((float)(1.0 / (6.0 * (double)v_scale))))
-        return FA_ERR_INVALID_ARG;
+    if (N < 1 || N > INT32_MAX / 2 || !tensor_scale_ok(k_scale) || !tensor_scale_ok(v_scale)) return FA_ERR_INVALID_ARG;
     const int64_t LIM = (int64_t)1 << 59;
     if (B * Hkv > LIM / N || B * Hkv * N > LIM / d) return FA_ERR_INVALID_ARG;
     int64_t s[2][3];
@@ -1190,10 +1192,18 @@ fa_status fa_qcache_append(const void* k, const int64_t* k_strides, const void* 
     const int64_t pages = std::min<int64_t>((N - 1 + fa::qc::PAGE - 1) / fa::qc::PAGE + 1, max_pages);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const dim3 grid((unsigned)pages, (unsigned)Hkv, (unsigned)B);
+    // Powers of two (1 is the usual one) need no look at remainders: 4 x 8 heads x 4096
+    // keys at d = 128 in 17.4 us, with other scales 21.6 (8 x 16 x 8192 keys: 109, 137).
+    auto pow2 = [](float x) {
+        int ex;
+        return std::frexp(x, &ex) == 0.5f;
+    };
+    auto launch = [&](auto* kernel) { return launch_pdl(kernel, grid, dim3(fa::qc::ROW_THREADS), 0, st, p); };
+    const bool easy = pow2(k_scale) && pow2(v_scale);
     const cudaError_t e =
         padded_head_size(d) == 128
-            ? launch_pdl(fa::qc::fa_qcache_append_kernel<128>, grid, dim3(fa::qc::ROW_THREADS), 0, st, p)
-            : launch_pdl(fa::qc::fa_qcache_append_kernel<64>, grid, dim3(fa::qc::ROW_THREADS), 0, st, p);
+            ? (easy ? launch(fa::qc::fa_qcache_append_kernel<128, true>) : launch(fa::qc::fa_qcache_append_kernel<128, false>))
+            : (easy ? launch(fa::qc::fa_qcache_append_kernel<64, true>) : launch(fa::qc::fa_qcache_append_kernel<64, false>));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -1204,7 +1214,8 @@ fa_status fa_qcache_read(const void* pool, int64_t num_pages, const int32_t* tab
     if (!k || !v) return FA_ERR_INVALID_ARG;
     const fa_status cs = qcache_check(pool, num_pages, table, max_pages, lens, B, Hkv, d);
     if (cs != FA_OK) return cs;
-    if (N < 1 || N > INT32_MAX / 2 || (newest != 0 && newest != 1) || !scale_ok(k_scale) || !scale_ok(v_scale))
+    if (N < 1 || N > INT32_MAX / 2 || (newest != 0 && newest != 1) || !tensor_scale_ok(k_scale) ||
+        !tensor_scale_ok(v_scale))
         return FA_ERR_INVALID_ARG;
     const int64_t LIM = (int64_t)1 << 59;
     if (B * Hkv > LIM / N || B * Hkv * N > LIM / d) return FA_ERR_INVALID_ARG;
@@ -1267,7 +1278,7 @@ fa_status fa_qcache_decode(const void* q, const void* pool, int64_t num_pages, c
     if (cs != FA_OK) return cs;
     const fa_status qs = qcache_query_check(q, B, H, Hkv, Nq, max_pages, causal, scale, k_scale);
     if (qs != FA_OK) return qs;
-    if (!scale_ok(v_scale)) return FA_ERR_INVALID_ARG;
+    if (!tensor_scale_ok(v_scale)) return FA_ERR_INVALID_ARG;
     if (((reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(workspace)) & 15u) != 0 ||
         (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
         return FA_ERR_UNSUPPORTED;

@@ -132,12 +132,21 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1
 // Scales for two blocks of 16 channels from their largest magnitudes:
 // amax / (6 scale) in e4m3, to nearest (halves to even), at most 448.  Returns
 // their bytes, lo first.  The quotient (by a reciprocal, within 2^-23) is rounded to
-// 17 bits first, which brings exact halves back and moves no other across one:
-// the quotient of bf16's 8-bit significand that is not half way between two e4m3
-// values differs from there by 2^-8 of itself.
-__device__ __forceinline__ uint32_t scale_bytes(float amax_lo, float amax_hi, float inv_six)
+// 17 bits first, which brings one beside a half (5 bits) onto it.  Where the scale is
+// a power of two (POW2) that moves no other across a half: the quotient of bf16's 8-bit
+// significand that is not half way differs from there by 2^-8 of itself.  With
+// any other scale it is then moved by a last place to the side that the remainder
+// 6 * quotient * scale - amax tells: six halves are exact, and the sign of a fused
+// multiply-add's result is the exact one's, so only what is half way stays there.
+template <bool POW2>
+__device__ __forceinline__ uint32_t scale_bytes(float amax_lo, float amax_hi, float inv_six, float scale)
 {
-    auto quotient = [&](float amax) { return __uint_as_float((__float_as_uint(amax * inv_six) + 0x40u) & 0xFFFFFF80u); };
+    auto quotient = [&](float amax) {
+        const uint32_t q = (__float_as_uint(amax * inv_six) + 0x40u) & 0xFFFFFF80u;
+        if constexpr (POW2) return __uint_as_float(q);
+        const float left = fmaf(6.0f * __uint_as_float(q), scale, -amax);
+        return __uint_as_float(left > 0.f ? q - 1u : left < 0.f ? q + 1u : q);
+    };
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(quotient(amax_hi)), "f"(quotient(amax_lo)));
     return r;
@@ -157,18 +166,37 @@ __device__ __forceinline__ float reciprocal(float s)
     return s > 0.f ? r : 0.f;
 }
 
-// Two quotients x / (e4m3 * scale) as e2m1, to nearest, halves to even,
-// magnitudes above 6 to 6: the first in the low nibble.  x and the reciprocals
-// come as pairs.  A product with a reciprocal lies up to 2^-22 off a quotient
-// that is half way between two codes (bf16 inputs meet exact halves often);
-// adding and subtracting 1.5 * 2^9 rounds to a multiple of 2^-14 first, which
-// brings those back and moves no other: a quotient of an 8-bit and a 4-bit
-// significand that is not half way differs from there by 2^-10 at least.
-__device__ __forceinline__ uint32_t codes2(uint64_t x, uint64_t inv)
+// x * y + 1/2, held within 0 and 1 (0 for NaN).
+__device__ __forceinline__ float half_more_saturated(float x, float y)
 {
-    constexpr float C = 768.0f;
+    float r;
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(0.5f));
+    return r;
+}
+
+// Two quotients x / (e4m3 * scale) as e2m1, to nearest, halves to even,
+// magnitudes above 6 to 6: the first in the low nibble.  x, the reciprocals inv of
+// e4m3 * scale and the e4m3 values, negated, come as pairs.  A product with a
+// reciprocal lies up to 2^-19 off a quotient that is half way between two codes; adding
+// and subtracting 1.5 * 2^9 rounds to a multiple of 2^-14 first, which brings it back.
+// Where the scale is a power of two (POW2) bf16 inputs meet exact halves often, and
+// a quotient of an 8-bit and a 4-bit significand that is not half way differs from
+// there by 2^-10 at least, so nothing else is moved.  With any other scale quotients
+// lie as near to a half as they like: the rounded quotient is moved off by 2^-15, half
+// way to the next multiple, to the side that the sign of x - quotient * e4m3 * scale
+// tells (exact where the quotient is a half: 7 bits before the fused multiply-add).
+template <bool POW2>
+__device__ __forceinline__ uint32_t codes2(uint64_t x, uint64_t inv, uint64_t minus_e4m3, float scale)
+{
+    constexpr float C = 768.0f, FAR = 0x1p127f, STEP = 0x1p-15f;
+    uint64_t q = ptx::f2_add(ptx::f2_fma(x, inv, ptx::f2_pack(C, C)), ptx::f2_pack(-C, -C));
     float a, b;
-    ptx::f2_unpack(ptx::f2_add(ptx::f2_fma(x, inv, ptx::f2_pack(C, C)), ptx::f2_pack(-C, -C)), a, b);
+    if constexpr (!POW2) {
+        ptx::f2_unpack(ptx::f2_fma(ptx::f2_mul(q, minus_e4m3), ptx::f2_pack(scale, scale), x), a, b);
+        const uint64_t side = ptx::f2_pack(half_more_saturated(a, FAR), half_more_saturated(b, FAR));  // 0, 1/2 or 1
+        q = ptx::f2_fma(side, ptx::f2_pack(2 * STEP, 2 * STEP), ptx::f2_add(q, ptx::f2_pack(-STEP, -STEP)));
+    }
+    ptx::f2_unpack(q, a, b);
     uint32_t r;
     asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b32 %0, {t, t, t, t};\n\t}" : "=r"(r) : "f"(b), "f"(a));
     return r & 0xFFu;
@@ -242,7 +270,7 @@ constexpr int ROW_THREADS = 256;
 // Bound by memory for prompts (4d bytes read and 9d/8 written a key), by its
 // launch for single keys.  Appending and reading back 4 x 8 heads x up to 4096
 // keys at d = 128: 24.8 us, about half of it here; 64 x 8 heads x 1 key: 6.2 us.
-template <int D>
+template <int D, bool POW2>
 __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const RowParams p)
 {
     ptx::griddep_wait();
@@ -286,12 +314,13 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const Row
         if (x < x0 || x >= x1) continue;
         float f[16];
         kr_[i].unpack(f);
-        const uint32_t sb = scale_bytes(kr_[i].amax(), 0.f, p.k_inv_six) & 0xFFu;
-        const float inv = reciprocal(scale_value(sb) * p.k_scale);
+        const uint32_t sb = scale_bytes<POW2>(kr_[i].amax(), 0.f, p.k_inv_six, p.k_scale) & 0xFFu;
+        const float unit = scale_value(sb), inv = reciprocal(unit * p.k_scale);
         uint32_t w[2] = {0, 0};
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            w[e / 4] |= codes2(ptx::f2_pack(f[2 * e], f[2 * e + 1]), ptx::f2_pack(inv, inv)) << (8 * (e % 4));
+            w[e / 4] |= codes2<POW2>(ptx::f2_pack(f[2 * e], f[2 * e + 1]), ptx::f2_pack(inv, inv), ptx::f2_pack(-unit, -unit), p.k_scale)
+                        << (8 * (e % 4));
         *reinterpret_cast<uint2*>(blk + L::kcode(x) + c * 8) = make_uint2(w[0], w[1]);
         blk[L::kscale(x, c)] = (uint8_t)sb;
     }
@@ -299,12 +328,13 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const Row
     float f[16], g[16];
     vr_[0].unpack(f);
     vr_[1].unpack(g);
-    const uint32_t both = scale_bytes(vr_[0].amax(), vr_[1].amax(), p.v_inv_six), sf = both & 0xFFu, sg = both >> 8;
-    const uint64_t inv = ptx::f2_pack(reciprocal(scale_value(sf) * p.v_scale), reciprocal(scale_value(sg) * p.v_scale));
+    const uint32_t both = scale_bytes<POW2>(vr_[0].amax(), vr_[1].amax(), p.v_inv_six, p.v_scale), sf = both & 0xFFu, sg = both >> 8;
+    const float uf = scale_value(sf), ug = scale_value(sg);
+    const uint64_t inv = ptx::f2_pack(reciprocal(uf * p.v_scale), reciprocal(ug * p.v_scale)), minus_units = ptx::f2_pack(-uf, -ug);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 16; ++i)  // channel i of both keys
-        w[i / 4] |= codes2(ptx::f2_pack(f[i], g[i]), inv) << (8 * (i % 4));
+        w[i / 4] |= codes2<POW2>(ptx::f2_pack(f[i], g[i]), inv, minus_units, p.v_scale) << (8 * (i % 4));
     uint4* const at = reinterpret_cast<uint4*>(blk + L::vcode(2 * r0) + c * 16);
     if (!(even && odd)) {
         const uint4 old = *at;
