@@ -660,7 +660,9 @@ struct Rows {
         const int lane = threadIdx.x & 31, t = lane & 3;
         const int r0 = p.rb == 1 ? 0 : hr % p.rb * (8 * NT);
         len = clamp_length(raw.len, p.max_pages);
-        min_lim = p.causal ? len - p.nq + 1 : len;
+        // A causal query stands at its place in the sequence, which a length beyond the page table does not move.
+        const int end = max(raw.len, 0) - p.nq + 1;
+        min_lim = p.causal ? min(len, end) : len;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float f[D / 4];
@@ -684,7 +686,7 @@ struct Rows {
             for (int j = 0; j < 2; ++j) {
                 sc[nt][j] = __shfl_sync(0xffffffffu, down, (2 * t + j) * 4);
                 const int r = r0 + nt * 8 + row_of(2 * t + j);
-                lim[nt][j] = p.causal && r < p.rows ? len - p.nq + (p.nq == 1 ? 0 : r % p.nq) + 1 : len;
+                lim[nt][j] = p.causal && r < p.rows ? min(len, end + (p.nq == 1 ? 0 : r % p.nq)) : len;
             }
         }
     }
