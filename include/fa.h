@@ -291,8 +291,11 @@ fa_status fa_bias_gelu_dropout(const void *x, const void *bias, const uint32_t *
  *              batches position_stride elements apart (0: one row for all), or
  *              NULL.  Negative positions turn backwards.
  *   lens       device pointer, int32 (B), or NULL: row i stands at position
- *              lens[b] - N + i (the newest N of a sequence).  With neither,
- *              row i stands at position i; both is FA_ERR_INVALID_ARG.
+ *              lens[b] - N + i (the newest N of a sequence).  A cache's lengths
+ *              are that only while nothing was evicted: kept keys stay turned
+ *              to the positions where they were produced, so after fa_qcache_evict
+ *              new rows need positions counted apart.  With neither, row i
+ *              stands at position i; both is FA_ERR_INVALID_ARG.
  *   stream     CUDA stream the one launch is enqueued on.
  *
  * Errors: FA_ERR_INVALID_ARG (null pointers, sizes, overlaps, strides that

@@ -34,13 +34,22 @@ turns queries and keys by their positions (half or interleaved pairs, all or
 part of the head, any position), and gives the gradient.
 
     pool = io_aware_attention_gb300.qcache_pool(num_pages, Hkv, d)
+
+is a paged cache held in 4 bits, and a decode step over it, of one token of
+every sequence (grouped heads, sequences of unequal lengths), is
+
+    q, k = io_aware_attention_gb300.rope(q, k, freqs, positions=positions, factor=factor)
+    positions += 1
+    lens += 1
     io_aware_attention_gb300.qcache_append(k, v, pool, table, lens)
     o, lse = io_aware_attention_gb300.qcache_decode(q, pool, table, lens)
     weights = io_aware_attention_gb300.qcache_weights(q, lse, pool, table, lens, weights)
     kept, lens, weights = io_aware_attention_gb300.qcache_evict(pool, table, lens, weights, keep)
 
-is decode over a paged cache held in 4 bits: grouped heads, sequences of
-unequal lengths, and eviction of the keys that gathered the least attention.
+the last line, now and then, dropping the keys that gathered the least
+attention.  positions, integers (B, 1), counts the tokens of the text and lens
+the keys that the cache holds: they part at the first eviction, after which kept
+keys still stand, turned, where they were produced.
 
 The ``*_into`` forms write into caller-provided tensors; their shapes, dtypes
 and devices are checked here, because the C ABI sees only pointers and sizes.
@@ -569,8 +578,9 @@ def rope(q, k, freqs, positions=None, lens=None, layout: str = "half", factor: f
     """Turns q (B, H, N, d) and k (B, Hk, N, d; or None) by their positions and
     returns new contiguous tensors.  freqs and factor: :func:`rope_frequencies`;
     2 * len(freqs) channels are turned, the others copied.  positions: int32 or
-    int64 (N,) or (B, N); or lens, int32 (B,): row i stands at lens[b] - N + i;
-    or neither: row i stands at i.  Strided views (heads of a fused
+    int64 (N,) or (B, N); or lens, int32 (B,): row i stands at lens[b] - N + i
+    (a cache's lens only as long as nothing was evicted from it: kept keys stand
+    where they were produced); or neither: row i stands at i.  Strided views (heads of a fused
     projection) are taken as they are."""
     import torch
 
