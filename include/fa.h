@@ -440,7 +440,9 @@ fa_status fa_qcache_weights(const void *q, const float *lse, const void *pool, i
  *             -1 after the last.
  *   lens_out  int32 (B): min(lens, keep).
  *   keep >= 1, sink >= 0, recent >= 0, sink + recent <= keep.
- * Places of the last destination page behind the kept keys are cleared.
+ * Places of the last destination page behind the kept keys are cleared, but for
+ * sequences that stay as they are: of at most `keep` keys, with table_out the
+ * table itself (same pointer and max_pages).  Nothing of their pages is written.
  */
 fa_status fa_qcache_evict(void *pool, int64_t num_pages, const int32_t *table, int64_t max_pages, const int32_t *lens,
                           const int32_t *table_out, int64_t max_pages_out, const float *weights, float *weights_out,

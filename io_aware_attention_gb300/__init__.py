@@ -453,7 +453,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", fac
     turns over ``original_length`` positions, keeps those that make more than
     ``fast``, blends linearly between, and scales the channels by
     0.1 ln(factor) + 1.  Computed in 64-bit floating point: a frequency is good to
-    2^-50 of itself, so an angle at position t to 2^-50 of the turns made by then."""
+    2^-46 of itself, so an angle at position t to 2^-46 of the turns made by then."""
     import torch
 
     if rot < 2 or rot % 2 or not (math.isfinite(base) and base > 1.0):

@@ -221,7 +221,7 @@ struct RowParams {
     uint8_t* pool;
     const int32_t *table, *lens;
     int64_t n;
-    int hkv, d, max_pages, num_pages, tiles;
+    int hkv, d, max_pages, num_pages;
     int newest;                    // row i is position lens - N + i (else i)
     float k_scale, v_scale, k_inv_six, v_inv_six;  // 1 / (6 scale)
 };

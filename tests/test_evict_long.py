@@ -66,3 +66,28 @@ def test_moves_of_many_rounds(d, apart):
             assert np.array_equal(kept[b, h].cpu().numpy(), want)
     at = kept.long()[..., None].expand(2, Hkv, keep, d)
     assert torch.equal(k2, k.gather(2, at)) and torch.equal(v2, v.gather(2, at))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_sequence_that_stays_is_not_written(d):
+    """At most `keep` keys and the table itself: the pages keep every byte, also behind the last key; copied to other
+    pages, the places behind the last key are cleared."""
+    lens, Hkv, keep = [100, 70, 0], 2, 100
+    pool, table, n = (t.cuda() for t in ref.make_cache(lens, Hkv, d, seed=d, spare=8))
+    before = pool.clone()
+    w = torch.rand((3, Hkv, 128), device="cuda")
+    kept, new, wo = fa.qcache_evict(pool, table, n, w, keep)
+    torch.cuda.synchronize()
+    assert torch.equal(pool, before) and new.tolist() == lens
+    assert kept[0, 0].tolist() == list(range(100)) and kept[1, 1].tolist() == list(range(70)) + [-1] * 30
+    used = set(table[0, :2].tolist() + table[1, :2].tolist())
+    free = [i for i in range(len(pool)) if i not in used]
+    out = torch.tensor([free[:2], free[2:4], free[4:6]], dtype=torch.int32, device="cuda")
+    fa.qcache_evict(pool, table, n, w, keep, table_out=out)
+    torch.cuda.synchronize()
+    assert fa.check_device_status() == 0
+    full = torch.full_like(n, 128)
+    for b, m in enumerate(lens[:2]):
+        k, v = fa.qcache_read(pool, out[b:b + 1].contiguous(), full[:1], 128, d)
+        k0, v0 = fa.qcache_read(before, table[b:b + 1].contiguous(), n[b:b + 1], 128, d)
+        assert torch.equal(k, k0) and torch.equal(v, v0) and not k[:, :, m:].any()
