@@ -20,12 +20,12 @@
 // pairs) of one position and U = 4 heads, whose loads are in flight while it
 // computes the 8 angles that they share.  Queries and keys go in one launch.
 // Measured at B8 H32 + 32 N4096 d128 (a forward and a gradient, 2.15 GB): 318 us,
-// 6746 GB/s, 1.00 of the measured copy bandwidth.  What brought it there: 4
+// 6744 GB/s, 1.00 of the measured copy bandwidth.  What brought it there: 4
 // blocks an SM instead of 3 (349 -> 328 us; 5 spill, 409 us) and, for results
 // larger than L2, streaming stores (328 -> 318 us); with 2 heads in flight 404
 // us, with the angles computed before the loads 383 us.  Where the results go is
 // worked out after the angles: 64 registers hold no more beside the loads in flight
-// (worked out before, 19 words spill: 327 us).
+// (worked out before, 19 words spill: 328 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -195,20 +195,16 @@ __global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
 
     // The vectors of the thread's heads, in flight while the angles are computed.
     constexpr int WORDS = W / 2 > 0 ? W / 2 : 1;
-    const __nv_bfloat16* src[U];
-    __nv_bfloat16* dst[U];
     uint32_t va[U][WORDS], vb[U][WORDS];
 #pragma unroll
     for (int e = 0; e < U; ++e) {
         const int h = (ht * U + e) * (int)blockDim.z + threadIdx.z;
-        src[e] = nullptr;
         if (h >= p.heads[0] + p.heads[1]) continue;
         const int t = h >= p.heads[0];
         const int64_t hl = t ? h - p.heads[0] : h;
-        src[e] = p.in[t].p + b * p.in[t].sb + hl * p.in[t].sh + i * p.in[t].sn;
-        dst[e] = p.out[t].p + b * p.out[t].sb + hl * p.out[t].sh + i * p.out[t].sn;
-        ld<W>(va[e], src[e] + ca);
-        if (have_b) ld<W>(vb[e], src[e] + cb);
+        const __nv_bfloat16* const src = p.in[t].p + b * p.in[t].sb + hl * p.in[t].sh + i * p.in[t].sn;
+        ld<W>(va[e], src + ca);
+        if (have_b) ld<W>(vb[e], src + cb);
     }
     const int64_t pos = position_of(p, b, i);
     float c[W], s[W];
@@ -220,7 +216,11 @@ __global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
     }
 #pragma unroll
     for (int e = 0; e < U; ++e) {
-        if (!src[e]) continue;
+        const int h = (ht * U + e) * (int)blockDim.z + threadIdx.z;
+        if (h >= p.heads[0] + p.heads[1]) continue;
+        const int t = h >= p.heads[0];
+        const int64_t hl = t ? h - p.heads[0] : h;
+        __nv_bfloat16* const dst = p.out[t].p + b * p.out[t].sb + hl * p.out[t].sh + i * p.out[t].sn;
         if constexpr (W == 1) {
             if (!pass_a) {
                 const float a = lo(va[e][0]), bb = lo(vb[e][0]);
@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(THREADS, 4) fa_rope_kernel(const Params p)
                 if (!pass_b) turn_word(vb[e][k], c[WORDS + k], s[WORDS + k]);
             }
         }
-        st<W>(dst[e] + ca, va[e], p.stream);
-        if (have_b) st<W>(dst[e] + cb, vb[e], p.stream);
+        st<W>(dst + ca, va[e], p.stream);
+        if (have_b) st<W>(dst + cb, vb[e], p.stream);
     }
 }
 
