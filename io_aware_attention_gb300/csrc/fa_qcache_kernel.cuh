@@ -270,6 +270,9 @@ constexpr int ROW_THREADS = 256;
 // Bound by memory for prompts (4d bytes read and 9d/8 written a key), by its
 // launch for single keys.  Appending and reading back 4 x 8 heads x up to 4096
 // keys at d = 128: 24.8 us, about half of it here; 64 x 8 heads x 1 key: 6.2 us.
+// Appending 4 x 8 x 4096 keys alone: 17.4 us, 0.73 of the measured copy bandwidth;
+// what is between is the rounding's integer and conversion instructions (that
+// pipe is 0.63 busy).
 template <int D, bool POW2>
 __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_append_kernel(const RowParams p)
 {
@@ -748,7 +751,9 @@ __device__ __forceinline__ void page_scores(const uint8_t* blk, const Rows<D, NT
 // (FOLD) take one product for both: the tile's rows 0 to 3 carry the roundings, rows
 // 4 to 7 what those left, and close() adds them up.  (8 x 32 heads x 32768 keys, one
 // row, d = 128: 226 us with two products, 205 folded;
-// 48 x 4 heads x 0 to 5000 keys, 16 rows, d = 64, two products: 28.5 us.)
+// More rows take two: 8 x 8 heads x 32768 keys, 8 rows 67.4 us (62.2 with one fp16
+// number a probability), 16 rows 111.8 (92.6); 48 x 4 heads x 0 to 5000 keys, 16 rows,
+// d = 64, 28.7 (27.2).)
 template <int D, int NT, bool FOLD>
 struct State {
     using R = Rows<D, NT, FOLD>;
