@@ -179,12 +179,19 @@ def _stream_handle(stream, device: int | None = None):
     return int(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _stream_on(stream, dev: int) -> None:
+    """A stream of another device is refused: the handle of that device's default
+    stream is 0, which would mean the current device's."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device} but the tensors are on cuda:{dev}")
+
+
 def _under(stream, t):
     """The context of a call on tensor t whose results belong to ``stream``."""
     import torch
 
-    if t.is_cuda and stream.device.index != t.get_device():
-        raise ValueError(f"stream is on {stream.device} but the tensors are on cuda:{t.get_device()}")
+    if t.is_cuda:
+        _stream_on(stream, t.get_device())
     return torch.cuda.stream(stream)
 
 
@@ -570,6 +577,7 @@ def rope_into(q, k, q_out, k_out, freqs, positions=None, lens=None, layout: str 
         if k_out.shape != k.shape:
             raise ValueError("k_out must have the shape of k")
     _on_current_device(dev)
+    _stream_on(stream, dev)
     return _rope_call(q, k, q_out, k_out, freqs, positions, lens, layout, factor, inverse, stream, sizes)
 
 
@@ -649,6 +657,7 @@ def qcache_append(k, v, pool, table, lens, k_scale: float = 1.0, v_scale: float 
         raise ValueError(f"k and v must be (B, Hkv, N, d) of the cache's batch, heads and device: {tuple(k.shape)} "
                          f"{tuple(v.shape)}")
     _on_current_device(dev)
+    _stream_on(stream, dev)
     rc = library().fa_qcache_append(k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), B, Hkv, N, d,
                                     float(k_scale), float(v_scale), pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(),
                                     _stream_handle(stream, dev))
@@ -739,6 +748,7 @@ def qcache_decode_into(q, pool, table, lens, o, lse, workspace, causal: bool = F
     if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
     _on_current_device(dev)
+    _stream_on(stream, dev)
     return _qcache_decode_call(q, pool, table, lens, o, lse, workspace, causal, scale, k_scale, v_scale, stream, sizes)
 
 
