@@ -1441,11 +1441,12 @@ fa_status fa_qcache_evict(void* pool, int64_t num_pages, const int32_t* table, i
     p.recent = (int)recent;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // A cluster of 4 blocks a head pays where heads are long and few; one block
-    // a head where they fill the SMs anyway.  (The lengths are on the device: the rule
-    // goes by the table's room, and the figures are of full tables.)  Whole call in us, cluster against
-    // one block, cutting 64-channel heads back to 64 keys: 8 heads of 2048 keys
-    // 10.4 / 9.2, of 8192 11.5 / 13.8; 64 heads of 8192 20.5 / 16.4, of 32768
-    // 30.0 / 35.4; 256 heads of 16384 51.8 / 33.6, of 65536 112 / 330.
+    // a head where they fill the SMs anyway.  (The lengths are on the device: the
+    // rule goes by the table's room, and the figures are of full tables.)  Whole
+    // call in us, cluster against one block, cutting 64-channel heads back to 64
+    // keys: 8 heads of 2048 keys 10.4 / 9.2, of 8192 11.5 / 13.8; 64 heads of 8192
+    // 20.5 / 16.4, of 32768 30.0 / 35.4; 256 heads of 16384 51.8 / 33.6, of 65536
+    // 112 / 330.
     const int64_t heads = B * Hkv, most = max_pages * fa::qc::PAGE;
     const bool wide = most > (heads * 4 <= info.sms ? 4096 : heads <= info.sms ? 16384 : 32768);
     const fa_status ss = wide ? launch_qcache_select<4>(p, Hkv, B, dev, st) : launch_qcache_select<1>(p, Hkv, B, dev, st);
