@@ -31,4 +31,5 @@ def test_into_calls_refuse_a_stream_of_another_device():
     fa.qcache_append(q, q, pool, table, lens, stream=side)
     fa.qcache_decode_into(q, pool, table, lens, o, lse, ws, stream=side)
     side.synchronize()
-    assert torch.equal(o, q) and fa.check_device_status() == 0
+    # One key of ones: its block's scale is the e4m3 number nearest to 1 / 6, 11 / 64, and its codes are 6.
+    assert torch.equal(o, torch.full_like(o, 6 * 11 / 64)) and fa.check_device_status() == 0
