@@ -321,7 +321,7 @@ fa_status fa_rope(const void *q, const int64_t *q_strides, const void *k, const 
  * largest magnitude / (6 * scale) to the nearest e4m3 (at most 448, 0 below
  * 2^-10), each code the nearest to value / (e4m3 * scale), halves to even,
  * magnitudes beyond 6 to 6; both as if computed exactly, whatever the scale.  Infinities are held as the largest value of their
- * block, NaN as the largest positive one.
+ * block, NaN as the largest positive one; neither is reported.
  *
  * Shared arguments
  *   pool      device pointer, 16-byte aligned: num_pages * Hkv blocks of
