@@ -226,6 +226,65 @@ fa_status fa_bwd(const void *q, const void *k, const void *v, const void *o, con
                  fa_stream_t stream);
 
 /*
+ * Cross attention (fa_cross_*): queries against an encoder's states of another
+ * length.  Query head h of sequence b reads kv head h / (H / Hkv), and every query
+ * sees keys 0 .. lens[b]-1:
+ *     O_i = sum_j softmax_j(scale * q_i . k_j) * v_j,  L_i = ln sum_j exp(scale * q_i . k_j)
+ * A sequence without keys gives O = 0 and L = -infinity.
+ *
+ * Shared arguments
+ *   q, o       (B, H, Nq, d) bf16; k, v (B, Hkv, Nk, d) bf16, H a multiple of Hkv.
+ *              Keys from lens[b] on are padding and may hold anything.
+ *   *_strides  host pointers to a view's three strides in elements (batch, head,
+ *              position; channels adjoin), or NULL for contiguous.  Multiples of 8
+ *              (where there is more than one entry), rows not closer than d.
+ *              Batches and heads of an input may repeat (stride 0); an output
+ *              may not repeat a place.  Groups of heads whose rows follow one
+ *              another at one stride (contiguous ones do) run fastest.
+ *   lse        fp32, contiguous (B, H, Nq).
+ *   lens       device pointer, int32 (B), or NULL: all Nk.  Negative counts as 0;
+ *              more than Nk as Nk, reported by fa_check_device_status as
+ *              FA_ERR_INVALID_ARG.  Read when the call runs.
+ *   d          a multiple of 8 from 8 to 128.  scale: finite, > 0.
+ *              B*H*Nq (Nq rounded up to 64), Nk*128 and B*H*ceil(Nk/128) at most 2^30.
+ *   workspace  device scratch, 16-byte aligned, of at least the bytes that
+ *              the call's fa_cross_*_workspace_bytes gives (NULL where that is 0);
+ *              calls that may run at the same time must not share it.
+ * Bf16 tensors 16-byte, lse and lens 4-byte aligned, else FA_ERR_UNSUPPORTED.
+ * Outputs and workspace may overlap no input and no other output; dk and dv may
+ * be views of one buffer.  Ownership, asynchrony and errors as for fa_fwd.
+ */
+
+/* Workspace of fa_cross_fwd on the current device: 0 where queries are many
+ * enough that the key range is not split. */
+fa_status fa_cross_fwd_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, size_t *bytes);
+
+/* fa_cross_fwd — o and lse, fully written.  Results do not depend on timing. */
+fa_status fa_cross_fwd(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, const void *v,
+                       const int64_t *v_strides, void *o, const int64_t *o_strides, float *lse, const int32_t *lens,
+                       int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, float scale,
+                       void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* Workspace of fa_cross_bwd: B*H*Nq' * (D + 2) floats, Nq' = Nq rounded up to a
+ * multiple of 64, D the padded head size.  Needs no device. */
+fa_status fa_cross_bwd_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, size_t *bytes);
+
+/*
+ * fa_cross_bwd — the gradients of fa_cross_fwd for the output gradient dout
+ * (B, H, Nq, d), by fa_bwd's formulas; dk and dv (B, Hkv, Nk, d) are summed over
+ * the heads of a group and zero from lens[b] on; dq of a sequence without keys is
+ * zero.  q, k, v, o, lse, lens and scale as in the forward.  dk and dv do not
+ * depend on timing; dq's fp32 sums are added up in the order in which its parts
+ * finish, as fa_bwd's are.
+ */
+fa_status fa_cross_bwd(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, const void *v,
+                       const int64_t *v_strides, const void *o, const int64_t *o_strides, const float *lse,
+                       const void *dout, const int64_t *dout_strides, void *dq, const int64_t *dq_strides, void *dk,
+                       const int64_t *dk_strides, void *dv, const int64_t *dv_strides, const int32_t *lens, int64_t B,
+                       int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, float scale, void *workspace,
+                       size_t workspace_bytes, fa_stream_t stream);
+
+/*
  * fa_bias_gelu_dropout — the fused elementwise chain of "Fusion and IO-aware
  * kernels" (§ The idea in one minute: a bias add, a GELU and a dropout, one
  * HBM read and one HBM write instead of three round trips), with the tanh

@@ -21,6 +21,13 @@ recomputing the probabilities from ``lse``.
 is split-KV decode of up to 8 query rows against a long cache (the same head
 sizes).
 
+    o, lse = io_aware_attention_gb300.cross_fwd(q, k, v, lens)
+    dq, dk, dv = io_aware_attention_gb300.cross_bwd(q, k, v, o, lse, do, lens)
+
+is attention to an encoder's states of another length (cross attention) and its
+gradient: grouped heads, padded sequences, views of fused projections, one query
+row or many.
+
     y = io_aware_attention_gb300.bias_gelu_dropout(x, bias, keep, p)
 
 is the fused elementwise chain (bias add, tanh GELU, dropout with a packed
@@ -67,7 +74,8 @@ import os
 
 from . import _build
 
-__all__ = ["fwd", "fwd_into", "bwd", "bwd_into", "bwd_workspace_bytes", "bias_gelu_dropout", "decode", "decode_into", "decode_workspace_bytes", "check_device_status", "get_device_status",
+__all__ = ["fwd", "fwd_into", "bwd", "bwd_into", "bwd_workspace_bytes", "bias_gelu_dropout", "decode", "decode_into", "decode_workspace_bytes", "cross_fwd", "cross_fwd_into", "cross_fwd_workspace_bytes", "cross_bwd", "cross_bwd_into",
+           "cross_bwd_workspace_bytes", "check_device_status", "get_device_status",
            "rope", "rope_into", "rope_bwd", "rope_frequencies", "qcache_pool", "qcache_append", "qcache_read",
            "qcache_decode", "qcache_decode_into", "qcache_decode_workspace_bytes", "qcache_weights", "qcache_evict",
            "set_wait_limit_ns", "debug_skip_k_tile", "debug_set_schedule", "FaError", "library", "library_path", "version", "STATUS"]
@@ -75,6 +83,7 @@ __all__ = ["fwd", "fwd_into", "bwd", "bwd_into", "bwd_workspace_bytes", "bias_ge
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_CUDA",
           4: "FA_ERR_TIMEOUT", 5: "FA_ERR_TOO_LARGE"}
 EXPORTS = ["fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_bias_gelu_dropout", "fa_decode", "fa_decode_workspace_bytes", "fa_decode_static",
+           "fa_cross_fwd", "fa_cross_fwd_workspace_bytes", "fa_cross_bwd", "fa_cross_bwd_workspace_bytes",
            "fa_rope", "fa_qcache_append", "fa_qcache_read", "fa_qcache_decode", "fa_qcache_decode_workspace_bytes",
            "fa_qcache_weights", "fa_qcache_evict", "fa_check_device_status", "fa_get_device_status",
            "fa_set_wait_limit_ns", "fa_debug_skip_k_tile", "fa_debug_set_schedule", "fa_debug_decode_plan", "fa_status_string",
@@ -125,6 +134,13 @@ def library():
                                      vp]
     lib.fa_decode_static.restype = ctypes.c_int
     ci, cf, sz = ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    lib.fa_cross_fwd.argtypes = [vp] * 10 + [i64] * 6 + [cf, vp, sz, vp]
+    lib.fa_cross_fwd.restype = ctypes.c_int
+    lib.fa_cross_bwd.argtypes = [vp] * 18 + [i64] * 6 + [cf, vp, sz, vp]
+    lib.fa_cross_bwd.restype = ctypes.c_int
+    for name in ("fa_cross_fwd_workspace_bytes", "fa_cross_bwd_workspace_bytes"):
+        getattr(lib, name).argtypes = [i64] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+        getattr(lib, name).restype = ctypes.c_int
     lib.fa_rope.argtypes = [vp] * 8 + [i64] * 5 + [vp, i64, ci, cf, ci, vp, ci, i64, vp, vp]
     lib.fa_rope.restype = ctypes.c_int
     lib.fa_qcache_append.argtypes = [vp] * 4 + [i64] * 4 + [cf, cf, vp, i64, vp, i64, vp, vp]
@@ -609,6 +625,157 @@ def rope_bwd(dq, dk, freqs, positions=None, lens=None, layout: str = "half", fac
     """The gradient of :func:`rope`: dLoss/dq and dLoss/dk from the gradients of
     its results (the transposed map; the other arguments as in the forward)."""
     return rope(dq, dk, freqs, positions, lens, layout, factor, True, stream)
+
+
+def _check_cross(q, k, v, lens, *rows):
+    """Checks of a cross-attention call's inputs, rows being (name, tensor) of more
+    tensors like q; returns (device, B, H, Hkv, Nq, Nk, d)."""
+    _check_rows("q", q)
+    dev = q.get_device()
+    _check_rows("k", k, dev)
+    _check_rows("v", v, dev)
+    B, H, Nq, d = q.shape
+    Bk, Hkv, Nk, dk = k.shape
+    if Bk != B or dk != d or v.shape != k.shape or Hkv < 1 or H % Hkv:
+        raise ValueError(f"k and v must be (B, Hkv, Nk, d) of q's batch and head size, Hkv a divisor of its heads: "
+                         f"{tuple(q.shape)} {tuple(k.shape)} {tuple(v.shape)}")
+    if lens is not None:
+        _check_int32("lens", lens, (B,), dev)
+    for name, t in rows:
+        _check_rows(name, t, dev)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} must have the shape of q")
+    return dev, B, H, Hkv, Nq, Nk, d
+
+
+def _bytes_of(what, *sizes) -> int:
+    out = ctypes.c_size_t(0)
+    rc = getattr(library(), what)(*(int(n) for n in sizes), ctypes.byref(out))
+    if rc != 0:
+        raise FaError(rc, what)
+    return int(out.value)
+
+
+def cross_fwd_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
+    """Workspace bytes fa_cross_fwd needs for these sizes on the current device."""
+    return _bytes_of("fa_cross_fwd_workspace_bytes", B, H, Hkv, Nq, Nk, d)
+
+
+def cross_bwd_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
+    """Workspace bytes fa_cross_bwd needs for these sizes."""
+    return _bytes_of("fa_cross_bwd_workspace_bytes", B, H, Hkv, Nq, Nk, d)
+
+
+@functools.lru_cache(maxsize=256)
+def _cross_workspace(dev, *sizes):
+    """The forward's workspace size on device dev (the current one), a function of the sizes alone."""
+    return cross_fwd_workspace_bytes(*sizes)
+
+
+def _check_workspace(workspace, dev):
+    if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
+
+
+def _cross_fwd_call(q, k, v, o, lse, lens, workspace, scale, stream, sizes):
+    dev = sizes[0]
+    if scale is None:
+        scale = 1.0 / math.sqrt(sizes[-1])
+    rc = library().fa_cross_fwd(q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), o.data_ptr(),
+                                _strides(o), lse.data_ptr(), None if lens is None else lens.data_ptr(), *sizes[1:], float(scale),
+                                None if workspace is None else workspace.data_ptr(),
+                                0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_cross_fwd")
+    return o, lse
+
+
+def cross_fwd_into(q, k, v, o, lse, workspace=None, lens=None, scale: float | None = None, stream=None):
+    """:func:`cross_fwd` into caller-provided o (bf16, q's shape; a strided view is
+    fine), lse (fp32, (B, H, Nq)) and workspace (a contiguous CUDA tensor of at
+    least cross_fwd_workspace_bytes bytes, or None when that is 0)."""
+    import torch
+
+    sizes = _check_cross(q, k, v, lens, ("o", o))
+    dev = sizes[0]
+    _check_out("lse", lse, q.shape[:3], torch.float32, q.device)
+    if workspace is not None:
+        _check_workspace(workspace, dev)
+    _on_current_device(dev)
+    _stream_on(stream, dev)
+    return _cross_fwd_call(q, k, v, o, lse, lens, workspace, scale, stream, sizes)
+
+
+def cross_fwd(q, k, v, lens=None, scale: float | None = None, stream=None):
+    """Attention of q (B, H, Nq, d) to the states k, v (B, Hkv, Nk, d) of an
+    encoder: query head h reads kv head h // (H // Hkv), every query sees keys
+    0 .. lens[b]-1 (lens int32 (B,); None: all).  Strided views are taken as they
+    are; batches and heads may be expanded ones.  Returns ``(o (B, H, Nq, d) bf16,
+    lse (B, H, Nq) fp32)``; a sequence without keys gives 0 and -inf."""
+    import torch
+
+    if stream is not None:  # the workspace and the results belong to the stream that writes them
+        with _under(stream, q):
+            return cross_fwd(q, k, v, lens, scale)
+    sizes = _check_cross(q, k, v, lens)
+    dev = sizes[0]
+    if _cuda_device() != dev:
+        with torch.cuda.device(dev):
+            return cross_fwd(q, k, v, lens, scale)
+    on, nbytes = q.device, _cross_workspace(*sizes)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=on) if nbytes else None
+    o = torch.empty(q.shape, dtype=torch.bfloat16, device=on)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=on)
+    return _cross_fwd_call(q, k, v, o, lse, lens, ws, scale, None, sizes)
+
+
+def cross_bwd_into(q, k, v, o, lse, do, dq, dk, dv, workspace, lens=None, scale: float | None = None, stream=None):
+    """:func:`cross_bwd` into caller-provided dq (q's shape), dk, dv (k's shape;
+    strided views are fine, also of one buffer) and workspace (a contiguous CUDA
+    tensor of at least cross_bwd_workspace_bytes bytes)."""
+    import torch
+
+    sizes = _check_cross(q, k, v, lens, ("o", o), ("do", do), ("dq", dq))
+    dev = sizes[0]
+    for name, t in (("dk", dk), ("dv", dv)):
+        _check_rows(name, t, dev)
+        if t.shape != k.shape:
+            raise ValueError(f"{name} must have the shape of k")
+    _check_out("lse", lse, q.shape[:3], torch.float32, q.device)
+    _check_workspace(workspace, dev)
+    _on_current_device(dev)
+    _stream_on(stream, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(sizes[-1])
+    rc = library().fa_cross_bwd(q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), o.data_ptr(),
+                                _strides(o), lse.data_ptr(), do.data_ptr(), _strides(do), dq.data_ptr(), _strides(dq),
+                                dk.data_ptr(), _strides(dk), dv.data_ptr(), _strides(dv),
+                                None if lens is None else lens.data_ptr(), *sizes[1:], float(scale), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_cross_bwd")
+    return dq, dk, dv
+
+
+def cross_bwd(q, k, v, o, lse, do, lens=None, scale: float | None = None, stream=None):
+    """Gradients ``(dq, dk, dv)`` of :func:`cross_fwd` (o, lse from it, with the same
+    lens and scale) for the output gradient do: dk and dv summed over the heads of a
+    group, zero where no key is."""
+    import torch
+
+    if stream is not None:
+        with _under(stream, q):
+            return cross_bwd(q, k, v, o, lse, do, lens, scale)
+    sizes = _check_cross(q, k, v, lens, ("o", o), ("do", do))
+    dev = sizes[0]
+    if _cuda_device() != dev:
+        with torch.cuda.device(dev):
+            return cross_bwd(q, k, v, o, lse, do, lens, scale)
+    ws = torch.empty(cross_bwd_workspace_bytes(*sizes[1:]), dtype=torch.uint8, device=q.device)
+    dq = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    dk, dv = (torch.empty(k.shape, dtype=torch.bfloat16, device=q.device) for _ in range(2))
+    return cross_bwd_into(q, k, v, o, lse, do, dq, dk, dv, ws, lens, scale)
 
 
 QCACHE_PAGE = 64

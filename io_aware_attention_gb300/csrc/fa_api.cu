@@ -12,6 +12,7 @@
 
 #include "fa.h"
 #include "fa_bwd_kernel.cuh"
+#include "fa_cross_kernel.cuh"
 #include "fa_decode_kernel.cuh"
 #include "fa_ew_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
@@ -589,6 +590,189 @@ fa_status launch_rope(const fa::rope::Params& p, dim3 block, int64_t blocks, cud
                                                                                                            : FA_ERR_CUDA;
 }
 
+// Opt-in shared memory of a kernel, once a device.
+template <typename K>
+fa_status allow_smem(K kernel, size_t bytes, std::atomic<int>* done, int dev)
+{
+    if (dev < 0 || dev >= MAX_DEVICES) return FA_ERR_CUDA;
+    if (done[dev].load(std::memory_order_acquire)) return FA_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+        return FA_ERR_CUDA;
+    done[dev].store(1, std::memory_order_release);
+    return FA_OK;
+}
+
+// ------------------------------------------------------------ cross attention
+
+// A (B, H, N, d) bf16 tensor of any strides (elements).
+struct View {
+    const void* p;
+    int64_t s[3];  // batch, head, position
+    int64_t H, N;
+};
+
+View view_of(const void* p, const int64_t* strides, int64_t H, int64_t N, int64_t d)
+{
+    View v = {p, {H * N * d, N * d, d}, H, N};
+    if (strides) std::copy(strides, strides + 3, v.s);
+    return v;
+}
+
+size_t view_bytes(const View& v, int64_t B, int64_t d) { return (size_t)extent(v.s, B, v.H, v.N, d) * 2; }
+
+// What a tensor map can hold: 16-byte aligned, the strides that count multiples of
+// 8 elements and below 2^40 bytes.  Batches and heads of an input may repeat (stride
+// 0), positions not; an output may not repeat a place.
+fa_status view_check(const View& v, int64_t B, int64_t d, bool written)
+{
+    if (!strides_ok(v.s, B, v.H, v.N)) return FA_ERR_INVALID_ARG;
+    const int64_t n[3] = {B, v.H, v.N};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (v.s[i] % 8 != 0 || v.s[i] >= (int64_t)1 << 39)) return FA_ERR_UNSUPPORTED;
+    if (v.N > 1 && v.s[2] < d) return written || v.s[2] != 0 ? FA_ERR_INVALID_ARG : FA_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(v.p) & 15u) != 0) return FA_ERR_UNSUPPORTED;
+    if (written && !no_overlap_within(v.s, B, v.H, v.N, d)) return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+// A view as a 4-D tensor map (channels, positions, heads, batches), box = 64
+// columns x `rows` rows, 128-byte swizzle; a dimension that repeats has one entry
+// (*mul: the factors of the head and batch coordinates, 0 or 1).  Through a
+// per-thread cache like cached_map's.
+bool view_map(CUtensorMap* map, int* mul_h, int* mul_b, const View& v, int64_t B, int64_t d, uint32_t rows)
+{
+    struct Key {
+        const void* p;
+        int64_t s[3], H, N, B, d;
+        uint32_t rows;
+    };
+    struct Entry {
+        CUtensorMap map;
+        Key key;
+        bool valid;
+    };
+    constexpr int SLOTS = 16;
+    thread_local Entry cache[SLOTS] = {};
+    thread_local unsigned next = 0;
+    *mul_h = v.H > 1 && v.s[1] == 0 ? 0 : 1;
+    *mul_b = B > 1 && v.s[0] == 0 ? 0 : 1;
+    const Key key = {v.p, {v.s[0], v.s[1], v.s[2]}, v.H, v.N, B, d, rows};
+    auto same = [](const Key& a, const Key& b) {
+        return a.p == b.p && a.s[0] == b.s[0] && a.s[1] == b.s[1] && a.s[2] == b.s[2] && a.H == b.H && a.N == b.N && a.B == b.B &&
+               a.d == b.d && a.rows == b.rows;
+    };
+    for (const Entry& e : cache)
+        if (e.valid && same(e.key, key)) {
+            *map = e.map;
+            return true;
+        }
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)v.N, (cuuint64_t)(*mul_h ? v.H : 1), (cuuint64_t)(*mul_b ? B : 1)};
+    // The stride of a single entry means nothing and may be anything: a row's bytes stand in.
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] > 1 ? (cuuint64_t)v.s[2 - i] * 2 : (cuuint64_t)(d + 7) / 8 * 16;
+    cuuint32_t box[4] = {64, rows, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    if (fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(v.p), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    Entry& e = cache[next++ % SLOTS];
+    e.map = *map;
+    e.key = key;
+    e.valid = true;
+    return true;
+}
+
+// Whether the rows of a group's heads follow one another at one stride, so that
+// the group can run as one head of group * N rows: nothing distinguishes its
+// heads where no mask depends on the query.
+bool folds(const View& v, int64_t group)
+{
+    return group == 1 || (v.N == 1 ? v.s[1] != 0 : v.s[1] == v.N * v.s[2]);
+}
+
+View folded(View v, int64_t group)
+{
+    if (v.N == 1) v.s[2] = v.s[1];
+    v.s[1] *= group;
+    v.H /= group;
+    v.N *= group;
+    return v;
+}
+
+// Sizes of a cross-attention call (no pointer, no device).
+fa_status cross_check(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d)
+{
+    if (B < 1 || H < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || d < 1 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
+    if (!head_size_ok(d)) return FA_ERR_UNSUPPORTED;
+    // Rows, items and their coordinates are 32-bit.
+    const int64_t LIM = (int64_t)1 << 30;
+    const int64_t nq = (Nq + fa::bwd::BQ - 1) / fa::bwd::BQ * fa::bwd::BQ;
+    if (B > LIM / H || nq > LIM / (B * H) || Nk > LIM / 128 || (Nk + 127) / 128 > LIM / (B * H)) return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+// Parts that the key range of every item is cut into.  An item costs its key
+// tiles and about one more; the CTAs take ceil(items / SMs) rounds of them.  Cut
+// items write partial results, which the combine kernel reads (in units of a key
+// tile's K and V on every SM), and that kernel itself costs about three tiles.
+int64_t cross_splits(int64_t B, int64_t heads, int64_t nq, int64_t nk, int64_t Dp, int sms)
+{
+    const int64_t items = B * heads * ((nq + fa::BM - 1) / fa::BM), tiles = (nk + fa::BN - 1) / fa::BN;
+    int64_t best = 1;
+    double least = 0.0;
+    for (int64_t s = 1; s <= std::min<int64_t>(tiles, 128) && (s == 1 || items * s <= 16 * (int64_t)sms); ++s) {
+        const double rounds = (double)((items * s + sms - 1) / sms), per = (double)((tiles + s - 1) / s);
+        const double parts = s == 1 ? 0.0 : 3.0 + 2.0 * (double)(B * heads * nq * s) * (double)(Dp + 1) * 4.0 / ((double)sms * 512.0 * (double)Dp);
+        const double cost = rounds * (per + 1.0) + parts;
+        if (s == 1 || cost < least) best = s, least = cost;
+    }
+    return best;
+}
+
+size_t cross_part_bytes(int64_t rows, int64_t splits, int64_t Dp)
+{
+    return splits > 1 ? (size_t)(rows * splits) * (size_t)(Dp + 1) * sizeof(float) : 0;
+}
+
+size_t cross_bwd_ws(int64_t B, int64_t H, int64_t Nq, int64_t d)
+{
+    const int64_t np = (Nq + fa::bwd::BQ - 1) / fa::bwd::BQ * fa::bwd::BQ;
+    return (size_t)(B * H * np) * (size_t)(padded_head_size(d) + 2) * sizeof(float);
+}
+
+fa::cross::Rows rows_of(const View& v) { return {v.s[0], v.s[1], v.s[2], (int)v.H, (int)v.N}; }
+
+// Whether [p, p + n) meets view v.
+bool hits(const void* p, size_t n, const View& v, int64_t B, int64_t d) { return overlaps(p, n, v.p, view_bytes(v, B, d)); }
+
+template <int D, bool PAD>
+fa_status launch_cross_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const fa::Params& p, unsigned grid,
+                           int dev, cudaStream_t st)
+{
+    static std::atomic<int> done[MAX_DEVICES];
+    constexpr size_t smem = fa::Layout<D>::SMEM_BYTES_CROSS;
+    auto* const kernel = fa::fa_fwd_kernel<D, false, PAD, false, true>;
+    const fa_status as = allow_smem(kernel, smem, done, dev);
+    if (as != FA_OK) return as;
+    return launch_pdl(kernel, dim3(grid), dim3(fa::NUM_THREADS), smem, st, mq, mk, mv, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D>
+fa_status launch_cross_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
+                           const CUtensorMap& mdq, const fa::bwd::Params& p, unsigned grid, int dev, cudaStream_t st)
+{
+    static std::atomic<int> done[MAX_DEVICES];
+    constexpr size_t smem = fa::bwd::Layout<D>::SMEM_BYTES_CROSS;
+    auto* const kernel = fa::bwd::fa_bwd_kernel<D, false, true>;
+    const fa_status as = allow_smem(kernel, smem, done, dev);
+    if (as != FA_OK) return as;
+    kernel<<<grid, fa::bwd::NUM_THREADS, smem, st>>>(mq, mk, mv, mdo, mdq, p);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 // --------------------------------------------------------------- 4-bit cache
 
 // The sizes of a cache, as every call on one gives them.
@@ -648,17 +832,6 @@ int64_t qcache_decode_blocks(int sms, int64_t B, int64_t Hkv, int64_t rb, int64_
 size_t qcache_decode_ws(int64_t blocks, int64_t Dp, int nt)
 {
     return (size_t)blocks * (2 * qcache_part_bytes(Dp, nt) + 8);
-}
-
-template <typename K>
-fa_status allow_smem(K kernel, size_t bytes, std::atomic<int>* done, int dev)
-{
-    if (dev < 0 || dev >= MAX_DEVICES) return FA_ERR_CUDA;
-    if (done[dev].load(std::memory_order_acquire)) return FA_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
-        return FA_ERR_CUDA;
-    done[dev].store(1, std::memory_order_release);
-    return FA_OK;
 }
 
 template <int D, int NT, bool FOLD>
@@ -979,6 +1152,231 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
     const int64_t n8 = BH * N * d / 8;
     fa::bwd::fa_bwd_dq_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, st>>>(
         acc, static_cast<__nv_bfloat16*>(dq), (int)N, (int)sh.Np, (int)d, (int)sh.Dp, n8, scale);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_cross_fwd_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, size_t* bytes)
+{
+    if (!bytes) return FA_ERR_INVALID_ARG;
+    const fa_status cs = cross_check(B, H, Hkv, Nq, Nk, d);
+    if (cs != FA_OK) return cs;
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    // Strides decide whether a group's heads run as one: room for either.
+    const int64_t Dp = padded_head_size(d), g = H / Hkv;
+    const int64_t most = std::max(cross_splits(B, H, Nq, Nk, Dp, info.sms), cross_splits(B, Hkv, g * Nq, Nk, Dp, info.sms));
+    *bytes = cross_part_bytes(B * H * Nq, most, Dp);
+    return FA_OK;
+}
+
+fa_status fa_cross_fwd(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides, const void* v,
+                       const int64_t* v_strides, void* o, const int64_t* o_strides, float* lse, const int32_t* lens, int64_t B,
+                       int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, float scale, void* workspace,
+                       size_t workspace_bytes, fa_stream_t stream)
+{
+    // ---- argument checks (no CUDA call before these pass)
+    if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
+    const fa_status cs = cross_check(B, H, Hkv, Nq, Nk, d);
+    if (cs != FA_OK) return cs;
+    if (!std::isfinite(scale) || !(scale > 0.0f)) return FA_ERR_INVALID_ARG;
+    View vq = view_of(q, q_strides, H, Nq, d), vo = view_of(o, o_strides, H, Nq, d);
+    const View vk = view_of(k, k_strides, Hkv, Nk, d), vv = view_of(v, v_strides, Hkv, Nk, d);
+    const View* const views[4] = {&vq, &vk, &vv, &vo};
+    for (int i = 0; i < 4; ++i) {
+        const fa_status vs = view_check(*views[i], B, d, i == 3);
+        if (vs != FA_OK) return vs;
+    }
+    if (((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(lens)) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+        return FA_ERR_UNSUPPORTED;
+    const size_t ob = view_bytes(vo, B, d), lb = (size_t)(B * H * Nq) * 4, nb = lens ? (size_t)B * 4 : 0;
+    for (int i = 0; i < 3; ++i)
+        if (hits(o, ob, *views[i], B, d) || hits(lse, lb, *views[i], B, d)) return FA_ERR_INVALID_ARG;
+    if (overlaps(o, ob, lse, lb) || (lens && (overlaps(o, ob, lens, nb) || overlaps(lse, lb, lens, nb)))) return FA_ERR_INVALID_ARG;
+
+    // ---- device
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    const int64_t g = H / Hkv, Dp = padded_head_size(d);
+    int64_t group = g;  // query heads of a kv head that run apart
+    if (folds(vq, g) && folds(vo, g)) {
+        vq = folded(vq, g);
+        vo = folded(vo, g);
+        group = 1;
+    }
+    const int64_t splits = cross_splits(B, vq.H, vq.N, Nk, Dp, info.sms), rows = B * H * Nq;
+    const size_t need = cross_part_bytes(rows, splits, Dp);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need || overlaps(workspace, need, o, ob) || overlaps(workspace, need, lse, lb) ||
+            (lens && overlaps(workspace, need, lens, nb)))
+            return FA_ERR_INVALID_ARG;
+        for (int i = 0; i < 3; ++i)
+            if (hits(workspace, need, *views[i], B, d)) return FA_ERR_INVALID_ARG;
+    }
+    fa::Params p = {};
+    CUtensorMap mq, mk, mv;
+    if (!view_map(&mq, &p.x.q_h, &p.x.q_b, vq, B, d, fa::BM) || !view_map(&mk, &p.x.k_h, &p.x.k_b, vk, B, d, fa::BN) ||
+        !view_map(&mv, &p.x.v_h, &p.x.v_b, vv, B, d, fa::BN))
+        return FA_ERR_CUDA;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.N = (int)vq.N;
+    p.d = (int)d;
+    p.num_m_blocks = (int)((vq.N + fa::BM - 1) / fa::BM);
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+    p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    p.debug_skip_k = g_debug_skip_k.load(std::memory_order_relaxed);
+    p.x.lens = lens;
+    p.x.part = static_cast<float*>(workspace);
+    p.x.rows = rows;
+    p.x.o_b = vo.s[0], p.x.o_h = vo.s[1], p.x.o_n = vo.s[2];
+    p.x.heads = (int)vq.H;
+    p.x.group = (int)group;
+    p.x.splits = (int)splits;
+    p.x.nk = (int)Nk;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    // A launch holds the lengths of MAX_SEQS sequences.
+    for (int64_t b0 = 0; b0 < B; b0 += fa::MAX_SEQS) {
+        p.x.b0 = (int)b0;
+        p.x.nb = (int)std::min<int64_t>(B - b0, fa::MAX_SEQS);
+        p.num_items = p.x.nb * p.x.heads * p.num_m_blocks * p.x.splits;
+        const unsigned grid = (unsigned)std::min(p.num_items, info.sms);
+        const fa_status ls = d == 128  ? launch_cross_fwd<128, false>(mq, mk, mv, p, grid, dev, st)
+                             : d == 64 ? launch_cross_fwd<64, false>(mq, mk, mv, p, grid, dev, st)
+                             : d > 64  ? launch_cross_fwd<128, true>(mq, mk, mv, p, grid, dev, st)
+                                       : launch_cross_fwd<64, true>(mq, mk, mv, p, grid, dev, st);
+        if (ls != FA_OK) return ls;
+    }
+    if (splits > 1) {
+        const unsigned blocks = (unsigned)((rows + fa::cross::THREADS / 32 - 1) / (fa::cross::THREADS / 32));
+        auto* const join = Dp == 128 ? fa::cross::fa_cross_combine_kernel<128> : fa::cross::fa_cross_combine_kernel<64>;
+        if (launch_pdl(join, dim3(blocks), dim3(fa::cross::THREADS), 0, st, static_cast<const float*>(p.x.part), p.o, lse, lens,
+                       rows_of(vo), rows, (int)Nk, (int)splits, (int)d) != cudaSuccess)
+            return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+fa_status fa_cross_bwd_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, size_t* bytes)
+{
+    if (!bytes) return FA_ERR_INVALID_ARG;
+    const fa_status cs = cross_check(B, H, Hkv, Nq, Nk, d);
+    if (cs != FA_OK) return cs;
+    *bytes = cross_bwd_ws(B, H, Nq, d);
+    return FA_OK;
+}
+
+fa_status fa_cross_bwd(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides, const void* v,
+                       const int64_t* v_strides, const void* o, const int64_t* o_strides, const float* lse, const void* dout,
+                       const int64_t* dout_strides, void* dq, const int64_t* dq_strides, void* dk, const int64_t* dk_strides,
+                       void* dv, const int64_t* dv_strides, const int32_t* lens, int64_t B, int64_t H, int64_t Hkv, int64_t Nq,
+                       int64_t Nk, int64_t d, float scale, void* workspace, size_t workspace_bytes, fa_stream_t stream)
+{
+    // ---- argument checks (no CUDA call before these pass)
+    if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !workspace) return FA_ERR_INVALID_ARG;
+    const fa_status cs = cross_check(B, H, Hkv, Nq, Nk, d);
+    if (cs != FA_OK) return cs;
+    if (!std::isfinite(scale) || !(scale > 0.0f)) return FA_ERR_INVALID_ARG;
+    enum { Q, K, V, O, DO, DQ, DK, DV, VIEWS };
+    View w[VIEWS] = {view_of(q, q_strides, H, Nq, d),       view_of(k, k_strides, Hkv, Nk, d),   view_of(v, v_strides, Hkv, Nk, d),
+                     view_of(o, o_strides, H, Nq, d),       view_of(dout, dout_strides, H, Nq, d), view_of(dq, dq_strides, H, Nq, d),
+                     view_of(dk, dk_strides, Hkv, Nk, d),   view_of(dv, dv_strides, Hkv, Nk, d)};
+    for (int i = 0; i < VIEWS; ++i) {
+        const fa_status vs = view_check(w[i], B, d, i >= DQ);
+        if (vs != FA_OK) return vs;
+    }
+    if (((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(lens)) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+        return FA_ERR_UNSUPPORTED;
+    const size_t need = cross_bwd_ws(B, H, Nq, d);
+    if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
+    // Outputs and the workspace may share no place with an input or one another
+    // (dk and dv may be views of one buffer).
+    const size_t lb = (size_t)(B * H * Nq) * 4, nb = (size_t)B * 4;
+    for (int i = DQ; i <= VIEWS; ++i) {
+        const void* const p = i < VIEWS ? w[i].p : workspace;
+        const size_t n = i < VIEWS ? view_bytes(w[i], B, d) : need;
+        if (overlaps(p, n, lse, lb) || (lens && overlaps(p, n, lens, nb))) return FA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j) {
+            if (i == DV && j == DK) {
+                const RopeView a = {w[DK].p, {w[DK].s[0], w[DK].s[1], w[DK].s[2]}, Hkv};
+                const RopeView b = {w[DV].p, {w[DV].s[0], w[DV].s[1], w[DV].s[2]}, Hkv};
+                if (may_overlap(a, b, B, Nk, d)) return FA_ERR_INVALID_ARG;
+            } else if (hits(p, n, w[j], B, d)) {
+                return FA_ERR_INVALID_ARG;
+            }
+        }
+    }
+
+    // ---- device
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    const int64_t g = H / Hkv, Dp = padded_head_size(d);
+    int64_t group = g;
+    if (folds(w[Q], g) && folds(w[O], g) && folds(w[DO], g) && folds(w[DQ], g)) {
+        for (int i : {Q, O, DO, DQ}) w[i] = folded(w[i], g);
+        group = 1;
+    }
+    const int64_t heads = w[Q].H, nq = w[Q].N, np = (nq + fa::bwd::BQ - 1) / fa::bwd::BQ * fa::bwd::BQ, rows = B * heads * np;
+    float* const lse2 = static_cast<float*>(workspace);
+    float* const dsum = lse2 + rows;
+    float* const acc = dsum + rows;
+    fa::bwd::Params p = {};
+    CUtensorMap mq, mk, mv, mdo, mdq;
+    if (!view_map(&mq, &p.x.q_h, &p.x.q_b, w[Q], B, d, fa::bwd::BQ) || !view_map(&mk, &p.x.k_h, &p.x.k_b, w[K], B, d, fa::bwd::BKV) ||
+        !view_map(&mv, &p.x.v_h, &p.x.v_b, w[V], B, d, fa::bwd::BKV) ||
+        !view_map(&mdo, &p.x.do_h, &p.x.do_b, w[DO], B, d, fa::bwd::BQ) || !make_acc_map(&mdq, acc, 1, rows, Dp))
+        return FA_ERR_CUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+
+    // 1. D, L * log2 e, zeroed dQ accumulator.
+    constexpr int64_t PER = 8 * fa::bwd::PREP_ROWS;
+    fa::cross::fa_cross_prep_kernel<<<(unsigned)((rows + PER - 1) / PER), fa::cross::THREADS, 0, st>>>(
+        static_cast<const __nv_bfloat16*>(o), rows_of(w[O]), static_cast<const __nv_bfloat16*>(dout), rows_of(w[DO]), lse, lse2,
+        dsum, acc, (int)np, (int)d, (int)Dp, rows);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+
+    // 2. dK, dV and the dQ accumulator.
+    p.dk = static_cast<__nv_bfloat16*>(dk);
+    p.dv = static_cast<__nv_bfloat16*>(dv);
+    p.lse2 = lse2;
+    p.dsum = dsum;
+    p.dq_acc = acc;
+    p.N = (int)nq;
+    p.d = (int)d;
+    p.Np = (int)np;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+    p.scale = scale;
+    p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    p.debug_skip_q = g_debug_skip_k.load(std::memory_order_relaxed);
+    p.x.lens = lens;
+    p.x.dk_b = w[DK].s[0], p.x.dk_h = w[DK].s[1], p.x.dk_n = w[DK].s[2];
+    p.x.dv_b = w[DV].s[0], p.x.dv_h = w[DV].s[1], p.x.dv_n = w[DV].s[2];
+    p.x.heads = (int)heads;
+    p.x.kv_heads = (int)Hkv;
+    p.x.group = (int)group;
+    p.x.nk = (int)Nk;
+    p.x.q_blocks = (int)(np / fa::bwd::BQ);
+    for (int64_t b0 = 0; b0 < B; b0 += fa::MAX_SEQS) {
+        p.x.b0 = (int)b0;
+        p.x.nb = (int)std::min<int64_t>(B - b0, fa::MAX_SEQS);
+        const int64_t items = p.x.nb * Hkv * ((Nk + fa::bwd::BKV - 1) / fa::bwd::BKV);
+        const unsigned grid = (unsigned)std::min<int64_t>(items, info.sms);
+        const fa_status ms = Dp == 128 ? launch_cross_bwd<128>(mq, mk, mv, mdo, mdq, p, grid, dev, st)
+                                       : launch_cross_bwd<64>(mq, mk, mv, mdo, mdq, p, grid, dev, st);
+        if (ms != FA_OK) return ms;
+    }
+
+    // 3. dQ = scale * accumulator, bf16.
+    const int64_t n8 = B * H * Nq * (d / 8);
+    fa::cross::fa_cross_dq_kernel<<<(unsigned)((n8 + fa::cross::THREADS - 1) / fa::cross::THREADS), fa::cross::THREADS, 0, st>>>(
+        acc, static_cast<__nv_bfloat16*>(dq), rows_of(w[DQ]), (int)np, (int)d, (int)Dp, n8, scale);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -76,6 +76,15 @@
 //   - the Q/dO ring is three stages deep, released as soon as dK(g), its
 //     last reader, is done.
 //
+// CROSS: the keys are an encoder's states, of another length than the queries,
+// of any strides, shared by a group of heads, and lens[b] of them real.  An item
+// is then 128 keys of one kv head, its steps run through the query blocks of all
+// the group's heads, and dK, dV are their sums without another pass; the items
+// with keys are listed from the lengths (prefix sums in shared memory), so that
+// every CTA takes as many.  Rows of K and V from lens[b] on hold anything, NaN
+// among it: the issuer clears them in shared memory before the first product
+// (0 * NaN must not be formed in dQ), and their gradients are zeros.
+//
 // Named barriers are counted, not timed: every role executes each of its
 // bar.arrive / bar.sync once per step (or item) whatever happened, so the
 // counts always match.  mbarrier waits are bounded in time (see wait_bar);
@@ -125,6 +134,15 @@ constexpr uint32_t NB_DQ_COUNT = 32 * 4 + 32;
 // The producer warps signal with nb_signal (the forward kernel's header):
 // bar.arrive while healthy, bar.sync after an abort.
 
+// What CROSS adds.  Query head h of the call reads kv head h / group.
+struct Cross {
+    const int32_t* lens;                            // keys of each sequence, or null: all nk
+    int64_t dk_b, dk_h, dk_n, dv_b, dv_h, dv_n;     // strides in elements
+    int b0, nb;                                     // the launch's sequences, at most MAX_SEQS
+    int heads, kv_heads, group, nk, q_blocks;       // q_blocks: query blocks of a head
+    int q_b, q_h, k_b, k_h, v_b, v_h, do_b, do_h;   // 0 where a view repeats (its map has one of them), else 1
+};
+
 struct Params {
     __nv_bfloat16* dk;
     __nv_bfloat16* dv;
@@ -140,6 +158,7 @@ struct Params {
     float scale;
     unsigned long long wait_limit_ns;
     int debug_skip_q;  // test hook: global step whose Q/dO tile the first CTA never loads (-1: none)
+    Cross x;
 };
 
 template <int D>
@@ -170,7 +189,11 @@ struct Layout {
     static constexpr int NUM_BARS = B_DRAIN + 1;
     static constexpr uint32_t OFF_MISC = OFF_BAR + NUM_BARS * 8;  // [0] TMEM base, [1] abort
     static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16;
-    static_assert(SMEM_BYTES <= 232448, "shared memory");
+    // CROSS: the sequences' lengths and the sums of their key blocks.
+    static constexpr uint32_t OFF_LEN = OFF_MISC + 16;
+    static constexpr uint32_t OFF_PREFIX = OFF_LEN + 4 * MAX_SEQS;
+    static constexpr uint32_t SMEM_BYTES_CROSS = OFF_PREFIX + 4 * (MAX_SEQS + 1);
+    static_assert(SMEM_BYTES_CROSS <= 232448, "shared memory");
     static_assert(OFF_Q % 1024 == 0 && OFF_DO % 1024 == 0 && OFF_DS % 1024 == 0, "swizzled tiles");
 };
 
@@ -180,7 +203,31 @@ struct Layout {
 // the query blocks from the diagonal on, so every pair costs about the same.
 struct Item {
     int bh, key0, m0, nq;  // first key, first query block, query blocks
+    int b, kvh, len;       // CROSS (bh: the group's first head, nq: blocks of the whole group)
 };
+
+// CROSS item i of those with keys: sequences in order, then kv heads, then key blocks.
+__device__ __forceinline__ Item cross_item(int i, const Params& p, const int* len, const int* prefix)
+{
+    const Cross& x = p.x;
+    const int y = i / x.kv_heads;
+    int lo = 0, hi = x.nb;  // prefix[lo] <= y < prefix[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= y) lo = mid;
+        else hi = mid;
+    }
+    const int blocks = prefix[lo + 1] - prefix[lo], rem = i - prefix[lo] * x.kv_heads;
+    Item it;
+    it.b = x.b0 + lo;
+    it.kvh = rem / blocks;
+    it.key0 = (rem - it.kvh * blocks) * BKV;
+    it.len = len[lo];
+    it.bh = it.b * x.heads + it.kvh * x.group;
+    it.m0 = 0;
+    it.nq = x.group * x.q_blocks;
+    return it;
+}
 
 template <bool CAUSAL>
 __device__ __forceinline__ Item item_of(int i, const Params& p)
@@ -196,7 +243,7 @@ __device__ __forceinline__ Item item_of(int i, const Params& p)
     return it;
 }
 
-template <int D, bool CAUSAL>
+template <int D, bool CAUSAL, bool CROSS = false>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -218,8 +265,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int lane = threadIdx.x & 31;
     const uint64_t limit = p.wait_limit_ns;
     const int N = p.N;
-    auto first_item = [&]() -> int { return 2 * (int)blockIdx.x; };
+    int num_items = p.num_items;
+    const int* const seq_len = reinterpret_cast<const int*>(sgen + L::OFF_LEN);  // CROSS only
+    const int* const seq_prefix = reinterpret_cast<const int*>(sgen + L::OFF_PREFIX);
+    auto item_at = [&](int i, const Params& pp) -> Item {
+        if constexpr (CROSS) return cross_item(i, pp, seq_len, seq_prefix);
+        else return item_of<CAUSAL>(i, pp);
+    };
+    auto first_item = [&]() -> int { return CROSS ? (int)blockIdx.x : 2 * (int)blockIdx.x; };
     auto next_item = [&](int i, int& step) -> int {
+        if constexpr (CROSS) return i + (int)gridDim.x;
         ++step;
         return (step & 1) ? i + 1 : i - 1 + 2 * (int)gridDim.x;
     };
@@ -257,25 +312,48 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ptx::st_shared_v4(sbase + L::OFF_K + L::KBLK + 16u * i, 0u, 0u, 0u, 0u);
         ptx::fence_proxy_async_smem();
     }
+    if constexpr (CROSS) {
+        int* const len = reinterpret_cast<int*>(sgen + L::OFF_LEN);
+        int* const prefix = reinterpret_cast<int*>(sgen + L::OFF_PREFIX);
+        const int nb = p.x.nb, t = (int)threadIdx.x;
+        if (t < nb) {
+            if (blockIdx.x == 0 && p.x.lens && p.x.lens[p.x.b0 + t] > p.x.nk) atomicOr(&g_status, STATUS_BAD_PAGE);
+            len[t] = cross_length(p.x.lens, p.x.b0 + t, p.x.nk);
+        }
+        __syncthreads();
+        if (t <= nb) {  // (nb <= MAX_SEQS < NUM_THREADS)
+            int sum = 0;
+            for (int u = 0; u < t; ++u) sum += (len[u] + BKV - 1) / BKV;
+            prefix[t] = sum;
+        }
+    }
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = misc[0];
+    if constexpr (CROSS) num_items = seq_prefix[p.x.nb] * p.x.kv_heads;
 
     if (warp == WARP_TMA) {
         // ---------------------------------------------------- TMA producer
         int g = 0, k = 0;
         bool ok = true;
-        for (int i = first_item(), step = 0; ok && i < p.num_items; i = next_item(i, step), ++k) {
-            const Item it = item_of<CAUSAL>(i, p);
+        for (int i = first_item(), step = 0; ok && i < num_items; i = next_item(i, step), ++k) {
+            const Item it = item_at(i, p);
             if (!(ok = warp_wait_bar(bar(L::B_KVEMPTY), (uint32_t)(k & 1) ^ 1u, limit, abort_flag,
                                      0x1100 + L::B_KVEMPTY)))
                 break;
             if (ptx::elect_one()) {
                 ptx::mbar_arrive_expect_tx(bar(L::B_KVFULL), 2 * L::KV_BYTES);
                 for (int c = 0; c < D / 64; ++c) {
-                    ptx::tma_load_3d(sbase + L::OFF_K + c * L::KBLK, &tm_k, bar(L::B_KVFULL), c * 64, it.key0, it.bh);
-                    ptx::tma_load_3d(sbase + L::OFF_V + c * L::KBLK, &tm_v, bar(L::B_KVFULL), c * 64, it.key0, it.bh);
+                    if constexpr (CROSS) {
+                        ptx::tma_load_4d(sbase + L::OFF_K + c * L::KBLK, &tm_k, bar(L::B_KVFULL), c * 64, it.key0,
+                                         it.kvh * p.x.k_h, it.b * p.x.k_b);
+                        ptx::tma_load_4d(sbase + L::OFF_V + c * L::KBLK, &tm_v, bar(L::B_KVFULL), c * 64, it.key0,
+                                         it.kvh * p.x.v_h, it.b * p.x.v_b);
+                    } else {
+                        ptx::tma_load_3d(sbase + L::OFF_K + c * L::KBLK, &tm_k, bar(L::B_KVFULL), c * 64, it.key0, it.bh);
+                        ptx::tma_load_3d(sbase + L::OFF_V + c * L::KBLK, &tm_v, bar(L::B_KVFULL), c * 64, it.key0, it.bh);
+                    }
                 }
             }
             for (int t = 0; ok && t < it.nq; ++t, ++g) {
@@ -286,13 +364,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 // Test hook: the first CTA leaves one step's tile unloaded, so
                 // the issuer's wait for it runs out (exercises the abort path).
                 if (ptx::elect_one() && !(g == p.debug_skip_q && blockIdx.x == 0)) {
-                    const int q0 = (it.m0 + t) * BQ;
+                    const int head = CROSS ? t / p.x.q_blocks : 0;  // of the group
+                    const int q0 = (it.m0 + t - (CROSS ? head * p.x.q_blocks : 0)) * BQ;
+                    const int h = CROSS ? it.kvh * p.x.group + head : 0;
                     const uint32_t fb = bar(L::B_QFULL + s);
                     ptx::mbar_arrive_expect_tx(fb, 2 * L::QT_BYTES);
                     for (int c = 0; c < D / 64; ++c) {
-                        ptx::tma_load_3d(sbase + L::OFF_Q + s * L::QT_BYTES + c * L::QBLK, &tm_q, fb, c * 64, q0, it.bh);
-                        ptx::tma_load_3d(sbase + L::OFF_DO + s * L::QT_BYTES + c * L::QBLK, &tm_do, fb, c * 64, q0,
-                                         it.bh);
+                        if constexpr (CROSS) {
+                            ptx::tma_load_4d(sbase + L::OFF_Q + s * L::QT_BYTES + c * L::QBLK, &tm_q, fb, c * 64, q0,
+                                             h * p.x.q_h, it.b * p.x.q_b);
+                            ptx::tma_load_4d(sbase + L::OFF_DO + s * L::QT_BYTES + c * L::QBLK, &tm_do, fb, c * 64, q0,
+                                             h * p.x.do_h, it.b * p.x.do_b);
+                        } else {
+                            ptx::tma_load_3d(sbase + L::OFF_Q + s * L::QT_BYTES + c * L::QBLK, &tm_q, fb, c * 64, q0, it.bh);
+                            ptx::tma_load_3d(sbase + L::OFF_DO + s * L::QT_BYTES + c * L::QBLK, &tm_do, fb, c * 64, q0,
+                                             it.bh);
+                        }
                     }
                 }
             }
@@ -351,9 +438,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         };
 
         int g = 0, k = 0;
-        for (int i = first_item(), step = 0; i < p.num_items; i = next_item(i, step), ++k) {
-            const Item it = item_of<CAUSAL>(i, p);
+        for (int i = first_item(), step = 0; i < num_items; i = next_item(i, step), ++k) {
+            const Item it = item_at(i, p);
             if (ok) ok = warp_wait_bar(bar(L::B_KVFULL), (uint32_t)(k & 1), limit, abort_flag, 0x1200 + L::B_KVFULL);
+            // CROSS: rows behind the sequence's last key are cleared (those from nk
+            // on came as zeros).
+            if (CROSS && ok && it.len < min(it.key0 + BKV, p.x.nk)) {
+                const uint32_t first = (uint32_t)(it.len - it.key0);
+                for (int c = 0; c < D / 64; ++c)
+                    for (uint32_t e = first * 8 + (uint32_t)lane; e < BKV * 8; e += 32) {
+                        ptx::st_shared_v4(sbase + L::OFF_K + c * L::KBLK + 16u * e, 0u, 0u, 0u, 0u);
+                        ptx::st_shared_v4(sbase + L::OFF_V + c * L::KBLK + 16u * e, 0u, 0u, 0u, 0u);
+                    }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            }
             issue_s_dp(g);
             for (int t = 0; t < it.nq; ++t, ++g) {
                 const int s = g % QSTAGES, b = g & 1;
@@ -429,8 +528,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool has_dims = quarter * 32 < p.d;  // this lane quarter of dQ^T holds head dims
         int g = 0, k = 0;
         bool ok = true;
-        for (int i = first_item(), step = 0; i < p.num_items; i = next_item(i, step), ++k) {
-            const Item it = item_of<CAUSAL>(i, p);
+        if constexpr (CROSS) {
+            // Key blocks without a key: zero gradients.
+            const int all = (p.x.nk + BKV - 1) / BKV, t = (int)threadIdx.x - 32 * WARP_DQ0;
+            for (int64_t u = blockIdx.x; u < (int64_t)p.x.nb * p.x.kv_heads * all; u += gridDim.x) {
+                const int sh = (int)(u / all), kb = (int)(u - (int64_t)sh * all);
+                const int s = sh / p.x.kv_heads, h = sh - s * p.x.kv_heads;
+                if (kb * BKV < seq_len[s]) continue;
+                const int words = p.d / 8, rows = min(BKV, p.x.nk - kb * BKV);
+                for (int e = t; e < rows * words; e += 128) {
+                    const int key = kb * BKV + e / words, c = e % words * 8;
+                    ptx::st_global_v4(p.dk + (p.x.b0 + s) * p.x.dk_b + h * p.x.dk_h + key * p.x.dk_n + c, 0u, 0u, 0u, 0u);
+                    ptx::st_global_v4(p.dv + (p.x.b0 + s) * p.x.dv_b + h * p.x.dv_h + key * p.x.dv_n + c, 0u, 0u, 0u, 0u);
+                }
+            }
+        }
+        for (int i = first_item(), step = 0; i < num_items; i = next_item(i, step), ++k) {
+            const Item it = item_at(i, p);
             for (int t = 0; t < it.nq; ++t, ++g) {
                 if (ok) ok = warp_wait_bar(bar(L::B_DQFULL), (uint32_t)g & 1u, limit, abort_flag, 0x1300 + L::B_DQFULL);
                 // Every dQ warp waits for dQ(g) before it signals, so that no
@@ -458,7 +572,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        ptx::tma_reduce_add_3d(&tm_dq, stg, quarter * 32, (it.m0 + t) * BQ, it.bh);
+                        // (CROSS: the rows of all heads as one run; a group's heads adjoin.)
+                        if constexpr (CROSS)
+                            ptx::tma_reduce_add_3d(&tm_dq, stg, quarter * 32, it.bh * p.Np + t * BQ, 0);
+                        else
+                            ptx::tma_reduce_add_3d(&tm_dq, stg, quarter * 32, (it.m0 + t) * BQ, it.bh);
                         ptx::tma_store_commit();
                     }
                 } else {
@@ -471,10 +589,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (ok) {
                 ptx::tc_fence_after_sync();
                 const int key = it.key0 + quarter * 32 + lane;
-                const bool key_ok = key < N;
+                const bool key_ok = key < (CROSS ? p.x.nk : N);
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {
-                    __nv_bfloat16* const dst = (which ? p.dk : p.dv) + ((int64_t)it.bh * N + key) * p.d;
+                    __nv_bfloat16* const dst =
+                        CROSS ? (which ? p.dk + it.b * p.x.dk_b + it.kvh * p.x.dk_h + key * p.x.dk_n
+                                       : p.dv + it.b * p.x.dv_b + it.kvh * p.x.dv_h + key * p.x.dv_n)
+                              : (which ? p.dk : p.dv) + ((int64_t)it.bh * N + key) * p.d;
                     const float mul = which ? p.scale : 1.0f;
 #pragma unroll
                     for (int ch = 0; ch < D / 32; ++ch) {
@@ -511,10 +632,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const float sl2 = p.scale_log2;
         int g = 0;
         bool ok = true;
-        for (int i = first_item(), step = 0; i < p.num_items; i = next_item(i, step)) {
-            const Item it = item_of<CAUSAL>(i, p);
+        for (int i = first_item(), step = 0; i < num_items; i = next_item(i, step)) {
+            const Item it = item_at(i, p);
             const int key = it.key0 + r;
-            const bool key_ok = key < N;
+            const bool key_ok = key < (CROSS ? it.len : N);
             for (int t = 0; t < it.nq; ++t, ++g) {
                 const int b = g & 1;
                 const int q0 = (it.m0 + t) * BQ + half * 32;  // first query of this thread's columns

@@ -89,6 +89,19 @@
 // TMA boxes are 64 columns wide and fill columns past d with zeros, which add
 // nothing to any dot product; the epilogue stores d columns with row stride d.
 //
+// CROSS: the keys are an encoder's states, of another length than the queries,
+// of any strides, shared by a group of heads, and lens[b] of them real.  Then
+//   - an item is 128 rows of one query head against one of `splits` equal runs of
+//     its sequence's key tiles (splits > 1 where rows alone do not fill the GPU:
+//     each item leaves a partial result, and fa_cross_combine_kernel joins them);
+//   - items come longest sequence first and are dealt out in snake order, so that
+//     unequal sequences load the CTAs alike; the heads and row blocks that read
+//     the same keys are neighbours, and so in flight at once (L2);
+//   - keys from lens[b] on hold anything, NaN among it.  Their scores are set to
+//     -inf (selected, not added), and as 0 * NaN must not be formed either, the
+//     P.V issuer skips the products of 16 keys that lie behind the last one and
+//     clears the rows of V within the last 16 in shared memory.
+//
 // Every mbarrier wait is bounded in time; on expiry the thread records the
 // wait in the device status word, raises a CTA-wide abort flag, and all roles
 // drain their in-flight copies / MMAs and reach the common exit, where TMEM is
@@ -129,6 +142,7 @@ constexpr uint32_t BLK_BYTES = BN * 128;  // one 64-column, 128-row swizzled blo
 
 constexpr uint32_t STATUS_TIMEOUT = 1u;
 constexpr uint32_t STATUS_BAD_SMEM = 2u;
+constexpr uint32_t STATUS_BAD_PAGE = 4u;  // a length or a page table entry out of range: its keys were skipped
 
 // Named barriers (0 is __syncthreads): 1..4 pair the two softmax warps of a
 // lane quarter; 5..7 carry "S of tile g is in TMEM" from the score MMA issuer
@@ -164,6 +178,18 @@ __device__ __forceinline__ void nb_signal(uint32_t id, uint32_t count, bool ok)
         ptx::named_barrier_sync(id, count);
 }
 
+// What CROSS adds.  A query head h of the call reads kv head h / group.
+struct Cross {
+    const int32_t* lens;  // keys of each sequence, or null: all nk
+    float* part;          // splits > 1: [split][row] of D outputs, then [split][row] of base-2 logsumexps
+    int64_t rows;         // query rows of the whole call (b, head, row)
+    int64_t o_b, o_h, o_n;  // strides of o in elements
+    int b0, nb;           // the launch's sequences: b0 .. b0 + nb - 1, at most MAX_SEQS
+    int heads, group, splits, nk;
+    int q_b, q_h, k_b, k_h, v_b, v_h;  // 0 where a view repeats (its map has one of them), else 1
+};
+constexpr int MAX_SEQS = 256;  // sequences of a CROSS launch (their lengths sit in shared memory)
+
 struct Params {
     __nv_bfloat16* o;
     float* lse;
@@ -175,6 +201,7 @@ struct Params {
     float scale_log2;  // scale * log2(e)
     unsigned long long wait_limit_ns;
     int debug_skip_k;  // test hook: global K tile the producer never loads (-1: none)
+    Cross x;
 };
 
 template <int D>
@@ -223,7 +250,11 @@ struct Layout {
     // The dynamic shared memory base is 1024-byte aligned (no static shared
     // memory); the kernel checks it and refuses to run otherwise.
     static constexpr uint32_t SMEM_BYTES = OFF_MISC + 16;
-    static_assert(SMEM_BYTES <= 232448, "shared memory");
+    // CROSS: the sequences' lengths, and their order by falling length.
+    static constexpr uint32_t OFF_LEN = OFF_MISC + 16;
+    static constexpr uint32_t OFF_ORDER = OFF_LEN + 4 * MAX_SEQS;
+    static constexpr uint32_t SMEM_BYTES_CROSS = OFF_ORDER + 2 * MAX_SEQS;
+    static_assert(SMEM_BYTES_CROSS <= 232448, "shared memory");
 };
 
 __device__ unsigned int g_status;        // STATUS_* bits, sticky until read by the host
@@ -364,8 +395,9 @@ __device__ __forceinline__ void scale_row(uint32_t taddr, float corr)
 // lines per instruction, where the rows straight from registers would touch
 // 32 lines per instruction and hold up the SM's memory pipeline.  Rows >=
 // rows_left are not stored.
+template <typename Stride>
 __device__ __forceinline__ void store_rows_coalesced(uint32_t (&w)[32], __nv_bfloat16* base, int lane, int rows_left,
-                                                     int stride)
+                                                     Stride stride)
 {
     const int j = lane & 7;
 #pragma unroll
@@ -408,6 +440,7 @@ __device__ __forceinline__ void store_rows_coalesced(uint32_t (&w)[32], __nv_bfl
 //    item_of serves both.
 struct Item {
     int bh, q0, n_kv;
+    int b, h, kvh, j0, len, split;  // CROSS: sequence, heads, first key tile, keys of the sequence, part
 };
 
 // Index (in the pair order) of the item of cost rank r; num_items once the
@@ -436,10 +469,44 @@ __device__ __forceinline__ Item item_of(int i, const Params& p)
     return it;
 }
 
+// The keys of sequence b of a CROSS call: negative counts as 0, more than there
+// are as all of them.
+__device__ __forceinline__ int cross_length(const int32_t* lens, int b, int nk)
+{
+    return lens ? min(max(lens[b], 0), nk) : nk;
+}
+
+// CROSS item i.  Per sequence (longest first), kv head and part: the group's heads
+// and their row blocks.
+__device__ __forceinline__ Item cross_item(int i, const Params& p, const int* len, const uint16_t* order)
+{
+    const Cross& x = p.x;
+    Item it;
+    const int per_part = x.group * p.num_m_blocks, per_head = per_part * x.splits;
+    const int seq_head = i / per_head, in_head = i - seq_head * per_head;
+    const int kv_heads = x.heads / x.group;
+    const int rank = seq_head / kv_heads;
+    it.kvh = seq_head - rank * kv_heads;
+    it.split = in_head / per_part;
+    const int in_part = in_head - it.split * per_part;
+    const int g = in_part / p.num_m_blocks;
+    it.q0 = (in_part - g * p.num_m_blocks) * BM;
+    it.h = it.kvh * x.group + g;
+    const int s = order[rank];
+    it.b = x.b0 + s;
+    it.bh = it.b * x.heads + it.h;
+    it.len = len[s];
+    const int tiles = (it.len + BN - 1) / BN;
+    it.j0 = (int)((int64_t)tiles * it.split / x.splits);
+    it.n_kv = (int)((int64_t)tiles * (it.split + 1) / x.splits) - it.j0;
+    return it;
+}
+
 // PAD: the caller's head size p.d is below D (stores are guarded and strided
 // by p.d); the instances for d = D compile without the guard.  SNAKE: the
 // items run in cost order (see item_of).
-template <int D, bool CAUSAL, bool PAD, bool SNAKE>
+// CROSS: see the file comment.
+template <int D, bool CAUSAL, bool PAD, bool SNAKE, bool CROSS = false>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const Params p)
@@ -463,11 +530,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // This CTA's items (see item_of): pairs p = blockIdx.x, blockIdx.x +
     // gridDim.x, ..., both items 2p and 2p + 1 of each pair; or ranks in snake
     // order.
-    auto first_item = [&]() -> int {
+    const int* const seq_len = reinterpret_cast<const int*>(sgen + L::OFF_LEN);            // CROSS only
+    const uint16_t* const seq_order = reinterpret_cast<const uint16_t*>(sgen + L::OFF_ORDER);
+    auto item_at = [&](int i, const Params& pp) -> Item {
+        if constexpr (CROSS) return cross_item(i, pp, seq_len, seq_order);
+        else return item_of<CAUSAL>(i, pp);
+    };
+    auto deal = [&](int step) -> int {  // CROSS: the CTA's item of this step
+        const int G = (int)gridDim.x;
+        return step * G + ((step & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    };
+    // CROSS: the first item from this step on that has keys (num_items: none).
+    auto deal_some = [&](int& step) -> int {
+        int i = deal(step);
+        while (step * (int64_t)gridDim.x < p.num_items && (i >= p.num_items || item_at(i, p).n_kv == 0)) i = deal(++step);
+        return i < p.num_items ? i : p.num_items;
+    };
+    auto first_item = [&](int& step) -> int {
+        step = 0;
+        if constexpr (CROSS) return deal_some(step);
         return SNAKE ? item_of_rank((int)blockIdx.x, p) : 2 * (int)blockIdx.x;
     };
     auto next_item = [&](int i, int& step) -> int {
         ++step;
+        if constexpr (CROSS) return deal_some(step);
         if constexpr (SNAKE) {
             const int G = (int)gridDim.x;
             return item_of_rank(step * G + ((step & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x), p);
@@ -545,6 +631,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // memory is touched only after it has completed.
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    if constexpr (CROSS) {
+        int* const len = reinterpret_cast<int*>(sgen + L::OFF_LEN);
+        uint16_t* const order = reinterpret_cast<uint16_t*>(sgen + L::OFF_ORDER);
+        const int nb = p.x.nb, t = (int)threadIdx.x;
+        if (t < nb) {
+            if (blockIdx.x == 0 && p.x.lens && p.x.lens[p.x.b0 + t] > p.x.nk) atomicOr(&g_status, STATUS_BAD_PAGE);
+            len[t] = cross_length(p.x.lens, p.x.b0 + t, p.x.nk);
+        }
+        __syncthreads();
+        if (t < nb) {
+            int rank = t;
+            if (p.x.lens) {  // longer ones first, equal ones as they come
+                const int mine = len[t];
+                rank = 0;
+                for (int u = 0; u < nb; ++u) rank += (len[u] > mine || (len[u] == mine && u < t)) ? 1 : 0;
+            }
+            order[rank] = (uint16_t)t;
+        }
+        __syncthreads();
+    }
     // Warpgroups 2-3 give up registers that warpgroups 0-1 (the softmax
     // warps) take; each register change heads the code of its warpgroups.
     if (warp >= SOFTMAX_WARPS) {
@@ -569,19 +675,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (!warp_wait_bar(bar(L::B_QEMPTY), (uint32_t)(nq & 1) ^ 1u, limit, abort_flag,
                                    0x100 + L::B_QEMPTY))
                     return false;
-                const Item iq = item_of<CAUSAL>(i, p);
+                const Item iq = item_at(i, p);
                 if (ptx::elect_one()) {
                     ptx::mbar_arrive_expect_tx(bar(L::B_QFULL), L::Q_BYTES);
-                    for (int c = 0; c < L::DBLK; ++c)
-                        ptx::tma_load_3d(sbase + L::OFF_Q + c * BLK_BYTES, &tm_q, bar(L::B_QFULL), c * 64, iq.q0,
-                                         iq.bh);
+                    for (int c = 0; c < L::DBLK; ++c) {
+                        if constexpr (CROSS)
+                            ptx::tma_load_4d(sbase + L::OFF_Q + c * BLK_BYTES, &tm_q, bar(L::B_QFULL), c * 64, iq.q0,
+                                             iq.h * p.x.q_h, iq.b * p.x.q_b);
+                        else
+                            ptx::tma_load_3d(sbase + L::OFF_Q + c * BLK_BYTES, &tm_q, bar(L::B_QFULL), c * 64, iq.q0,
+                                             iq.bh);
+                    }
                 }
                 ++nq;
                 return true;
             };
-            int i = first_item(), step = 0;
+            int step, i = first_item(step);
             while (ok && i < p.num_items) {
-                const Item it = item_of<CAUSAL>(i, p);
+                const Item it = item_at(i, p);
                 for (int j = 0; ok && j < it.n_kv; ++j) {
                     const int s = gk % L::KSTAGES;
                     const uint32_t ph = (uint32_t)(gk / L::KSTAGES) & 1u;
@@ -594,9 +705,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (!skip && ptx::elect_one()) {
                         ptx::mbar_arrive_expect_tx(bar(L::B_KFULL + s), L::KV_BYTES);
                         FA_TRACE_EV(WARP_TMA, gk, 0);
-                        for (int c = 0; c < L::DBLK; ++c)
-                            ptx::tma_load_3d(sbase + L::OFF_K + s * L::KV_BYTES + c * BLK_BYTES, &tm_k,
-                                             bar(L::B_KFULL + s), c * 64, j * BN, it.bh);
+                        for (int c = 0; c < L::DBLK; ++c) {
+                            if constexpr (CROSS)
+                                ptx::tma_load_4d(sbase + L::OFF_K + s * L::KV_BYTES + c * BLK_BYTES, &tm_k,
+                                                 bar(L::B_KFULL + s), c * 64, (it.j0 + j) * BN, it.kvh * p.x.k_h,
+                                                 it.b * p.x.k_b);
+                            else
+                                ptx::tma_load_3d(sbase + L::OFF_K + s * L::KV_BYTES + c * BLK_BYTES, &tm_k,
+                                                 bar(L::B_KFULL + s), c * 64, j * BN, it.bh);
+                        }
                     }
                     ++gk;
                     if (j == 0) {
@@ -607,8 +724,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         int step_next = step;
                         const int i_next = next_item(i, step_next);
                         if (i_next < p.num_items && ptx::elect_one()) {
-                            const Item in = item_of<CAUSAL>(i_next, p);
-                            for (int c = 0; c < L::DBLK; ++c) ptx::tma_prefetch_3d(&tm_q, c * 64, in.q0, in.bh);
+                            const Item in = item_at(i_next, p);
+                            for (int c = 0; c < L::DBLK; ++c) {
+                                if constexpr (CROSS)
+                                    ptx::tma_prefetch_4d(&tm_q, c * 64, in.q0, in.h * p.x.q_h, in.b * p.x.q_b);
+                                else
+                                    ptx::tma_prefetch_3d(&tm_q, c * 64, in.q0, in.bh);
+                            }
                         }
                     }
                 }
@@ -626,8 +748,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // that read the stage VSTAGES tiles before is complete.
             int gv = 0;
             bool ok = true;
-            for (int i = first_item(), step = 0; ok && i < p.num_items; i = next_item(i, step)) {
-                const Item it = item_of<CAUSAL>(i, p);
+            for (int step, i = first_item(step); ok && i < p.num_items; i = next_item(i, step)) {
+                const Item it = item_at(i, p);
                 for (int j = 0; ok && j < it.n_kv; ++j) {
                     const int s = gv % L::VSTAGES;
                     const uint32_t ph = (uint32_t)(gv / L::VSTAGES) & 1u;
@@ -637,9 +759,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (ptx::elect_one()) {
                         ptx::mbar_arrive_expect_tx(bar(L::B_VFULL + s), L::KV_BYTES);
                         FA_TRACE_EV(WARP_TMA_V, gv, 1);
-                        for (int c = 0; c < L::DBLK; ++c)
-                            ptx::tma_load_3d(sbase + L::OFF_V + s * L::VSTAGE + c * BLK_BYTES, &tm_v,
-                                             bar(L::B_VFULL + s), c * 64, j * BN, it.bh);
+                        for (int c = 0; c < L::DBLK; ++c) {
+                            if constexpr (CROSS)
+                                ptx::tma_load_4d(sbase + L::OFF_V + s * L::VSTAGE + c * BLK_BYTES, &tm_v,
+                                                 bar(L::B_VFULL + s), c * 64, (it.j0 + j) * BN, it.kvh * p.x.v_h,
+                                                 it.b * p.x.v_b);
+                            else
+                                ptx::tma_load_3d(sbase + L::OFF_V + s * L::VSTAGE + c * BLK_BYTES, &tm_v,
+                                                 bar(L::B_VFULL + s), c * 64, j * BN, it.bh);
+                        }
                     }
                     ++gv;
                 }
@@ -680,8 +808,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     nb_signal(NB_SREADY0 + (uint32_t)(gg % 3), NB_SREADY_COUNT, ok);
                 }
             };
-            for (int i = first_item(), step = 0; i < p.num_items; i = next_item(i, step), ++k) {
-                const int n = item_of<CAUSAL>(i, p).n_kv;
+            for (int step, i = first_item(step); i < p.num_items; i = next_item(i, step), ++k) {
+                const int n = item_at(i, p).n_kv;
                 for (int j = 0; j < n; ++j, ++g) {
                     const int b = g & 1;
                     const int s = g % L::KSTAGES;
@@ -731,6 +859,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // per column, 8 columns per 16 keys); B MN-major (value columns
             // contiguous): 64-column blocks BLK_BYTES apart (the ones block follows
             // the value blocks), 8-key groups 1024 bytes apart.
+            //
+            // CROSS: clears the rows first .. end - 1 of V stage s (the whole warp,
+            // before the products that read them).
+            [[maybe_unused]] auto clear_rows = [&](int s, int first, int end) {
+                const uint32_t v = sbase + L::OFF_V + (uint32_t)s * L::VSTAGE + (uint32_t)first * 128;
+                for (int c = 0; c < L::DBLK; ++c)
+                    for (int e = lane; e < (end - first) * 8; e += 32)
+                        ptx::st_shared_v4(v + (uint32_t)c * BLK_BYTES + 16u * (uint32_t)e, 0u, 0u, 0u, 0u);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            };
             if constexpr (L::SPLIT) {
                 // [O_h | l~_h] (+)= P_h [V_h | 1] for global tile g and each half h:
                 // A = P_h from TMEM (over the half's scores in S buffer g & 1; 2 bf16
@@ -742,8 +881,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint64_t v_desc0 = ptx::sdesc_sw128(sbase + L::OFF_V, BLK_BYTES, 1024);
                 int g = 0, k = 0;  // tiles and items done
                 bool ok = true;
-                for (int i = first_item(), step = 0; ok && i < p.num_items; i = next_item(i, step), ++k) {
-                    const int n = item_of<CAUSAL>(i, p).n_kv;
+                for (int step, i = first_item(step); ok && i < p.num_items; i = next_item(i, step), ++k) {
+                    const Item it = item_at(i, p);
+                    const int n = it.n_kv;
                     // The first P.V of an item overwrites O: wait until the softmax
                     // warps have read out the previous item's O.
                     if (!(ok = warp_wait_bar(bar(L::B_OFREE), (uint32_t)(k & 1) ^ 1u, limit, abort_flag,
@@ -761,6 +901,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         if (lane == 0) FA_TRACE_EV(WARP_MMA_O, g, 3);
                         const uint64_t v_desc = v_desc0 + (uint64_t)((s * L::VSTAGE) >> 4);
                         const uint32_t s_tm = tmem + (b ? TM_S1 : TM_S0);
+                        // CROSS: keys of this tile that are real, and the products of 16
+                        // that a half takes (one at least: an item's first sets O_h).
+                        const int left = CROSS ? it.len - (it.j0 + j) * BN : BN;
+                        auto products = [&](int h) { return left >= BN ? 4 : min(4, max(1, (left - 64 * h + 15) / 16)); };
+                        if (CROSS && left < BN) {
+                            const int end0 = 16 * products(0), end1 = 64 + 16 * products(1);
+                            if (left < end0) clear_rows(s, left, end0);
+                            if (left < end1) clear_rows(s, max(left, 64), end1);
+                        }
     #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             // P_h of tile g (per S buffer: the phase before, tile g - 2,
@@ -771,6 +920,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             ptx::tc_fence_after_sync();
     #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
+                                if (CROSS && kk >= products(h)) break;
                                 if (ptx::elect_one())
                                     ptx::mma_ts(tmem + TM_O + (uint32_t)h * L::O_STRIDE, s_tm + (uint32_t)(h * 64 + kk * 8),
                                                 v_desc + (uint64_t)(((h * 64 + kk * 16) * 128) >> 4), IDESC_O,
@@ -793,8 +943,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t p_tmem = tmem + TM_P;
                 int g = 0, k = 0;  // tiles and items done
                 bool ok = true;
-                for (int i = first_item(), step = 0; ok && i < p.num_items; i = next_item(i, step), ++k) {
-                    const int n = item_of<CAUSAL>(i, p).n_kv;
+                for (int step, i = first_item(step); ok && i < p.num_items; i = next_item(i, step), ++k) {
+                    const Item it = item_at(i, p);
+                    const int n = it.n_kv;
                     // The first P.V of an item overwrites O: wait until the softmax
                     // warps have read out the previous item's O.
                     if (!(ok = warp_wait_bar(bar(L::B_OFREE), (uint32_t)(k & 1) ^ 1u, limit, abort_flag,
@@ -811,6 +962,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                                  abort_flag, 0x200 + L::B_VFULL + s)))
                             break;
                         if (lane == 0) FA_TRACE_EV(WARP_MMA_O, g, 3);
+                        // CROSS: keys of this tile that are real.
+                        const int left = CROSS ? it.len - (it.j0 + j) * BN : BN;
+                        if (CROSS && left < BN && left % 16 != 0) clear_rows(s, left, (left + 15) / 16 * 16);
                         if (!(ok = warp_wait_bar(bar(L::B_PFULL), (uint32_t)(g & 1), limit, abort_flag,
                                                  0x200 + L::B_PFULL)))
                             break;
@@ -819,6 +973,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         const uint64_t v_desc = v_desc0 + (uint64_t)((s * L::VSTAGE) >> 4);
     #pragma unroll
                         for (int kk = 0; kk < BN / 16; ++kk) {
+                            if (CROSS && kk * 16 >= left) break;
                             if (ptx::elect_one())
                                 ptx::mma_ts(tmem + TM_O, p_tmem + (uint32_t)kk * 8,
                                             v_desc + (uint64_t)(kk * ((16 * 128) >> 4)), IDESC_O,
@@ -859,8 +1014,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int ostride = PAD ? p.d : D;
             bool ok = true;
             int kitem = 0;
-            for (int i = first_item(), step = 0; ok && i < p.num_items; i = next_item(i, step), ++kitem) {
-                const Item it = item_of<CAUSAL>(i, p);
+            if constexpr (CROSS) {
+                // Sequences without keys: nothing is seen (parts without keys are
+                // not read when parts are joined).
+                for (int i = (int)blockIdx.x; p.x.splits == 1 && i < p.num_items; i += (int)gridDim.x) {
+                    const Item it = item_at(i, p);
+                    const int q_idx = it.q0 + row;
+                    if (it.n_kv != 0 || q_idx >= N) continue;
+                    __nv_bfloat16* const orow = p.o + it.b * p.x.o_b + it.h * p.x.o_h + q_idx * p.x.o_n;
+                    for (int c = 0; c < p.d; c += 8) ptx::st_global_v4(orow + c, 0u, 0u, 0u, 0u);
+                    p.lse[(int64_t)it.bh * N + q_idx] = -INFINITY;
+                }
+            }
+            for (int step, i = first_item(step); ok && i < p.num_items; i = next_item(i, step), ++kitem) {
+                const Item it = item_at(i, p);
                 const int slot = kitem & 1;
                 if (!(ok = warp_wait_bar(bar(L::B_STFULL + slot), (uint32_t)(kitem >> 1) & 1u, limit, abort_flag,
                                          0x480 + L::B_STFULL + slot)))
@@ -883,7 +1050,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 ptx::tc_fence_after_sync();
                 const int q_idx = it.q0 + row;
                 const bool row_ok = q_idx < N;
-                __nv_bfloat16* const orow = p.o + ((int64_t)it.bh * N + q_idx) * ostride;
+                __nv_bfloat16* const orow = CROSS ? p.o + it.b * p.x.o_b + it.h * p.x.o_h + q_idx * p.x.o_n
+                                                  : p.o + ((int64_t)it.bh * N + q_idx) * ostride;
+                const bool parts = CROSS && p.x.splits > 1;
+                // A part's row of the workspace (its place in o else).
+                const int64_t part_row = CROSS ? it.split * p.x.rows + (int64_t)it.bh * N + q_idx : 0;
+                float* const prow = CROSS ? p.x.part + part_row * D : nullptr;
                 const uint32_t o0 = tmem + lane_off + TM_O;
                 float m, l;
                 if constexpr (L::SPLIT) {
@@ -896,7 +1068,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const float lr1 = __uint_as_float(ptx::tmem_ld1_wait(o1 + D));
                     const float inv = 1.0f / (lr0 * w0 + lr1 * w1);
                     const float c0 = w0 * inv, c1 = w1 * inv;
-                        if constexpr (!PAD) {
+                    if (parts) {
+                        if constexpr (CROSS) {
+#pragma unroll
+                            for (int ch = 0; ch < D / 16; ++ch) {
+                                uint32_t oa[16], ob[16];
+                                ptx::tmem_ld16(o0 + ch * 16, oa);
+                                ptx::tmem_ld16(o1 + ch * 16, ob);
+                                ptx::tmem_wait_ld_only();
+                                ptx::reg_fence16(oa);
+                                ptx::reg_fence16(ob);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c)
+                                    oa[c] = __float_as_uint(fmaf(__uint_as_float(oa[c]), c0, __uint_as_float(ob[c]) * c1));
+                                if (row_ok) {
+#pragma unroll
+                                    for (int u = 0; u < 4; ++u)
+                                        ptx::st_global_v4(prow + ch * 16 + u * 4, oa[4 * u], oa[4 * u + 1], oa[4 * u + 2],
+                                                          oa[4 * u + 3]);
+                                }
+                            }
+                            if constexpr (!PAD) {  // (the padded path releases O at its end)
+                                ptx::tc_fence_before_sync();
+                                __syncwarp();
+                                if (lane == 0) ptx::mbar_arrive_relaxed(bar(L::B_OFREE));
+                            }
+                        }
+                    } else if constexpr (!PAD) {
                         uint32_t w[32];  // the row: D = 64 columns
 #pragma unroll
                         for (int ch = 0; ch < D / 16; ++ch) {
@@ -919,7 +1117,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive_relaxed(bar(L::B_OFREE));
                         const int row0 = it.q0 + quarter * 32;
-                        store_rows_coalesced(w, p.o + ((int64_t)it.bh * N + row0) * D, lane, N - row0, D);
+                        if constexpr (CROSS)
+                            store_rows_coalesced(w, p.o + it.b * p.x.o_b + it.h * p.x.o_h + row0 * p.x.o_n, lane, N - row0, p.x.o_n);
+                        else
+                            store_rows_coalesced(w, p.o + ((int64_t)it.bh * N + row0) * D, lane, N - row0, D);
                     } else {
     #pragma unroll
                         for (int ch = 0; ch < D / 16; ++ch) {
@@ -948,7 +1149,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     m = __uint_as_float(st[0]);
                     l = __uint_as_float(st[2]) + __uint_as_float(st[3]);
                     const float inv = 1.0f / __uint_as_float(ptx::tmem_ld1_wait(o0 + D));  // l~
-                        if constexpr (!PAD) {
+                    if (parts) {
+                        if constexpr (CROSS) {
+#pragma unroll
+                            for (int ch = 0; ch < D / 16; ++ch) {
+                                uint32_t o[16];
+                                ptx::tmem_ld16(o0 + ch * 16, o);
+                                ptx::tmem_wait_ld_only();
+                                ptx::reg_fence16(o);
+                                if (row_ok) {
+#pragma unroll
+                                    for (int u = 0; u < 4; ++u)
+                                        ptx::st_global_v4(prow + ch * 16 + u * 4, __float_as_uint(__uint_as_float(o[4 * u]) * inv),
+                                                          __float_as_uint(__uint_as_float(o[4 * u + 1]) * inv),
+                                                          __float_as_uint(__uint_as_float(o[4 * u + 2]) * inv),
+                                                          __float_as_uint(__uint_as_float(o[4 * u + 3]) * inv));
+                                }
+                            }
+                        }
+                    } else if constexpr (!PAD) {
                         const int row0 = it.q0 + quarter * 32;
 #pragma unroll
                         for (int hh = 0; hh < D / 64; ++hh) {
@@ -964,7 +1183,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                     w[8 * ch + c] = ptx::pack_bf16x2(__uint_as_float(o[2 * c]) * inv,
                                                                      __uint_as_float(o[2 * c + 1]) * inv);
                             }
-                            store_rows_coalesced(w, p.o + ((int64_t)it.bh * N + row0) * D + hh * 64, lane, N - row0, D);
+                            if constexpr (CROSS)
+                                store_rows_coalesced(w, p.o + it.b * p.x.o_b + it.h * p.x.o_h + row0 * p.x.o_n + hh * 64, lane,
+                                                     N - row0, p.x.o_n);
+                            else
+                                store_rows_coalesced(w, p.o + ((int64_t)it.bh * N + row0) * D + hh * 64, lane, N - row0, D);
                         }
                     } else {
     #pragma unroll
@@ -996,7 +1219,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_relaxed(bar(L::B_OFREE));
                 }
-                if (row_ok) p.lse[(int64_t)it.bh * N + q_idx] = (m + ptx::lg2(l)) * 0.69314718055994530942f;
+                if (row_ok) {
+                    if (parts)
+                        p.x.part[p.x.splits * p.x.rows * D + part_row] = m + ptx::lg2(l);
+                    else
+                        p.lse[(int64_t)it.bh * N + q_idx] = (m + ptx::lg2(l)) * 0.69314718055994530942f;
+                }
             }
         }
     } else {
@@ -1020,11 +1248,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 int g = 0;      // tiles done
                 int kitem = 0;  // items done
 
-                for (int i = first_item(), step = 0; i < p.num_items; i = next_item(i, step)) {
-                    const Item it = item_of<CAUSAL>(i, p);
+                for (int step, i = first_item(step); i < p.num_items; i = next_item(i, step)) {
+                    const Item it = item_at(i, p);
                     const int q_idx = it.q0 + row;
-                    const int key_max = CAUSAL ? min(q_idx, N - 1) : N - 1;
-                    const int cta_key_max = CAUSAL ? min(it.q0, N - 1) : N - 1;  // smallest key_max of the item
+                    const int key_max = CROSS ? it.len - 1 : CAUSAL ? min(q_idx, N - 1) : N - 1;
+                    const int cta_key_max = CROSS ? key_max : CAUSAL ? min(it.q0, N - 1) : N - 1;  // smallest key_max of the item
+                    const int j0 = CROSS ? it.j0 : 0;  // the item's first key tile
                     float m_ref = -INFINITY;
                     // This half-row's sum of probabilities, as four packed fp32 pairs.
                     uint64_t lsum[4] = {0ull, 0ull, 0ull, 0ull};
@@ -1050,8 +1279,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         ptx::tmem_wait_ld64_max(sr, red);
                         if (lane == 0) FA_TRACE_EV(warp, g, 1);
                         // Causal diagonal tile / keys past N: -inf before the max.
-                        const int k0 = j * BN + half * 64;
-                        if (j * BN + BN - 1 > cta_key_max) {
+                        const int k0 = (j0 + j) * BN + half * 64;
+                        if ((j0 + j) * BN + BN - 1 > cta_key_max) {
     #pragma unroll
                             for (int c = 0; c < 64; ++c)
                                 if (k0 + c > key_max) sr[c] = __float_as_uint(-INFINITY);
@@ -1167,11 +1396,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 // named barrier the same number of times, also after an abort
                 // (ok == false: the work is skipped, the barriers are not), so a named
                 // barrier never waits for a warp that has left the loop.
-                for (int i = first_item(), step = 0; i < p.num_items; i = next_item(i, step)) {
-                    const Item it = item_of<CAUSAL>(i, p);
+                for (int step, i = first_item(step); i < p.num_items; i = next_item(i, step)) {
+                    const Item it = item_at(i, p);
                     const int q_idx = it.q0 + row;
-                    const int key_max = CAUSAL ? min(q_idx, N - 1) : N - 1;
-                    const int cta_key_max = CAUSAL ? min(it.q0, N - 1) : N - 1;  // smallest key_max of the item
+                    const int key_max = CROSS ? it.len - 1 : CAUSAL ? min(q_idx, N - 1) : N - 1;
+                    const int cta_key_max = CROSS ? key_max : CAUSAL ? min(it.q0, N - 1) : N - 1;  // smallest key_max of the item
+                    const int j0 = CROSS ? it.j0 : 0;  // the item's first key tile
                     float m_ref = -INFINITY;
                     // This half-row's sum of probabilities, as four packed fp32 pairs.
                     uint64_t lsum[4] = {0ull, 0ull, 0ull, 0ull};
@@ -1204,8 +1434,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             if (lane == 0) ptx::mbar_arrive(bar(L::B_SREAD + b));
                             if (lane == 0) FA_TRACE_EV(warp, g, 1);
                             // Causal diagonal tile / keys past N: -inf before the max.
-                            const int k0 = j * BN + half * 64;
-                            if (j * BN + BN - 1 > cta_key_max) {
+                            const int k0 = (j0 + j) * BN + half * 64;
+                            if ((j0 + j) * BN + BN - 1 > cta_key_max) {
     #pragma unroll
                                 for (int c = 0; c < 64; ++c)
                                     if (k0 + c > key_max) sr[c] = __float_as_uint(-INFINITY);

@@ -27,11 +27,10 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "fa_fwd_kernel.cuh"  // the status word and its bits
 #include "ptx.cuh"
 
 namespace fa {
-
-constexpr uint32_t STATUS_BAD_PAGE = 4u;  // a page table entry outside the pool: its keys were skipped
 
 namespace qc {
 
