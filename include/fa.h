@@ -465,6 +465,45 @@ fa_status fa_qcache_decode(const void *q, const void *pool, int64_t num_pages, c
                            void *workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * fa_qcache_tree — attention of a tree of drafted tokens over the 4-bit cache, to
+ * verify them all at once.  The newest T keys of every sequence are the drafts
+ * (appended in the order of the tree's nodes; lens counts them): draft i stands at
+ * key lens[b] - T + i, sees every key before lens[b] - T, and draft j where bit j
+ * of its word is set.  In a tree these are its ancestors' bits and its own, but any
+ * set will do, an empty one too (padding: a draft that no word names is seen by
+ * none).  Bits from T on, and drafts of negative position, stand for no key.
+ * Otherwise fa_qcache_decode's operation: query head h reads kv head h / (H / Hkv);
+ * a query that sees no key gives O = 0 and L = -infinity.
+ *   q         device pointer, bf16, contiguous (B, H, T, d), 16-byte aligned;
+ *             1 <= T <= 64, H a multiple of Hkv, B <= 2048.
+ *   words     device pointer, uint64 (B, T).
+ *   o, lse, scale, k_scale, v_scale, workspace  as for fa_qcache_decode (the bytes
+ *             by fa_qcache_tree_workspace_bytes).
+ * Results do not depend on timing.
+ */
+fa_status fa_qcache_tree_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d, int64_t max_pages,
+                                         size_t *bytes);
+fa_status fa_qcache_tree(const void *q, const uint64_t *words, const void *pool, int64_t num_pages, const int32_t *table,
+                         int64_t max_pages, const int32_t *lens, void *o, float *lse, int64_t B, int64_t H, int64_t Hkv,
+                         int64_t T, int64_t d, float scale, float k_scale, float v_scale, void *workspace,
+                         size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_qcache_commit — keeps the accepted path of a verified tree: of the newest T
+ * keys (the drafts), those that `path` names move, as they are held, to the places
+ * behind the context, in order; the others are given up (their places may keep
+ * what they held).
+ *   path      device pointer, int32 (B, width), 1 <= width <= T <= 64: rising drafts,
+ *             0 .. T-1; the first negative entry ends it.  An entry that is no draft of its
+ *             sequence or not above the one before ends it too and is reported by
+ *             fa_check_device_status as FA_ERR_INVALID_ARG.
+ *   lens_out  int32 (B), not lens itself: max(lens - T, 0) + the path's length.
+ */
+fa_status fa_qcache_commit(void *pool, int64_t num_pages, const int32_t *table, int64_t max_pages, const int32_t *lens,
+                           const int32_t *path, int64_t width, int32_t *lens_out, int64_t B, int64_t Hkv, int64_t T,
+                           int64_t d, fa_stream_t stream);
+
+/*
  * fa_qcache_weights — adds up the attention weight each cached key receives,
  * the measure that fa_qcache_evict goes by:
  *     weights_out[b][h][j] = weights[b][h][j] + sum over the query rows of kv

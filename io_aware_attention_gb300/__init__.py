@@ -77,7 +77,8 @@ from . import _build
 __all__ = ["fwd", "fwd_into", "bwd", "bwd_into", "bwd_workspace_bytes", "bias_gelu_dropout", "decode", "decode_into", "decode_workspace_bytes", "cross_fwd", "cross_fwd_into", "cross_fwd_workspace_bytes", "cross_bwd", "cross_bwd_into",
            "cross_bwd_workspace_bytes", "check_device_status", "get_device_status",
            "rope", "rope_into", "rope_bwd", "rope_frequencies", "qcache_pool", "qcache_append", "qcache_read",
-           "qcache_decode", "qcache_decode_into", "qcache_decode_workspace_bytes", "qcache_weights", "qcache_evict",
+           "qcache_decode", "qcache_decode_into", "qcache_decode_workspace_bytes", "qcache_tree", "qcache_tree_into",
+           "qcache_tree_workspace_bytes", "qcache_commit", "tree_words", "qcache_weights", "qcache_evict",
            "set_wait_limit_ns", "debug_skip_k_tile", "debug_set_schedule", "FaError", "library", "library_path", "version", "STATUS"]
 
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_CUDA",
@@ -85,6 +86,7 @@ STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_E
 EXPORTS = ["fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_bias_gelu_dropout", "fa_decode", "fa_decode_workspace_bytes", "fa_decode_static",
            "fa_cross_fwd", "fa_cross_fwd_workspace_bytes", "fa_cross_bwd", "fa_cross_bwd_workspace_bytes",
            "fa_rope", "fa_qcache_append", "fa_qcache_read", "fa_qcache_decode", "fa_qcache_decode_workspace_bytes",
+           "fa_qcache_tree", "fa_qcache_tree_workspace_bytes", "fa_qcache_commit",
            "fa_qcache_weights", "fa_qcache_evict", "fa_check_device_status", "fa_get_device_status",
            "fa_set_wait_limit_ns", "fa_debug_skip_k_tile", "fa_debug_set_schedule", "fa_debug_decode_plan", "fa_status_string",
            "fa_version"]
@@ -151,6 +153,12 @@ def library():
     lib.fa_qcache_decode.restype = ctypes.c_int
     lib.fa_qcache_decode_workspace_bytes.argtypes = [i64] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.fa_qcache_decode_workspace_bytes.restype = ctypes.c_int
+    lib.fa_qcache_tree.argtypes = [vp, vp, vp, i64, vp, i64, vp, vp, vp] + [i64] * 5 + [cf, cf, cf, vp, sz, vp]
+    lib.fa_qcache_tree.restype = ctypes.c_int
+    lib.fa_qcache_tree_workspace_bytes.argtypes = [i64] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.fa_qcache_tree_workspace_bytes.restype = ctypes.c_int
+    lib.fa_qcache_commit.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp] + [i64] * 4 + [vp]
+    lib.fa_qcache_commit.restype = ctypes.c_int
     lib.fa_qcache_weights.argtypes = [vp, vp, vp, i64, vp, i64, vp, vp, vp] + [i64] * 6 + [ci, cf, cf, vp]
     lib.fa_qcache_weights.restype = ctypes.c_int
     lib.fa_qcache_evict.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, vp] + [i64] * 6 + [vp]
@@ -941,6 +949,134 @@ def qcache_decode(q, pool, table, lens, causal: bool = False, scale: float | Non
     o = torch.empty_like(q)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=on)
     return _qcache_decode_call(q, pool, table, lens, o, lse, ws, causal, scale, k_scale, v_scale, None, sizes)
+
+
+def tree_words(parents):
+    """The words of drafted trees for :func:`qcache_tree`, and the drafts' depths:
+    parents is an integer tensor (B, T) or (T,), T <= 64, each entry the index of an
+    earlier draft or negative for a child of the last accepted token.  Returns
+    ``(words int64, depths int64)`` of its shape and device: draft i's own bit and its
+    ancestors', and how many ancestors it has (its token stands at the last accepted
+    one's position + 1 + depth)."""
+    import torch
+
+    if parents.dim() not in (1, 2) or parents.dtype.is_floating_point or not 1 <= parents.shape[-1] <= 64:
+        raise ValueError("parents must be an integer (B, T) or (T,) tensor, T between 1 and 64")
+    T = parents.shape[-1]
+    index = torch.arange(T, device=parents.device)
+    up = torch.where(parents >= 0, parents.long(), index)  # a root is its own
+    if not parents.is_cuda and bool((up > index).any() | (parents == index).any()):
+        raise ValueError("a parent must come before its child")
+    up = torch.minimum(up, index)
+    words = torch.ones_like(up) << index
+    # Every round doubles the ancestors that a word holds.
+    for _ in range((T - 1).bit_length()):
+        words, up = words | words.gather(-1, up), up.gather(-1, up)
+    depths = (words.unsqueeze(-1) >> index & 1).sum(-1) - 1
+    return words, depths
+
+
+def qcache_tree_workspace_bytes(B: int, H: int, Hkv: int, T: int, d: int, max_pages: int) -> int:
+    """Workspace bytes fa_qcache_tree needs for these sizes on the current device."""
+    return _bytes_of("fa_qcache_tree_workspace_bytes", B, H, Hkv, T, d, max_pages)
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(dev, B, H, Hkv, T, d, max_pages):
+    """The workspace size on device dev (the current one), a function of the sizes alone."""
+    return qcache_tree_workspace_bytes(B, H, Hkv, T, d, max_pages)
+
+
+def _check_words(q, words, dev):
+    import torch
+
+    B, _, T, _ = q.shape
+    if words.get_device() != dev or words.dtype is not torch.int64 or not words.is_contiguous() or tuple(words.shape) != (B, T):
+        raise ValueError(f"words must be a contiguous CUDA int64 tensor ({B}, {T}) on cuda:{dev} (see tree_words)")
+
+
+def _qcache_tree_call(q, words, pool, table, lens, o, lse, workspace, scale, k_scale, v_scale, stream, sizes):
+    dev, num_pages, Hkv, max_pages = sizes
+    B, H, T, d = q.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    rc = library().fa_qcache_tree(q.data_ptr(), words.data_ptr(), pool.data_ptr(), num_pages, table.data_ptr(), max_pages,
+                                  lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, T, d, float(scale),
+                                  float(k_scale), float(v_scale), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_qcache_tree")
+    return o, lse
+
+
+def qcache_tree_into(q, words, pool, table, lens, o, lse, workspace, scale: float | None = None, k_scale: float = 1.0,
+                     v_scale: float = 1.0, stream=None):
+    """:func:`qcache_tree` into caller-provided o (bf16, like q), lse (fp32,
+    (B, H, T)) and workspace (a contiguous CUDA tensor of at least
+    qcache_tree_workspace_bytes bytes)."""
+    import torch
+
+    sizes = _check_qcache_query(q, pool, table, lens)
+    dev = sizes[0]
+    _check_words(q, words, dev)
+    _check_out("o", o, q.shape, torch.bfloat16, q.device)
+    _check_out("lse", lse, q.shape[:3], torch.float32, q.device)
+    _check_workspace(workspace, dev)
+    _on_current_device(dev)
+    _stream_on(stream, dev)
+    return _qcache_tree_call(q, words, pool, table, lens, o, lse, workspace, scale, k_scale, v_scale, stream, sizes)
+
+
+def qcache_tree(q, words, pool, table, lens, scale: float | None = None, k_scale: float = 1.0, v_scale: float = 1.0,
+                stream=None):
+    """Attention of a tree of T <= 64 drafted tokens, q (B, H, T, d), over the 4-bit
+    cache whose newest T keys they are (appended; lens counts them).  Draft i sees
+    every key before the drafts, and draft j where bit j of words[b, i] is set
+    (words int64 (B, T), see :func:`tree_words`).  Grouped heads and results as in
+    :func:`qcache_decode`."""
+    import torch
+
+    if stream is not None:  # the workspace and the results belong to the stream that writes them
+        with _under(stream, q):
+            return qcache_tree(q, words, pool, table, lens, scale, k_scale, v_scale)
+    sizes = _check_qcache_query(q, pool, table, lens)
+    dev, _, Hkv, max_pages = sizes
+    _check_words(q, words, dev)
+    if _cuda_device() != dev:
+        with torch.cuda.device(dev):
+            return qcache_tree(q, words, pool, table, lens, scale, k_scale, v_scale)
+    B, H, T, d = q.shape
+    on = q.device
+    ws = torch.empty(_tree_workspace(dev, B, H, Hkv, T, d, max_pages), dtype=torch.uint8, device=on)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, T), dtype=torch.float32, device=on)
+    return _qcache_tree_call(q, words, pool, table, lens, o, lse, ws, scale, k_scale, v_scale, None, sizes)
+
+
+def qcache_commit(pool, table, lens, path, drafts: int, stream=None):
+    """Keeps the accepted path of a verified tree: of the newest ``drafts`` keys of
+    every sequence, those that path (int32 (B, A), rising, -1 after the last) names
+    move to the places behind the context, in order, as they are held.  Returns the
+    new lengths, int32 (B): max(lens - drafts, 0) + accepted ones."""
+    import torch
+
+    if stream is not None:
+        with _under(stream, pool):
+            return qcache_commit(pool, table, lens, path, drafts)
+    dev, B, num_pages, Hkv, max_pages = _check_qcache(pool, table, lens, None)
+    if path.dim() != 2 or path.shape[0] != B:
+        raise ValueError("path must be (B, A)")
+    _check_int32("path", path, None, dev)
+    if _cuda_device() != dev:
+        with torch.cuda.device(dev):
+            return qcache_commit(pool, table, lens, path, drafts)
+    lens_out = torch.empty_like(lens)
+    rc = library().fa_qcache_commit(pool.data_ptr(), num_pages, table.data_ptr(), max_pages, lens.data_ptr(), path.data_ptr(),
+                                    path.shape[1], lens_out.data_ptr(), B, Hkv, int(drafts), pool.shape[2] // 72,
+                                    _stream_handle(None, dev))
+    if rc != 0:
+        raise FaError(rc, "fa_qcache_commit")
+    return lens_out
 
 
 def qcache_weights(q, lse, pool, table, lens, weights, causal: bool = False, scale: float | None = None,

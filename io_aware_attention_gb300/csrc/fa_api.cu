@@ -834,14 +834,23 @@ size_t qcache_decode_ws(int64_t blocks, int64_t Dp, int nt)
     return (size_t)blocks * (2 * qcache_part_bytes(Dp, nt) + 8);
 }
 
-template <int D, int NT, bool FOLD>
+// Rows and pages of a tree call are 32-bit numbers.
+fa_status qcache_tree_sizes(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t max_pages)
+{
+    if (H > INT32_MAX / 64 / B || max_pages > INT32_MAX / fa::qc::PAGE / B ||
+        B * Hkv * qcache_rows(H / Hkv, T).rb > INT32_MAX / max_pages)
+        return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+template <int D, int NT, bool FOLD, bool TREE>
 fa_status launch_qcache_decode(const fa::qc::DecParams& p, int64_t blocks, int dev, cudaStream_t st)
 {
     using Y = fa::qc::DecLayout<D, NT>;
     static std::atomic<int> done[MAX_DEVICES];
-    const fa_status as = allow_smem(fa::qc::fa_qcache_decode_kernel<D, NT, FOLD>, (size_t)Y::bytes(fa::qc::MAX_B), done, dev);
+    const fa_status as = allow_smem(fa::qc::fa_qcache_decode_kernel<D, NT, FOLD, TREE>, (size_t)Y::bytes(fa::qc::MAX_B), done, dev);
     if (as != FA_OK) return as;
-    if (launch_pdl(fa::qc::fa_qcache_decode_kernel<D, NT, FOLD>, dim3((unsigned)blocks), dim3(Y::THREADS),
+    if (launch_pdl(fa::qc::fa_qcache_decode_kernel<D, NT, FOLD, TREE>, dim3((unsigned)blocks), dim3(Y::THREADS),
                    (size_t)Y::bytes(p.B), st, p) != cudaSuccess ||
         launch_pdl(fa::qc::fa_qcache_combine_kernel<D, NT>,
                    dim3((unsigned)blocks, (unsigned)std::min(p.rows, 8 * NT)), dim3(256), 0, st, p) != cudaSuccess)
@@ -1722,12 +1731,130 @@ fa_status fa_qcache_decode(const void* q, const void* pool, int64_t num_pages, c
     p.v_scale = v_scale;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (Dp == 128)
-        return r.rows <= 4 ? launch_qcache_decode<128, 1, true>(p, blocks, dev, st)
-               : r.nt == 1 ? launch_qcache_decode<128, 1, false>(p, blocks, dev, st)
-                           : launch_qcache_decode<128, 2, false>(p, blocks, dev, st);
-    return r.rows <= 4 ? launch_qcache_decode<64, 1, true>(p, blocks, dev, st)
-           : r.nt == 1 ? launch_qcache_decode<64, 1, false>(p, blocks, dev, st)
-                       : launch_qcache_decode<64, 2, false>(p, blocks, dev, st);
+        return r.rows <= 4 ? launch_qcache_decode<128, 1, true, false>(p, blocks, dev, st)
+               : r.nt == 1 ? launch_qcache_decode<128, 1, false, false>(p, blocks, dev, st)
+                           : launch_qcache_decode<128, 2, false, false>(p, blocks, dev, st);
+    return r.rows <= 4 ? launch_qcache_decode<64, 1, true, false>(p, blocks, dev, st)
+           : r.nt == 1 ? launch_qcache_decode<64, 1, false, false>(p, blocks, dev, st)
+                       : launch_qcache_decode<64, 2, false, false>(p, blocks, dev, st);
+}
+
+fa_status fa_qcache_tree_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d, int64_t max_pages,
+                                         size_t* bytes)
+{
+    if (!bytes || B < 1 || H < 1 || Hkv < 1 || T < 1 || d < 1 || max_pages < 1 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
+    if (!head_size_ok(d) || T > fa::qc::MAX_DRAFTS || B > fa::qc::MAX_B) return FA_ERR_UNSUPPORTED;
+    const fa_status ts = qcache_tree_sizes(B, H, Hkv, T, max_pages);
+    if (ts != FA_OK) return ts;
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    const QRows r = qcache_rows(H / Hkv, T);
+    *bytes = qcache_decode_ws(qcache_decode_blocks(info.sms, B, Hkv, r.rb, max_pages), padded_head_size(d), r.nt);
+    return FA_OK;
+}
+
+fa_status fa_qcache_tree(const void* q, const uint64_t* words, const void* pool, int64_t num_pages, const int32_t* table,
+                         int64_t max_pages, const int32_t* lens, void* o, float* lse, int64_t B, int64_t H, int64_t Hkv,
+                         int64_t T, int64_t d, float scale, float k_scale, float v_scale, void* workspace,
+                         size_t workspace_bytes, fa_stream_t stream)
+{
+    if (!q || !words || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
+    const fa_status cs = qcache_check(pool, num_pages, table, max_pages, lens, B, Hkv, d);
+    if (cs != FA_OK) return cs;
+    if (H < 1 || H % Hkv != 0 || T < 1 || !scale_ok(scale) || !tensor_scale_ok(k_scale) || !tensor_scale_ok(v_scale))
+        return FA_ERR_INVALID_ARG;
+    if (T > fa::qc::MAX_DRAFTS || B > fa::qc::MAX_B) return FA_ERR_UNSUPPORTED;
+    const fa_status ts = qcache_tree_sizes(B, H, Hkv, T, max_pages);
+    if (ts != FA_OK) return ts;
+    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(workspace)) & 15u) != 0 ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || (reinterpret_cast<uintptr_t>(words) & 7u) != 0)
+        return FA_ERR_UNSUPPORTED;
+    const size_t qb = (size_t)(B * H * T * d) * 2, lb = (size_t)(B * H * T) * 4, wb = (size_t)(B * T) * 8;
+    auto taken = [&](const void* p, size_t n) {
+        return overlaps(p, n, q, qb) || overlaps(p, n, words, wb) ||
+               hits_cache(p, n, pool, num_pages, Hkv, d, table, max_pages, lens, B);
+    };
+    if (taken(o, qb) || taken(lse, lb) || overlaps(o, qb, lse, lb)) return FA_ERR_INVALID_ARG;
+
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    const QRows r = qcache_rows(H / Hkv, T);
+    const int64_t Dp = padded_head_size(d);
+    const int64_t blocks = qcache_decode_blocks(info.sms, B, Hkv, r.rb, max_pages);
+    const size_t need = qcache_decode_ws(blocks, Dp, r.nt);
+    if (workspace_bytes < need || taken(workspace, need) || overlaps(workspace, need, o, qb) || overlaps(workspace, need, lse, lb))
+        return FA_ERR_INVALID_ARG;
+    fa::qc::DecParams p = {};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.words = words;
+    p.pool = static_cast<const uint8_t*>(pool);
+    p.table = table;
+    p.lens = lens;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.ws = static_cast<float*>(workspace);
+    p.desc = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + (size_t)blocks * 2 * qcache_part_bytes(Dp, r.nt));
+    p.B = (int)B;
+    p.hkv = (int)Hkv;
+    p.nq = (int)T;
+    p.rows = (int)r.rows;
+    p.rb = (int)r.rb;
+    p.d = (int)d;
+    p.max_pages = (int)max_pages;
+    p.num_pages = (int)num_pages;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634074 * (double)k_scale);
+    p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    p.debug_skip = g_debug_skip_k.load(std::memory_order_relaxed);
+    p.v_scale = v_scale;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (Dp == 128)
+        return r.rows <= 4 ? launch_qcache_decode<128, 1, true, true>(p, blocks, dev, st)
+               : r.nt == 1 ? launch_qcache_decode<128, 1, false, true>(p, blocks, dev, st)
+                           : launch_qcache_decode<128, 2, false, true>(p, blocks, dev, st);
+    return r.rows <= 4 ? launch_qcache_decode<64, 1, true, true>(p, blocks, dev, st)
+           : r.nt == 1 ? launch_qcache_decode<64, 1, false, true>(p, blocks, dev, st)
+                       : launch_qcache_decode<64, 2, false, true>(p, blocks, dev, st);
+}
+
+fa_status fa_qcache_commit(void* pool, int64_t num_pages, const int32_t* table, int64_t max_pages, const int32_t* lens,
+                           const int32_t* path, int64_t width, int32_t* lens_out, int64_t B, int64_t Hkv, int64_t T, int64_t d,
+                           fa_stream_t stream)
+{
+    if (!path || !lens_out) return FA_ERR_INVALID_ARG;
+    const fa_status cs = qcache_check(pool, num_pages, table, max_pages, lens, B, Hkv, d);
+    if (cs != FA_OK) return cs;
+    if (T < 1 || width < 1 || width > T) return FA_ERR_INVALID_ARG;
+    if (T > fa::qc::MAX_DRAFTS) return FA_ERR_UNSUPPORTED;
+    if (((reinterpret_cast<uintptr_t>(path) | reinterpret_cast<uintptr_t>(lens_out)) & 3u) != 0) return FA_ERR_UNSUPPORTED;
+    const size_t pb = (size_t)(num_pages * Hkv) * qcache_block_bytes(d), nb = (size_t)(B * width) * 4, lb = (size_t)B * 4;
+    if (hits_cache(lens_out, lb, pool, num_pages, Hkv, d, table, max_pages, lens, B) || overlaps(lens_out, lb, path, nb) ||
+        overlaps(pool, pb, path, nb) || overlaps(pool, pb, table, (size_t)(B * max_pages) * 4) || overlaps(pool, pb, lens, lb))
+        return FA_ERR_INVALID_ARG;
+
+    int dev = -1;
+    DevInfo info;
+    const fa_status ds = sm103_device(&dev, &info);
+    if (ds != FA_OK) return ds;
+    fa::qc::CommitParams p = {};
+    p.pool = static_cast<uint8_t*>(pool);
+    p.table = table;
+    p.lens = lens;
+    p.path = path;
+    p.lens_out = lens_out;
+    p.hkv = (int)Hkv;
+    p.max_pages = (int)max_pages;
+    p.num_pages = (int)num_pages;
+    p.drafts = (int)T;
+    p.width = (int)width;
+    auto* const kernel = padded_head_size(d) == 128 ? fa::qc::fa_qcache_commit_kernel<128> : fa::qc::fa_qcache_commit_kernel<64>;
+    return launch_pdl(kernel, dim3((unsigned)Hkv, (unsigned)B), dim3(fa::qc::ROW_THREADS), 0, reinterpret_cast<cudaStream_t>(stream),
+                      p) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
 }
 
 fa_status fa_qcache_weights(const void* q, const float* lse, const void* pool, int64_t num_pages, const int32_t* table,

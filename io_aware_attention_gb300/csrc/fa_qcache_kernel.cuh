@@ -37,6 +37,7 @@ namespace qc {
 constexpr int PAGE = 64;
 constexpr int MAX_B = 2048;   // sequences of a call (their page counts' prefix sums sit in shared memory)
 constexpr int MAX_NQ = 8;
+constexpr int MAX_DRAFTS = 64;  // a draft's ancestors are one word
 constexpr float LN2 = 0.69314718055994530942f;
 
 template <int D>
@@ -249,6 +250,9 @@ struct Raw16 {
         return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
     }
 };
+
+// A sequence's length, at most what its page table holds.
+__device__ __forceinline__ int clamp_length(int len, int max_pages) { return (int)min((int64_t)max(len, 0), (int64_t)max_pages * PAGE); }
 
 // The page of position x of sequence b, or -1 (and the status bit).
 __device__ __forceinline__ int page_of(const int32_t* table, int max_pages, int num_pages, int b, int slot)
@@ -463,6 +467,131 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_qcache_read_kernel(const RowPa
     }
 }
 
+// ------------------------------------------------------------------- commit
+
+struct CommitParams {
+    uint8_t* pool;
+    const int32_t *table, *lens, *path;  // path: (B, width)
+    int32_t* lens_out;
+    int hkv, max_pages, num_pages, drafts, width;
+};
+
+// Keeps the accepted drafts of one (kv head, sequence): draft path[i] moves to the
+// i-th place after the context.  Paths rise, so that a place's new key lies at it or
+// behind it; every load is done before the first store, which is all that moving in
+// place needs.  A thread takes a channel block of some rows of K, and of some pairs
+// of V rows (they share bytes: where only one of a pair is written, the other nibble
+// is kept).
+//
+// Bound by its launch: its loads, stores and one chain through the lengths, the page table and
+// the rows.
+template <int D>
+__global__ void __launch_bounds__(ROW_THREADS) fa_qcache_commit_kernel(const CommitParams p)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    using L = Block<D>;
+    __shared__ int src[MAX_DRAFTS];  // the moved rows' former positions
+    __shared__ int first_end[2];
+    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
+    const int raw = max(p.lens[b], 0), len = clamp_length(raw, p.max_pages);
+    const int draft0 = raw - p.drafts, base = max(draft0, 0);
+    // The path ends at its first entry that is none: negative, or (reported) no draft
+    // of this sequence or not behind the one before it.
+    int entry = -1;
+    bool ends = true;
+    if (tid < MAX_DRAFTS) {
+        const int32_t* const path = p.path + (int64_t)b * p.width;
+        if (tid < p.width) {
+            entry = path[tid];
+            ends = entry < 0 || entry >= p.drafts || draft0 + entry < 0 || (tid > 0 && entry <= path[tid - 1]);
+        }
+        src[tid] = draft0 + entry;
+        const uint32_t stop = __ballot_sync(0xffffffffu, ends);
+        if ((tid & 31) == 0) first_end[tid >> 5] = stop ? __ffs(stop) - 1 : 32;
+    }
+    __syncthreads();
+    const int count = first_end[0] < 32 ? first_end[0] : 32 + first_end[1];
+    if (h == 0 && ((tid == count && entry >= 0) || (tid == 0 && raw > len))) atomicOr(&g_status, STATUS_BAD_PAGE);
+    if (h == 0 && tid == 0) p.lens_out[b] = base + count;
+
+    auto block_at = [&](int x) -> uint8_t* {  // the block that holds position x, or null
+        const int id = x < len ? page_of(p.table, p.max_pages, p.num_pages, b, x / PAGE) : -1;
+        return id < 0 ? nullptr : p.pool + ((int64_t)id * p.hkv + h) * L::BYTES;
+    };
+    constexpr int STEP = ROW_THREADS / L::NB, KPER = (MAX_DRAFTS + STEP - 1) / STEP;
+    constexpr int PAIRS = MAX_DRAFTS / 2 + 1, VPER = (PAIRS + STEP - 1) / STEP;
+    const int c = tid % L::NB, r0 = tid / L::NB;
+    uint2 kc[KPER];
+    uint8_t ks[KPER];
+    uint8_t* kdst[KPER];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < KPER; ++i) {
+        const int r = r0 + i * STEP;
+        kdst[i] = nullptr;
+        if (r >= count || src[r] == base + r) continue;
+        const uint8_t* const from = block_at(src[r]);
+        uint8_t* const to = block_at(base + r);
+        bad |= !from || !to;
+        if (!from || !to) continue;
+        kc[i] = *reinterpret_cast<const uint2*>(from + L::kcode(src[r] % PAGE) + c * 8);
+        ks[i] = from[L::kscale(src[r] % PAGE, c)];
+        kdst[i] = to;
+    }
+    uint32_t vc[VPER][4];
+    uint8_t vs[VPER][2];
+    uint8_t* vdst[VPER];
+    int vrows[VPER];  // bit 0: the even row is written, bit 1: the odd one
+#pragma unroll
+    for (int i = 0; i < VPER; ++i) {
+        const int even = (base / 2 + r0 + i * STEP) * 2, r = even - base;  // row r lies at the even place
+        vrows[i] = 0;
+        vdst[i] = nullptr;
+        if (r >= count) continue;
+        vdst[i] = block_at(even);
+        bad |= !vdst[i];
+        if (!vdst[i]) continue;
+        const uint4 old = *reinterpret_cast<const uint4*>(vdst[i] + L::vcode(even % PAGE) + c * 16);
+        vc[i][0] = old.x, vc[i][1] = old.y, vc[i][2] = old.z, vc[i][3] = old.w;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row = r + half;
+            if (row < 0 || row >= count || src[row] == base + row) continue;
+            const uint8_t* const from = block_at(src[row]);
+            bad |= !from;
+            if (!from) continue;
+            const uint4 w = *reinterpret_cast<const uint4*>(from + L::vcode(src[row] % PAGE) + c * 16);
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            const int nibble = src[row] % 2 * 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t n = in[e] >> nibble & 0x0F0F0F0Fu;
+                vc[i][e] = half ? (vc[i][e] & 0x0F0F0F0Fu) | n << 4 : (vc[i][e] & 0xF0F0F0F0u) | n;
+            }
+            vs[i][half] = from[L::vscale(src[row] % PAGE, c)];
+            vrows[i] |= 1 << half;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < KPER; ++i) {
+        if (!kdst[i]) continue;
+        const int x = (base + r0 + i * STEP) % PAGE;
+        *reinterpret_cast<uint2*>(kdst[i] + L::kcode(x) + c * 8) = kc[i];
+        kdst[i][L::kscale(x, c)] = ks[i];
+    }
+#pragma unroll
+    for (int i = 0; i < VPER; ++i) {
+        if (!vrows[i]) continue;
+        const int x = (base / 2 + r0 + i * STEP) * 2 % PAGE;
+        *reinterpret_cast<uint4*>(vdst[i] + L::vcode(x) + c * 16) = make_uint4(vc[i][0], vc[i][1], vc[i][2], vc[i][3]);
+        if (vrows[i] & 1) vdst[i][L::vscale(x, c)] = vs[i][0];
+        if (vrows[i] & 2) vdst[i][L::vscale(x + 1, c)] = vs[i][1];
+    }
+    if (bad) atomicOr(&g_status, STATUS_BAD_PAGE);
+}
+
 // ---------------------------------------------------------- the work's division
 
 // The calls over whole caches (decode, weights) divide a list of units: all
@@ -498,8 +627,6 @@ struct Work {
     }
 };
 
-// A sequence's length, at most what its page table holds.
-__device__ __forceinline__ int clamp_length(int len, int max_pages) { return (int)min((int64_t)max(len, 0), (int64_t)max_pages * PAGE); }
 __device__ __forceinline__ int length_of(const int32_t* lens, int b, int max_pages) { return clamp_length(lens[b], max_pages); }
 
 // prefix[0 .. B] by a block of NTHREADS threads (scratch: one int per warp).
@@ -572,6 +699,7 @@ struct DecParams {
     float v_scale;
     uint64_t wait_limit_ns;
     int debug_skip;               // test hook: block 0's first warp never copies this one of its pages (-1: off)
+    const uint64_t* words;        // tree: (B, nq), bit j of word i: draft i sees draft j
     const float* lse_in;          // weights: (B, H, nq)
     const float* w_in;            // (B, hkv, w_len)
     float* w_out;
@@ -623,7 +751,9 @@ __device__ __forceinline__ uint32_t hmul2_by(uint32_t a, uint32_t f)
 // entry lies in [2^14, 2^15): bf16 entries down to 2^-31 of it are exact in
 // fp16 whatever the row's size.  FOLD: at most 4 rows, and the tile's rows 4 to 7 are
 // rows 0 to 3 again (decode uses them for the second halves of probabilities).
-template <int D, int NT, bool FOLD = false>
+// TREE: the newest nq keys are drafts; a row sees all keys before them (lim), and of
+// them those that its word tells.
+template <int D, int NT, bool FOLD = false, bool TREE = false>
 struct Rows {
     static_assert(!FOLD || NT == 1, "one tile, folded");
     // The query row of a tile's row.
@@ -632,6 +762,27 @@ struct Rows {
     float sc[NT][2];
     int lim[NT][2];
     int len, min_lim;
+    int drafts;             // TREE: place of draft 0 (below 0 where the sequence is shorter)
+    const uint64_t* words;  // TREE: of the rows' sequence
+    int row0, nq;           // TREE: the row block's first row
+
+    // Whether column j of tile nt sees key x.
+    __device__ __forceinline__ bool sees(int nt, int j, int x) const
+    {
+        if constexpr (!TREE) return x < lim[nt][j];
+        if (x < lim[nt][j]) return true;
+        const int bit = x - drafts;
+        return x < len && bit < nq && (word[nt][j] >> (bit & 63) & 1u);
+    }
+    uint64_t word[NT][2];   // TREE: valid after load_words
+    __device__ __forceinline__ void load_words()
+    {
+        const int t = threadIdx.x & 3;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) word[nt][j] = __ldg(words + (row0 + nt * 8 + row_of(2 * t + j)) % nq);
+    }
 
     // The rows' raw entries: issued before a warp's first copies, so that they
     // do not wait behind them.
@@ -657,7 +808,7 @@ struct Rows {
         }
     }
 
-    __device__ __forceinline__ void load(const Raw& raw, const DecParams& p, int hr)
+    __device__ __forceinline__ void load(const Raw& raw, const DecParams& p, [[maybe_unused]] int b, int hr)
     {
         const int lane = threadIdx.x & 31, t = lane & 3;
         const int r0 = p.rb == 1 ? 0 : hr % p.rb * (8 * NT);
@@ -665,6 +816,13 @@ struct Rows {
         // A causal query stands at its place in the sequence, which a length beyond the page table does not move.
         const int end = max(raw.len, 0) - p.nq + 1;
         min_lim = p.causal ? min(len, end) : len;
+        if constexpr (TREE) {
+            drafts = max(raw.len, 0) - p.nq;
+            min_lim = min(len, drafts);
+            words = p.words + (int64_t)b * p.nq;
+            row0 = r0;
+            nq = p.nq;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float f[D / 4];
@@ -688,7 +846,7 @@ struct Rows {
             for (int j = 0; j < 2; ++j) {
                 sc[nt][j] = __shfl_sync(0xffffffffu, down, (2 * t + j) * 4);
                 const int r = r0 + nt * 8 + row_of(2 * t + j);
-                lim[nt][j] = p.causal && r < p.rows ? min(len, end + (p.nq == 1 ? 0 : r % p.nq)) : len;
+                lim[nt][j] = TREE ? min_lim : p.causal && r < p.rows ? min(len, end + (p.nq == 1 ? 0 : r % p.nq)) : len;
             }
         }
     }
@@ -698,8 +856,8 @@ struct Rows {
 // product, so that few rows waste no tensor work.  Lane (g, t) of s[r][nt]
 // holds keys 16r + g (entries 0, 1) and 16r + 8 + g (2, 3) against rows 2t and
 // 2t + 1.  blk: a page's block in shared or global memory.
-template <int D, int NT, int TOGETHER, bool FOLD>
-__device__ __forceinline__ void page_scores(const uint8_t* blk, const Rows<D, NT, FOLD>& rows, float (&s)[4][NT][4])
+template <int D, int NT, int TOGETHER, bool FOLD, bool TREE>
+__device__ __forceinline__ void page_scores(const uint8_t* blk, const Rows<D, NT, FOLD, TREE>& rows, float (&s)[4][NT][4])
 {
     using L = Block<D>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -753,9 +911,9 @@ __device__ __forceinline__ void page_scores(const uint8_t* blk, const Rows<D, NT
 // More rows take two: 8 x 8 heads x 32768 keys, 8 rows 67.4 us (62.2 with one fp16
 // number a probability), 16 rows 111.8 (92.6); 48 x 4 heads x 0 to 5000 keys, 16 rows,
 // d = 64, 28.7 (27.2).)
-template <int D, int NT, bool FOLD>
+template <int D, int NT, bool FOLD, bool TREE = false>
 struct State {
-    using R = Rows<D, NT, FOLD>;
+    using R = Rows<D, NT, FOLD, TREE>;
     float o[D / 16][NT][4];
     // Largest unscaled score (differences to it are scaled, so that the
     // largest key's weight is 1 however large the scores are); this lane's
@@ -783,12 +941,13 @@ struct State {
     };
 
     // Takes a page's scores in: the running maxima and sums, and the probabilities.
-    __device__ __forceinline__ void add_scores(float (&s)[4][NT][4], const R& rows, int page, Probs& pb)
+    __device__ __forceinline__ void add_scores(float (&s)[4][NT][4], R& rows, int page, Probs& pb)
     {
         const int lane = threadIdx.x & 31, g = lane >> 2;
         const bool second = FOLD && (lane & 2);  // its columns carry the rests
         const int key0 = page * PAGE;
         const bool whole = key0 + PAGE <= rows.min_lim;  // every row sees every key
+        if (TREE && !whole) rows.load_words();
         bool rises = false;
         float mm[NT][2];
 #pragma unroll
@@ -798,8 +957,8 @@ struct State {
                 if (!whole) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        if (key0 + 16 * r + g >= rows.lim[nt][j]) s[r][nt][j] = -INFINITY;
-                        if (key0 + 16 * r + 8 + g >= rows.lim[nt][j]) s[r][nt][2 + j] = -INFINITY;
+                        if (!rows.sees(nt, j, key0 + 16 * r + g)) s[r][nt][j] = -INFINITY;
+                        if (!rows.sees(nt, j, key0 + 16 * r + 8 + g)) s[r][nt][2 + j] = -INFINITY;
                     }
                 }
                 float x = fmaxf(s[0][nt][j], s[0][nt][2 + j]);
@@ -1141,7 +1300,7 @@ struct Feed {
 // about 400; the conversions (280 a page, 2 a clock) need 140 of them, the fp16
 // multiplies 128 and the products 128, on pipes of their own.  The rest is the
 // start (lengths, page table, query rows: 7 us) and the join.
-template <int D, int NT, bool FOLD>
+template <int D, int NT, bool FOLD, bool TREE>
 __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode_kernel(const DecParams p)
 {
     using Y = DecLayout<D, NT>;
@@ -1201,8 +1360,8 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
     int slot = 0;
     if (warp < nw) {
         const int x0 = lo + (int)((int64_t)(hi - lo) * warp / nw), x1 = lo + (int)((int64_t)(hi - lo) * (warp + 1) / nw);
-        Rows<D, NT, FOLD> rows;
-        State<D, NT, FOLD> st;
+        Rows<D, NT, FOLD, TREE> rows;
+        State<D, NT, FOLD, TREE> st;
         int seg = -1, begins = 0, page = 0;
         auto finish = [&] {
             st.close(rows);
@@ -1253,7 +1412,7 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
         // of the pages in turn, each slot refilled as soon as the warp has read it.
         Feed<D, Y::SLOTS, true, Y::WHOLE> feed(smem + Y::ring(warp), ptx::smem_addr(&bars[warp * Y::SLOTS]), p, work);
         feed.start(x0, x1);
-        typename Rows<D, NT, FOLD>::Raw raw;
+        typename Rows<D, NT, FOLD, TREE>::Raw raw;
         for (int x = x0; x < x1; ++x) {
             const int next_seg = feed.place(x);
             ++page;
@@ -1269,12 +1428,12 @@ __global__ void __launch_bounds__(DecLayout<D, NT>::THREADS, 1) fa_qcache_decode
                 page = seg < 0 ? feed.first_page : 0;
                 seg = next_seg;
                 begins = page == 0;
-                rows.load(raw, p, hr);
+                rows.load(raw, p, b, hr);
                 st.clear();
             }
             const bool there = feed.there(x);
             float s[4][NT][4];
-            typename State<D, NT, FOLD>::Probs pb;
+            typename State<D, NT, FOLD, TREE>::Probs pb;
             const uint8_t* blk = feed.wait(abort_flag);
             if (!blk) break;
             page_scores<D, NT, 1>(blk, rows, s);
@@ -1550,7 +1709,7 @@ __global__ void __launch_bounds__(WeightLayout<D>::THREADS, 2) fa_qcache_weights
                             // A row that saw nothing (or is none) gives nothing: 2^-inf.
                             e[nt][j] = r < p.rows ? lse[r] : -INFINITY;
                         }
-                    rows.load(raw, p, hr);
+                    rows.load(raw, p, b, hr);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
