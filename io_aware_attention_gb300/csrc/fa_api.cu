@@ -18,6 +18,7 @@
 #include "fa_fwd_kernel.cuh"
 #include "fa_qcache_kernel.cuh"
 #include "fa_rope_kernel.cuh"
+#include "fa_tree_kernel.cuh"
 
 namespace {
 
@@ -832,6 +833,52 @@ int64_t qcache_decode_blocks(int sms, int64_t B, int64_t Hkv, int64_t rb, int64_
 size_t qcache_decode_ws(int64_t blocks, int64_t Dp, int nt)
 {
     return (size_t)blocks * (2 * qcache_part_bytes(Dp, nt) + 8);
+}
+
+// Query rows of a kv head in the kernel of many rows: blocks of n.
+struct TreeRows {
+    int64_t rb;
+    int n;
+};
+TreeRows tree_rows(int64_t rows)
+{
+    const int n = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    return {(rows + n - 1) / n, n};
+}
+int64_t tree_blocks(int sms, int64_t B, int64_t Hkv, int64_t rb, int64_t max_pages)
+{
+    return std::min<int64_t>(sms, B * Hkv * rb * ((max_pages + 1) / 2));
+}
+// 8 rows and fewer run in the kernel of few rows.
+bool tree_many(int64_t rows) { return rows > 8; }
+size_t tree_part_bytes(int64_t Dp, int n) { return (size_t)n * (size_t)(Dp + 2) * 4; }
+size_t tree_ws(int64_t blocks, int64_t Dp, int n) { return (size_t)blocks * (2 * tree_part_bytes(Dp, n) + 8); }
+
+template <int D, int N>
+fa_status launch_tree(const CUtensorMap& mq, const fa::qc::DecParams& p, int64_t blocks, int dev, cudaStream_t st)
+{
+    using Y = fa::tree::Layout<D, N>;
+    static std::atomic<int> done[MAX_DEVICES];
+    const fa_status as = allow_smem(fa::tree::fa_tree_kernel<D, N>, (size_t)Y::bytes(fa::qc::MAX_B), done, dev);
+    if (as != FA_OK) return as;
+    if (launch_pdl(fa::tree::fa_tree_kernel<D, N>, dim3((unsigned)blocks), dim3(fa::tree::THREADS), (size_t)Y::bytes(p.B), st, mq, p) !=
+            cudaSuccess ||
+        launch_pdl(fa::tree::fa_tree_combine_kernel<D, N>,
+                   dim3((unsigned)blocks, (unsigned)((std::min(p.rows, N) + fa::tree::JOIN_ROWS - 1) / fa::tree::JOIN_ROWS)),
+                   dim3(32 * fa::tree::JOIN_ROWS), 0, st, p) != cudaSuccess)
+        return FA_ERR_CUDA;
+    return FA_OK;
+}
+
+template <int D>
+fa_status launch_tree_n(int n, const fa::qc::DecParams& p, int64_t blocks, int dev, cudaStream_t st)
+{
+    CUtensorMap mq;
+    if (!cached_map(&mq, p.q, (int64_t)p.B * p.hkv, p.rows, p.d, (uint32_t)n)) return FA_ERR_CUDA;
+    return n == 16   ? launch_tree<D, 16>(mq, p, blocks, dev, st)
+           : n == 32 ? launch_tree<D, 32>(mq, p, blocks, dev, st)
+           : n == 64 ? launch_tree<D, 64>(mq, p, blocks, dev, st)
+                     : launch_tree<D, 128>(mq, p, blocks, dev, st);
 }
 
 // Rows and pages of a tree call are 32-bit numbers.
@@ -1750,8 +1797,14 @@ fa_status fa_qcache_tree_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int6
     DevInfo info;
     const fa_status ds = sm103_device(&dev, &info);
     if (ds != FA_OK) return ds;
-    const QRows r = qcache_rows(H / Hkv, T);
-    *bytes = qcache_decode_ws(qcache_decode_blocks(info.sms, B, Hkv, r.rb, max_pages), padded_head_size(d), r.nt);
+    const int64_t rows = H / Hkv * T, Dp = padded_head_size(d);
+    if (tree_many(rows)) {
+        const TreeRows r = tree_rows(rows);
+        *bytes = tree_ws(tree_blocks(info.sms, B, Hkv, r.rb, max_pages), Dp, r.n);
+    } else {
+        const QRows r = qcache_rows(H / Hkv, T);
+        *bytes = qcache_decode_ws(qcache_decode_blocks(info.sms, B, Hkv, r.rb, max_pages), Dp, r.nt);
+    }
     return FA_OK;
 }
 
@@ -1782,10 +1835,13 @@ fa_status fa_qcache_tree(const void* q, const uint64_t* words, const void* pool,
     DevInfo info;
     const fa_status ds = sm103_device(&dev, &info);
     if (ds != FA_OK) return ds;
+    const int64_t rows = H / Hkv * T, Dp = padded_head_size(d);
+    const bool many = tree_many(rows);
     const QRows r = qcache_rows(H / Hkv, T);
-    const int64_t Dp = padded_head_size(d);
-    const int64_t blocks = qcache_decode_blocks(info.sms, B, Hkv, r.rb, max_pages);
-    const size_t need = qcache_decode_ws(blocks, Dp, r.nt);
+    const TreeRows tr = tree_rows(rows);
+    const int64_t blocks = many ? tree_blocks(info.sms, B, Hkv, tr.rb, max_pages) : qcache_decode_blocks(info.sms, B, Hkv, r.rb, max_pages);
+    const size_t part = many ? tree_part_bytes(Dp, tr.n) : qcache_part_bytes(Dp, r.nt);
+    const size_t need = (size_t)blocks * (2 * part + 8);
     if (workspace_bytes < need || taken(workspace, need) || overlaps(workspace, need, o, qb) || overlaps(workspace, need, lse, lb))
         return FA_ERR_INVALID_ARG;
     fa::qc::DecParams p = {};
@@ -1797,12 +1853,12 @@ fa_status fa_qcache_tree(const void* q, const uint64_t* words, const void* pool,
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
     p.ws = static_cast<float*>(workspace);
-    p.desc = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + (size_t)blocks * 2 * qcache_part_bytes(Dp, r.nt));
+    p.desc = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + (size_t)blocks * 2 * part);
     p.B = (int)B;
     p.hkv = (int)Hkv;
     p.nq = (int)T;
-    p.rows = (int)r.rows;
-    p.rb = (int)r.rb;
+    p.rows = (int)rows;
+    p.rb = (int)(many ? tr.rb : r.rb);
     p.d = (int)d;
     p.max_pages = (int)max_pages;
     p.num_pages = (int)num_pages;
@@ -1811,6 +1867,7 @@ fa_status fa_qcache_tree(const void* q, const uint64_t* words, const void* pool,
     p.debug_skip = g_debug_skip_k.load(std::memory_order_relaxed);
     p.v_scale = v_scale;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (many) return Dp == 128 ? launch_tree_n<128>(tr.n, p, blocks, dev, st) : launch_tree_n<64>(tr.n, p, blocks, dev, st);
     if (Dp == 128)
         return r.rows <= 4 ? launch_qcache_decode<128, 1, true, true>(p, blocks, dev, st)
                : r.nt == 1 ? launch_qcache_decode<128, 1, false, true>(p, blocks, dev, st)

@@ -629,15 +629,16 @@ struct Work {
 
 __device__ __forceinline__ int length_of(const int32_t* lens, int b, int max_pages) { return clamp_length(lens[b], max_pages); }
 
-// prefix[0 .. B] by a block of NTHREADS threads (scratch: one int per warp).
-// Up to 32 sequences every warp computes them all and waits for no other.
-template <int NTHREADS>
+// prefix[0 .. B] by a block of NTHREADS threads (scratch: one int per warp), counting
+// units of KEYS keys.  Up to 32 sequences every warp computes them all and waits for no
+// other.
+template <int NTHREADS, int KEYS = PAGE>
 __device__ __forceinline__ void page_prefix(const int32_t* lens, int B, int max_pages, int* prefix, int* scratch)
 {
     constexpr int W = NTHREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto scan = [&](int b) {
-        int v = b < B ? (length_of(lens, b, max_pages) + PAGE - 1) / PAGE : 0;
+        int v = b < B ? (length_of(lens, b, max_pages) + KEYS - 1) / KEYS : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int n = __shfl_up_sync(0xffffffffu, v, o);
@@ -1110,9 +1111,9 @@ struct Piece {
     static __device__ __forceinline__ int l(int row) { return D * (R + 1) + R + row; }
 };
 
-__device__ __forceinline__ float natural_lse(float m, float l)
+__device__ __forceinline__ float natural_lse(float m, float l, float shift = SHIFT)
 {
-    return l > 0.f || !(l == l) ? (m + ptx::lg2(l) - SHIFT) * LN2 : -INFINITY;
+    return l > 0.f || !(l == l) ? (m + ptx::lg2(l) - shift) * LN2 : -INFINITY;
 }
 
 // Shared memory of the decode kernel: a ring of half pages for each warp, one
