@@ -885,7 +885,7 @@ fa_status launch_tree_n(int n, const fa::qc::DecParams& p, int64_t blocks, int d
 fa_status qcache_tree_sizes(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t max_pages)
 {
     if (H > INT32_MAX / 64 / B || max_pages > INT32_MAX / fa::qc::PAGE / B ||
-        B * Hkv * qcache_rows(H / Hkv, T).rb > INT32_MAX / max_pages)
+        B * Hkv * qcache_rows(H / Hkv, T).rb > INT32_MAX / (max_pages + 8))
         return FA_ERR_INVALID_ARG;
     return FA_OK;
 }

@@ -28,7 +28,7 @@
 // rows, with few rows they take tiles in turn, each with references, sums and an O^T of
 // its own, which meet at a segment's end.  (N rows: tiles in flight x rows of a thread.
 // 16: 4 x 16, 32: 4 x 32, 64: 2 x 32, 128: 1 x 32.  Two groups that shared the rows of
-// every tile took 1740 cycles a tile of 16 rows and 4200 of 128, PLACE now.)
+// every tile took 1740 cycles a tile of 16 rows and 4200 of 128.)
 //
 // Warps (1024 threads, one block an SM):
 //   0-15      softmax, four groups: a thread a key; at a segment's end they write its result.
@@ -47,8 +47,8 @@
 // their results are not read.
 //
 // The tiles of all sequences, kv heads and row blocks are one list (see Work), of
-// which every block takes an equal run; segments that cross blocks leave partial results
-// that the combine kernel joins.  A block's pipeline runs on across segments.
+// which every block takes an equal run (see Units); segments that cross
+// blocks leave partial results that the combine kernel joins.  A block's pipeline runs on across segments.
 //
 // The roles' loops share the SM's instruction caches: what does not fit is fetched at
 // some 20 cycles an instruction, and the first form of this kernel, with everything
@@ -95,7 +95,12 @@ struct Layout {
     static constexpr int SHARES = GROUPS / TURNS;                // groups that share a tile's rows
     static constexpr int NC = N / SHARES;                        // rows of a thread
     static constexpr int NO = NC / TURNS;                        // rows whose results a group writes
+    // Where a tile has all groups' rows, the products are made in two streams of half
+    // the rows each, which need not keep step: one's exponentials run beside the other's
+    // loads and waits.
+    static constexpr int STREAMS = TURNS == 1 ? 2 : 1, NM = N / STREAMS;  // rows of a product
     static constexpr int PBUFS = TURNS == 1 ? 2 : TURNS;
+    static constexpr int EXTRA = TURNS == 1 ? 2 : 4;
     static constexpr int RAW_STAGES = N == 128 ? 4 : 6;  // tiles' codes on their way
     static_assert(NOTES >= RAW_STAGES + 2, "notes");
     static constexpr uint32_t TM_O = TM_S + TURNS * N;
@@ -180,6 +185,28 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
+// C columns of this warp's lanes and their largest, as tcgen05.ld.red gives it (valid
+// after load_cols_end).
+template <int C>
+__device__ __forceinline__ void load_cols_max(uint32_t taddr, uint32_t (&r)[C], float& red)
+{
+    static_assert(C == 16 || C == 32, "columns");
+    if constexpr (C == 32)
+        asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                     "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                       "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+                       "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+                       "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(red)
+                     : "r"(taddr));
+    else
+        asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+                     "%16, [%17];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                       "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=f"(red)
+                     : "r"(taddr));
+}
+
 // TMEM <-> registers, C columns of this warp's lanes.
 template <int C>
 __device__ __forceinline__ void load_cols_begin(uint32_t taddr, uint32_t (&r)[C])
@@ -250,6 +277,62 @@ struct Note {
     uint32_t what;  // which pages are there; first and last tile of its segment
     int left;       // keys of the sequence from the tile's first on
 };
+
+// The work's division.  A segment counts `extra` units more than its tiles, for its rows,
+// first maxima and result, which cost about as much; none where blocks have few tiles
+// anyway.  The list: sequence 0's (kv heads x row blocks), each its extra units, then its
+// tiles, and so on.
+struct Units {
+    const int* prefix;  // sums of the sequences' tiles
+    int B, hr, extra;
+    __device__ __forceinline__ int before(int b) const { return prefix[b] + extra * b; }  // a (kv head, row block)'s units
+    __device__ __forceinline__ int total() const { return before(B) * hr; }
+    struct Place {
+        int b, hr, at, tiles;  // at: unit of the segment
+    };
+    __device__ __forceinline__ Place find(int x) const
+    {
+        const int y = x / hr;
+        int lo = 0, hi = B;  // before(lo) <= y < before(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before(mid) <= y) lo = mid;
+            else hi = mid;
+        }
+        Place u;
+        u.b = lo;
+        u.tiles = prefix[lo + 1] - prefix[lo];
+        const int rem = x - before(lo) * hr, units = u.tiles + extra;
+        u.hr = rem / units;
+        u.at = rem - u.hr * units;
+        return u;
+    }
+    // Tiles before unit x.
+    __device__ __forceinline__ int tiles_before(int x) const
+    {
+        if (x >= total()) return prefix[B] * hr;
+        const Place u = find(x);
+        return prefix[u.b] * hr + u.hr * u.tiles + max(0, u.at - extra);
+    }
+};
+// The next segment with tiles of a run x .. end - 1 of units; x moves behind it.
+struct Run {
+    int b, hr, tile0, n, tiles;
+};
+__device__ __forceinline__ bool next_run(const Units& work, int& x, int end, Run& r)
+{
+#pragma unroll 1
+    while (x < end) {
+        const Units::Place u = work.find(x);
+        const int at = uniform(u.at), tiles = uniform(u.tiles), units = min(end - x, tiles + work.extra - at);
+        const int tile0 = max(0, at - work.extra), tile1 = max(0, at + units - work.extra);
+        x += units;
+        if (tile1 == tile0) continue;
+        r.b = uniform(u.b), r.hr = uniform(u.hr), r.tile0 = tile0, r.n = tile1 - tile0, r.tiles = tiles;
+        return true;
+    }
+    return false;
+}
 
 // Query rows in shared memory (K-major, 128-byte swizzle), TOGETHER rows at a time, every
 // step-th such batch: the largest magnitude's bf16 bits, and the rows to fp16 in place.
@@ -379,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
 {
     using L = Layout<D, N>;
     using PB = qc::Block<D>;
-    constexpr int NC = L::NC, TURNS = L::TURNS, SHARES = L::SHARES, NO = L::NO;
+    constexpr int NC = L::NC, TURNS = L::TURNS, SHARES = L::SHARES, NO = L::NO, STREAMS = L::STREAMS;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_addr(smem);
     if (sbase & 1023u) {
@@ -413,8 +496,8 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
         }
         for (int s = 0; s < 4; ++s) {
             ptx::mbar_init(bar(L::B_SFULL + s), 1);
-            ptx::mbar_init(bar(L::B_SREAD + s), 4 * SHARES);
-            ptx::mbar_init(bar(L::B_PFULL + s), 4 * SHARES);
+            ptx::mbar_init(bar(L::B_SREAD + s), 4 * SHARES / STREAMS);
+            ptx::mbar_init(bar(L::B_PFULL + s), 4 * SHARES / STREAMS);
             ptx::mbar_init(bar(L::B_PDONE + s), 1);
         }
         ptx::mbar_init(bar(L::B_OFREE), SOFTMAX_WARPS);
@@ -427,7 +510,8 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     qc::page_prefix<THREADS, TILE>(p.lens, p.B, p.max_pages, prefix, scratch);
-    const qc::Work work{prefix, p.B, p.hkv * p.rb};
+    const int hr_all = p.hkv * p.rb;
+    const Units work{prefix, p.B, hr_all, uniform(prefix[p.B]) * hr_all >= 4 * (int)gridDim.x ? L::EXTRA : 0};
 
     // Sequences of no key: nothing is seen.
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -440,7 +524,9 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
     const int T = uniform(work.total()), G = min((int)gridDim.x, T), cta = blockIdx.x;
     if (threadIdx.x == 0) p.desc[2 * cta] = -1;
     if (cta >= G) return;
-    const int lo = (int)((int64_t)cta * T / G), hi = (int)((int64_t)(cta + 1) * T / G), n_tiles = hi - lo;
+    const int lo = (int)((int64_t)cta * T / G), hi = (int)((int64_t)(cta + 1) * T / G);
+    const int n_tiles = uniform(work.tiles_before(hi) - work.tiles_before(lo));
+    if (n_tiles == 0) return;
 
     if (warp == WARP_S) {
         ptx::tmem_alloc(sbase + L::OFF_MISC, TM_COLS);
@@ -458,10 +544,11 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
             int g = 0;
             bool ok = true;
 #pragma unroll 1
-            for (int x = lo; ok && x < hi;) {
-                const qc::Work::Unit u = work.at(x);
-                const int b = uniform(u.b), h = uniform(u.hr) / p.rb, tile0 = uniform(u.page);
-                const int n = min(hi - x, uniform(u.pages) - tile0), len = uniform(qc::length_of(p.lens, b, p.max_pages));
+            for (int x = lo; ok;) {
+                Run run;
+                if (!next_run(work, x, hi, run)) break;
+                const int b = run.b, h = run.hr / p.rb, tile0 = run.tile0, n = run.n;
+                const int len = uniform(qc::length_of(p.lens, b, p.max_pages));
                 const int pages = (len + PAGE - 1) / PAGE;
                 int id = -1;
 #pragma unroll 1
@@ -502,7 +589,6 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                     }
                     __syncwarp();
                 }
-                x += n;
             }
             // Every copy lands before the block leaves.
 #pragma unroll 1
@@ -511,30 +597,36 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                     drain_bar(bar(L::B_RAWFULL + e % L::RAW_STAGES), (uint32_t)(e / L::RAW_STAGES) & 1u, limit, abort_flag, 0x2180);
         } else if (warp == WARP_S) {
             // ------------------------------------------------------------ S^T
-            constexpr uint32_t ID = idesc_f16(128, N, false);
+            constexpr uint32_t ID = idesc_f16(128, L::NM, false);
             const uint64_t q_desc = ptx::sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
             int k = 0;
             bool ok = true;
 #pragma unroll 1
             for (int g = 0; ok && g < n_tiles; ++g) {
-                const int kb = g & 1, sb = g % TURNS;
+                const int kb = g & 1, turn = g % TURNS;
                 ok = warp_wait(bar(L::B_KFULL + kb), (uint32_t)(g >> 1) & 1u, limit, abort_flag, 0x2200 + L::B_KFULL + kb);
                 const uint32_t what = (uint32_t)uniform((int)notes[g % NOTES].what);
                 const int qb = k & 1;
                 if ((what & Note::FIRST) && ok)
                     ok = warp_wait(bar(L::B_QFULL + qb), (uint32_t)(k >> 1) & 1u, limit, abort_flag, 0x2200 + L::B_QFULL + qb);
-                if (ok) ok = warp_wait(bar(L::B_SREAD + sb), ((uint32_t)(g / TURNS) & 1u) ^ 1u, limit, abort_flag, 0x2200 + L::B_SREAD + sb);
-                if (!ok) break;
-                ptx::tc_fence_after_sync();
+                const uint64_t q_at = q_desc + (uint64_t)(((uint32_t)qb * L::Q_BYTES) >> 4);
+#pragma unroll 1
+                for (int st = 0; st < STREAMS; ++st) {
+                    const int sb = STREAMS > 1 ? st : turn;
+                    if (ok) ok = warp_wait(bar(L::B_SREAD + sb), ((uint32_t)(g / TURNS) & 1u) ^ 1u, limit, abort_flag, 0x2200 + L::B_SREAD + sb);
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+                    const uint64_t q_rows = q_at + (uint64_t)(((uint32_t)st * L::NM * 128) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    if (ptx::elect_one())
-                        ptx::mma_ts(tmem + TM_S + (uint32_t)(sb * N), tmem + TM_K + (uint32_t)(kb * 64 + kk * 8),
-                                    q_desc + (uint64_t)(((uint32_t)qb * L::Q_BYTES + (uint32_t)(kk >> 2) * L::QBLK + (uint32_t)(kk & 3) * 32) >> 4),
-                                    ID, kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        if (ptx::elect_one())
+                            ptx::mma_ts(tmem + TM_S + (uint32_t)(turn * N + st * L::NM), tmem + TM_K + (uint32_t)(kb * 64 + kk * 8),
+                                        q_rows + (uint64_t)(((uint32_t)(kk >> 2) * L::QBLK + (uint32_t)(kk & 3) * 32) >> 4), ID, kk > 0 ? 1u : 0u);
+                    if (ptx::elect_one()) ptx::tc_commit(bar(L::B_SFULL + sb));
+                }
+                if (!ok) break;
                 if (ptx::elect_one()) {
                     ptx::tc_commit(bar(L::B_KEMPTY + kb));
-                    ptx::tc_commit(bar(L::B_SFULL + sb));
                     if (what & Note::LAST) ptx::tc_commit(bar(L::B_QEMPTY + qb));
                 }
                 if (what & Note::LAST) ++k;
@@ -543,7 +635,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
             drain_bar(bar(L::B_DRAIN), 0, limit, abort_flag, 0x2280);
         } else if (warp == WARP_O) {
             // ------------------------------------------------------------ O^T
-            constexpr uint32_t ID = idesc_f16(128, N, true);
+            constexpr uint32_t ID = idesc_f16(128, L::NM, true);
             const uint64_t p_desc = ptx::sdesc_sw128(sbase + L::OFF_P, L::PBLK, 1024);
             int k = 0;
             bool ok = true;
@@ -555,19 +647,23 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 // A segment's first products overwrite O^T: what was there has been read.
                 if ((what & Note::FIRST) && ok)
                     ok = warp_wait(bar(L::B_OFREE), (uint32_t)(k & 1) ^ 1u, limit, abort_flag, 0x2300 + L::B_OFREE);
-                if (ok) ok = warp_wait(bar(L::B_PFULL + pb), (uint32_t)(g / L::PBUFS) & 1u, limit, abort_flag, 0x2300 + L::B_PFULL + pb);
-                if (!ok) break;
-                ptx::tc_fence_after_sync();
                 const uint32_t keep = (what >> Note::INDEX) < TURNS ? 0u : 1u;
+#pragma unroll 1
+                for (int st = 0; st < STREAMS; ++st) {
+                    const int ps = st * L::PBUFS + pb;
+                    if (ok) ok = warp_wait(bar(L::B_PFULL + ps), (uint32_t)(g / L::PBUFS) & 1u, limit, abort_flag, 0x2300 + L::B_PFULL + ps);
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+                    const uint64_t p_at = p_desc + (uint64_t)(((uint32_t)pb * L::P_BYTES + (uint32_t)st * L::PBLK) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < TILE / 16; ++kk)
-                    if (ptx::elect_one())
-                        ptx::mma_ts(tmem + L::TM_O + (uint32_t)(g % TURNS * N), tmem + TM_V + (uint32_t)(vb * 64 + kk * 8),
-                                    p_desc + (uint64_t)(((uint32_t)pb * L::P_BYTES + (uint32_t)kk * 2048) >> 4), ID, kk > 0 ? 1u : keep);
-                if (ptx::elect_one()) {
-                    ptx::tc_commit(bar(L::B_VEMPTY + vb));
-                    ptx::tc_commit(bar(L::B_PDONE + pb));
+                    for (int kk = 0; kk < TILE / 16; ++kk)
+                        if (ptx::elect_one())
+                            ptx::mma_ts(tmem + L::TM_O + (uint32_t)(g % TURNS * N + st * L::NM), tmem + TM_V + (uint32_t)(vb * 64 + kk * 8),
+                                        p_at + (uint64_t)(((uint32_t)kk * 2048) >> 4), ID, kk > 0 ? 1u : keep);
+                    if (ptx::elect_one()) ptx::tc_commit(bar(L::B_PDONE + ps));
                 }
+                if (!ok) break;
+                if (ptx::elect_one()) ptx::tc_commit(bar(L::B_VEMPTY + vb));
                 if (what & Note::LAST) ++k;
             }
             if (ptx::elect_one()) ptx::tc_commit(bar(L::B_DRAIN + 1));
@@ -577,10 +673,10 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
             int k = 0, loads = 0;
             bool ok = true;
 #pragma unroll 1
-            for (int x = lo; ok && x < hi; ++k) {
-                const qc::Work::Unit u = work.at(x);
-                const int b = uniform(u.b), hr = uniform(u.hr), h = hr / p.rb, qb = k & 1;
-                x += min(hi - x, uniform(u.pages) - uniform(u.page));
+            for (int x = lo; ok; ++k) {
+                Run run;
+                if (!next_run(work, x, hi, run)) break;
+                const int b = run.b, hr = run.hr, h = hr / p.rb, qb = k & 1;
                 if (!(ok = warp_wait(bar(L::B_QEMPTY + qb), ((uint32_t)(k >> 1) & 1u) ^ 1u, limit, abort_flag, 0x2400 + L::B_QEMPTY + qb)))
                     break;
                 const uint32_t q = sbase + L::OFF_Q + (uint32_t)qb * L::Q_BYTES;
@@ -723,7 +819,8 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
         const int group = warp >> 2, quarter = warp & 3, mine = quarter * 32 + lane;  // this thread's lane of a tile
         const int turn = group / SHARES, share = group % SHARES;  // its tiles, and its rows of them
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const int c0 = share * NC;
+        const int stream = share / (SHARES / STREAMS), c0 = share * NC;
+        const int sb = STREAMS > 1 ? stream : turn;  // its barriers of S^T
         const uint32_t par = sbase + L::OFF_PAR + (uint32_t)(group * NC) * 4, refs = sbase + L::OFF_REF + (uint32_t)(group * NC) * 4;
         const uint32_t sums = sbase + L::OFF_SUM + (uint32_t)(group * NC) * 4, corr = sbase + L::OFF_CORR + (uint32_t)(group * NC) * 4;
         const uint32_t warps = sbase + L::OFF_WARP + (uint32_t)(group * NC) * 16, word = sbase + L::OFF_WORD + (uint32_t)(group * NC) * 8;
@@ -744,10 +841,10 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
         }
         int g0 = 0;  // the segment's first tile, of the block's
 #pragma unroll 1
-        for (int k = 0; g0 < n_tiles; ++k) {
-            const qc::Work::Unit u = work.at(lo + g0);
-            const int b = uniform(u.b), hr = uniform(u.hr), tile0 = uniform(u.page), tiles = uniform(u.pages);
-            const int n = min(n_tiles - g0, tiles - tile0), h = hr / p.rb, row0 = (hr - h * p.rb) * N + c0;
+        for (int k = 0, x = lo;; ++k) {
+            Run run;
+            if (!next_run(work, x, hi, run)) break;
+            const int b = run.b, hr = run.hr, tile0 = run.tile0, tiles = run.tiles, n = run.n, h = hr / p.rb, row0 = (hr - h * p.rb) * N + c0;
             const int raw_len = uniform(max(p.lens[b], 0)), len = qc::clamp_length(raw_len, p.max_pages), draft0 = raw_len - p.nq;
             const int qb = k & 1;
             const uint64_t mine_word = t < NC ? __ldg(p.words + (int64_t)b * p.nq + (row0 + t) % p.nq) : 0;
@@ -765,18 +862,21 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
             for (int c = 0; c < NC / 2; ++c) l[c] = 0ull;
 
             bool dead = false;
+            float lowest = UNSET;  // what is added to the scores of the row with the lowest reference
             int last = -1;  // the group's last tile of the segment
 #pragma unroll 1
             for (int g = g0 + (turn + TURNS - g0 % TURNS) % TURNS; g < g0 + n; g += TURNS) {
-                const int pb = g % L::PBUFS;
-                if (ok) ok = warp_wait(bar(L::B_SFULL + turn), (uint32_t)(g / TURNS) & 1u, limit, abort_flag, 0x2700 + L::B_SFULL + turn);
+                const int pb = g % L::PBUFS, ps = stream * L::PBUFS + pb;
+                if (ok) ok = warp_wait(bar(L::B_SFULL + sb), (uint32_t)(g / TURNS) & 1u, limit, abort_flag, 0x2700 + L::B_SFULL + sb);
                 ptx::tc_fence_after_sync();
                 const int key0 = (tile0 + g - g0) * TILE;
                 // y = score - reference + SHIFT in base-2 units.
                 uint32_t y[NC];
-                load_cols_begin<NC>(s_cols, y);
+                float red;  // the largest score of this thread's key
+                load_cols_max<NC>(s_cols, y, red);
                 const uint32_t what = notes[g % NOTES].what;
                 load_cols_end<NC>(y);
+                asm volatile("" : "+f"(red));
                 if (__builtin_expect((what & 3u) != 3u || key0 + TILE > min(len, draft0), 0)) {
                     // Rows that do not see this thread's key: -inf in S^T itself.
                     const int key = key0 + (quarter >> 1) * PAGE + key_of(mine % PAGE), bit = key - draft0;
@@ -797,6 +897,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                     }
                     ptx::tmem_wait_st();
                     load_cols<NC>(s_cols, y);
+                    red = INFINITY;
                 }
                 auto refer = [&] {
 #pragma unroll
@@ -813,10 +914,16 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                     }
                 };
                 refer();
-                float top = -INFINITY;
+                // Whether a score exceeds its row's reference.  Seldom a look at each: none can
+                // where the key's largest score does not exceed the lowest reference.
+                bool exceeds = !(fmaf(red, factor, lowest) <= SHIFT + RISE);
+                if (__builtin_expect(__any_sync(0xffffffffu, exceeds), 0)) {
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < NC; c += 2) top = ptx::fmax3(top, __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
-                if (__builtin_expect(any_of(NB_VOTE + group, 128, !ok || top > SHIFT + RISE), 0)) {
+                    for (int c = 0; c < NC; c += 2) top[c / 2 % 4] = ptx::fmax3(top[c / 2 % 4], __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
+                    exceeds = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > SHIFT + RISE;
+                }
+                if (__builtin_expect(any_of(NB_VOTE + group, 128, !ok || exceeds), 0)) {
                     // An abort that one warp of the group has met: all four leave here together.
                     dead = any_of(NB_VOTE + group, 128, !ok);
                     if (dead) break;
@@ -846,7 +953,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                     for (int c = 0; c < NC / 2; ++c)
                         l[c] = ptx::f2_mul(l[c], ptx::f2_pack(lds_f32(corr + (uint32_t)c * 8), lds_f32(corr + (uint32_t)c * 8 + 4)));
                     if (last >= 0 && ok) {  // what the products have summed
-                        ok = warp_wait(bar(L::B_PDONE + last % L::PBUFS), (uint32_t)(last / L::PBUFS) & 1u, limit, abort_flag,
+                        ok = warp_wait(bar(L::B_PDONE + stream * L::PBUFS + last % L::PBUFS), (uint32_t)(last / L::PBUFS) & 1u, limit, abort_flag,
                                        0x2700 + L::B_PDONE + last % L::PBUFS);
                         ptx::tc_fence_after_sync();
 #pragma unroll 1
@@ -861,13 +968,15 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                     }
                     load_cols<NC>(s_cols, y);
                     refer();
+                    lowest = lds_f32(par + (uint32_t)(lane % NC) * 4);
+                    lowest = warp_max(lowest);
                 }
                 // S^T of this tile is in registers.
                 ptx::tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(L::B_SREAD + turn));
+                if (lane == 0) ptx::mbar_arrive(bar(L::B_SREAD + sb));
                 // P^T: a row of 128 bytes a key (64 query rows), 16-byte pieces swizzled.
-                if (ok) ok = warp_wait(bar(L::B_PDONE + pb), ((uint32_t)(g / L::PBUFS) & 1u) ^ 1u, limit, abort_flag, 0x2700 + L::B_PDONE + pb);
+                if (ok) ok = warp_wait(bar(L::B_PDONE + ps), ((uint32_t)(g / L::PBUFS) & 1u) ^ 1u, limit, abort_flag, 0x2700 + L::B_PDONE + ps);
                 const uint32_t row = sbase + L::OFF_P + (uint32_t)pb * L::P_BYTES + (uint32_t)mine * 128;
 #pragma unroll
                 for (int e8 = 0; e8 < NC / 8; ++e8) {
@@ -885,7 +994,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(L::B_PFULL + pb));
+                if (lane == 0) ptx::mbar_arrive(bar(L::B_PFULL + ps));
                 last = g;
             }
 
@@ -906,7 +1015,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 sts_f32(sums + (uint32_t)t * 4, sum);
             }
             if (ok && last >= 0)
-                ok = warp_wait(bar(L::B_PDONE + last % L::PBUFS), (uint32_t)(last / L::PBUFS) & 1u, limit, abort_flag,
+                ok = warp_wait(bar(L::B_PDONE + stream * L::PBUFS + last % L::PBUFS), (uint32_t)(last / L::PBUFS) & 1u, limit, abort_flag,
                                0x2700 + L::B_PDONE + last % L::PBUFS);
             ptx::tc_fence_before_sync();
             // All groups of these rows are here, their products done (or none goes on).
@@ -971,8 +1080,8 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
             if (lane == 0) ptx::mbar_arrive_relaxed(bar(L::B_OFREE));
             if (threadIdx.x == 0 && begins && !joined) {
                 // The block that holds the segment's last unit x: the c with c T / G <= x < (c + 1) T / G.
-                const int end = prefix[b] * work.hr + (hr + 1) * (prefix[b + 1] - prefix[b]) - 1;
-                p.desc[2 * cta] = b * work.hr + hr;
+                const int end = work.before(b) * hr_all + (hr + 1) * (tiles + work.extra) - 1;
+                p.desc[2 * cta] = b * hr_all + hr;
                 p.desc[2 * cta + 1] = (int)(((int64_t)(end + 1) * G - 1) / T);
             }
             g0 += n;
