@@ -523,11 +523,14 @@ def _check_rows(name, t, dev=None):
         raise ValueError(f"{name} must be on cuda:{dev}")
 
 
+_Strides = ctypes.c_int64 * 3
+
+
 def _strides(t):
     """A host array of the batch, head and position strides, or None when contiguous."""
     if t.is_contiguous():
         return None
-    return (ctypes.c_int64 * 3)(t.stride(0), t.stride(1), t.stride(2))
+    return _Strides(*t.stride()[:3])
 
 
 def _check_int32(name, t, shape, dev):

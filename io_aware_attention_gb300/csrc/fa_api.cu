@@ -716,9 +716,11 @@ fa_status cross_check(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk,
 }
 
 // Parts that the key range of every item is cut into.  An item costs its key
-// tiles and about one more; the CTAs take ceil(items / SMs) rounds of them.  Cut
+// tiles and about three more; the CTAs take ceil(items / SMs) rounds of them.  Cut
 // items write partial results, which the combine kernel reads (in units of a key
-// tile's K and V on every SM), and that kernel itself costs about three tiles.
+// tile's K and V on every SM), and that launch itself costs about nine tiles.
+// (One row each: 48 sequences x 8 kv heads x up to 8192 keys 141 us whole, 150 cut in 2,
+// 204 in 5; 8 kv heads x 20000 keys 134 us whole, 27.5 cut in 16, 42 in 32.)
 int64_t cross_splits(int64_t B, int64_t heads, int64_t nq, int64_t nk, int64_t Dp, int sms)
 {
     const int64_t items = B * heads * ((nq + fa::BM - 1) / fa::BM), tiles = (nk + fa::BN - 1) / fa::BN;
@@ -726,8 +728,8 @@ int64_t cross_splits(int64_t B, int64_t heads, int64_t nq, int64_t nk, int64_t D
     double least = 0.0;
     for (int64_t s = 1; s <= std::min<int64_t>(tiles, 128) && (s == 1 || items * s <= 16 * (int64_t)sms); ++s) {
         const double rounds = (double)((items * s + sms - 1) / sms), per = (double)((tiles + s - 1) / s);
-        const double parts = s == 1 ? 0.0 : 3.0 + 2.0 * (double)(B * heads * nq * s) * (double)(Dp + 1) * 4.0 / ((double)sms * 512.0 * (double)Dp);
-        const double cost = rounds * (per + 1.0) + parts;
+        const double parts = s == 1 ? 0.0 : 9.0 + 2.0 * (double)(B * heads * nq * s) * (double)(Dp + 1) * 4.0 / ((double)sms * 512.0 * (double)Dp);
+        const double cost = rounds * (per + 3.0) + parts;
         if (s == 1 || cost < least) best = s, least = cost;
     }
     return best;

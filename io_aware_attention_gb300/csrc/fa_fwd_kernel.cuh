@@ -100,7 +100,9 @@
 //   - keys from lens[b] on hold anything, NaN among it.  Their scores are set to
 //     -inf (selected, not added), and as 0 * NaN must not be formed either, the
 //     P.V issuer skips the products of 16 keys that lie behind the last one and
-//     clears the rows of V within the last 16 in shared memory.
+//     clears the rows of V within the last 16 in shared memory;
+//   - warps whose 32 rows do not exist (a few query rows in a block of 128) only meet
+//     the barriers.
 //
 // Every mbarrier wait is bounded in time; on expiry the thread records the
 // wait in the device status word, raises a CTA-wide abort flag, and all roles
@@ -1254,6 +1256,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const int key_max = CROSS ? it.len - 1 : CAUSAL ? min(q_idx, N - 1) : N - 1;
                     const int cta_key_max = CROSS ? key_max : CAUSAL ? min(it.q0, N - 1) : N - 1;  // smallest key_max of the item
                     const int j0 = CROSS ? it.j0 : 0;  // the item's first key tile
+                    const bool idle = CROSS && it.q0 + quarter * 32 >= N;  // none of this warp's rows exists
                     float m_ref = -INFINITY;
                     // This half-row's sum of probabilities, as four packed fp32 pairs.
                     uint64_t lsum[4] = {0ull, 0ull, 0ull, 0ull};
@@ -1269,6 +1272,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         // S of tile g is in TMEM (met on every tile, also after an abort).
                         ptx::named_barrier_sync(nb_sready + (uint32_t)(g % 3), NB_SREADY_SPLIT_COUNT);
                         if (!ok) continue;
+                        if (CROSS && idle) {
+                            if (lane == 0) ptx::mbar_arrive(bar(L::B_PFULL + 2 * half + b));
+                            continue;
+                        }
                         ptx::tc_fence_after_sync();
                         // The load also returns the max of the 64 scores (the TMEM
                         // load's reduction); a masked tile takes it again after the
@@ -1402,6 +1409,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const int key_max = CROSS ? it.len - 1 : CAUSAL ? min(q_idx, N - 1) : N - 1;
                     const int cta_key_max = CROSS ? key_max : CAUSAL ? min(it.q0, N - 1) : N - 1;  // smallest key_max of the item
                     const int j0 = CROSS ? it.j0 : 0;  // the item's first key tile
+                    const bool idle = CROSS && it.q0 + quarter * 32 >= N;  // none of this warp's rows exists
                     float m_ref = -INFINITY;
                     // This half-row's sum of probabilities, as four packed fp32 pairs.
                     uint64_t lsum[4] = {0ull, 0ull, 0ull, 0ull};
@@ -1415,6 +1423,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         const int b = g & 1;
                         // S of tile g is in TMEM (met on every tile, also after an abort).
                         ptx::named_barrier_sync(NB_SREADY0 + (uint32_t)(g % 3), NB_SREADY_COUNT);
+                        if (CROSS && idle) {  // (nor any of its partner's)
+                            if (ok && lane == 0) {
+                                ptx::mbar_arrive(bar(L::B_SREAD + b));
+                                ptx::mbar_arrive(bar(L::B_PFULL));
+                            }
+                            continue;
+                        }
                         // The load also returns the max of the 64 scores (the TMEM
                         // load's reduction); a masked tile takes it again after the
                         // mask.
