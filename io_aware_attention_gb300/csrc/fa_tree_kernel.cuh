@@ -18,7 +18,7 @@
 // what has been summed scaled.
 //
 // A probability is one fp16 number (11 bits) of at most 2^(SHIFT + RISE) = 2^15, its sum
-// fp32 over the unrounded ones: a result is off by at most 2^-12 of sum p |v|, an eighth
+// fp32 over the unrounded ones: a result is off by at most 2^-11 of sum p |v|, an eighth
 // of its own rounding to bf16 where terms do not cancel.  (Two numbers a
 // probability, as with few rows, would double the products and the traffic of P in
 // shared memory, which bound the kernel.)
@@ -38,9 +38,11 @@
 //             need to know of each tile.
 //   29, 30    the two products (an elected lane each); 29 also allocates TMEM.
 //   31        query rows of the next segment: from TMA to fp16 in place, all scaled by the
-//             power of two that puts their largest entry into [2^14, 2^15) (bf16 entries
-//             down to 2^-31 of it stay exact, smaller ones are off by at most 2^-40 of it);
-//             the softmax warps do the first segment's.
+//             power of two that puts their largest entry into [2^14, 2^15): bf16 entries
+//             down to 2^-31 of it stay exact, smaller ones are off by at most 2^-40 of it.
+//             Where a row's own largest entry is more than 2^15 times smaller, every row
+//             gets a power of its own (APART), and the softmax warps bring its scores back; they
+//             also do the first segment's rows.
 //
 // TMEM columns: [0, 128) two K tiles, [128, 256) two V tiles, then the tiles of S^T in
 // flight and their O^T.  At D = 64 V^T has 64 rows: the upper lanes hold anything, and
@@ -81,6 +83,7 @@ constexpr int THREADS = 1024, GROUPS = 4, SOFTMAX_WARPS = 4 * GROUPS;
 constexpr int WARP_K = 16, WARP_V = 20, WARP_COPY = 28, WARP_S = 29, WARP_O = 30, WARP_Q = 31;
 constexpr int NOTES = 16;
 constexpr float SHIFT = 7.0f, RISE = 8.0f;
+constexpr int APART = 15, TOGETHER = 1 << 20;  // binades; "power" of rows that share one
 constexpr float UNSET = 3e38f;  // added to a row's scores before it has a reference: any finite one exceeds it
 constexpr uint32_t TM_K = 0, TM_V = 128, TM_S = 256, TM_COLS = 512;
 constexpr uint32_t NB_VOTE = 1, NB_GROUP = 5, NB_END = 9, NB_ALL = 13;  // + group, group, rows' share
@@ -121,7 +124,9 @@ struct Layout {
     static constexpr uint32_t OFF_SUM = OFF_REF + GROUPS * NC * 4;
     static constexpr uint32_t OFF_CORR = OFF_SUM + GROUPS * NC * 4;
     static constexpr uint32_t OFF_WARP = OFF_CORR + GROUPS * NC * 4;
-    static constexpr uint32_t OFF_QSC = OFF_WARP + GROUPS * NC * 16;  // the two query blocks' factors to base-2 scores
+    static constexpr uint32_t OFF_APART = OFF_WARP + GROUPS * NC * 16;  // exponents, where rows have powers of their own
+    static constexpr uint32_t OFF_LARGEST = OFF_APART + GROUPS * NC * 4;  // the two query blocks' rows' largest entries
+    static constexpr uint32_t OFF_QSC = OFF_LARGEST + 2 * N * 4;  // their factors to base-2 scores and powers
     static constexpr uint32_t OFF_FACTORS = OFF_QSC + 16;      // the V warps' scales
     static constexpr uint32_t OFF_NOTES = OFF_FACTORS + 8 * 256;
     static constexpr uint32_t OFF_BAR = OFF_NOTES + NOTES * 8;
@@ -334,12 +339,19 @@ __device__ __forceinline__ bool next_run(const Units& work, int& x, int end, Run
     return false;
 }
 
-// Query rows in shared memory (K-major, 128-byte swizzle), TOGETHER rows at a time, every
-// step-th such batch: the largest magnitude's bf16 bits, and the rows to fp16 in place.
+// What the softmax warps need to know of a query block's scaling.
+__device__ __forceinline__ void set_scaling(uint32_t at, float scale_log2, int power, bool apart)
+{
+    sts_f32(at, scale_log2 * __uint_as_float((uint32_t)(127 - power) << 23));
+    sts_f32(at + 4, __int_as_float(apart ? power : TOGETHER));
+}
+
+// Query rows in shared memory (K-major, 128-byte swizzle), BATCH rows at a time, every
+// step-th such batch: each row's largest magnitude (bf16 bits), and the rows to fp16 in place.
 template <int D, int N>
 struct QueryRows {
-    static constexpr int PER = D / 32, TOGETHER = 4;  // channels a lane
-    uint32_t q;
+    static constexpr int PER = D / 32, BATCH = 4;  // channels a lane
+    uint32_t q, largest_at;
     int first, step;
     __device__ __forceinline__ uint32_t at(int r) const
     {
@@ -351,37 +363,67 @@ struct QueryRows {
         if constexpr (PER == 4) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at(r)));
         else asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at(r)));
     }
-    __device__ __forceinline__ uint32_t largest() const
+    __device__ __forceinline__ uint32_t row_largest(int r) const
     {
-        uint32_t am = 0;
-#pragma unroll 1
-        for (int r0 = first * TOGETHER; r0 < N; r0 += step * TOGETHER) {
-            uint32_t w[TOGETHER][PER / 2];
-#pragma unroll
-            for (int e = 0; e < TOGETHER; ++e) load(r0 + e, w[e]);
-#pragma unroll
-            for (int e = 0; e < TOGETHER; ++e)
-#pragma unroll
-                for (int i = 0; i < PER / 2; ++i) am = max(am, max(w[e][i] & 0x7FFFu, w[e][i] >> 16 & 0x7FFFu));
-        }
-        return __reduce_max_sync(0xffffffffu, am);
+        uint32_t am;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(am) : "r"(largest_at + (uint32_t)r * 4));
+        return am;
     }
-    // The power of two that puts the largest entry (bits am) into [2^14, 2^15).
+    __device__ __forceinline__ void measure() const
+    {
+#pragma unroll 1
+        for (int r0 = first * BATCH; r0 < N; r0 += step * BATCH) {
+            uint32_t w[BATCH][PER / 2], am[BATCH];
+#pragma unroll
+            for (int e = 0; e < BATCH; ++e) load(r0 + e, w[e]);
+#pragma unroll
+            for (int e = 0; e < BATCH; ++e) {
+                am[e] = 0;
+#pragma unroll
+                for (int i = 0; i < PER / 2; ++i) am[e] = max(am[e], max(w[e][i] & 0x7FFFu, w[e][i] >> 16 & 0x7FFFu));
+            }
+#pragma unroll
+            for (int e = 0; e < BATCH; ++e) am[e] = __reduce_max_sync(0xffffffffu, am[e]);
+            if ((threadIdx.x & 31) == 0)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(largest_at + (uint32_t)r0 * 4), "r"(am[0]), "r"(am[1]), "r"(am[2]),
+                             "r"(am[3])
+                             : "memory");
+        }
+        __syncwarp();
+    }
+    // The power of two that puts a largest entry (bits am) into [2^14, 2^15).
     static __device__ __forceinline__ int power(uint32_t am)
     {
         const int ex = (int)(am >> 7) - 127;
         return am > 0 && ex < 128 ? min(126, max(-126, 14 - ex)) : 0;
     }
-    __device__ __forceinline__ void convert(int power_) const
+    // The power of all rows' largest finite entry, and whether a row's is too far below it.
+    // (Rows that are zero count for neither, and rows with infinities or NaN, whose results
+    // are NaN in any scaling.)
+    __device__ __forceinline__ int power_of_all(bool& apart) const
     {
-        const float up = __uint_as_float((uint32_t)(127 + power_) << 23);
+        uint32_t high = 0, low = 0x7F80u;
+#pragma unroll
+        for (int e = 0; e < (N + 31) / 32; ++e) {
+            const uint32_t am = row_largest((e * 32 + (int)(threadIdx.x & 31)) % N);
+            if (am > 0 && am < 0x7F80u) high = max(high, am), low = min(low, am);
+        }
+        high = __reduce_max_sync(0xffffffffu, high);
+        low = __reduce_min_sync(0xffffffffu, low);
+        apart = (int)(high >> 7) - (int)(low >> 7) > APART;
+        return power(high);
+    }
+    __device__ __forceinline__ void convert(int power_, bool apart) const
+    {
+        float up = __uint_as_float((uint32_t)(127 + power_) << 23);
 #pragma unroll 1
-        for (int r0 = first * TOGETHER; r0 < N; r0 += step * TOGETHER) {
-            uint32_t w[TOGETHER][PER / 2];
+        for (int r0 = first * BATCH; r0 < N; r0 += step * BATCH) {
+            uint32_t w[BATCH][PER / 2];
 #pragma unroll
-            for (int e = 0; e < TOGETHER; ++e) load(r0 + e, w[e]);
+            for (int e = 0; e < BATCH; ++e) load(r0 + e, w[e]);
 #pragma unroll
-            for (int e = 0; e < TOGETHER; ++e) {
+            for (int e = 0; e < BATCH; ++e) {
+                if (apart) up = __uint_as_float((uint32_t)(127 + power(row_largest(r0 + e))) << 23);
 #pragma unroll
                 for (int i = 0; i < PER / 2; ++i)
                     w[e][i] = qc::pack_h2(__uint_as_float(w[e][i] << 16) * up, __uint_as_float(w[e][i] & 0xFFFF0000u) * up);
@@ -689,10 +731,12 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 ++loads;
                 if (k == 0) continue;  // (the softmax warps')
                 if (!(ok = warp_wait(bar(L::B_QRAW + qb), (uint32_t)(k >> 1) & 1u, limit, abort_flag, 0x2400 + L::B_QRAW + qb))) break;
-                const QueryRows<D, N> rows{q, 0, 1};
-                const int power = rows.power(rows.largest());
-                rows.convert(power);
-                if (lane == 0) sts_f32(sbase + L::OFF_QSC + (uint32_t)qb * 4, p.scale_log2 * __uint_as_float((uint32_t)(127 - power) << 23));
+                const QueryRows<D, N> rows{q, sbase + L::OFF_LARGEST + (uint32_t)qb * (N * 4), 0, 1};
+                rows.measure();
+                bool apart;
+                const int power = rows.power_of_all(apart);
+                rows.convert(power, apart);
+                if (lane == 0) set_scaling(sbase + L::OFF_QSC + (uint32_t)qb * 8, p.scale_log2, power, apart);
                 __syncwarp();
                 if (lane < SOFTMAX_WARPS) ptx::mbar_arrive(bar(L::B_QFULL + qb));  // (as those for the first)
             }
@@ -823,20 +867,20 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
         const int sb = STREAMS > 1 ? stream : turn;  // its barriers of S^T
         const uint32_t par = sbase + L::OFF_PAR + (uint32_t)(group * NC) * 4, refs = sbase + L::OFF_REF + (uint32_t)(group * NC) * 4;
         const uint32_t sums = sbase + L::OFF_SUM + (uint32_t)(group * NC) * 4, corr = sbase + L::OFF_CORR + (uint32_t)(group * NC) * 4;
+        const uint32_t exps = sbase + L::OFF_APART + (uint32_t)(group * NC) * 4;
         const uint32_t warps = sbase + L::OFF_WARP + (uint32_t)(group * NC) * 16, word = sbase + L::OFF_WORD + (uint32_t)(group * NC) * 8;
         const uint32_t s_cols = tmem + lane_off + TM_S + (uint32_t)(turn * N + c0);
         const uint32_t o_cols = tmem + lane_off + L::TM_O + (uint32_t)(turn * N + c0);
         const int t = (int)threadIdx.x & 127;  // thread of the group
         bool ok = warp_wait(bar(L::B_QRAW), 0, limit, abort_flag, 0x2700 + L::B_QRAW);
         {
-            const QueryRows<D, N> rows{sbase + L::OFF_Q, warp, SOFTMAX_WARPS};
-            uint32_t am = ok ? rows.largest() : 0u;
-            if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + L::OFF_SUM + (uint32_t)warp * 4), "r"(am) : "memory");
+            const QueryRows<D, N> rows{sbase + L::OFF_Q, sbase + L::OFF_LARGEST, warp, SOFTMAX_WARPS};
+            if (ok) rows.measure();
             ptx::named_barrier_sync(NB_ALL, 32 * SOFTMAX_WARPS);
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(am) : "r"(sbase + L::OFF_SUM + (uint32_t)(lane % SOFTMAX_WARPS) * 4));
-            const int power = rows.power(__reduce_max_sync(0xffffffffu, am));
-            if (ok) rows.convert(power);
-            if (warp == 0 && lane == 0) sts_f32(sbase + L::OFF_QSC, p.scale_log2 * __uint_as_float((uint32_t)(127 - power) << 23));
+            bool apart;
+            const int power = rows.power_of_all(apart);
+            if (ok) rows.convert(power, apart);
+            if (warp == 0 && lane == 0) set_scaling(sbase + L::OFF_QSC, p.scale_log2, power, apart);
             if (lane == 0) ptx::mbar_arrive(bar(L::B_QFULL));
         }
         int g0 = 0;  // the segment's first tile, of the block's
@@ -854,7 +898,13 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 sts_f32(par + (uint32_t)t * 4, UNSET);
                 sts_f32(refs + (uint32_t)t * 4, -INFINITY);
             }
-            const float factor = lds_f32(sbase + L::OFF_QSC + (uint32_t)qb * 4);
+            const float factor = lds_f32(sbase + L::OFF_QSC + (uint32_t)qb * 8);
+            const int power = __float_as_int(lds_f32(sbase + L::OFF_QSC + (uint32_t)qb * 8 + 4));
+            const bool apart = power != TOGETHER;
+            if (apart && t < NC) {
+                const uint32_t own = __float_as_uint(lds_f32(sbase + L::OFF_LARGEST + (uint32_t)(qb * N + c0 + t) * 4));
+                sts_f32(exps + (uint32_t)t * 4, __int_as_float(own > 0 && own < 0x7F80u ? power - QueryRows<D, N>::power(own) : 0));
+            }
             ptx::named_barrier_sync(NB_GROUP + group, 128);
             if (lane == 0) ptx::mbar_arrive(bar(L::B_QEMPTY + qb));
             uint64_t l[NC / 2];
@@ -877,8 +927,9 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 const uint32_t what = notes[g % NOTES].what;
                 load_cols_end<NC>(y);
                 asm volatile("" : "+f"(red));
-                if (__builtin_expect((what & 3u) != 3u || key0 + TILE > min(len, draft0), 0)) {
-                    // Rows that do not see this thread's key: -inf in S^T itself.
+                if (__builtin_expect((what & 3u) != 3u || key0 + TILE > min(len, draft0) || apart, 0)) {
+                    // Rows that do not see this thread's key: -inf in S^T itself; rows with a
+                    // power of their own: the common one (in two steps, each a power of two that exists).
                     const int key = key0 + (quarter >> 1) * PAGE + key_of(mine % PAGE), bit = key - draft0;
                     const bool there = key < len && (what >> (quarter >> 1) & 1u), named = bit >= 0;
                     const uint64_t mask = named && bit < p.nq ? 1ull << bit : 0ull;
@@ -886,6 +937,14 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                     for (int c = 0; c < NC; c += 8) {
                         uint32_t r[8];
                         load_cols<8>(s_cols + (uint32_t)c, r);
+                        if (apart) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int down = -__float_as_int(lds_f32(exps + (uint32_t)(c + e) * 4)), half = down >> 1;
+                                r[e] = __float_as_uint(__uint_as_float(r[e]) * __uint_as_float((uint32_t)(127 - half) << 23) *
+                                                       __uint_as_float((uint32_t)(127 - (down - half)) << 23));
+                            }
+                        }
 #pragma unroll
                         for (int e = 0; e < 8; e += 2) {
                             const uint4 w = lds128(word + (uint32_t)(c + e) * 8);

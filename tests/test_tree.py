@@ -2,7 +2,7 @@
 accepted path (fa_qcache_commit), against the definition in 64 bits.
 
 Attention's bound is that of the cache's decode: a score is off by delta = 2^-18 * big
-(big the largest scale * sum |q k|), a probability by its two roundings to fp16, the
+(big the largest scale * sum |q k|), a probability by its rounding to fp16 (2^-11), the
 sums by 2^-20, and the result by its rounding to bf16.  Where one key takes nearly
 all of a row's weight and holds 0 in a channel, what the others hold there is all
 there is: fp16's smallest step is 2^-24, of probabilities whose largest is at least
@@ -34,10 +34,11 @@ def trees(B, T, seed):
     return torch.from_numpy(_tree.ancestors(_tree.random_parents(B, T, np.random.default_rng(seed))))
 
 
-def check(o, lse, q, words, cache, d, scale, k_scale=1.0, v_scale=1.0):
+def check(o, lse, q, words, cache, d, scale, k_scale=1.0, v_scale=1.0, rows=slice(None)):
     ks, vs = ref.unpack(*cache, d, k_scale, v_scale)
     o64, lse64, mag, big = _tree.attention(q, words, ks, vs, scale)
-    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    o, lse = o.double().cpu().numpy()[:, :, rows], lse.double().cpu().numpy()[:, :, rows]
+    o64, lse64, mag, big = (x[:, :, rows] for x in (o64, lse64, mag, big))
     delta = 2.0 ** -18 * big
     most = np.zeros((len(ks), o64.shape[1], 1, 1))  # a bound on sum |v| of every head
     for b, v in enumerate(vs):
@@ -159,6 +160,26 @@ def test_scales_and_large_scores(T, H):
     q[:, :, -1] *= 2.0 ** -90
     o, lse = run(q, words, cache, scale=0.2, k_scale=k_scale, v_scale=v_scale)
     check(o, lse, q, words, cache, 128, 0.2, k_scale, v_scale)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T, H", [(5, 2), (9, 2), (12, 4), (30, 4), (64, 4)])
+@pytest.mark.parametrize("B, powers", [(3, (0, -12)), (3, (-110, -30, -16, 0, 3, 18)), (90, (-110, -30, -16, 0, 3, 18))])
+def test_queries_of_unequal_size(B, powers, T, H, d):
+    """Rows far apart in size share a product, each as exact as if it were alone, and rows
+    that hold NaN, infinities or the largest numbers leave the others as they are."""
+    rng = np.random.default_rng(T + B)
+    lens = [int(n) for n in rng.integers(T, T + 250, B)]
+    cache = ref.make_cache(lens, 2, d, seed=T)
+    words = trees(B, T, 11)
+    q = rand((B, H, T, d), 12) * torch.from_numpy(2.0 ** rng.choice(powers, (B, H, T, 1))).to(torch.bfloat16)
+    o, lse = run(q, words, cache)
+    check(o, lse, q, words, cache, d, d ** -0.5)
+    bad = q.clone()
+    bad[:, :, 1], bad[:, :, 2], bad[:, :, 3] = float("nan"), float("inf"), torch.finfo(torch.bfloat16).max
+    o, lse = run(bad, words, cache)
+    check(o, lse, q, words, cache, d, d ** -0.5, rows=[i for i in range(T) if i not in (1, 2, 3)])
 
 
 @gpu
