@@ -752,7 +752,7 @@ fa::cross::Rows rows_of(const View& v) { return {v.s[0], v.s[1], v.s[2], (int)v.
 bool hits(const void* p, size_t n, const View& v, int64_t B, int64_t d) { return overlaps(p, n, v.p, view_bytes(v, B, d)); }
 
 template <int D, bool PAD>
-fa_status launch_cross_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const fa::Params& p, unsigned grid,
+fa_status launch_cross_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const fa::CrossParams& p, unsigned grid,
                            int dev, cudaStream_t st)
 {
     static std::atomic<int> done[MAX_DEVICES];
@@ -765,7 +765,7 @@ fa_status launch_cross_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const C
 
 template <int D>
 fa_status launch_cross_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
-                           const CUtensorMap& mdq, const fa::bwd::Params& p, unsigned grid, int dev, cudaStream_t st)
+                           const CUtensorMap& mdq, const fa::bwd::CrossParams& p, unsigned grid, int dev, cudaStream_t st)
 {
     static std::atomic<int> done[MAX_DEVICES];
     constexpr size_t smem = fa::bwd::Layout<D>::SMEM_BYTES_CROSS;
@@ -1275,7 +1275,7 @@ fa_status fa_cross_fwd(const void* q, const int64_t* q_strides, const void* k, c
         for (int i = 0; i < 3; ++i)
             if (hits(workspace, need, *views[i], B, d)) return FA_ERR_INVALID_ARG;
     }
-    fa::Params p = {};
+    fa::CrossParams p = {};
     CUtensorMap mq, mk, mv;
     if (!view_map(&mq, &p.x.q_h, &p.x.q_b, vq, B, d, fa::BM) || !view_map(&mk, &p.x.k_h, &p.x.k_b, vk, B, d, fa::BN) ||
         !view_map(&mv, &p.x.v_h, &p.x.v_b, vv, B, d, fa::BN))
@@ -1385,7 +1385,7 @@ fa_status fa_cross_bwd(const void* q, const int64_t* q_strides, const void* k, c
     float* const lse2 = static_cast<float*>(workspace);
     float* const dsum = lse2 + rows;
     float* const acc = dsum + rows;
-    fa::bwd::Params p = {};
+    fa::bwd::CrossParams p = {};
     CUtensorMap mq, mk, mv, mdo, mdq;
     if (!view_map(&mq, &p.x.q_h, &p.x.q_b, w[Q], B, d, fa::bwd::BQ) || !view_map(&mk, &p.x.k_h, &p.x.k_b, w[K], B, d, fa::bwd::BKV) ||
         !view_map(&mv, &p.x.v_h, &p.x.v_b, w[V], B, d, fa::bwd::BKV) ||

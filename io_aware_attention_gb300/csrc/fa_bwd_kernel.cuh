@@ -158,6 +158,9 @@ struct Params {
     float scale;
     unsigned long long wait_limit_ns;
     int debug_skip_q;  // test hook: global step whose Q/dO tile the first CTA never loads (-1: none)
+    static constexpr Cross x = {};  // (for CROSS only: CrossParams)
+};
+struct CrossParams : Params {
     Cross x;
 };
 
@@ -207,7 +210,7 @@ struct Item {
 };
 
 // CROSS item i of those with keys: sequences in order, then kv heads, then key blocks.
-__device__ __forceinline__ Item cross_item(int i, const Params& p, const int* len, const int* prefix)
+__device__ __forceinline__ Item cross_item(int i, const CrossParams& p, const int* len, const int* prefix)
 {
     const Cross& x = p.x;
     const int y = i / x.kv_heads;
@@ -247,7 +250,7 @@ template <int D, bool CAUSAL, bool CROSS = false>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
-                  const __grid_constant__ CUtensorMap tm_dq, const Params p)
+                  const __grid_constant__ CUtensorMap tm_dq, const std::conditional_t<CROSS, CrossParams, Params> p)
 {
     using L = Layout<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int num_items = p.num_items;
     const int* const seq_len = reinterpret_cast<const int*>(sgen + L::OFF_LEN);  // CROSS only
     const int* const seq_prefix = reinterpret_cast<const int*>(sgen + L::OFF_PREFIX);
-    auto item_at = [&](int i, const Params& pp) -> Item {
+    auto item_at = [&](int i, const auto& pp) -> Item {
         if constexpr (CROSS) return cross_item(i, pp, seq_len, seq_prefix);
         else return item_of<CAUSAL>(i, pp);
     };

@@ -116,6 +116,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ptx.cuh"
 
 namespace fa {
@@ -203,6 +205,10 @@ struct Params {
     float scale_log2;  // scale * log2(e)
     unsigned long long wait_limit_ns;
     int debug_skip_k;  // test hook: global K tile the producer never loads (-1: none)
+    static constexpr Cross x = {};  // (for CROSS only: CrossParams)
+};
+// (Apart, as the registers of the other instances depend on the size of what is passed.)
+struct CrossParams : Params {
     Cross x;
 };
 
@@ -480,7 +486,7 @@ __device__ __forceinline__ int cross_length(const int32_t* lens, int b, int nk)
 
 // CROSS item i.  Per sequence (longest first), kv head and part: the group's heads
 // and their row blocks.
-__device__ __forceinline__ Item cross_item(int i, const Params& p, const int* len, const uint16_t* order)
+__device__ __forceinline__ Item cross_item(int i, const CrossParams& p, const int* len, const uint16_t* order)
 {
     const Cross& x = p.x;
     Item it;
@@ -511,7 +517,7 @@ __device__ __forceinline__ Item cross_item(int i, const Params& p, const int* le
 template <int D, bool CAUSAL, bool PAD, bool SNAKE, bool CROSS = false>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const Params p)
+                  const __grid_constant__ CUtensorMap tm_v, const std::conditional_t<CROSS, CrossParams, Params> p)
 {
     using L = Layout<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // order.
     const int* const seq_len = reinterpret_cast<const int*>(sgen + L::OFF_LEN);            // CROSS only
     const uint16_t* const seq_order = reinterpret_cast<const uint16_t*>(sgen + L::OFF_ORDER);
-    auto item_at = [&](int i, const Params& pp) -> Item {
+    auto item_at = [&](int i, const auto& pp) -> Item {
         if constexpr (CROSS) return cross_item(i, pp, seq_len, seq_order);
         else return item_of<CAUSAL>(i, pp);
     };
