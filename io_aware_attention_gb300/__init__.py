@@ -645,7 +645,8 @@ def _check_cross(q, k, v, lens, *rows):
     dev = q.get_device()
     _check_rows("k", k, dev)
     _check_rows("v", v, dev)
-    B, H, Nq, d = q.shape
+    shape = q.shape
+    B, H, Nq, d = shape
     Bk, Hkv, Nk, dk = k.shape
     if Bk != B or dk != d or v.shape != k.shape or Hkv < 1 or H % Hkv:
         raise ValueError(f"k and v must be (B, Hkv, Nk, d) of q's batch and head size, Hkv a divisor of its heads: "
@@ -654,9 +655,15 @@ def _check_cross(q, k, v, lens, *rows):
         _check_int32("lens", lens, (B,), dev)
     for name, t in rows:
         _check_rows(name, t, dev)
-        if t.shape != q.shape:
+        if t.shape != shape:
             raise ValueError(f"{name} must have the shape of q")
     return dev, B, H, Hkv, Nq, Nk, d
+
+
+@functools.lru_cache(maxsize=256)
+def _stride_array(strides):
+    """A host array of a view's strides, which calls only read."""
+    return _Strides(*strides[:3])
 
 
 def _bytes_of(what, *sizes) -> int:
@@ -689,14 +696,13 @@ def _check_workspace(workspace, dev):
 
 
 def _cross_fwd_call(q, k, v, o, lse, lens, workspace, scale, stream, sizes):
-    dev = sizes[0]
-    if scale is None:
-        scale = 1.0 / math.sqrt(sizes[-1])
-    rc = library().fa_cross_fwd(q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), o.data_ptr(),
-                                _strides(o), lse.data_ptr(), None if lens is None else lens.data_ptr(), *sizes[1:], float(scale),
+    at = _stride_array
+    rc = library().fa_cross_fwd(q.data_ptr(), at(q.stride()), k.data_ptr(), at(k.stride()), v.data_ptr(), at(v.stride()),
+                                o.data_ptr(), at(o.stride()), lse.data_ptr(), None if lens is None else lens.data_ptr(), *sizes[1:],
+                                1.0 / math.sqrt(sizes[-1]) if scale is None else float(scale),
                                 None if workspace is None else workspace.data_ptr(),
                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                _stream_handle(stream, dev))
+                                _stream_handle(stream, sizes[0]))
     if rc != 0:
         raise FaError(rc, "fa_cross_fwd")
     return o, lse
@@ -741,6 +747,25 @@ def cross_fwd(q, k, v, lens=None, scale: float | None = None, stream=None):
     return _cross_fwd_call(q, k, v, o, lse, lens, ws, scale, None, sizes)
 
 
+@functools.lru_cache(maxsize=256)
+def _cross_bwd_workspace(*sizes):
+    """The backward's workspace size, a function of the sizes alone."""
+    return cross_bwd_workspace_bytes(*sizes)
+
+
+def _cross_bwd_call(q, k, v, o, lse, do, dq, dk, dv, lens, workspace, scale, stream, sizes):
+    at = _stride_array
+    rc = library().fa_cross_bwd(q.data_ptr(), at(q.stride()), k.data_ptr(), at(k.stride()), v.data_ptr(), at(v.stride()),
+                                o.data_ptr(), at(o.stride()), lse.data_ptr(), do.data_ptr(), at(do.stride()), dq.data_ptr(),
+                                at(dq.stride()), dk.data_ptr(), at(dk.stride()), dv.data_ptr(), at(dv.stride()),
+                                None if lens is None else lens.data_ptr(), *sizes[1:],
+                                1.0 / math.sqrt(sizes[-1]) if scale is None else float(scale), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream_handle(stream, sizes[0]))
+    if rc != 0:
+        raise FaError(rc, "fa_cross_bwd")
+    return dq, dk, dv
+
+
 def cross_bwd_into(q, k, v, o, lse, do, dq, dk, dv, workspace, lens=None, scale: float | None = None, stream=None):
     """:func:`cross_bwd` into caller-provided dq (q's shape), dk, dv (k's shape;
     strided views are fine, also of one buffer) and workspace (a contiguous CUDA
@@ -757,16 +782,7 @@ def cross_bwd_into(q, k, v, o, lse, do, dq, dk, dv, workspace, lens=None, scale:
     _check_workspace(workspace, dev)
     _on_current_device(dev)
     _stream_on(stream, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(sizes[-1])
-    rc = library().fa_cross_bwd(q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), o.data_ptr(),
-                                _strides(o), lse.data_ptr(), do.data_ptr(), _strides(do), dq.data_ptr(), _strides(dq),
-                                dk.data_ptr(), _strides(dk), dv.data_ptr(), _strides(dv),
-                                None if lens is None else lens.data_ptr(), *sizes[1:], float(scale), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
-    if rc != 0:
-        raise FaError(rc, "fa_cross_bwd")
-    return dq, dk, dv
+    return _cross_bwd_call(q, k, v, o, lse, do, dq, dk, dv, lens, workspace, scale, stream, sizes)
 
 
 def cross_bwd(q, k, v, o, lse, do, lens=None, scale: float | None = None, stream=None):
@@ -779,14 +795,16 @@ def cross_bwd(q, k, v, o, lse, do, lens=None, scale: float | None = None, stream
         with _under(stream, q):
             return cross_bwd(q, k, v, o, lse, do, lens, scale)
     sizes = _check_cross(q, k, v, lens, ("o", o), ("do", do))
-    dev = sizes[0]
+    dev, on = sizes[0], q.device
+    _check_out("lse", lse, q.shape[:3], torch.float32, on)
     if _cuda_device() != dev:
         with torch.cuda.device(dev):
             return cross_bwd(q, k, v, o, lse, do, lens, scale)
-    ws = torch.empty(cross_bwd_workspace_bytes(*sizes[1:]), dtype=torch.uint8, device=q.device)
-    dq = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    dk, dv = (torch.empty(k.shape, dtype=torch.bfloat16, device=q.device) for _ in range(2))
-    return cross_bwd_into(q, k, v, o, lse, do, dq, dk, dv, ws, lens, scale)
+    ws = torch.empty(_cross_bwd_workspace(*sizes[1:]), dtype=torch.uint8, device=on)
+    dq = torch.empty(q.shape, dtype=torch.bfloat16, device=on)
+    dk = torch.empty(k.shape, dtype=torch.bfloat16, device=on)
+    dv = torch.empty(k.shape, dtype=torch.bfloat16, device=on)
+    return _cross_bwd_call(q, k, v, o, lse, do, dq, dk, dv, lens, ws, scale, None, sizes)
 
 
 QCACHE_PAGE = 64
