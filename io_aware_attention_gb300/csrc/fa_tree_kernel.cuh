@@ -80,7 +80,7 @@ using qc::PAGE;
 
 constexpr int TILE = 2 * PAGE;
 constexpr int THREADS = 1024, GROUPS = 4, SOFTMAX_WARPS = 4 * GROUPS;
-constexpr int WARP_K = 16, WARP_V = 20, WARP_COPY = 28, WARP_S = 29, WARP_O = 30, WARP_Q = 31;
+constexpr int WARP_CODES = 16, SETS = 3, WARP_COPY = 28, WARP_S = 29, WARP_O = 30, WARP_Q = 31;
 constexpr int NOTES = 16;
 constexpr float SHIFT = 7.0f, RISE = 8.0f;
 constexpr int APART = 15, TOGETHER = 1 << 20;  // binades; "power" of rows that share one
@@ -88,8 +88,8 @@ constexpr float UNSET = 3e38f;  // added to a row's scores before it has a refer
 constexpr uint32_t TM_K = 0, TM_V = 128, TM_S = 256, TM_COLS = 512;
 constexpr uint32_t NB_VOTE = 1, NB_GROUP = 5, NB_END = 9, NB_ALL = 13;  // + group, group, rows' share
 // Registers a thread after the split; launched with 64 (65536 / 1024).
-constexpr uint32_t REGS_SOFTMAX = 88, REGS_K = 48, REGS_V = 40, REGS_OTHER = 32;
-static_assert(512 * REGS_SOFTMAX + 128 * REGS_K + 256 * REGS_V + 128 * REGS_OTHER <= 65536, "register split");
+constexpr uint32_t REGS_SOFTMAX = 88, REGS_CODES = 40, REGS_OTHER = 32;
+static_assert(512 * REGS_SOFTMAX + 128 * SETS * REGS_CODES + 128 * REGS_OTHER <= 65536, "register split");
 
 template <int D, int N>
 struct Layout {
@@ -104,8 +104,14 @@ struct Layout {
     static constexpr int STREAMS = TURNS == 1 ? 2 : 1, NM = N / STREAMS;  // rows of a product
     static constexpr int PBUFS = TURNS == 1 ? 2 : TURNS;
     static constexpr int EXTRA = TURNS == 1 ? 2 : 4;
-    static constexpr int RAW_STAGES = N == 128 ? 4 : 6;  // tiles' codes on their way
-    static_assert(NOTES >= RAW_STAGES + 2, "notes");
+    // Tiles' codes on their way: as many for each set of warps that takes them, so that
+    // a stage's next tile is waited for by the warps that emptied it.
+    static constexpr int RAW_STAGES = N == 128 ? SETS : 2 * SETS;
+    static_assert(NOTES >= RAW_STAGES + 2 + SETS, "notes");
+    // Tiles whose products are done, told of in turn by EMPTIES barriers: a set that
+    // waits for tile g - 2 left tile g - 3 when the products of g - 5 were done, so of
+    // the barrier's earlier tiles (g - 2 - EMPTIES) none is out, and its parity is clear.
+    static constexpr int EMPTIES = 2 * SETS;
     static constexpr uint32_t TM_O = TM_S + TURNS * N;
     static_assert(TM_O + TURNS * N <= TM_COLS && NO % 4 == 0, "TMEM");
     static constexpr uint32_t QBLK = N * 128;              // 64 channels of the rows
@@ -128,10 +134,10 @@ struct Layout {
     static constexpr uint32_t OFF_LARGEST = OFF_APART + GROUPS * NC * 4;  // the two query blocks' rows' largest entries
     static constexpr uint32_t OFF_QSC = OFF_LARGEST + 2 * N * 4;  // their factors to base-2 scores and powers
     static constexpr uint32_t OFF_FACTORS = OFF_QSC + 16;      // the V warps' scales
-    static constexpr uint32_t OFF_NOTES = OFF_FACTORS + 8 * 256;
+    static constexpr uint32_t OFF_NOTES = OFF_FACTORS + 4 * SETS * 512;
     static constexpr uint32_t OFF_BAR = OFF_NOTES + NOTES * 8;
     static constexpr int B_RAWFULL = 0, B_RAWEMPTY = B_RAWFULL + RAW_STAGES, B_KFULL = B_RAWEMPTY + RAW_STAGES, B_KEMPTY = B_KFULL + 2,
-                         B_VFULL = B_KEMPTY + 2, B_VEMPTY = B_VFULL + 2, B_QRAW = B_VEMPTY + 2, B_QFULL = B_QRAW + 2, B_QEMPTY = B_QFULL + 2,
+                         B_VFULL = B_KEMPTY + EMPTIES, B_VEMPTY = B_VFULL + 2, B_QRAW = B_VEMPTY + EMPTIES, B_QFULL = B_QRAW + 2, B_QEMPTY = B_QFULL + 2,
                          B_SFULL = B_QEMPTY + 2, B_SREAD = B_SFULL + 4, B_PFULL = B_SREAD + 4, B_PDONE = B_PFULL + 4,
                          B_OFREE = B_PDONE + 4, B_DRAIN = B_OFREE + 1, NUM_BARS = B_DRAIN + 2;
     static constexpr uint32_t OFF_MISC = OFF_BAR + NUM_BARS * 8;  // TMEM base, abort
@@ -250,6 +256,12 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t addr)
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
+__device__ __forceinline__ uint32_t lds_u32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
 __device__ __forceinline__ uint32_t lds_u16(uint32_t addr)
 {
     uint16_t v;
@@ -268,6 +280,9 @@ __device__ __forceinline__ void sts_f32(uint32_t addr, float v) { asm volatile("
 // r of a page's 64 holds key 8 (r / 2 % 8) + 2 (r / 16) + r % 2, which makes the pairs
 // of keys whose V scales adjoin in a page (pairs q, q + 4, ...) neighbouring columns.
 __device__ __forceinline__ int key_of(int r) { return (r >> 1 & 7) * 8 + (r >> 4 & 3) * 2 + (r & 1); }
+
+// The channel, of a warp's 32, that TMEM lane r of V^T (and of O^T) holds.
+__device__ __forceinline__ int channel_of(int r) { return (r & 7) * 4 + (r >> 3); }
 
 // x, the same in every lane, by an instruction whose result the compiler knows to be:
 // loops and addresses made of it run on the uniform datapath, and the products'
@@ -524,17 +539,19 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::RAW_STAGES; ++s) {
             ptx::mbar_init(bar(L::B_RAWFULL + s), 1);
-            ptx::mbar_init(bar(L::B_RAWEMPTY + s), 4 + 8);
+            ptx::mbar_init(bar(L::B_RAWEMPTY + s), 4);
         }
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(bar(L::B_KFULL + s), 4);
-            ptx::mbar_init(bar(L::B_KEMPTY + s), 1);
-            ptx::mbar_init(bar(L::B_VFULL + s), 8);
-            ptx::mbar_init(bar(L::B_VEMPTY + s), 1);
+            ptx::mbar_init(bar(L::B_VFULL + s), 4);
             ptx::mbar_init(bar(L::B_QRAW + s), 1);
             ptx::mbar_init(bar(L::B_QFULL + s), SOFTMAX_WARPS);
             ptx::mbar_init(bar(L::B_QEMPTY + s), 1 + SOFTMAX_WARPS);
             ptx::mbar_init(bar(L::B_DRAIN + s), 1);
+        }
+        for (int s = 0; s < L::EMPTIES; ++s) {
+            ptx::mbar_init(bar(L::B_KEMPTY + s), 1);
+            ptx::mbar_init(bar(L::B_VEMPTY + s), 1);
         }
         for (int s = 0; s < 4; ++s) {
             ptx::mbar_init(bar(L::B_SFULL + s), 1);
@@ -668,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 }
                 if (!ok) break;
                 if (ptx::elect_one()) {
-                    ptx::tc_commit(bar(L::B_KEMPTY + kb));
+                    ptx::tc_commit(bar(L::B_KEMPTY + g % L::EMPTIES));
                     if (what & Note::LAST) ptx::tc_commit(bar(L::B_QEMPTY + qb));
                 }
                 if (what & Note::LAST) ++k;
@@ -705,7 +722,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                     if (ptx::elect_one()) ptx::tc_commit(bar(L::B_PDONE + ps));
                 }
                 if (!ok) break;
-                if (ptx::elect_one()) ptx::tc_commit(bar(L::B_VEMPTY + vb));
+                if (ptx::elect_one()) ptx::tc_commit(bar(L::B_VEMPTY + g % L::EMPTIES));
                 if (what & Note::LAST) ++k;
             }
             if (ptx::elect_one()) ptx::tc_commit(bar(L::B_DRAIN + 1));
@@ -744,83 +761,37 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
 #pragma unroll 1
             for (int e = max(0, loads - 2); e < loads; ++e) drain_bar(bar(L::B_QRAW + (e & 1)), (uint32_t)(e >> 1) & 1u, limit, abort_flag, 0x2480);
         }
-    } else if (warp >= WARP_V) {
-        ptx::setmaxnreg_dec<REGS_V>();
-        // ---------------------------------------------------------------- V
-        // This thread's channel of one of a tile's pages; a byte is a pair of keys.
-        const int quarter = warp & 3, ch = quarter * 32 + lane, page = (warp - WARP_V) >> 2;
-        const uint32_t factors = sbase + L::OFF_FACTORS + (uint32_t)(warp - WARP_V) * 256;
+    } else if (warp >= WARP_CODES) {
+        ptx::setmaxnreg_dec<REGS_CODES>();
+        // --------------------------------------------------------------- codes
+        // Three sets of warps take tiles in turn: first the keys, then the values.
+        const int quarter = warp & 3, set = (warp - WARP_CODES) >> 2;
+        // Of the keys, key x of page `page`.
+        const int page = quarter >> 1, x = key_of((quarter & 1) * 32 + lane);
+        const bool other = D == 128 ? (lane >> 1) & 1 : (lane >> 2) & 1;
+        // Of the values 32 channels; a byte is a pair of keys.  A thread takes four channels
+        // of every fourth pair at a time: a word of codes, whose bytes go to four TMEM
+        // lanes (16x128b: the fragment of a product's operand; see channel_of).
+        const int fourth = lane & 3;
+        const uint32_t factors = sbase + L::OFF_FACTORS + (uint32_t)(warp - WARP_CODES) * 512;
         bool ok = true;
 #pragma unroll 1
-        for (int g = 0; ok && g < n_tiles; ++g) {
+        for (int g = set; ok && g < n_tiles; g += SETS) {
             const int st = g % L::RAW_STAGES, buf = g & 1;
             ok = warp_wait(bar(L::B_RAWFULL + st), (uint32_t)(g / L::RAW_STAGES) & 1u, limit, abort_flag, 0x2500 + L::B_RAWFULL + st);
-            if (!ok) break;
-            if (quarter * 32 < D) {
-                const Note note = notes[g % NOTES];
-                const int left = note.what >> page & 1u ? note.left - page * PAGE : 0;
-                const uint32_t blk = sbase + L::OFF_RAW + (uint32_t)st * L::RAW_BYTES + (uint32_t)page * L::PAGE_BYTES;
-                // The scales of the warp's 2 channel blocks to fp16, pairs of keys: [block][q][8
-                // pairs q, q + 4, ...], a lane two of 64.  Places of no key hold anything:
-                // their scale becomes 0 (their weight is 0, and 0 * NaN must not be formed).
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = e * 32 + lane, b = i >> 5, q = i >> 3 & 3, r = i & 7, pair = q + 4 * r;
-                    uint32_t two = lds_u16(blk + (uint32_t)(PB::VS + (q * PB::NB + quarter * 2 + b) * 16 + 2 * r));
-                    two &= left > 2 * pair + 1 ? 0xFFFFu : left > 2 * pair ? 0xFFu : 0u;
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(factors + (uint32_t)i * 4), "r"(qc::e4m3x2(two)) : "memory");
-                }
-                __syncwarp();
-            }
-            ok = warp_wait(bar(L::B_VEMPTY + buf), ((uint32_t)(g >> 1) & 1u) ^ 1u, limit, abort_flag, 0x2500 + L::B_VEMPTY + buf);
+            const int before = g - 2, empty = (g + L::EMPTIES - 2) % L::EMPTIES;
+            const uint32_t turns = (uint32_t)(before / L::EMPTIES) & 1u;
+            if (ok && before >= 0) ok = warp_wait(bar(L::B_KEMPTY + empty), turns, limit, abort_flag, 0x2500 + L::B_KEMPTY + empty);
             if (!ok) break;
             ptx::tc_fence_after_sync();
-            if (quarter * 32 < D) {
-                const uint32_t blk = sbase + L::OFF_RAW + (uint32_t)st * L::RAW_BYTES + (uint32_t)page * L::PAGE_BYTES;
-                const uint32_t codes = blk + PB::VC + (uint32_t)ch, mine = factors + (uint32_t)(lane >> 4) * 128;
-                const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + TM_V + (uint32_t)(buf * 64 + page * 32);
-#pragma unroll 2
-                for (int q = 0; q < 4; ++q) {  // pairs q, q + 4, ...: columns 8 q and on
-                    uint32_t o[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = lds_u8(codes + (uint32_t)((q + 4 * e) * D));
-                    const uint4 f0 = lds128(mine + (uint32_t)(q * 32)), f1 = lds128(mine + (uint32_t)(q * 32 + 16));
-                    const uint32_t f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = qc::hmul2(qc::e2m1x2<0>(o[e]), f[e]);
-                    ptx::tmem_st8(to + (uint32_t)(q * 8), o);
-                }
-                ptx::tmem_wait_st();
-            }
-            ptx::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(bar(L::B_RAWEMPTY + st));
-                ptx::mbar_arrive(bar(L::B_VFULL + buf));
-            }
-        }
-    } else if (warp >= WARP_K) {
-        ptx::setmaxnreg_dec<REGS_K>();
-        // ---------------------------------------------------------------- K
-        // This thread's key: x of page `page`.
-        const int quarter = warp & 3, page = quarter >> 1, x = key_of((quarter & 1) * 32 + lane);
-        const bool other = D == 128 ? (lane >> 1) & 1 : (lane >> 2) & 1;
-        bool ok = true;
-#pragma unroll 1
-        for (int g = 0; ok && g < n_tiles; ++g) {
-            const int st = g % L::RAW_STAGES, buf = g & 1;
-            ok = warp_wait(bar(L::B_RAWFULL + st), (uint32_t)(g / L::RAW_STAGES) & 1u, limit, abort_flag, 0x2600 + L::B_RAWFULL + st);
-            if (ok) ok = warp_wait(bar(L::B_KEMPTY + buf), ((uint32_t)(g >> 1) & 1u) ^ 1u, limit, abort_flag, 0x2600 + L::B_KEMPTY + buf);
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            const uint32_t blk = sbase + L::OFF_RAW + (uint32_t)st * L::RAW_BYTES + (uint32_t)page * L::PAGE_BYTES;
-            const uint32_t row = blk + (uint32_t)PB::kcode(x);
+            const uint32_t raw = sbase + L::OFF_RAW + (uint32_t)st * L::RAW_BYTES;
             // (A page that is not there, and places of no key, leave anything: their
             // scores are not used.)
 #pragma unroll 1
             for (int part = 0; part < D / 64; ++part) {
                 // 64 channels: two pieces of 16 bytes, the second one first in every other
                 // lane of those whose rows share banks.
+                const uint32_t blk = raw + (uint32_t)page * L::PAGE_BYTES, row = blk + (uint32_t)PB::kcode(x);
                 const uint4 first = lds128(row + (uint32_t)(part * 32 + (other ? 16 : 0)));
                 const uint4 then = lds128(row + (uint32_t)(part * 32 + (other ? 0 : 16)));
                 uint32_t sc[2];  // scales of two channel blocks each
@@ -835,26 +806,72 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                                        other ? first.x : then.x, other ? first.y : then.y, other ? first.z : then.z, other ? first.w : then.w};
                 const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + TM_K + (uint32_t)(buf * 64 + part * 32);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t f = qc::e4m3x2(sc[half]);
-                    uint32_t o[16];
+                for (int half = 0; half < 4; ++half) {
+                    const uint32_t f = qc::e4m3x2(sc[half >> 1]);
+                    uint32_t o[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        auto by = [&](uint32_t a) { return j < 2 ? qc::hmul2_by<0>(a, f) : qc::hmul2_by<1>(a, f); };
-                        o[4 * j + 0] = by(qc::e2m1x2<0>(w[4 * half + j]));
-                        o[4 * j + 1] = by(qc::e2m1x2<1>(w[4 * half + j]));
-                        o[4 * j + 2] = by(qc::e2m1x2<2>(w[4 * half + j]));
-                        o[4 * j + 3] = by(qc::e2m1x2<3>(w[4 * half + j]));
+                    for (int j = 0; j < 2; ++j) {
+                        auto by = [&](uint32_t a) { return half % 2 == 0 ? qc::hmul2_by<0>(a, f) : qc::hmul2_by<1>(a, f); };
+                        o[4 * j + 0] = by(qc::e2m1x2<0>(w[2 * half + j]));
+                        o[4 * j + 1] = by(qc::e2m1x2<1>(w[2 * half + j]));
+                        o[4 * j + 2] = by(qc::e2m1x2<2>(w[2 * half + j]));
+                        o[4 * j + 3] = by(qc::e2m1x2<3>(w[2 * half + j]));
                     }
-                    ptx::tmem_st16(to + (uint32_t)(half * 16), o);
+                    ptx::tmem_st8(to + (uint32_t)(half * 8), o);
                 }
             }
             ptx::tmem_wait_st();
             ptx::tc_fence_before_sync();
             __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(L::B_KFULL + buf));
+            if (quarter * 32 < D) {
+                // The scales of the warp's 2 channel blocks to fp16, pairs of keys: [page][block]
+                // [column % 4][column / 4], column 8 q + r being pair q + 4 r, a lane two of a
+                // page's 64.  Places of no key hold anything: their scale becomes 0 (their weight
+                // is 0, and 0 * NaN must not be formed).
+                const Note note = notes[g % NOTES];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = (e & 1) * 32 + lane, b = e & 1, q = i >> 3 & 3, r = i & 7, pair = q + 4 * r, pg = e >> 1;
+                    const int left = note.what >> pg & 1u ? note.left - pg * PAGE : 0;
+                    uint32_t two = lds_u16(raw + (uint32_t)(pg * L::PAGE_BYTES + PB::VS + (q * PB::NB + quarter * 2 + b) * 16 + 2 * r));
+                    two &= left > 2 * pair + 1 ? 0xFFFFu : left > 2 * pair ? 0xFFu : 0u;
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(factors + (uint32_t)(pg * 64 + b * 32 + (i & 3) * 8 + (i >> 2 & 7)) * 4), "r"(qc::e4m3x2(two)) : "memory");
+                }
+                __syncwarp();
+            }
+            if (before >= 0) ok = warp_wait(bar(L::B_VEMPTY + empty), turns, limit, abort_flag, 0x2500 + L::B_VEMPTY + empty);
+            if (!ok) break;
+            ptx::tc_fence_after_sync();
+            if (quarter * 32 < D) {
+                const uint32_t codes = raw + PB::VC + (uint32_t)(fourth * 4 * D + quarter * 32 + (lane >> 2) * 4);
+                const uint32_t mine = factors + (uint32_t)((lane >> 4) * 32 + fourth * 8) * 4;
+                const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + TM_V + (uint32_t)(buf * 64);
+#pragma unroll 1
+                for (int half = 0; half < 4; ++half) {  // columns 16 half + 4 e + fourth
+                    uint32_t w[4], low[8], high[8];
+                    const uint32_t at = codes + (uint32_t)((half >> 1) * L::PAGE_BYTES + (half & 1) * 2 * D);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = lds_u32(at + (uint32_t)((e / 2 + 16 * (e & 1)) * D));
+                    const uint4 f4 = lds128(mine + (uint32_t)((half >> 1) * 256 + (half & 1) * 16));
+                    const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        low[2 * e] = qc::hmul2(qc::e2m1x2<0>(w[e]), f[e]);
+                        low[2 * e + 1] = qc::hmul2(qc::e2m1x2<1>(w[e]), f[e]);
+                        high[2 * e] = qc::hmul2(qc::e2m1x2<2>(w[e]), f[e]);
+                        high[2 * e + 1] = qc::hmul2(qc::e2m1x2<3>(w[e]), f[e]);
+                    }
+                    ptx::tmem_st_16x128b_x4(to + (uint32_t)(half * 16), low);
+                    ptx::tmem_st_16x128b_x4(to + (16u << 16) + (uint32_t)(half * 16), high);
+                }
+                ptx::tmem_wait_st();
+            }
+            ptx::tc_fence_before_sync();
+            __syncwarp();
             if (lane == 0) {
                 ptx::mbar_arrive(bar(L::B_RAWEMPTY + st));
-                ptx::mbar_arrive(bar(L::B_KFULL + buf));
+                ptx::mbar_arrive(bar(L::B_VFULL + buf));
             }
         }
     } else {
@@ -1113,6 +1130,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
             // (All groups have read the others' references before any begins the next segment.)
             ptx::named_barrier_sync(NB_END + share, 128 * TURNS);
             if (quarter * 32 < D) {  // O^T: this thread's channel
+                const int ch = quarter * 32 + channel_of(lane);
 #pragma unroll 1
                 for (int c = 0; c < rows; c += 4) {
                     float v[4] = {};
@@ -1129,8 +1147,8 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         if (c + e >= rows) continue;
-                        if (!joined) part[qc::Partial<D, N>::o(c0 + out0 + c + e) + mine] = v[e];
-                        else if (mine < p.d) p.o[(at + c + e) * p.d + mine] = __float2bfloat16_rn(v[e]);
+                        if (!joined) part[qc::Partial<D, N>::o(c0 + out0 + c + e) + ch] = v[e];
+                        else if (ch < p.d) p.o[(at + c + e) * p.d + ch] = __float2bfloat16_rn(v[e]);
                     }
                 }
             }

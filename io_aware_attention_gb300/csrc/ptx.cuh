@@ -528,6 +528,17 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  : "memory");
 }
 
+// 16 columns of 16 TMEM lanes: thread t holds, of every 4 columns, column t % 4 in lanes
+// t / 4 (even registers) and t / 4 + 8 (odd ones).
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                     taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+                 : "memory");
+}
+
 // One / two TMEM columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v)
 {
