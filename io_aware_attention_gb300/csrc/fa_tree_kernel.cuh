@@ -10,8 +10,8 @@
 //   O^T += V^T P^T  M = D channels (TMEM lanes), N rows, K = 128 A = V^T from TMEM, B = P^T in shared memory
 //
 // K codes of one key are neighbours in a page, and V codes of one channel come as
-// pairs of keys, so a thread turns its key's (its channel's) codes into 16-bit
-// operands in registers and stores them to its own TMEM lane.  e2m1 * e4m3 is exact in
+// pairs of keys, so a thread turns a key's codes (a few channels' of some pairs) into
+// 16-bit operands in registers and stores them to TMEM lanes.  e2m1 * e4m3 is exact in
 // fp16.  The maximum over keys runs across TMEM lanes and threads, which is dear:
 // the reference of a row is kept until a score exceeds it by more than 2^RISE, which one
 // barrier with a reduction (128 threads) tells; only then is the maximum taken and
@@ -32,8 +32,10 @@
 //
 // Warps (1024 threads, one block an SM):
 //   0-15      softmax, four groups: a thread a key; at a segment's end they write its result.
-//   16-19     K: codes from shared memory to fp16 in TMEM, a thread a key.
-//   20-27     V: the same, a thread a channel of one page of the tile.
+//   16-27     codes: three sets that take tiles in turn, from shared memory to fp16 in TMEM,
+//             K a thread a key, then V.  (4 warps for K and 8 for V, every tile: V's, busy
+//             for 1100 cycles a tile, held up the rest; 16 rows x 8 x 32 heads x 16384 keys
+//             149 us, 139 with the sets.)
 //   28        pages from the cache into a ring (bulk copies), and what the other roles
 //             need to know of each tile.
 //   29, 30    the two products (an elected lane each); 29 also allocates TMEM.
