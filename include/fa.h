@@ -266,7 +266,8 @@ fa_status fa_cross_fwd(const void *q, const int64_t *q_strides, const void *k, c
                        void *workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /* Workspace of fa_cross_bwd: B*H*Nq' * (D + 2) floats, Nq' = Nq rounded up to a
- * multiple of 64, D the padded head size.  Needs no device. */
+ * multiple of 64, D the padded head size, and up to 40 MB more where keys are few and
+ * the queries of a key block are cut into parts.  Needs no device. */
 fa_status fa_cross_bwd_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, size_t *bytes);
 
 /*
@@ -479,6 +480,10 @@ fa_status fa_qcache_decode(const void *q, const void *pool, int64_t num_pages, c
  *   words     device pointer, uint64 (B, T).
  *   o, lse, scale, k_scale, v_scale, workspace  as for fa_qcache_decode (the bytes
  *             by fa_qcache_tree_workspace_bytes).
+ * Queries may be of any size, and a row that holds NaN or infinities (a padded
+ * draft's) leaves the others as they are.  With more than 8 rows a kv head (H / Hkv * T)
+ * a probability is rounded to fp16: o is off by at most 2^-11 * sum p |v| more than its
+ * rounding to bf16, where fa_qcache_decode's 22 bits do not show.
  * Results do not depend on timing.
  */
 fa_status fa_qcache_tree_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d, int64_t max_pages,
@@ -498,6 +503,7 @@ fa_status fa_qcache_tree(const void *q, const uint64_t *words, const void *pool,
  *             sequence or not above the one before ends it too and is reported by
  *             fa_check_device_status as FA_ERR_INVALID_ARG.
  *   lens_out  int32 (B), not lens itself: max(lens - T, 0) + the path's length.
+ * No two sequences of a call may hold drafts in one page.
  */
 fa_status fa_qcache_commit(void *pool, int64_t num_pages, const int32_t *table, int64_t max_pages, const int32_t *lens,
                            const int32_t *path, int64_t width, int32_t *lens_out, int64_t B, int64_t Hkv, int64_t T,
@@ -554,7 +560,8 @@ fa_status fa_qcache_evict(void *pool, int64_t num_pages, const int32_t *table, i
  * then incomplete), FA_ERR_CUDA if the copy or synchronisation failed or a
  * kernel refused to run (shared memory not 1024-byte aligned), FA_OK
  * otherwise; FA_ERR_INVALID_ARG if a cache call met a page or a length outside
- * its pool or page table (and skipped it).  `where`, if not NULL, receives the code of the first wait that
+ * its pool or page table (and skipped it), a cross-attention call a length beyond
+ * its keys, or fa_qcache_commit an entry of no path.  `where`, if not NULL, receives the code of the first wait that
  * gave up (0 if none).
  *
  * The status word is per device, not per stream: it collects the reports of
@@ -587,12 +594,13 @@ fa_status fa_set_wait_limit_ns(uint64_t ns);
 
 /*
  * fa_debug_skip_k_tile — test hook for the failure path.  With tile >= 0, the
- * first CTA of every later fa_fwd launch never loads its tile-th K tile, and
- * that of every later fa_bwd launch never loads the Q / dout tile of its
- * tile-th step (and the first warp of that of every later fa_qcache_decode or
- * fa_qcache_weights launch its tile-th page), so the MMA warp's wait for it runs out after the wait limit,
- * the kernel abandons its work and fa_check_device_status reports
- * FA_ERR_TIMEOUT; no fault, trap or hang is involved.  -1 (the default) turns
+ * first CTA of every later fa_fwd or fa_cross_fwd launch never loads its tile-th K
+ * tile, and that of every later fa_bwd or fa_cross_bwd launch never loads the Q /
+ * dout tile of its tile-th step (and the first warp of that of every later
+ * fa_qcache_decode, fa_qcache_weights or fa_qcache_tree launch its tile-th page, with
+ * more than 8 rows a kv head its tile-th two pages), so the MMA warp's wait for it
+ * runs out after the wait limit, the kernel abandons its work and
+ * fa_check_device_status reports FA_ERR_TIMEOUT; no fault, trap or hang is involved.  -1 (the default) turns
  * it off.  Outputs of a launch made with the hook on are incomplete.
  */
 fa_status fa_debug_skip_k_tile(int tile);

@@ -740,10 +740,30 @@ size_t cross_part_bytes(int64_t rows, int64_t splits, int64_t Dp)
     return splits > 1 ? (size_t)(rows * splits) * (size_t)(Dp + 1) * sizeof(float) : 0;
 }
 
-size_t cross_bwd_ws(int64_t B, int64_t H, int64_t Nq, int64_t d)
+// Parts that the query blocks of every key block are cut into, where key blocks alone
+// leave SMs idle.  An item costs its query blocks and about three more, one more where it
+// leaves a part, and joining the parts about two.  (By GB300's 152 SMs, so that the
+// workspace's size needs no device.)  4096 queries of 8 heads against 77 keys of one
+// kv head, d64: 711 us whole, 59 in parts; 8 heads x 2 sequences with keys of their own 106
+// and 36; 32 heads x 2000 queries against 8 kv heads x 500 keys, d128, 214 and 87.
+int64_t cross_bwd_parts(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk)
 {
-    const int64_t np = (Nq + fa::bwd::BQ - 1) / fa::bwd::BQ * fa::bwd::BQ;
-    return (size_t)(B * H * np) * (size_t)(padded_head_size(d) + 2) * sizeof(float);
+    constexpr int64_t SMS = 152;
+    const int64_t items = B * Hkv * ((Nk + fa::bwd::BKV - 1) / fa::bwd::BKV);
+    const int64_t blocks = (H / Hkv * Nq + fa::bwd::BQ - 1) / fa::bwd::BQ;
+    int64_t best = 1, least = 0;
+    for (int64_t s = 1; s <= blocks && (s == 1 || items * s <= 2 * SMS); ++s) {
+        const int64_t cost = (items * s + SMS - 1) / SMS * ((blocks + s - 1) / s + 3 + (s > 1)) + (s > 1 ? 2 : 0);
+        if (s == 1 || cost < least) best = s, least = cost;
+    }
+    return best;
+}
+
+size_t cross_bwd_ws(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d)
+{
+    const int64_t np = (Nq + fa::bwd::BQ - 1) / fa::bwd::BQ * fa::bwd::BQ, Dp = padded_head_size(d);
+    const int64_t parts = cross_bwd_parts(B, H, Hkv, Nq, Nk);
+    return ((size_t)(B * H * np) * (size_t)(Dp + 2) + (parts > 1 ? (size_t)(2 * parts * B * Hkv * Nk) * (size_t)Dp : 0)) * sizeof(float);
 }
 
 fa::cross::Rows rows_of(const View& v) { return {v.s[0], v.s[1], v.s[2], (int)v.H, (int)v.N}; }
@@ -1327,7 +1347,7 @@ fa_status fa_cross_bwd_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_
     if (!bytes) return FA_ERR_INVALID_ARG;
     const fa_status cs = cross_check(B, H, Hkv, Nq, Nk, d);
     if (cs != FA_OK) return cs;
-    *bytes = cross_bwd_ws(B, H, Nq, d);
+    *bytes = cross_bwd_ws(B, H, Hkv, Nq, Nk, d);
     return FA_OK;
 }
 
@@ -1353,7 +1373,7 @@ fa_status fa_cross_bwd(const void* q, const int64_t* q_strides, const void* k, c
     if (((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(lens)) & 3u) != 0 ||
         (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
         return FA_ERR_UNSUPPORTED;
-    const size_t need = cross_bwd_ws(B, H, Nq, d);
+    const size_t need = cross_bwd_ws(B, H, Hkv, Nq, Nk, d);
     if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
     // Outputs and the workspace may share no place with an input or one another
     // (dk and dv may be views of one buffer).
@@ -1388,6 +1408,8 @@ fa_status fa_cross_bwd(const void* q, const int64_t* q_strides, const void* k, c
     float* const lse2 = static_cast<float*>(workspace);
     float* const dsum = lse2 + rows;
     float* const acc = dsum + rows;
+    const int64_t parts = cross_bwd_parts(B, H, Hkv, Nq, Nk);
+    float* const part = acc + rows * Dp;
     fa::bwd::CrossParams p = {};
     CUtensorMap mq, mk, mv, mdo, mdq;
     if (!view_map(&mq, &p.x.q_h, &p.x.q_b, w[Q], B, d, fa::bwd::BQ) || !view_map(&mk, &p.x.k_h, &p.x.k_b, w[K], B, d, fa::bwd::BKV) ||
@@ -1424,20 +1446,25 @@ fa_status fa_cross_bwd(const void* q, const int64_t* q_strides, const void* k, c
     p.x.group = (int)group;
     p.x.nk = (int)Nk;
     p.x.q_blocks = (int)(np / fa::bwd::BQ);
+    p.x.part = part;
+    p.x.parts = (int)parts;
+    p.x.all = (int)B;
     for (int64_t b0 = 0; b0 < B; b0 += fa::MAX_SEQS) {
         p.x.b0 = (int)b0;
         p.x.nb = (int)std::min<int64_t>(B - b0, fa::MAX_SEQS);
-        const int64_t items = p.x.nb * Hkv * ((Nk + fa::bwd::BKV - 1) / fa::bwd::BKV);
+        const int64_t items = p.x.nb * Hkv * ((Nk + fa::bwd::BKV - 1) / fa::bwd::BKV) * parts;
         const unsigned grid = (unsigned)std::min<int64_t>(items, info.sms);
         const fa_status ms = Dp == 128 ? launch_cross_bwd<128>(mq, mk, mv, mdo, mdq, p, grid, dev, st)
                                        : launch_cross_bwd<64>(mq, mk, mv, mdo, mdq, p, grid, dev, st);
         if (ms != FA_OK) return ms;
     }
 
-    // 3. dQ = scale * accumulator, bf16.
-    const int64_t n8 = B * H * Nq * (d / 8);
-    fa::cross::fa_cross_dq_kernel<<<(unsigned)((n8 + fa::cross::THREADS - 1) / fa::cross::THREADS), fa::cross::THREADS, 0, st>>>(
-        acc, static_cast<__nv_bfloat16*>(dq), rows_of(w[DQ]), (int)np, (int)d, (int)Dp, n8, scale);
+    // 3. dQ = scale * accumulator, bf16, and the parts of dK and dV joined.
+    const int64_t n8 = B * H * Nq * (d / 8), kv_rows = B * Hkv * Nk, all8 = n8 + (parts > 1 ? 2 * kv_rows * (d / 8) : 0);
+    const fa::cross::Parts join = {part, (int)parts, kv_rows, p.dv, p.dk, rows_of(w[DV]), rows_of(w[DK]), lens};
+    auto* const finish = parts > 1 ? fa::cross::fa_cross_dq_kernel<true> : fa::cross::fa_cross_dq_kernel<false>;
+    finish<<<(unsigned)((all8 + fa::cross::THREADS - 1) / fa::cross::THREADS), fa::cross::THREADS, 0, st>>>(
+        acc, static_cast<__nv_bfloat16*>(dq), rows_of(w[DQ]), (int)np, (int)d, (int)Dp, n8, scale, join);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -141,6 +141,8 @@ struct Cross {
     int b0, nb;                                     // the launch's sequences, at most MAX_SEQS
     int heads, kv_heads, group, nk, q_blocks;       // q_blocks: query blocks of a head
     int q_b, q_h, k_b, k_h, v_b, v_h, do_b, do_h;   // 0 where a view repeats (its map has one of them), else 1
+    float* part;                                    // parts > 1: sums of dV, then of dK, [part][b][kv head][key][D]
+    int parts, all;                                 // that the query blocks of an item are cut into; B of the call
 };
 
 struct Params {
@@ -206,13 +208,25 @@ struct Layout {
 // the query blocks from the diagonal on, so every pair costs about the same.
 struct Item {
     int bh, key0, m0, nq;  // first key, first query block, query blocks
-    int b, kvh, len;       // CROSS (bh: the group's first head, nq: blocks of the whole group)
+    int b, kvh, len, part; // CROSS (bh: the group's first head, whose blocks m0 and nq count through)
 };
 
-// CROSS item i of those with keys: sequences in order, then kv heads, then key blocks.
+// CROSS item i of those with keys: sequences in order, then kv heads, then key blocks,
+// then the parts of their query blocks.
 __device__ __forceinline__ Item cross_item(int i, const CrossParams& p, const int* len, const int* prefix)
 {
     const Cross& x = p.x;
+    Item it;
+    it.part = 0;
+    it.m0 = 0;
+    it.nq = x.group * x.q_blocks;
+    if (x.parts > 1) {
+        const int64_t all = it.nq;
+        it.part = i % x.parts;
+        i /= x.parts;
+        it.m0 = (int)(all * it.part / x.parts);
+        it.nq = (int)(all * (it.part + 1) / x.parts) - it.m0;
+    }
     const int y = i / x.kv_heads;
     int lo = 0, hi = x.nb;  // prefix[lo] <= y < prefix[hi]
     while (hi - lo > 1) {
@@ -221,14 +235,11 @@ __device__ __forceinline__ Item cross_item(int i, const CrossParams& p, const in
         else hi = mid;
     }
     const int blocks = prefix[lo + 1] - prefix[lo], rem = i - prefix[lo] * x.kv_heads;
-    Item it;
     it.b = x.b0 + lo;
     it.kvh = rem / blocks;
     it.key0 = (rem - it.kvh * blocks) * BKV;
     it.len = len[lo];
     it.bh = it.b * x.heads + it.kvh * x.group;
-    it.m0 = 0;
-    it.nq = x.group * x.q_blocks;
     return it;
 }
 
@@ -334,7 +345,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem = misc[0];
-    if constexpr (CROSS) num_items = seq_prefix[p.x.nb] * p.x.kv_heads;
+    if constexpr (CROSS) num_items = seq_prefix[p.x.nb] * p.x.kv_heads * p.x.parts;
 
     if (warp == WARP_TMA) {
         // ---------------------------------------------------- TMA producer
@@ -367,7 +378,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 // Test hook: the first CTA leaves one step's tile unloaded, so
                 // the issuer's wait for it runs out (exercises the abort path).
                 if (ptx::elect_one() && !(g == p.debug_skip_q && blockIdx.x == 0)) {
-                    const int head = CROSS ? t / p.x.q_blocks : 0;  // of the group
+                    const int head = CROSS ? (it.m0 + t) / p.x.q_blocks : 0;  // of the group
                     const int q0 = (it.m0 + t - (CROSS ? head * p.x.q_blocks : 0)) * BQ;
                     const int h = CROSS ? it.kvh * p.x.group + head : 0;
                     const uint32_t fb = bar(L::B_QFULL + s);
@@ -532,9 +543,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int g = 0, k = 0;
         bool ok = true;
         if constexpr (CROSS) {
-            // Key blocks without a key: zero gradients.
+            // Key blocks without a key: zero gradients (where parts are joined, that writes them).
             const int all = (p.x.nk + BKV - 1) / BKV, t = (int)threadIdx.x - 32 * WARP_DQ0;
-            for (int64_t u = blockIdx.x; u < (int64_t)p.x.nb * p.x.kv_heads * all; u += gridDim.x) {
+            for (int64_t u = blockIdx.x; p.x.parts == 1 && u < (int64_t)p.x.nb * p.x.kv_heads * all; u += gridDim.x) {
                 const int sh = (int)(u / all), kb = (int)(u - (int64_t)sh * all);
                 const int s = sh / p.x.kv_heads, h = sh - s * p.x.kv_heads;
                 if (kb * BKV < seq_len[s]) continue;
@@ -577,7 +588,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (lane == 0) {
                         // (CROSS: the rows of all heads as one run; a group's heads adjoin.)
                         if constexpr (CROSS)
-                            ptx::tma_reduce_add_3d(&tm_dq, stg, quarter * 32, it.bh * p.Np + t * BQ, 0);
+                            ptx::tma_reduce_add_3d(&tm_dq, stg, quarter * 32, it.bh * p.Np + (it.m0 + t) * BQ, 0);
                         else
                             ptx::tma_reduce_add_3d(&tm_dq, stg, quarter * 32, (it.m0 + t) * BQ, it.bh);
                         ptx::tma_store_commit();
@@ -605,6 +616,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         uint32_t o[32];
                         ptx::tmem_ld32(tmem + lane_off + (which ? TM_DK : TM_DV) + ch * 32, o);
                         ptx::tmem_wait_ld(o);
+                        if constexpr (CROSS) {
+                            if (p.x.parts > 1) {
+                                float* const to = p.x.part + ((((int64_t)(which * p.x.parts + it.part) * p.x.all + it.b) * p.x.kv_heads +
+                                                               it.kvh) * p.x.nk + key) * D + ch * 32;
+                                if (key < it.len) {
+#pragma unroll
+                                    for (int u = 0; u < 8; ++u)
+                                        ptx::st_global_v4(to + u * 4, o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                                }
+                                continue;
+                            }
+                        }
                         uint32_t w[16];
 #pragma unroll
                         for (int c = 0; c < 16; ++c)

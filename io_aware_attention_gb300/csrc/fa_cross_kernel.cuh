@@ -4,7 +4,7 @@
 //
 //   fa_cross_combine_kernel  joins the parts of a forward whose key range was split;
 //   fa_cross_prep_kernel     D_i = dO_i . O_i, L_i log2 e and the zeroed dQ sums;
-//   fa_cross_dq_kernel       dQ = bf16(scale * sums).
+//   fa_cross_dq_kernel       dQ = bf16(scale * sums), and dK, dV where their sums came in parts.
 //
 // The latter two are the backward's, over views of any strides.
 #pragma once
@@ -136,21 +136,55 @@ __global__ void __launch_bounds__(THREADS, 4)
     for (int k = lane; k < PER * dp / 4; k += 32) z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-// As fa_bwd_dq_kernel, over a view: 8 elements a thread.
+// Where the query blocks of a key block were cut into parts: their sums of dV and dK.
+struct Parts {
+    const float* part;  // dV, then dK: [part][b][kv head][key][dp]
+    int parts;          // 1: none
+    int64_t rows;       // b, kv head, key
+    __nv_bfloat16 *dv, *dk;
+    Rows vv, kv;
+    const int32_t* lens;
+};
+
+// 8 elements a thread: those at src, times mul, to dst.
+__device__ __forceinline__ void put8(__nv_bfloat16* dst, const float4 a, const float4 b, float mul)
+{
+    ptx::st_global_v4(dst, ptx::pack_bf16x2(a.x * mul, a.y * mul), ptx::pack_bf16x2(a.z * mul, a.w * mul),
+                      ptx::pack_bf16x2(b.x * mul, b.y * mul), ptx::pack_bf16x2(b.z * mul, b.w * mul));
+}
+
+// As fa_bwd_dq_kernel, over a view.  With PARTS, dV's and dK's elements come behind
+// dQ's: their parts are joined (in order, so that results repeat); rows behind the last
+// key are zero.
+template <bool PARTS>
 __global__ void __launch_bounds__(THREADS)
     fa_cross_dq_kernel(const float* __restrict__ dq_acc, __nv_bfloat16* __restrict__ dq, const Rows view, int np, int d,
-                       int dp, int64_t n8, float scale)
+                       int dp, int64_t n8, float scale, const Parts x)
 {
-    const int64_t e8 = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-    if (e8 >= n8) return;
-    const int64_t row = e8 / (d / 8);
-    const int col = (int)(e8 - row * (d / 8)) * 8;
-    const int64_t bh = row / view.n;
-    const float4* const src = reinterpret_cast<const float4*>(dq_acc + (bh * np + (row - bh * view.n)) * dp + col);
-    const float4 a = src[0], b = src[1];
-    ptx::st_global_v4(dq + view.at(row) + col, ptx::pack_bf16x2(a.x * scale, a.y * scale),
-                      ptx::pack_bf16x2(a.z * scale, a.w * scale), ptx::pack_bf16x2(b.x * scale, b.y * scale),
-                      ptx::pack_bf16x2(b.z * scale, b.w * scale));
+    int64_t e8 = (int64_t)blockIdx.x * THREADS + threadIdx.x;
+    if (e8 < n8) {
+        const int64_t row = e8 / (d / 8);
+        const int col = (int)(e8 - row * (d / 8)) * 8;
+        const int64_t bh = row / view.n;
+        const float4* const src = reinterpret_cast<const float4*>(dq_acc + (bh * np + (row - bh * view.n)) * dp + col);
+        put8(dq + view.at(row) + col, src[0], src[1], scale);
+    } else if (PARTS) {
+        e8 -= n8;
+        const int64_t line = e8 / (d / 8), which = line / x.rows, row = line - which * x.rows;
+        if (which > 1) return;
+        const int col = (int)(e8 - line * (d / 8)) * 8;
+        const int64_t b = row / ((int64_t)x.kv.n * x.kv.heads), key = row % x.kv.n, step = x.rows * dp;
+        const float* const src = x.part + which * x.parts * step + row * dp + col;
+        const int parts = key < cross_length(x.lens, (int)b, x.kv.n) ? x.parts : 0;
+        float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+            const float4 u = *reinterpret_cast<const float4*>(src + s * step), v = *reinterpret_cast<const float4*>(src + s * step + 4);
+            lo.x += u.x, lo.y += u.y, lo.z += u.z, lo.w += u.w;
+            hi.x += v.x, hi.y += v.y, hi.z += v.z, hi.w += v.w;
+        }
+        put8((which ? x.dk + x.kv.at(row) : x.dv + x.vv.at(row)) + col, lo, hi, which ? scale : 1.0f);
+    }
 }
 
 }  // namespace cross

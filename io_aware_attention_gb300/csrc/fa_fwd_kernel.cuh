@@ -505,8 +505,12 @@ __device__ __forceinline__ Item cross_item(int i, const CrossParams& p, const in
     it.bh = it.b * x.heads + it.h;
     it.len = len[s];
     const int tiles = (it.len + BN - 1) / BN;
-    it.j0 = (int)((int64_t)tiles * it.split / x.splits);
-    it.n_kv = (int)((int64_t)tiles * (it.split + 1) / x.splits) - it.j0;
+    it.j0 = 0;
+    it.n_kv = tiles;
+    if (x.splits > 1) {  // (at most 2^16 tiles, 128 splits)
+        it.j0 = tiles * it.split / x.splits;
+        it.n_kv = tiles * (it.split + 1) / x.splits - it.j0;
+    }
     return it;
 }
 

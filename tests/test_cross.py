@@ -84,6 +84,20 @@ def test_split_keys(d, B, H, Hkv, Nq, Nk, lens):
     compare(*args, lens, run_all(*args, lens))
 
 
+# Many queries against few keys: the query blocks of a key block are cut into parts.
+@pytest.mark.parametrize("d", [64, 128, 40])
+@pytest.mark.parametrize("B, H, Hkv, Nq, Nk, lens", [
+    (1, 1, 1, 2000, 1, None), (1, 8, 1, 300, 77, [70]), (2, 6, 2, 700, 200, [200, 5]), (3, 4, 4, 513, 130, [0, 129, 128]),
+    (2, 14, 2, 111, 90, [0, 0])])
+def test_queries_in_parts(d, B, H, Hkv, Nq, Nk, lens):
+    args = draw(B, H, Hkv, Nq, Nk, d, lens, Nq + d)
+    rows = B * H * -(-Nq // 64) * 64
+    assert fa.cross_bwd_workspace_bytes(B, H, Hkv, Nq, Nk, d) > rows * ((64 if d <= 64 else 128) + 2) * 4
+    compare(*args, lens, run_all(*args, lens))
+    apart = (args[0].transpose(1, 2).contiguous().transpose(1, 2), *args[1:])  # heads that do not run as one
+    compare(*args, lens, run_all(*apart, lens))
+
+
 def test_more_sequences_than_a_launch_holds():
     B = 600
     lens = [(7 * b) % 41 for b in range(B)]
