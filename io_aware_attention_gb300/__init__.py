@@ -58,6 +58,18 @@ attention.  positions, integers (B, 1), counts the tokens of the text and lens
 the keys that the cache holds: they part at the first eviction, after which kept
 keys still stand, turned, where they were produced.
 
+    words, depths = io_aware_attention_gb300.tree_words(parents)
+    q, k = io_aware_attention_gb300.rope(q, k, freqs, positions=positions + depths, factor=factor)
+    lens += T
+    io_aware_attention_gb300.qcache_append(k, v, pool, table, lens)
+    o, lse = io_aware_attention_gb300.qcache_tree(q, words, pool, table, lens)
+    lens = io_aware_attention_gb300.qcache_commit(pool, table, lens, path, T)
+    positions += (path >= 0).sum(1, keepdim=True)
+
+verifies a tree of T drafted tokens at once (parents (B, T): the draft that each
+follows, -1 for the last token) and keeps those of the accepted path (path int32
+(B, A), rising, -1 after the last).
+
 The ``*_into`` forms write into caller-provided tensors; their shapes, dtypes
 and devices are checked here, because the C ABI sees only pointers and sizes.
 Work is enqueued on ``stream``, by default the current stream, of the current
