@@ -135,6 +135,31 @@ def test_any_set_of_drafts(T):
 
 
 @gpu
+@pytest.mark.parametrize("T, H", [(7, 2), (40, 4)])
+def test_padded_drafts_hold_anything(T, H):
+    """Drafts that no word names: their keys, values and queries reach no other row."""
+    B, d, n = 2, 64, 90
+    words, real = trees(B, T, 13), T - 3
+    words[:, real:] = 0
+    q, k, v = rand((B, H, T, d), 14), rand((B, 2, n, d), 15), rand((B, 2, n, d), 16)
+    pool, table = fa.qcache_pool(6, 2, d), torch.arange(6, dtype=torch.int32, device="cuda").reshape(B, 3).contiguous()
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    fa.qcache_append(k.cuda(), v.cuda(), pool, table, lens)
+    want = fa.qcache_tree(q.cuda(), words.cuda(), pool, table, lens)
+    for i, x in enumerate((float("nan"), float("inf"), -3e38)):
+        k[:, :, n - 3 + i], v[:, :, n - 3 + i], q[:, :, real + i] = x, x, x
+    fa.qcache_append(k.cuda(), v.cuda(), pool, table, lens)
+    got = fa.qcache_tree(q.cuda(), words.cuda(), pool, table, lens)
+    torch.cuda.synchronize()
+    assert fa.check_device_status() == 0
+    assert torch.isfinite(want[0]).all()
+    for a, b in zip(got, want):
+        # (The rows may be scaled by powers of two of their own, which changes no rounding of
+        # queries above 2^-31 of the largest: all of them.)
+        assert torch.equal(a[:, :, :real], b[:, :, :real])
+
+
+@gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("Nq", [1, 4, 8])
 def test_a_chain_is_causal_decode(Nq, d):
