@@ -891,6 +891,9 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
         const uint32_t s_cols = tmem + lane_off + TM_S + (uint32_t)(turn * N + c0);
         const uint32_t o_cols = tmem + lane_off + L::TM_O + (uint32_t)(turn * N + c0);
         const int t = (int)threadIdx.x & 127;  // thread of the group
+        // The first of its pieces of a row of P^T; the others differ in the bits that e8 has
+        // (c0 / 8 is a multiple of NC / 8, a row starts on 128 bytes).
+        const uint32_t p_row = sbase + L::OFF_P + (uint32_t)(c0 >> 6) * L::PBLK + (uint32_t)mine * 128 + (uint32_t)((((c0 >> 3) & 7) ^ (mine & 7)) * 16);
         bool ok = warp_wait(bar(L::B_QRAW), 0, limit, abort_flag, 0x2700 + L::B_QRAW);
         {
             const QueryRows<D, N> rows{sbase + L::OFF_Q, sbase + L::OFF_LARGEST, warp, SOFTMAX_WARPS};
@@ -1055,7 +1058,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 if (lane == 0) ptx::mbar_arrive(bar(L::B_SREAD + sb));
                 // P^T: a row of 128 bytes a key (64 query rows), 16-byte pieces swizzled.
                 if (ok) ok = warp_wait(bar(L::B_PDONE + ps), ((uint32_t)(g / L::PBUFS) & 1u) ^ 1u, limit, abort_flag, 0x2700 + L::B_PDONE + ps);
-                const uint32_t row = sbase + L::OFF_P + (uint32_t)pb * L::P_BYTES + (uint32_t)mine * 128;
+                const uint32_t row = p_row + (uint32_t)pb * L::P_BYTES;
 #pragma unroll
                 for (int e8 = 0; e8 < NC / 8; ++e8) {
                     uint32_t w[4];
@@ -1066,8 +1069,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                         l[c / 2] = ptx::f2_add(l[c / 2], ptx::f2_pack(a, b2));
                         w[e] = qc::pack_h2(a, b2);
                     }
-                    const int piece = c0 / 8 + e8;
-                    ptx::st_shared_v4(row + (uint32_t)(piece >> 3) * L::PBLK + (uint32_t)(((piece & 7) ^ (mine & 7)) * 16), w[0], w[1], w[2], w[3]);
+                    ptx::st_shared_v4(row ^ (uint32_t)(e8 * 16), w[0], w[1], w[2], w[3]);
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before_sync();
