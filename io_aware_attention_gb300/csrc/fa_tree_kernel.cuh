@@ -627,8 +627,8 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                         }
                     }
                     const int id0 = __shfl_sync(0xffffffffu, id, 2 * (i % 16)), id1 = __shfl_sync(0xffffffffu, id, 2 * (i % 16) + 1);
-                    const int st = g % L::RAW_STAGES;
-                    if (!(ok = warp_wait(bar(L::B_RAWEMPTY + st), ((uint32_t)(g / L::RAW_STAGES) & 1u) ^ 1u, limit, abort_flag,
+                    const int st = (int)((uint32_t)g % L::RAW_STAGES);
+                    if (!(ok = warp_wait(bar(L::B_RAWEMPTY + st), ((uint32_t)g / L::RAW_STAGES & 1u) ^ 1u, limit, abort_flag,
                                          0x2100 + L::B_RAWEMPTY + st)))
                         break;
                     if (ptx::elect_one()) {
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                         note.what = (id0 >= 0 ? Note::PAGE0 : 0u) | (id1 >= 0 ? Note::PAGE1 : 0u) | (i == 0 ? Note::FIRST : 0u) |
                                     (i == n - 1 ? Note::LAST : 0u) | (uint32_t)min(i, 15) << Note::INDEX;
                         note.left = len - (tile0 + i) * TILE;
-                        notes[g % NOTES] = note;
+                        notes[(uint32_t)g % NOTES] = note;
                         const uint32_t fb = bar(L::B_RAWFULL + st), dst = sbase + L::OFF_RAW + st * L::RAW_BYTES;
                         ptx::mbar_arrive_expect_tx(fb, ((id0 >= 0) + (id1 >= 0)) * L::PAGE_BYTES);
                         if (!(g == p.debug_skip && blockIdx.x == 0)) {
@@ -664,9 +664,9 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
             bool ok = true;
 #pragma unroll 1
             for (int g = 0; ok && g < n_tiles; ++g) {
-                const int kb = g & 1, turn = g % TURNS;
+                const int kb = g & 1, turn = (int)((uint32_t)g % TURNS);
                 ok = warp_wait(bar(L::B_KFULL + kb), (uint32_t)(g >> 1) & 1u, limit, abort_flag, 0x2200 + L::B_KFULL + kb);
-                const uint32_t what = (uint32_t)uniform((int)notes[g % NOTES].what);
+                const uint32_t what = (uint32_t)uniform((int)notes[(uint32_t)g % NOTES].what);
                 const int qb = k & 1;
                 if ((what & Note::FIRST) && ok)
                     ok = warp_wait(bar(L::B_QFULL + qb), (uint32_t)(k >> 1) & 1u, limit, abort_flag, 0x2200 + L::B_QFULL + qb);
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
 #pragma unroll 1
                 for (int st = 0; st < STREAMS; ++st) {
                     const int sb = STREAMS > 1 ? st : turn;
-                    if (ok) ok = warp_wait(bar(L::B_SREAD + sb), ((uint32_t)(g / TURNS) & 1u) ^ 1u, limit, abort_flag, 0x2200 + L::B_SREAD + sb);
+                    if (ok) ok = warp_wait(bar(L::B_SREAD + sb), ((uint32_t)g / TURNS & 1u) ^ 1u, limit, abort_flag, 0x2200 + L::B_SREAD + sb);
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
                     const uint64_t q_rows = q_at + (uint64_t)(((uint32_t)st * L::NM * 128) >> 4);
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 }
                 if (!ok) break;
                 if (ptx::elect_one()) {
-                    ptx::tc_commit(bar(L::B_KEMPTY + g % L::EMPTIES));
+                    ptx::tc_commit(bar(L::B_KEMPTY + (int)((uint32_t)g % L::EMPTIES)));
                     if (what & Note::LAST) ptx::tc_commit(bar(L::B_QEMPTY + qb));
                 }
                 if (what & Note::LAST) ++k;
@@ -702,9 +702,9 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
             bool ok = true;
 #pragma unroll 1
             for (int g = 0; ok && g < n_tiles; ++g) {
-                const int vb = g & 1, pb = g % L::PBUFS;
+                const int vb = g & 1, pb = (int)((uint32_t)g % L::PBUFS);
                 ok = warp_wait(bar(L::B_VFULL + vb), (uint32_t)(g >> 1) & 1u, limit, abort_flag, 0x2300 + L::B_VFULL + vb);
-                const uint32_t what = (uint32_t)uniform((int)notes[g % NOTES].what);
+                const uint32_t what = (uint32_t)uniform((int)notes[(uint32_t)g % NOTES].what);
                 // A segment's first products overwrite O^T: what was there has been read.
                 if ((what & Note::FIRST) && ok)
                     ok = warp_wait(bar(L::B_OFREE), (uint32_t)(k & 1) ^ 1u, limit, abort_flag, 0x2300 + L::B_OFREE);
@@ -712,19 +712,19 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
 #pragma unroll 1
                 for (int st = 0; st < STREAMS; ++st) {
                     const int ps = st * L::PBUFS + pb;
-                    if (ok) ok = warp_wait(bar(L::B_PFULL + ps), (uint32_t)(g / L::PBUFS) & 1u, limit, abort_flag, 0x2300 + L::B_PFULL + ps);
+                    if (ok) ok = warp_wait(bar(L::B_PFULL + ps), (uint32_t)g / L::PBUFS & 1u, limit, abort_flag, 0x2300 + L::B_PFULL + ps);
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
                     const uint64_t p_at = p_desc + (uint64_t)(((uint32_t)pb * L::P_BYTES + (uint32_t)st * L::PBLK) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < TILE / 16; ++kk)
                         if (ptx::elect_one())
-                            ptx::mma_ts(tmem + L::TM_O + (uint32_t)(g % TURNS * N + st * L::NM), tmem + TM_V + (uint32_t)(vb * 64 + kk * 8),
+                            ptx::mma_ts(tmem + L::TM_O + ((uint32_t)g % TURNS * N + (uint32_t)(st * L::NM)), tmem + TM_V + (uint32_t)(vb * 64 + kk * 8),
                                         p_at + (uint64_t)(((uint32_t)kk * 2048) >> 4), ID, kk > 0 ? 1u : keep);
                     if (ptx::elect_one()) ptx::tc_commit(bar(L::B_PDONE + ps));
                 }
                 if (!ok) break;
-                if (ptx::elect_one()) ptx::tc_commit(bar(L::B_VEMPTY + g % L::EMPTIES));
+                if (ptx::elect_one()) ptx::tc_commit(bar(L::B_VEMPTY + (int)((uint32_t)g % L::EMPTIES)));
                 if (what & Note::LAST) ++k;
             }
             if (ptx::elect_one()) ptx::tc_commit(bar(L::B_DRAIN + 1));
@@ -778,11 +778,12 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
         const uint32_t factors = sbase + L::OFF_FACTORS + (uint32_t)(warp - WARP_CODES) * 512;
         bool ok = true;
 #pragma unroll 1
-        for (int g = set; ok && g < n_tiles; g += SETS) {
-            const int st = g % L::RAW_STAGES, buf = g & 1;
-            ok = warp_wait(bar(L::B_RAWFULL + st), (uint32_t)(g / L::RAW_STAGES) & 1u, limit, abort_flag, 0x2500 + L::B_RAWFULL + st);
-            const int before = g - 2, empty = (g + L::EMPTIES - 2) % L::EMPTIES;
-            const uint32_t turns = (uint32_t)(before / L::EMPTIES) & 1u;
+        for (int g = set, turn = 0; ok && g < n_tiles; g += SETS, ++turn) {  // (g = set + SETS * turn)
+            constexpr int OWN = L::RAW_STAGES / SETS;  // stages of a set, 1 or 2
+            const int st = set + SETS * (turn & (OWN - 1)), buf = g & 1;
+            ok = warp_wait(bar(L::B_RAWFULL + st), (uint32_t)turn / OWN & 1u, limit, abort_flag, 0x2500 + L::B_RAWFULL + st);
+            const int before = g - 2;
+            const uint32_t empty = (uint32_t)max(before, 0) % L::EMPTIES, turns = (uint32_t)max(before, 0) / L::EMPTIES & 1u;
             if (ok && before >= 0) ok = warp_wait(bar(L::B_KEMPTY + empty), turns, limit, abort_flag, 0x2500 + L::B_KEMPTY + empty);
             if (!ok) break;
             ptx::tc_fence_after_sync();
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 // [column % 4][column / 4], column 8 q + r being pair q + 4 r, a lane two of a
                 // page's 64.  Places of no key hold anything: their scale becomes 0 (their weight
                 // is 0, and 0 * NaN must not be formed).
-                const Note note = notes[g % NOTES];
+                const Note note = notes[(uint32_t)g % NOTES];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = (e & 1) * 32 + lane, b = e & 1, q = i >> 3 & 3, r = i & 7, pair = q + 4 * r, pg = e >> 1;
@@ -938,15 +939,16 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
             int last = -1;  // the group's last tile of the segment
 #pragma unroll 1
             for (int g = g0 + (turn + TURNS - g0 % TURNS) % TURNS; g < g0 + n; g += TURNS) {
-                const int pb = g % L::PBUFS, ps = stream * L::PBUFS + pb;
-                if (ok) ok = warp_wait(bar(L::B_SFULL + sb), (uint32_t)(g / TURNS) & 1u, limit, abort_flag, 0x2700 + L::B_SFULL + sb);
+                static_assert(L::PBUFS == (TURNS > 1 ? TURNS : 2), "a group that takes tiles in turn has a buffer of its own");
+                const int pb = TURNS > 1 ? turn : g & 1, ps = stream * L::PBUFS + pb;
+                if (ok) ok = warp_wait(bar(L::B_SFULL + sb), (uint32_t)g / TURNS & 1u, limit, abort_flag, 0x2700 + L::B_SFULL + sb);
                 ptx::tc_fence_after_sync();
                 const int key0 = (tile0 + g - g0) * TILE;
                 // y = score - reference + SHIFT in base-2 units.
                 uint32_t y[NC];
                 float red;  // the largest score of this thread's key
                 load_cols_max<NC>(s_cols, y, red);
-                const uint32_t what = notes[g % NOTES].what;
+                const uint32_t what = notes[(uint32_t)g % NOTES].what;
                 load_cols_end<NC>(y);
                 asm volatile("" : "+f"(red));
                 if (__builtin_expect((what & 3u) != 3u || key0 + TILE > min(len, draft0) || apart, 0)) {
@@ -1057,7 +1059,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(L::B_SREAD + sb));
                 // P^T: a row of 128 bytes a key (64 query rows), 16-byte pieces swizzled.
-                if (ok) ok = warp_wait(bar(L::B_PDONE + ps), ((uint32_t)(g / L::PBUFS) & 1u) ^ 1u, limit, abort_flag, 0x2700 + L::B_PDONE + ps);
+                if (ok) ok = warp_wait(bar(L::B_PDONE + ps), ((uint32_t)g / L::PBUFS & 1u) ^ 1u, limit, abort_flag, 0x2700 + L::B_PDONE + ps);
                 const uint32_t row = p_row + (uint32_t)pb * L::P_BYTES;
 #pragma unroll
                 for (int e8 = 0; e8 < NC / 8; ++e8) {
