@@ -947,66 +947,70 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                 // y = score - reference + SHIFT in base-2 units.
                 uint32_t y[NC];
                 float red;  // the largest score of this thread's key
-                load_cols_max<NC>(s_cols, y, red);
-                const uint32_t what = notes[(uint32_t)g % NOTES].what;
-                load_cols_end<NC>(y);
-                asm volatile("" : "+f"(red));
-                if (__builtin_expect((what & 3u) != 3u || key0 + TILE > min(len, draft0) || apart, 0)) {
-                    // Rows that do not see this thread's key: -inf in S^T itself; rows with a
-                    // power of their own: the common one (in two steps, each a power of two that exists).
-                    const int key = key0 + (quarter >> 1) * PAGE + key_of(mine % PAGE), bit = key - draft0;
-                    const bool there = key < len && (what >> (quarter >> 1) & 1u), named = bit >= 0;
-                    const uint64_t mask = named && bit < p.nq ? 1ull << bit : 0ull;
+                // Once more where references rise: the same code, as it is there already.
 #pragma unroll 1
-                    for (int c = 0; c < NC; c += 8) {
-                        uint32_t r[8];
-                        load_cols<8>(s_cols + (uint32_t)c, r);
-                        if (apart) {
+                for (bool settled = false;; settled = true) {
+                    load_cols_max<NC>(s_cols, y, red);
+                    const uint32_t what = notes[(uint32_t)g % NOTES].what;
+                    load_cols_end<NC>(y);
+                    asm volatile("" : "+f"(red));
+                    if (__builtin_expect(!settled && ((what & 3u) != 3u || key0 + TILE > min(len, draft0) || apart), 0)) {
+                        // Rows that do not see this thread's key: -inf in S^T itself; rows with a
+                        // power of their own: the common one (in two steps, each a power of two that exists).
+                        const int key = key0 + (quarter >> 1) * PAGE + key_of(mine % PAGE), bit = key - draft0;
+                        const bool there = key < len && (what >> (quarter >> 1) & 1u), named = bit >= 0;
+                        const uint64_t mask = named && bit < p.nq ? 1ull << bit : 0ull;
+#pragma unroll 1
+                        for (int c = 0; c < NC; c += 8) {
+                            uint32_t r[8];
+                            load_cols<8>(s_cols + (uint32_t)c, r);
+                            if (apart) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int down = -__float_as_int(lds_f32(exps + (uint32_t)(c + e) * 4)), half = down >> 1;
-                                r[e] = __float_as_uint(__uint_as_float(r[e]) * __uint_as_float((uint32_t)(127 - half) << 23) *
-                                                       __uint_as_float((uint32_t)(127 - (down - half)) << 23));
+                                for (int e = 0; e < 8; ++e) {
+                                    const int down = -__float_as_int(lds_f32(exps + (uint32_t)(c + e) * 4)), half = down >> 1;
+                                    r[e] = __float_as_uint(__uint_as_float(r[e]) * __uint_as_float((uint32_t)(127 - half) << 23) *
+                                                           __uint_as_float((uint32_t)(127 - (down - half)) << 23));
+                                }
                             }
+#pragma unroll
+                            for (int e = 0; e < 8; e += 2) {
+                                const uint4 w = lds128(word + (uint32_t)(c + e) * 8);
+                                const uint64_t w0 = (uint64_t)w.y << 32 | w.x, w1 = (uint64_t)w.w << 32 | w.z;
+                                if (!there || (named && !(w0 & mask))) r[e] = 0xFF800000u;
+                                if (!there || (named && !(w1 & mask))) r[e + 1] = 0xFF800000u;
+                            }
+                            ptx::tmem_st8(s_cols + (uint32_t)c, r);
                         }
+                        ptx::tmem_wait_st();
+                        load_cols<NC>(s_cols, y);
+                        red = INFINITY;
+                    }
+                    auto refer = [&] {
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            const uint4 w = lds128(word + (uint32_t)(c + e) * 8);
-                            const uint64_t w0 = (uint64_t)w.y << 32 | w.x, w1 = (uint64_t)w.w << 32 | w.z;
-                            if (!there || (named && !(w0 & mask))) r[e] = 0xFF800000u;
-                            if (!there || (named && !(w1 & mask))) r[e + 1] = 0xFF800000u;
+                        for (int c = 0; c < NC; c += 4) {
+                            const uint4 a = lds128(par + (uint32_t)(c * 4));
+                            const uint64_t f = ptx::f2_pack(factor, factor);
+                            float v[4];
+                            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), f,
+                                                       ptx::f2_pack(__uint_as_float(a.x), __uint_as_float(a.y))), v[0], v[1]);
+                            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), f,
+                                                       ptx::f2_pack(__uint_as_float(a.z), __uint_as_float(a.w))), v[2], v[3]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) y[c + e] = __float_as_uint(v[e]);
                         }
-                        ptx::tmem_st8(s_cols + (uint32_t)c, r);
+                    };
+                    refer();
+                    if (settled) break;
+                    // Whether a score exceeds its row's reference.  Seldom a look at each: none can
+                    // where the key's largest score does not exceed the lowest reference.
+                    bool exceeds = !(fmaf(red, factor, lowest) <= SHIFT + RISE);
+                    if (__builtin_expect(__any_sync(0xffffffffu, exceeds), 0)) {
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < NC; c += 2) top[c / 2 % 4] = ptx::fmax3(top[c / 2 % 4], __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
+                        exceeds = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > SHIFT + RISE;
                     }
-                    ptx::tmem_wait_st();
-                    load_cols<NC>(s_cols, y);
-                    red = INFINITY;
-                }
-                auto refer = [&] {
-#pragma unroll
-                    for (int c = 0; c < NC; c += 4) {
-                        const uint4 a = lds128(par + (uint32_t)(c * 4));
-                        const uint64_t f = ptx::f2_pack(factor, factor);
-                        float v[4];
-                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), f,
-                                                   ptx::f2_pack(__uint_as_float(a.x), __uint_as_float(a.y))), v[0], v[1]);
-                        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), f,
-                                                   ptx::f2_pack(__uint_as_float(a.z), __uint_as_float(a.w))), v[2], v[3]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[c + e] = __float_as_uint(v[e]);
-                    }
-                };
-                refer();
-                // Whether a score exceeds its row's reference.  Seldom a look at each: none can
-                // where the key's largest score does not exceed the lowest reference.
-                bool exceeds = !(fmaf(red, factor, lowest) <= SHIFT + RISE);
-                if (__builtin_expect(__any_sync(0xffffffffu, exceeds), 0)) {
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < NC; c += 2) top[c / 2 % 4] = ptx::fmax3(top[c / 2 % 4], __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
-                    exceeds = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > SHIFT + RISE;
-                }
-                if (__builtin_expect(any_of(NB_VOTE + group, 128, !ok || exceeds), 0)) {
+                    if (__builtin_expect(!any_of(NB_VOTE + group, 128, !ok || exceeds), 1)) break;
                     // An abort that one warp of the group has met: all four leave here together.
                     dead = any_of(NB_VOTE + group, 128, !ok);
                     if (dead) break;
@@ -1032,9 +1036,11 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                         sts_f32(corr + (uint32_t)t * 4, old == -INFINITY ? 0.f : ptx::ex2(old - now));
                     }
                     ptx::named_barrier_sync(NB_GROUP + group, 128);
+                    if (last >= 0) {
 #pragma unroll
-                    for (int c = 0; c < NC / 2; ++c)
-                        l[c] = ptx::f2_mul(l[c], ptx::f2_pack(lds_f32(corr + (uint32_t)c * 8), lds_f32(corr + (uint32_t)c * 8 + 4)));
+                        for (int c = 0; c < NC / 2; ++c)
+                            l[c] = ptx::f2_mul(l[c], ptx::f2_pack(lds_f32(corr + (uint32_t)c * 8), lds_f32(corr + (uint32_t)c * 8 + 4)));
+                    }
                     if (last >= 0 && ok) {  // what the products have summed
                         ok = warp_wait(bar(L::B_PDONE + stream * L::PBUFS + last % L::PBUFS), (uint32_t)(last / L::PBUFS) & 1u, limit, abort_flag,
                                        0x2700 + L::B_PDONE + last % L::PBUFS);
@@ -1049,11 +1055,10 @@ __global__ void __launch_bounds__(THREADS, 1) fa_tree_kernel(const __grid_consta
                         }
                         ptx::tmem_wait_st();
                     }
-                    load_cols<NC>(s_cols, y);
-                    refer();
                     lowest = lds_f32(par + (uint32_t)(lane % NC) * 4);
                     lowest = warp_max(lowest);
                 }
+                if (dead) break;
                 // S^T of this tile is in registers.
                 ptx::tc_fence_before_sync();
                 __syncwarp();
