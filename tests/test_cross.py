@@ -150,6 +150,38 @@ def test_one_row_views():
     compare(q, k, v, do, None, run_all(qv, k, v, do, None))
 
 
+def test_places_beyond_32_bits():
+    """Batches 2^31 elements apart, in what is read and in what is written."""
+    B, H, Hkv, Nq, Nk, d = 2, 4, 2, 40, 150, 64
+    lens = [150, 77]
+    q, k, v, do = draw(B, H, Hkv, Nq, Nk, d, lens, 31)
+    want = run_all(q, k, v, do, lens)
+    wide = [torch.empty((1 << 31) + (1 << 20), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    at = [0] * 4  # (an output shares a buffer with no other tensor, but dk with dv)
+
+    def far(side, like, fill):
+        """A view of one of the wide buffers, its batches 2^31 elements apart."""
+        b, h, n, c = like.shape
+        t = wide[side][at[side]:].as_strided((b, h, n, c), (1 << 31, n * c, c, 1))
+        at[side] += h * n * c
+        if fill:
+            t.copy_(like)
+        return t
+
+    n = device_lens(lens)
+    q2, k2, v2, do2 = (far(0, t, True) for t in (q, k, v, do))
+    o2, dq2, dk2, dv2 = (far(side, t, False) for side, t in ((1, q), (2, q), (3, k), (3, v)))
+    lse = torch.empty((B, H, Nq), device="cuda")
+    ws = torch.empty(max(16, fa.cross_fwd_workspace_bytes(B, H, Hkv, Nq, Nk, d)), dtype=torch.uint8, device="cuda")
+    fa.cross_fwd_into(q2, k2, v2, o2, lse, ws, n)
+    ws = torch.empty(fa.cross_bwd_workspace_bytes(B, H, Hkv, Nq, Nk, d), dtype=torch.uint8, device="cuda")
+    fa.cross_bwd_into(q2, k2, v2, o2, lse, do2, dq2, dk2, dv2, ws, n)
+    torch.cuda.synchronize()
+    assert fa.check_device_status() == 0
+    assert torch.equal(o2, want["o"]) and torch.equal(lse, want["lse"])
+    compare(q, k, v, do, lens, {"o": o2, "lse": lse, "dq": dq2, "dk": dk2, "dv": dv2})
+
+
 def test_expanded_states():
     """Beams share one encoder's states: batch stride 0; a shared head: head stride 0."""
     gen = torch.Generator("cuda").manual_seed(11)

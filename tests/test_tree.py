@@ -221,6 +221,26 @@ def test_long_and_many(B, H, T, n, d):
 
 
 @gpu
+@pytest.mark.parametrize("T", [4, 40])
+def test_pages_beyond_32_bits(T):
+    """A pool of more than 2^32 bytes, its last pages in use."""
+    d, lens = 128, [150, T + 64]
+    pool, table, n = ref.make_cache(lens, 2, d, seed=T)
+    pages, first = pool.shape[0], (1 << 32) // (2 * 9216) + 5
+    wide = torch.empty((first + pages, 2, 9216), dtype=torch.uint8, device="cuda")
+    wide[first:] = pool.cuda()
+    q, words = rand((2, 4, T, d), T), trees(2, T, 5)
+    small, large = dev(pool, table, n), (wide, (table + first).to(torch.int32).cuda(), n.cuda())
+    for a, b in zip(fa.qcache_tree(q.cuda(), words.cuda(), *small), fa.qcache_tree(q.cuda(), words.cuda(), *large)):
+        assert torch.equal(a, b)
+    path = torch.tensor([[1, 3], [0, 2]], dtype=torch.int32, device="cuda")
+    assert torch.equal(fa.qcache_commit(*small, path, T), fa.qcache_commit(*large, path, T))
+    torch.cuda.synchronize()
+    assert fa.check_device_status() == 0
+    assert torch.equal(small[0], wide[first:])
+
+
+@gpu
 @pytest.mark.parametrize("T, H", [(4, 4), (48, 4)])
 def test_pages_and_lengths_out_of_range_are_skipped_and_reported(T, H):
     lens = [300, 200]
