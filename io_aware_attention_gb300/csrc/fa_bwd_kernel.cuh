@@ -632,6 +632,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
                             w[c] = ptx::pack_bf16x2(__uint_as_float(o[2 * c]) * mul, __uint_as_float(o[2 * c + 1]) * mul);
+                        // Rows behind the last key: selected, as 0 * NaN of a query's or dO's row is NaN.
+                        if (CROSS && key >= it.len) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) w[c] = 0u;
+                        }
                         if (key_ok) {
 #pragma unroll
                             for (int u = 0; u < 4; ++u)
