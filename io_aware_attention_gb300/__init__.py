@@ -988,16 +988,17 @@ def tree_words(parents):
     """The words of drafted trees for :func:`qcache_tree`, and the drafts' depths:
     parents is an integer tensor (B, T) or (T,), T <= 64, each entry the index of an
     earlier draft or negative for a child of the last accepted token.  Returns
-    ``(words int64, depths int64)`` of its shape and device: draft i's own bit and its
-    ancestors', and how many ancestors it has (its token stands at the last accepted
-    one's position + 1 + depth)."""
+    ``(words int64, depths int64)`` of its shape and device, contiguous: draft i's own
+    bit and its ancestors', and how many ancestors it has (its token stands at the last
+    accepted one's position + 1 + depth)."""
     import torch
 
     if parents.dim() not in (1, 2) or parents.dtype.is_floating_point or not 1 <= parents.shape[-1] <= 64:
         raise ValueError("parents must be an integer (B, T) or (T,) tensor, T between 1 and 64")
     T = parents.shape[-1]
+    parents = parents.long().contiguous()
     index = torch.arange(T, device=parents.device)
-    up = torch.where(parents >= 0, parents.long(), index)  # a root is its own
+    up = torch.where(parents >= 0, parents, index)  # a root is its own
     if not parents.is_cuda and bool((up > index).any() | (parents == index).any()):
         raise ValueError("a parent must come before its child")
     up = torch.minimum(up, index)
