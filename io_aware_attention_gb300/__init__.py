@@ -990,7 +990,11 @@ def tree_words(parents):
     earlier draft or negative for a child of the last accepted token.  Returns
     ``(words int64, depths int64)`` of its shape and device, contiguous: draft i's own
     bit and its ancestors', and how many ancestors it has (its token stands at the last
-    accepted one's position + 1 + depth)."""
+    accepted one's position + 1 + depth).
+
+    A parent that does not come before its child is an error, raised where parents are
+    on the CPU.  On a GPU, which is not waited for, such a draft gets the word 0 and the
+    depth -1: no draft sees it, and neither it nor what follows from it is to be accepted."""
     import torch
 
     if parents.dim() not in (1, 2) or parents.dtype.is_floating_point or not 1 <= parents.shape[-1] <= 64:
@@ -998,14 +1002,18 @@ def tree_words(parents):
     T = parents.shape[-1]
     parents = parents.long().contiguous()
     index = torch.arange(T, device=parents.device)
-    up = torch.where(parents >= 0, parents, index)  # a root is its own
-    if not parents.is_cuda and bool((up > index).any() | (parents == index).any()):
+    early = parents < index
+    if not parents.is_cuda and not bool(early.all()):
         raise ValueError("a parent must come before its child")
-    up = torch.minimum(up, index)
-    words = torch.ones_like(up) << index
+    up = torch.where(early & (parents >= 0), parents, index)  # a root is its own
+    words = early.long() << index
     # Every round doubles the ancestors that a word holds.
-    for _ in range((T - 1).bit_length()):
-        words, up = words | words.gather(-1, up), up.gather(-1, up)
+    reach = 1
+    while reach < T:
+        words = words | words.gather(-1, up)
+        reach *= 2
+        if reach < T:
+            up = up.gather(-1, up)
     depths = (words.unsqueeze(-1) >> index & 1).sum(-1) - 1
     return words, depths
 
