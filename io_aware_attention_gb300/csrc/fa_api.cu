@@ -873,7 +873,7 @@ int64_t tree_blocks(int sms, int64_t B, int64_t Hkv, int64_t rb, int64_t max_pag
 }
 // 8 rows and fewer, one operand of the legacy product, run in the kernel of few rows:
 // 8 x 32 kv heads x 16384 keys, d128, 125 us with 8 rows against 138 in that of many,
-// and 217 against 139 with 16.  (Where a call is all latency, 16 rows x 8 kv heads x
+// and in a form of two operands 217 against 139 with 16.  (Where a call is all latency, 16 rows x 8 kv heads x
 // 2000 keys, it is 13 against 16, less than the call takes on the host.)
 bool tree_many(int64_t rows) { return rows > 8; }
 size_t tree_part_bytes(int64_t Dp, int n) { return (size_t)n * (size_t)(Dp + 2) * 4; }
@@ -1834,8 +1834,7 @@ fa_status fa_qcache_tree_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int6
         const TreeRows r = tree_rows(rows);
         *bytes = tree_ws(tree_blocks(info.sms, B, Hkv, r.rb, max_pages), Dp, r.n);
     } else {
-        const QRows r = qcache_rows(H / Hkv, T);
-        *bytes = qcache_decode_ws(qcache_decode_blocks(info.sms, B, Hkv, r.rb, max_pages), Dp, r.nt);
+        *bytes = qcache_decode_ws(qcache_decode_blocks(info.sms, B, Hkv, 1, max_pages), Dp, 1);
     }
     return FA_OK;
 }
@@ -1869,10 +1868,9 @@ fa_status fa_qcache_tree(const void* q, const uint64_t* words, const void* pool,
     if (ds != FA_OK) return ds;
     const int64_t rows = H / Hkv * T, Dp = padded_head_size(d);
     const bool many = tree_many(rows);
-    const QRows r = qcache_rows(H / Hkv, T);
-    const TreeRows tr = tree_rows(rows);
-    const int64_t blocks = many ? tree_blocks(info.sms, B, Hkv, tr.rb, max_pages) : qcache_decode_blocks(info.sms, B, Hkv, r.rb, max_pages);
-    const size_t part = many ? tree_part_bytes(Dp, tr.n) : qcache_part_bytes(Dp, r.nt);
+    const TreeRows r = tree_rows(rows);  // (few rows are one block of one tile)
+    const int64_t blocks = many ? tree_blocks(info.sms, B, Hkv, r.rb, max_pages) : qcache_decode_blocks(info.sms, B, Hkv, 1, max_pages);
+    const size_t part = many ? tree_part_bytes(Dp, r.n) : qcache_part_bytes(Dp, 1);
     const size_t need = (size_t)blocks * (2 * part + 8);
     if (workspace_bytes < need || taken(workspace, need) || overlaps(workspace, need, o, qb) || overlaps(workspace, need, lse, lb))
         return FA_ERR_INVALID_ARG;
@@ -1890,7 +1888,7 @@ fa_status fa_qcache_tree(const void* q, const uint64_t* words, const void* pool,
     p.hkv = (int)Hkv;
     p.nq = (int)T;
     p.rows = (int)rows;
-    p.rb = (int)(many ? tr.rb : r.rb);
+    p.rb = (int)(many ? r.rb : 1);
     p.d = (int)d;
     p.max_pages = (int)max_pages;
     p.num_pages = (int)num_pages;
@@ -1899,14 +1897,12 @@ fa_status fa_qcache_tree(const void* q, const uint64_t* words, const void* pool,
     p.debug_skip = g_debug_skip_k.load(std::memory_order_relaxed);
     p.v_scale = v_scale;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (many) return Dp == 128 ? launch_tree_n<128>(tr.n, p, blocks, dev, st) : launch_tree_n<64>(tr.n, p, blocks, dev, st);
+    if (many) return Dp == 128 ? launch_tree_n<128>(r.n, p, blocks, dev, st) : launch_tree_n<64>(r.n, p, blocks, dev, st);
     if (Dp == 128)
-        return r.rows <= 4 ? launch_qcache_decode<128, 1, true, true>(p, blocks, dev, st)
-               : r.nt == 1 ? launch_qcache_decode<128, 1, false, true>(p, blocks, dev, st)
-                           : launch_qcache_decode<128, 2, false, true>(p, blocks, dev, st);
-    return r.rows <= 4 ? launch_qcache_decode<64, 1, true, true>(p, blocks, dev, st)
-           : r.nt == 1 ? launch_qcache_decode<64, 1, false, true>(p, blocks, dev, st)
-                       : launch_qcache_decode<64, 2, false, true>(p, blocks, dev, st);
+        return rows <= 4 ? launch_qcache_decode<128, 1, true, true>(p, blocks, dev, st)
+                         : launch_qcache_decode<128, 1, false, true>(p, blocks, dev, st);
+    return rows <= 4 ? launch_qcache_decode<64, 1, true, true>(p, blocks, dev, st)
+                     : launch_qcache_decode<64, 1, false, true>(p, blocks, dev, st);
 }
 
 fa_status fa_qcache_commit(void* pool, int64_t num_pages, const int32_t* table, int64_t max_pages, const int32_t* lens,

@@ -757,6 +757,7 @@ __device__ __forceinline__ uint32_t hmul2_by(uint32_t a, uint32_t f)
 template <int D, int NT, bool FOLD = false, bool TREE = false>
 struct Rows {
     static_assert(!FOLD || NT == 1, "one tile, folded");
+    static_assert(!TREE || NT == 1, "a tree of more rows than a tile holds runs in fa_tree_kernel");
     // The query row of a tile's row.
     static __device__ __forceinline__ int row_of(int r) { return FOLD ? r & 3 : r; }
     uint32_t q[NT][D / 16][2];
@@ -765,7 +766,7 @@ struct Rows {
     int len, min_lim;
     int drafts;             // TREE: place of draft 0 (below 0 where the sequence is shorter)
     const uint64_t* words;  // TREE: of the rows' sequence
-    int row0, nq;           // TREE: the row block's first row
+    int nq;                 // TREE
 
     // Whether column j of tile nt sees key x.
     __device__ __forceinline__ bool sees(int nt, int j, int x) const
@@ -773,16 +774,14 @@ struct Rows {
         if constexpr (!TREE) return x < lim[nt][j];
         if (x < lim[nt][j]) return true;
         const int bit = x - drafts;
-        return x < len && bit < nq && (word[nt][j] >> (bit & 63) & 1u);
+        return x < len && bit < nq && (word[j] >> (bit & 63) & 1u);
     }
-    uint64_t word[NT][2];   // TREE: valid after load_words
+    uint64_t word[2];  // TREE: of the columns' rows, valid after load_words
     __device__ __forceinline__ void load_words()
     {
         const int t = threadIdx.x & 3;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) word[nt][j] = __ldg(words + (row0 + nt * 8 + row_of(2 * t + j)) % nq);
+        for (int j = 0; j < 2; ++j) word[j] = __ldg(words + row_of(2 * t + j) % nq);
     }
 
     // The rows' raw entries: issued before a warp's first copies, so that they
@@ -821,7 +820,6 @@ struct Rows {
             drafts = max(raw.len, 0) - p.nq;
             min_lim = min(len, drafts);
             words = p.words + (int64_t)b * p.nq;
-            row0 = r0;
             nq = p.nq;
         }
 #pragma unroll
