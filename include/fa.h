@@ -482,8 +482,11 @@ fa_status fa_qcache_decode(const void *q, const void *pool, int64_t num_pages, c
  *             by fa_qcache_tree_workspace_bytes).
  * Queries may be of any size, and a row that holds NaN or infinities (a padded
  * draft's) leaves the others as they are.  With more than 8 rows a kv head (H / Hkv * T)
- * a probability is rounded to fp16: o is off by at most 2^-11 * sum p |v| more than its
- * rounding to bf16, where fa_qcache_decode's 22 bits do not show.
+ * a probability p is held as one fp16 number, its sum in fp32 from the unrounded ones:
+ * beside fp32's own errors and the rounding to bf16, o is off by at most
+ *     2^-11 * sum p |v| + 2^-32 * max p * sum |v|
+ * (keys below 2^-21 of the row's heaviest keep fewer bits, below 2^-32 none).  With up
+ * to 8 rows, and in fa_qcache_decode, p has 22 bits, which do not show.
  * Results do not depend on timing.
  */
 fa_status fa_qcache_tree_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t T, int64_t d, int64_t max_pages,
@@ -502,7 +505,9 @@ fa_status fa_qcache_tree(const void *q, const uint64_t *words, const void *pool,
  *             0 .. T-1; the first negative entry ends it.  An entry that is no draft of its
  *             sequence or not above the one before ends it too and is reported by
  *             fa_check_device_status as FA_ERR_INVALID_ARG.
- *   lens_out  int32 (B), not lens itself: max(lens - T, 0) + the path's length.
+ *   lens_out  int32 (B), not lens itself, which every kv head's part of the call reads:
+ *             max(lens - T, 0) + the path's length.  A captured loop copies it into
+ *             lens before the next step.
  * No two sequences of a call may hold drafts in one page.
  */
 fa_status fa_qcache_commit(void *pool, int64_t num_pages, const int32_t *table, int64_t max_pages, const int32_t *lens,

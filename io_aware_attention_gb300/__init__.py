@@ -1074,8 +1074,8 @@ def qcache_tree(q, words, pool, table, lens, scale: float | None = None, k_scale
     """Attention of a tree of T <= 64 drafted tokens, q (B, H, T, d), over the 4-bit
     cache whose newest T keys they are (appended; lens counts them).  Draft i sees
     every key before the drafts, and draft j where bit j of words[b, i] is set
-    (words int64 (B, T), see :func:`tree_words`).  Grouped heads and results as in
-    :func:`qcache_decode`."""
+    (words int64 (B, T), see :func:`tree_words`).  q is contiguous, as rope returns it;
+    grouped heads and results as in :func:`qcache_decode`."""
     import torch
 
     if stream is not None:  # the workspace and the results belong to the stream that writes them
@@ -1099,7 +1099,8 @@ def qcache_commit(pool, table, lens, path, drafts: int, stream=None):
     """Keeps the accepted path of a verified tree: of the newest ``drafts`` keys of
     every sequence, those that path (int32 (B, A), rising, -1 after the last) names
     move to the places behind the context, in order, as they are held.  Returns the
-    new lengths, int32 (B): max(lens - drafts, 0) + accepted ones."""
+    new lengths, int32 (B): max(lens - drafts, 0) + accepted ones, in a tensor of their own
+    (a captured loop copies them into lens)."""
     import torch
 
     if stream is not None:

@@ -857,7 +857,13 @@ size_t qcache_decode_ws(int64_t blocks, int64_t Dp, int nt)
     return (size_t)blocks * (2 * qcache_part_bytes(Dp, nt) + 8);
 }
 
-// Query rows of a kv head in the kernel of many rows: blocks of n.
+// Query rows of a kv head in the kernel of many rows: blocks of n, the smallest that
+// holds them all, as every block goes through all keys.  Device us with blocks of
+// 16 / 32 / 64 / 128, 8 x 8 kv heads x 16384 keys, d128: 9 to 16 rows 46 / 55 / 61 / 87,
+// 18 to 32 rows 76 / 56 / 62 / 88, 33 to 64 rows - / 90 / 62 / 88, 66 to 128 rows
+// - / - / 102 / 90 (24 x 4 kv heads x 30 to 5000 keys, d64, 84 rows: 56 / 49).  One row
+// past 128 costs a second block, 91 -> 154; three blocks of 64 would take 146 with 132
+// to 192 rows, two of 128 155 to 157, and 158 with 256.
 struct TreeRows {
     int64_t rb;
     int n;
